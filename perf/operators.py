@@ -138,7 +138,11 @@ def prepare(case, seed):
         t, k, d, p = (case[x] for x in ("tokens", "kv_heads", "dim", "page"))
         pages = (t + t // 4) // p + 1
         shape = _pool_shape(case, pages)
-        s["loc"] = torch.randperm(pages * p, generator=g, device=DEV)[:t].to(torch.int32)
+        if t < 512:  # a decoding step: every token at its own request's place
+            s["loc"] = torch.randperm(pages * p, generator=g, device=DEV)[:t].to(torch.int32)
+        else:  # prompts: whole pages, anywhere in the pool
+            at = torch.arange(t, device=DEV)
+            s["loc"] = (torch.randperm(pages, generator=g, device=DEV)[at // p] * p + at % p).to(torch.int32)
         # the pools start as other requests left them
         codes = [torch.randint(0, 127, shape, generator=g, device=DEV, dtype=torch.uint8).view(E4M3) for _ in "kv"]
         s["pools"] = tuple(codes)
