@@ -91,10 +91,13 @@ enum b2pa_device_error {
     B2PA_DEV_TIMEOUT = 4,       /* a pipeline wait in a kernel gave up; the call's output is undefined */
     B2PA_DEV_BAD_CUM_KV = 8,    /* cum_kv[b+1] - cum_kv[b] != seq_lens[b] (checked only where cum_kv is read) */
     B2PA_DEV_OVERFLOW = 16,     /* more work items than the workspace holds (cannot happen for valid bounds) */
-    B2PA_DEV_BAD_SLOT = 32,     /* b2pa_append_kv: a cache_loc entry outside [0, num_pages * page_size);
-                                   that token is not written */
-    B2PA_DEV_BAD_SCALE = 64     /* b2pa_context_attention_tensor_scales: the device bmm1_scale is not
+    B2PA_DEV_BAD_SLOT = 32,     /* b2pa_append_kv, b2pa_append_kv_scaled: a cache_loc entry outside
+                                   [0, num_pages * page_size); that token is not written.
+                                   b2pa_read_kv_scaled: it reads as zeros */
+    B2PA_DEV_BAD_SCALE = 64,    /* b2pa_context_attention_tensor_scales: the device bmm1_scale is not
                                    finite and > 0, or bmm2_scale is not finite; nothing is written */
+    B2PA_DEV_BAD_POSITION = 128 /* b2pa_qk_norm_rope: a position outside the table; that token's rows are
+                                   not written */
 };
 
 /* Kernel paths (b2pa_set_kernel_path). */
@@ -368,6 +371,84 @@ B2PA_API int b2pa_debug_gather_ragged(const b2pa_tensor* k_pool, const b2pa_tens
 B2PA_API int b2pa_append_kv(const b2pa_tensor* k_new, const b2pa_tensor* v_new, const b2pa_tensor* k_pool,
                             const b2pa_tensor* v_pool, const b2pa_tensor* cache_loc, float k_scale, float v_scale,
                             int32_t layout, b2pa_stream_t stream);
+
+/*
+ * b2pa_qk_norm_rope -- RMS norm of each query and key head, then the rotary
+ * position rotation, in one pass: the step before the K/V write.  No
+ * counterpart on the pages.
+ *
+ * For a row x (token t, head h), with w the norm weight of its tensor:
+ *     y = w * x / sqrt(mean(x^2) + eps)           (NULL weight: y = x)
+ * and for each frequency i < R / 2, with row `pos` of cos_sin holding c_i and
+ * s_i and pos = positions[axis_of[i], t]:
+ *     (a, b) -> (a c_i - b s_i, b c_i + a s_i)
+ * where (a, b) = (y[i], y[i + R/2]), or (y[2i], y[2i + 1]) if interleaved.
+ * Elements from R on are not rotated.  Computed in binary32 and rounded to
+ * bf16 once.
+ *
+ *  q, q_out      [T, H, D] bf16; k, k_out [T, Hkv, D] bf16 (any H and Hkv >= 1).
+ *                D is a multiple of 8, at most 256; stride[2] == 1, the other
+ *                strides multiples of 8, 16-byte aligned.  q_out may be q itself
+ *                and k_out k itself (same pointer and strides); otherwise outputs
+ *                must not overlap any input, and the rows of an output never
+ *                overlap.
+ *  cos_sin       [max_position, R] fp32, stride[1] == 1, R even, 2 <= R <= D: row
+ *                p holds the R / 2 cosines of position p, then its R / 2 sines
+ *                (with any scaling of frequencies or amplitudes folded in).
+ *  positions     int32 [T], or [axes, T] with 1 to 4 axes (time, height, width of
+ *                image and video tokens); stride 1 along T.  A token with a
+ *                position outside [0, max_position) on any axis sets
+ *                B2PA_DEV_BAD_POSITION and its rows are not written.
+ *  q_weight, k_weight  NULL, or contiguous bf16 or fp32 [D], 16-byte aligned.
+ *  eps           finite, >= 0.
+ *  axis_of       HOST array of R / 2 axis numbers, one per frequency; NULL with
+ *                one axis.  Read before the call returns.
+ *
+ * Asynchronous on `stream`; one kernel.
+ */
+B2PA_API int b2pa_qk_norm_rope(const b2pa_tensor* q, const b2pa_tensor* k, const b2pa_tensor* cos_sin,
+                               const b2pa_tensor* positions, const b2pa_tensor* q_weight, const b2pa_tensor* k_weight,
+                               float eps, const int32_t* axis_of, int32_t interleaved, b2pa_tensor* q_out,
+                               b2pa_tensor* k_out, b2pa_stream_t stream);
+
+/*
+ * b2pa_append_kv_scaled -- b2pa_append_kv into e4m3 pools that hold one scale
+ * per (token, kv head) row instead of one per tensor.  No counterpart on the
+ * pages.
+ *
+ *  k_new, v_new  [T, Hkv, D] bf16, layout rules of b2pa_qk_norm_rope's rows (K and
+ *                V may have different strides).
+ *  k_pool, v_pool      e4m3 pools; 8-byte aligned, strides multiples of 8, D a
+ *                multiple of 8, at most 256.
+ *  k_scales, v_scales  fp32, the pool's shape without its last dim ([N, Hkv, P] or
+ *                [N, P, Hkv]), any positive strides.
+ *  cache_loc     contiguous int32 [T]: token n goes to slot cache_loc[n], as in
+ *                b2pa_append_kv.  The slots must be distinct: a slot named twice
+ *                ends with codes and a scale that may come from different tokens.
+ * Row x is stored as scale = 2^e, the smallest power of two (at least 2^-126)
+ * with max|x| / 2^e <= 448, and the codes x / 2^e rounded to the nearest e4m3
+ * value, ties to even.  Only finite values count for the maximum: infinities
+ * are stored as +-448 * scale and NaN as NaN.  A row without a finite nonzero
+ * value has scale 1.
+ * Asynchronous on `stream`; one kernel.  T = 0 is a no-op.
+ */
+B2PA_API int b2pa_append_kv_scaled(const b2pa_tensor* k_new, const b2pa_tensor* v_new, const b2pa_tensor* k_pool,
+                                   const b2pa_tensor* v_pool, const b2pa_tensor* k_scales,
+                                   const b2pa_tensor* v_scales, const b2pa_tensor* cache_loc, int32_t layout,
+                                   b2pa_stream_t stream);
+
+/*
+ * b2pa_read_kv_scaled -- read rows of such a cache back as bf16: row n of k_out
+ * and v_out is code * scale of slot cache_loc[n] (any order, repeats allowed),
+ * the binary32 product rounded to bf16 (exact for rows that
+ * b2pa_append_kv_scaled wrote, down to bf16's smallest values).  For code that needs 16-bit K and V of a cached
+ * prefix: k_out and v_out may be views of bf16 pools that the attention reads.
+ * A slot outside the pool reads as zeros and sets B2PA_DEV_BAD_SLOT.  The
+ * outputs' rows must not overlap.  Otherwise as b2pa_append_kv_scaled.
+ */
+B2PA_API int b2pa_read_kv_scaled(const b2pa_tensor* k_pool, const b2pa_tensor* v_pool, const b2pa_tensor* k_scales,
+                                 const b2pa_tensor* v_scales, const b2pa_tensor* cache_loc, int32_t layout,
+                                 b2pa_tensor* k_out, b2pa_tensor* v_out, b2pa_stream_t stream);
 
 /*
  * b2pa_get_device_status -- synchronise `stream`, read and clear the device

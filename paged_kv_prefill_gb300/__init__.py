@@ -29,7 +29,7 @@ PATH_AUTO, PATH_TCGEN05, PATH_GENERIC = 0, 1, 2
 STATUS = {0: "B2PA_OK", -1: "B2PA_ERR_INVALID_ARG", -2: "B2PA_ERR_UNSUPPORTED", -3: "B2PA_ERR_CUDA",
           -4: "B2PA_ERR_DEVICE"}
 DEV_BAD_REQUEST, DEV_BAD_PAGE, DEV_TIMEOUT, DEV_BAD_CUM_KV, DEV_OVERFLOW = 1, 2, 4, 8, 16
-DEV_BAD_SLOT, DEV_BAD_SCALE = 32, 64
+DEV_BAD_SLOT, DEV_BAD_SCALE, DEV_BAD_POSITION = 32, 64, 128
 
 _DTYPES = {
     torch.bfloat16: B2PA_BF16,
@@ -48,6 +48,9 @@ EXPORTED = [
     "b2pa_debug_worklist",
     "b2pa_debug_gather",
     "b2pa_append_kv",
+    "b2pa_append_kv_scaled",
+    "b2pa_read_kv_scaled",
+    "b2pa_qk_norm_rope",
     "b2pa_get_device_status",
     "b2pa_set_kernel_path",
     "b2pa_query_path",
@@ -115,6 +118,13 @@ def load(path: str = LIB_PATH):
     lib.b2pa_debug_gather.argtypes = [P, P, P, P, P, ctypes.c_int32, P, P, ctypes.c_void_p]
     lib.b2pa_debug_gather.restype = ctypes.c_int
     lib.b2pa_append_kv.argtypes = [P, P, P, P, P, ctypes.c_float, ctypes.c_float, ctypes.c_int32, ctypes.c_void_p]
+    lib.b2pa_append_kv_scaled.argtypes = [P, P, P, P, P, P, P, ctypes.c_int32, ctypes.c_void_p]
+    lib.b2pa_append_kv_scaled.restype = ctypes.c_int
+    lib.b2pa_read_kv_scaled.argtypes = [P, P, P, P, P, ctypes.c_int32, P, P, ctypes.c_void_p]
+    lib.b2pa_read_kv_scaled.restype = ctypes.c_int
+    lib.b2pa_qk_norm_rope.argtypes = [P, P, P, P, P, P, ctypes.c_float, ctypes.POINTER(ctypes.c_int32),
+                                      ctypes.c_int32, P, P, ctypes.c_void_p]
+    lib.b2pa_qk_norm_rope.restype = ctypes.c_int
     lib.b2pa_get_device_status.argtypes = [ctypes.c_void_p, ctypes.c_void_p]
     lib.b2pa_get_device_status.restype = ctypes.c_int
     lib.b2pa_set_kernel_path.argtypes = [ctypes.c_int32]
@@ -147,14 +157,7 @@ def desc(t: Optional[torch.Tensor]) -> Optional[B2paTensor]:
         raise TypeError(f"unsupported dtype {t.dtype}")
     if t.dim() > 5:
         raise ValueError("rank > 5")
-    d = B2paTensor()
-    d.data = t.data_ptr()
-    d.dtype = _DTYPES[t.dtype]
-    d.ndim = t.dim()
-    for i in range(t.dim()):
-        d.shape[i] = t.shape[i]
-        d.stride[i] = t.stride(i)
-    return d
+    return B2paTensor(t.data_ptr(), _DTYPES[t.dtype], t.dim(), tuple(t.shape), t.stride())
 
 
 def _ref(d):
@@ -167,6 +170,44 @@ def _stream_handle(stream) -> int:
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
+
+
+def _new(shape, device, stream, dtype=torch.bfloat16) -> torch.Tensor:
+    """A new tensor from the memory of the stream that the call runs on."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+class _On:
+    """The device of a call's tensors, made current for it, and the stream it runs on there.
+
+    All tensors must be on one CUDA device; an int stream handle or a torch
+    stream must belong to it."""
+
+    def __init__(self, stream, *tensors):
+        first = tensors[0].device
+        for t in tensors:
+            if t is not None and t.device != first:
+                raise ValueError(f"tensors on {first} and {t.device}: one device per call")
+        if first.type != "cuda":
+            raise ValueError(f"tensors on {first}: CUDA tensors are needed")
+        if isinstance(stream, torch.cuda.Stream) and stream.device != first:
+            raise ValueError(f"a stream of {stream.device} for tensors on {first}")
+        self.device, self.stream, self.guard = first, stream, None
+
+    def __enter__(self) -> ctypes.c_void_p:
+        if torch.cuda.current_device() != self.device.index:
+            self.guard = torch.cuda.device(self.device)
+            self.guard.__enter__()
+        return ctypes.c_void_p(_stream_handle(self.stream))
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
 
 
 def _check(status: int, where: str):
@@ -427,6 +468,92 @@ def append_kv(k_new: torch.Tensor, v_new: torch.Tensor, kv_cache, cache_loc: tor
     st = lib.b2pa_append_kv(*(ctypes.byref(x) for x in d), ctypes.c_float(k_scale), ctypes.c_float(v_scale),
                             LAYOUTS[kv_layout], ctypes.c_void_p(_stream_handle(stream)))
     _check(st, "b2pa_append_kv")
+
+
+def _two(pair, what: str):
+    if not isinstance(pair, (tuple, list)) or len(pair) != 2:
+        raise TypeError(f"{what}: a pair of tensors (K, V)")
+    return pair
+
+
+def append_kv_scaled(k_new: torch.Tensor, v_new: torch.Tensor, kv_cache, kv_scales, cache_loc: torch.Tensor,
+                     kv_layout: str = "HND", stream=None):
+    """append_kv into e4m3 pools with one scale per (token, kv head) row, in place.
+
+    kv_scales is (k_scales, v_scales), fp32 with the pools' shape without head_dim.  Each row gets
+    the smallest power of two that brings its largest value to 448 at most, and its values
+    divided by that, rounded to the nearest e4m3 value (see include/b2pa.h)."""
+    lib = load()
+    k, v = split_kv_cache(kv_cache, kv_layout)
+    ks, vs = _two(kv_scales, "kv_scales")
+    with _On(stream, k_new, v_new, k, v, ks, vs, cache_loc) as handle:
+        d = [desc(x) for x in (k_new, v_new, k, v, ks, vs, cache_loc)]
+        st = lib.b2pa_append_kv_scaled(*map(ctypes.byref, d), LAYOUTS[kv_layout], handle)
+    _check(st, "b2pa_append_kv_scaled")
+
+
+def read_kv_scaled(kv_cache, kv_scales, cache_loc: torch.Tensor, k_out: Optional[torch.Tensor] = None,
+                   v_out: Optional[torch.Tensor] = None, kv_layout: str = "HND",
+                   stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """K and V rows (bf16 [T, Hkv, D]) of slots cache_loc of a cache that append_kv_scaled wrote.
+
+    k_out and v_out may be given, as views of bf16 pools for example.  A slot outside the pool
+    reads as zeros and is flagged in device_status()."""
+    lib = load()
+    k, v = split_kv_cache(kv_cache, kv_layout)
+    ks, vs = _two(kv_scales, "kv_scales")
+    with _On(stream, k, v, ks, vs, cache_loc, k_out, v_out) as handle:
+        shape = (cache_loc.shape[0], k.shape[1 if kv_layout == "HND" else 2], k.shape[3])
+        if k_out is None:
+            k_out = _new(shape, k.device, stream)
+        if v_out is None:
+            v_out = _new(shape, k.device, stream)
+        d = [desc(x) for x in (k, v, ks, vs, cache_loc)]
+        dko, dvo = desc(k_out), desc(v_out)
+        st = lib.b2pa_read_kv_scaled(*map(ctypes.byref, d), LAYOUTS[kv_layout], ctypes.byref(dko), ctypes.byref(dvo),
+                                     handle)
+    _check(st, "b2pa_read_kv_scaled")
+    return k_out, v_out
+
+
+def qk_norm_rope(
+    query: torch.Tensor,
+    key: torch.Tensor,
+    cos_sin: torch.Tensor,
+    positions: torch.Tensor,
+    q_weight: Optional[torch.Tensor] = None,
+    k_weight: Optional[torch.Tensor] = None,
+    eps: float = 1e-6,
+    axis_of: Optional[Sequence[int]] = None,
+    interleaved: bool = False,
+    q_out: Optional[torch.Tensor] = None,
+    k_out: Optional[torch.Tensor] = None,
+    stream=None,
+) -> Tuple[torch.Tensor, torch.Tensor]:
+    """RMS norm of each query and key head (where its weight is given) and the rotary rotation, in
+    one pass; returns (q_out, k_out), bf16 (see include/b2pa.h).
+
+    query [T, H, D] and key [T, Hkv, D] may be views of one projection's output, and q_out / k_out
+    may be query / key themselves.  cos_sin [max_position, R] fp32 holds R / 2 cosines and R / 2
+    sines per position.  positions is int32 [T], or [axes, T] with axis_of naming the axis of
+    each of the R / 2 frequencies."""
+    lib = load()
+    axes = None
+    if axis_of is not None:
+        if len(axis_of) != cos_sin.shape[-1] // 2:
+            raise ValueError(f"axis_of: one axis for each of the {cos_sin.shape[-1] // 2} frequencies")
+        axes = (ctypes.c_int32 * len(axis_of))(*axis_of)
+    with _On(stream, query, key, cos_sin, positions, q_weight, k_weight, q_out, k_out) as handle:
+        if q_out is None:
+            q_out = _new(query.shape, query.device, stream)
+        if k_out is None:
+            k_out = _new(key.shape, query.device, stream)
+        d = [desc(x) for x in (query, key, cos_sin, positions, q_weight, k_weight)]
+        dqo, dko = desc(q_out), desc(k_out)
+        st = lib.b2pa_qk_norm_rope(*map(_ref, d), float(eps), axes, 1 if interleaved else 0, ctypes.byref(dqo),
+                                   ctypes.byref(dko), handle)
+    _check(st, "b2pa_qk_norm_rope")
+    return q_out, k_out
 
 
 def device_status(stream=None) -> int:

@@ -16,6 +16,7 @@
 #include "../../include/b2pa.h"
 #include "append.cuh"
 #include "common.cuh"
+#include "host.cuh"
 
 using namespace b2pa;
 
@@ -29,7 +30,16 @@ std::atomic<void*> g_ev_stop{nullptr};
 std::atomic<unsigned long long> g_wait_limit_ns{kWaitLimitNs};
 std::atomic<int> g_inject_stall{0};
 
-int fail(int status, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
+}  // namespace
+
+// The helpers that the entry points of ops.cu share (declared in host.cuh).
+namespace b2pa {
+
+void clear_error() { g_last_error.clear(); }
+int kernel_path() { return g_path.load(); }
+unsigned long long wait_limit_ns() { return g_wait_limit_ns.load(); }
+int inject_stall() { return g_inject_stall.load(); }
+
 int fail(int status, const char* fmt, ...)
 {
     char buf[512];
@@ -48,13 +58,8 @@ int cuda_fail(cudaError_t e, const char* what)
 
 // ------------------------------------------------------------------ device info
 
-struct DevInfo {
-    bool init = false;
-    int sms = 0;
-    int major = 0, minor = 0;
-};
-std::mutex g_dev_mu;
-DevInfo g_dev[64];
+static std::mutex g_dev_mu;
+static DevInfo g_dev[64];
 
 int device_info(int* dev_out, DevInfo* info)
 {
@@ -89,8 +94,8 @@ struct Workspace {
     uint8_t* mem;
     size_t bytes;
 };
-std::mutex g_ws_mu;
-std::vector<Workspace> g_ws;
+static std::mutex g_ws_mu;
+static std::vector<Workspace> g_ws;
 constexpr size_t kWsHeader = 256;
 
 int get_workspace_bytes(int dev, cudaStream_t stream, size_t need, Workspace* out);
@@ -163,11 +168,61 @@ bool find_workspace(int dev, cudaStream_t stream, Workspace* out)
     return false;
 }
 
-// ------------------------------------------------------------------ tensor maps
+// ------------------------------------------------------------------ status words
 
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+// Device error words of the entry points without a workspace: one word per
+// (device, stream), cut from pages that stay where they are until
+// b2pa_release, so that a captured graph may keep its word's address and a
+// stream seen first during a capture needs no allocation once its device has
+// a page with room.
+struct StatusPage {
+    int dev;
+    unsigned* mem;
+    std::vector<cudaStream_t> streams;  // owner of word i
+};
+static std::vector<StatusPage> g_status;  // under g_ws_mu
+constexpr size_t kStatusWords = 1024;
+
+static unsigned* find_status_word(int dev, cudaStream_t stream)  // g_ws_mu held
+{
+    for (auto& pg : g_status)
+        for (size_t i = 0; pg.dev == dev && i < pg.streams.size(); ++i)
+            if (pg.streams[i] == stream)
+                return pg.mem + i;
+    return nullptr;
+}
+
+int status_word(int dev, cudaStream_t stream, unsigned** out)
+{
+    std::lock_guard<std::mutex> lk(g_ws_mu);
+    if ((*out = find_status_word(dev, stream)) != nullptr)
+        return B2PA_OK;
+    for (auto& pg : g_status)
+        if (pg.dev == dev && pg.streams.size() < kStatusWords) {
+            pg.streams.push_back(stream);
+            *out = pg.mem + pg.streams.size() - 1;
+            return B2PA_OK;
+        }
+    cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
+    cudaStreamIsCapturing(stream, &cs);
+    if (cs != cudaStreamCaptureStatusNone)
+        return fail(B2PA_ERR_CUDA, "the first call on a device cannot be captured; make one call before capturing");
+    StatusPage pg{dev, nullptr, {stream}};
+    cudaError_t e = cudaMalloc(&pg.mem, kStatusWords * sizeof(unsigned));
+    if (e != cudaSuccess)
+        return cuda_fail(e, "cudaMalloc(status words)");
+    // complete before any stream's kernel may set a bit
+    if ((e = cudaMemset(pg.mem, 0, kStatusWords * sizeof(unsigned))) != cudaSuccess ||
+        (e = cudaDeviceSynchronize()) != cudaSuccess) {
+        cudaFree(pg.mem);
+        return cuda_fail(e, "cudaMemset(status words)");
+    }
+    g_status.push_back(pg);
+    *out = pg.mem;
+    return B2PA_OK;
+}
+
+// ------------------------------------------------------------------ tensor maps
 
 EncodeTiledFn encode_fn()
 {
@@ -190,20 +245,6 @@ bool is_vec(const b2pa_tensor* t, int dtype, int64_t n)
 {
     return t && t->data && t->dtype == dtype && t->ndim == 1 && t->shape[0] == n && (n <= 1 || t->stride[0] == 1);
 }
-
-struct Problem {
-    int T, H, D, B, Hkv, P, N, max_pages, layout;
-    bool fp8;
-    long long q_st_tok, q_st_head, out_st_tok, out_st_head, bt_stride;
-    long long k_st[3], v_st[3];  // page, head, slot (elements)
-    const void *q, *k, *v;
-    const int *bt, *seq, *cum_q, *cum_kv;
-    int q_per_req;  // > 0: decode batch, request b owns query rows b * q_per_req .. (cum_q null)
-    const int* kv_indptr;      // ragged page table: bt = the flat page ids, seq = derived on the device
-    const int* last_page_len;
-    const float* sinks;
-    void* out;
-};
 
 int parse_pools(const b2pa_tensor* k, const b2pa_tensor* v, int32_t layout, Problem* pr)
 {
@@ -399,6 +440,10 @@ int encode_pool_map(CUtensorMap* m, const Problem& pr, const void* base, const l
         return fail(B2PA_ERR_UNSUPPORTED, "cuTensorMapEncodeTiled(pool) failed with %d", (int)r);
     return B2PA_OK;
 }
+
+}  // namespace b2pa
+
+namespace {
 
 int encode_q_map(CUtensorMap* m, const Problem& pr, int rows_per_tile)
 {
@@ -1118,16 +1163,22 @@ int b2pa_get_device_status(b2pa_stream_t stream_h, uint32_t* bits_out)
     if (e != cudaSuccess)
         return cuda_fail(e, "cudaGetDevice");
     Workspace ws;
-    if (!find_workspace(dev, stream, &ws)) {
-        if ((e = cudaStreamSynchronize(stream)) != cudaSuccess)
-            return cuda_fail(e, "cudaStreamSynchronize");
-        return B2PA_OK;
+    void* words[2] = {nullptr, nullptr};
+    if (find_workspace(dev, stream, &ws))
+        words[0] = ws.mem;
+    {
+        std::lock_guard<std::mutex> lk(g_ws_mu);
+        words[1] = find_status_word(dev, stream);
     }
-    uint32_t bits = 0;
-    if ((e = cudaMemcpyAsync(&bits, ws.mem, sizeof bits, cudaMemcpyDeviceToHost, stream)) != cudaSuccess ||
-        (e = cudaMemsetAsync(ws.mem, 0, sizeof bits, stream)) != cudaSuccess ||
-        (e = cudaStreamSynchronize(stream)) != cudaSuccess)
+    uint32_t got[2] = {0, 0};
+    for (int i = 0; i < 2; ++i)
+        if (words[i] != nullptr &&
+            ((e = cudaMemcpyAsync(&got[i], words[i], sizeof got[i], cudaMemcpyDeviceToHost, stream)) != cudaSuccess ||
+             (e = cudaMemsetAsync(words[i], 0, sizeof got[i], stream)) != cudaSuccess))
+            return cuda_fail(e, "reading the device error word");
+    if ((e = cudaStreamSynchronize(stream)) != cudaSuccess)
         return cuda_fail(e, "reading the device error word");
+    const uint32_t bits = got[0] | got[1];
     if (bits_out)
         *bits_out = bits;
     return bits ? B2PA_ERR_DEVICE : B2PA_OK;
@@ -1228,8 +1279,13 @@ void b2pa_release(void)
         cudaSetDevice(w.dev);
         cudaFree(w.mem);
     }
+    for (auto& pg : g_status) {
+        cudaSetDevice(pg.dev);
+        cudaFree(pg.mem);
+    }
     cudaSetDevice(cur);
     g_ws.clear();
+    g_status.clear();
 }
 
 }  // extern "C"
