@@ -16,6 +16,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import Optional, Sequence, Tuple, Union
 
 import torch
@@ -118,12 +119,12 @@ def load(path: str = LIB_PATH):
     lib.b2pa_debug_gather.argtypes = [P, P, P, P, P, ctypes.c_int32, P, P, ctypes.c_void_p]
     lib.b2pa_debug_gather.restype = ctypes.c_int
     lib.b2pa_append_kv.argtypes = [P, P, P, P, P, ctypes.c_float, ctypes.c_float, ctypes.c_int32, ctypes.c_void_p]
-    lib.b2pa_append_kv_scaled.argtypes = [P, P, P, P, P, P, P, ctypes.c_int32, ctypes.c_void_p]
+    V, I, F = ctypes.c_void_p, ctypes.c_int32, ctypes.c_float  # (tensors as bytes: _packed)
+    lib.b2pa_append_kv_scaled.argtypes = [V] * 7 + [I, V]
     lib.b2pa_append_kv_scaled.restype = ctypes.c_int
-    lib.b2pa_read_kv_scaled.argtypes = [P, P, P, P, P, ctypes.c_int32, P, P, ctypes.c_void_p]
+    lib.b2pa_read_kv_scaled.argtypes = [V] * 5 + [I, V, V, V]
     lib.b2pa_read_kv_scaled.restype = ctypes.c_int
-    lib.b2pa_qk_norm_rope.argtypes = [P, P, P, P, P, P, ctypes.c_float, ctypes.POINTER(ctypes.c_int32),
-                                      ctypes.c_int32, P, P, ctypes.c_void_p]
+    lib.b2pa_qk_norm_rope.argtypes = [V] * 6 + [F, V, I, V, V, V]
     lib.b2pa_qk_norm_rope.restype = ctypes.c_int
     lib.b2pa_get_device_status.argtypes = [ctypes.c_void_p, ctypes.c_void_p]
     lib.b2pa_get_device_status.restype = ctypes.c_int
@@ -172,42 +173,49 @@ def _stream_handle(stream) -> int:
     return int(stream)
 
 
-def _new(shape, device, stream, dtype=torch.bfloat16) -> torch.Tensor:
-    """A new tensor from the memory of the stream that the call runs on."""
+# a b2pa_tensor of each rank as bytes: pointer, dtype, rank, shape[5], stride[5]
+_PACK = [struct.Struct(f"Pii{n}q{8 * (5 - n)}x{n}q{8 * (5 - n)}x").pack for n in range(6)]
+
+
+def _packed(t: Optional[torch.Tensor]) -> Optional[bytes]:
+    """b2pa_tensor describing a torch tensor, as bytes (a quarter of desc()'s time, which small calls feel)."""
+    if t is None:
+        return None
+    n = t.dim()
+    if n > 5:
+        raise ValueError("rank > 5")
+    code = _DTYPES.get(t.dtype)
+    if code is None:
+        raise TypeError(f"unsupported dtype {t.dtype}")
+    return _PACK[n](t.data_ptr(), code, n, *t.shape, *t.stride())
+
+
+def _device_of(stream, *tensors) -> int:
+    """The one CUDA device that a call's tensors (None: not given) and its stream are on."""
+    dev = tensors[0].get_device()
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"tensors on {tensors[0].device} and {t.device}: one device per call")
+    if dev < 0:
+        raise ValueError(f"tensors on {tensors[0].device}: CUDA tensors are needed")
+    if isinstance(stream, torch.cuda.Stream) and stream.device.index != dev:
+        raise ValueError(f"a stream of {stream.device} for tensors on {tensors[0].device}")
+    return dev
+
+
+def _handle(stream, dev: int) -> int:
+    """The stream's handle; None: the current stream of device dev, which is current."""
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream_handle(stream)
+
+
+def _new(like: torch.Tensor, shape, stream, dtype=torch.bfloat16) -> torch.Tensor:
+    """A new contiguous tensor on like's device from the memory of the stream that the call runs on."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return like.new_empty(shape, dtype=dtype)
     if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(int(stream), device=device)
+        stream = torch.cuda.ExternalStream(int(stream), device=like.device)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
-
-
-class _On:
-    """The device of a call's tensors, made current for it, and the stream it runs on there.
-
-    All tensors must be on one CUDA device; an int stream handle or a torch
-    stream must belong to it."""
-
-    def __init__(self, stream, *tensors):
-        first = tensors[0].device
-        for t in tensors:
-            if t is not None and t.device != first:
-                raise ValueError(f"tensors on {first} and {t.device}: one device per call")
-        if first.type != "cuda":
-            raise ValueError(f"tensors on {first}: CUDA tensors are needed")
-        if isinstance(stream, torch.cuda.Stream) and stream.device != first:
-            raise ValueError(f"a stream of {stream.device} for tensors on {first}")
-        self.device, self.stream, self.guard = first, stream, None
-
-    def __enter__(self) -> ctypes.c_void_p:
-        if torch.cuda.current_device() != self.device.index:
-            self.guard = torch.cuda.device(self.device)
-            self.guard.__enter__()
-        return ctypes.c_void_p(_stream_handle(self.stream))
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
+        return like.new_empty(shape, dtype=dtype)
 
 
 def _check(status: int, where: str):
@@ -483,12 +491,14 @@ def append_kv_scaled(k_new: torch.Tensor, v_new: torch.Tensor, kv_cache, kv_scal
     kv_scales is (k_scales, v_scales), fp32 with the pools' shape without head_dim.  Each row gets
     the smallest power of two that brings its largest value to 448 at most, and its values
     divided by that, rounded to the nearest e4m3 value (see include/b2pa.h)."""
-    lib = load()
     k, v = split_kv_cache(kv_cache, kv_layout)
     ks, vs = _two(kv_scales, "kv_scales")
-    with _On(stream, k_new, v_new, k, v, ks, vs, cache_loc) as handle:
-        d = [desc(x) for x in (k_new, v_new, k, v, ks, vs, cache_loc)]
-        st = lib.b2pa_append_kv_scaled(*map(ctypes.byref, d), LAYOUTS[kv_layout], handle)
+    args = (k_new, v_new, k, v, ks, vs, cache_loc)
+    dev = _device_of(stream, *args)
+    if dev != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return append_kv_scaled(k_new, v_new, kv_cache, kv_scales, cache_loc, kv_layout, stream)
+    st = load().b2pa_append_kv_scaled(*map(_packed, args), LAYOUTS[kv_layout], _handle(stream, dev))
     _check(st, "b2pa_append_kv_scaled")
 
 
@@ -499,19 +509,20 @@ def read_kv_scaled(kv_cache, kv_scales, cache_loc: torch.Tensor, k_out: Optional
 
     k_out and v_out may be given, as views of bf16 pools for example.  A slot outside the pool
     reads as zeros and is flagged in device_status()."""
-    lib = load()
     k, v = split_kv_cache(kv_cache, kv_layout)
     ks, vs = _two(kv_scales, "kv_scales")
-    with _On(stream, k, v, ks, vs, cache_loc, k_out, v_out) as handle:
-        shape = (cache_loc.shape[0], k.shape[1 if kv_layout == "HND" else 2], k.shape[3])
-        if k_out is None:
-            k_out = _new(shape, k.device, stream)
-        if v_out is None:
-            v_out = _new(shape, k.device, stream)
-        d = [desc(x) for x in (k, v, ks, vs, cache_loc)]
-        dko, dvo = desc(k_out), desc(v_out)
-        st = lib.b2pa_read_kv_scaled(*map(ctypes.byref, d), LAYOUTS[kv_layout], ctypes.byref(dko), ctypes.byref(dvo),
-                                     handle)
+    dev = _device_of(stream, k, v, ks, vs, cache_loc, k_out, v_out)
+    if dev != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return read_kv_scaled(kv_cache, kv_scales, cache_loc, k_out, v_out, kv_layout, stream)
+    layout = LAYOUTS[kv_layout]
+    shape = (cache_loc.numel(), k.shape[1 + layout], k.shape[3]) if k.dim() == 4 else (0, 0, 0)
+    if k_out is None:
+        k_out = _new(k, shape, stream)
+    if v_out is None:
+        v_out = _new(k, shape, stream)
+    st = load().b2pa_read_kv_scaled(*map(_packed, (k, v, ks, vs, cache_loc)), layout, _packed(k_out), _packed(v_out),
+                                    _handle(stream, dev))
     _check(st, "b2pa_read_kv_scaled")
     return k_out, v_out
 
@@ -537,21 +548,22 @@ def qk_norm_rope(
     may be query / key themselves.  cos_sin [max_position, R] fp32 holds R / 2 cosines and R / 2
     sines per position.  positions is int32 [T], or [axes, T] with axis_of naming the axis of
     each of the R / 2 frequencies."""
-    lib = load()
+    dev = _device_of(stream, query, key, cos_sin, positions, q_weight, k_weight, q_out, k_out)
+    if dev != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return qk_norm_rope(query, key, cos_sin, positions, q_weight, k_weight, eps, axis_of, interleaved, q_out,
+                                k_out, stream)
     axes = None
     if axis_of is not None:
         if len(axis_of) != cos_sin.shape[-1] // 2:
             raise ValueError(f"axis_of: one axis for each of the {cos_sin.shape[-1] // 2} frequencies")
-        axes = (ctypes.c_int32 * len(axis_of))(*axis_of)
-    with _On(stream, query, key, cos_sin, positions, q_weight, k_weight, q_out, k_out) as handle:
-        if q_out is None:
-            q_out = _new(query.shape, query.device, stream)
-        if k_out is None:
-            k_out = _new(key.shape, query.device, stream)
-        d = [desc(x) for x in (query, key, cos_sin, positions, q_weight, k_weight)]
-        dqo, dko = desc(q_out), desc(k_out)
-        st = lib.b2pa_qk_norm_rope(*map(_ref, d), float(eps), axes, 1 if interleaved else 0, ctypes.byref(dqo),
-                                   ctypes.byref(dko), handle)
+        axes = struct.pack(f"{len(axis_of)}i", *axis_of)
+    if q_out is None:
+        q_out = _new(query, query.shape, stream)
+    if k_out is None:
+        k_out = _new(key, key.shape, stream)
+    st = load().b2pa_qk_norm_rope(*map(_packed, (query, key, cos_sin, positions, q_weight, k_weight)), eps, axes,
+                                  1 if interleaved else 0, _packed(q_out), _packed(k_out), _handle(stream, dev))
     _check(st, "b2pa_qk_norm_rope")
     return q_out, k_out
 

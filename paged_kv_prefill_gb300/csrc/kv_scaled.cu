@@ -10,11 +10,15 @@
 // scales of the caller's own, one rounding).
 //
 // Both are bound by HBM: 2 bytes of bf16 and 1 of e4m3 per element, 4 bytes
-// per row for the scale, no reuse.  A group of lanes (a power of two) holds a
-// row, 8 elements (one 16-byte chunk of bf16) per lane, so that the row's
-// maximum takes log2(lanes) shuffles.  A group takes the K and the V row of
-// kRows (token, kv head) pairs and issues all their loads before the first
-// store.
+// per row for the scale, no reuse; behind that by the instructions per
+// element.  A group of lanes (a power of two) takes the K and the V row of one
+// (token, kv head), kChunks 16-byte pieces of bf16 per lane and tensor, and
+// the maxima of the two rows ride in the two halves of one word, through one
+// chain of log2(lanes) shuffles.  More rows per group, with their loads issued
+// together, were slower: the registers they take cost more loads in flight
+// than they add (write of 32768 tokens x 8 heads x 128: 34.8 us with one row,
+// 36.9 with two, 37.1 with four, 47.3 with eight; read of 131072 x 8 x 64:
+// 67.7, 72.2, 78.1, 82.5).
 #include "kv_scaled.cuh"
 
 #include "../../include/b2pa.h"
@@ -25,13 +29,6 @@ namespace b2pa {
 namespace {
 
 constexpr int kThreads = 256;
-
-struct Row {
-    bool on;      // a row to move
-    long long n;  // token
-    int h;        // kv head
-    long long page, slot;
-};
 
 __device__ __forceinline__ uint32_t two_e4m3(float lo, float hi)
 {
@@ -51,16 +48,27 @@ __device__ __forceinline__ uint2 quantise8(uint4 v, float inv)
     return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
 }
 
-// Largest finite magnitude of eight bf16 values, as bf16 bits.
-__device__ __forceinline__ uint32_t top8(uint4 v)
+// Largest finite magnitude of kChunks x 8 bf16 values, as bf16 bits.
+template <int kChunks>
+__device__ __forceinline__ uint32_t top_of(const uint4* v)
 {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
     uint32_t m = 0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const uint32_t lo = w[i] & 0x7FFFu, hi = (w[i] >> 16) & 0x7FFFu;
-        m = max(m, lo < 0x7F80u ? lo : 0u);
-        m = max(m, hi < 0x7F80u ? hi : 0u);
+    for (int c = 0; c < kChunks; ++c)
+        m = __vmaxu2(m, __vmaxu2(__vmaxu2(v[c].x & 0x7FFF7FFFu, v[c].y & 0x7FFF7FFFu),
+                                 __vmaxu2(v[c].z & 0x7FFF7FFFu, v[c].w & 0x7FFF7FFFu)));
+    m = max(m & 0xFFFFu, m >> 16);
+    if (m >= 0x7F80u) {  // an infinity or NaN among them: again, without those
+        m = 0;
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c) {
+            const uint32_t w[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t lo = w[i] & 0x7FFFu, hi = (w[i] >> 16) & 0x7FFFu;
+                m = max(m, max(lo < 0x7F80u ? lo : 0u, hi < 0x7F80u ? hi : 0u));
+            }
+        }
     }
     return m;
 }
@@ -77,73 +85,86 @@ __device__ __forceinline__ int scale_exponent(uint32_t top)
     return max(e, -126);
 }
 
-template <int kLanes, int kRows, typename Idx>
-__device__ __forceinline__ Row row_of(const ScaledKvParams& p, int r)
+// The (token, kv head) of a lane group and its slot.
+struct Row {
+    bool on;
+    long long n;     // token
+    int h;           // kv head
+    long long page;  // -1: a slot outside the pool
+    int slot;
+};
+
+template <int kLanes>
+__device__ __forceinline__ Row row_of(const ScaledKvParams& p)
 {
-    constexpr int kGroups = kThreads / kLanes;
-    const Idx id = ((Idx)blockIdx.x * kRows + r) * kGroups + threadIdx.x / kLanes;
-    Row w;
-    const Idx n = id / (Idx)p.Hkv;
-    w.n = (long long)n;
-    w.h = (int)(id - n * (Idx)p.Hkv);
-    w.on = n < (Idx)p.T;
-    w.page = w.slot = 0;
-    if (w.on) {
-        const int loc = p.cache_loc[w.n];
-        w.page = loc / p.page_size;
-        w.slot = loc - w.page * p.page_size;
-        if (loc < 0 || w.page >= p.num_pages) {
-            w.page = -1;
-            if (w.h == 0 && threadIdx.x % kLanes == 0)
+    const unsigned long long id = (unsigned long long)blockIdx.x * (kThreads / kLanes) + threadIdx.x / kLanes;
+    const unsigned heads = (unsigned)p.Hkv;
+    Row s;
+    // (a 32-bit division where the number allows it)
+    s.n = id <= 0xFFFFFFFFull ? (long long)((unsigned)id / heads) : (long long)(id / heads);
+    s.h = (int)((long long)id - s.n * heads);
+    s.on = s.n < p.T;
+    s.page = s.slot = 0;
+    if (s.on) {
+        const int loc = p.cache_loc[s.n];
+        const int page = loc / p.page_size;
+        s.page = page;
+        s.slot = loc - page * p.page_size;
+        if (loc < 0 || page >= p.num_pages) {
+            s.page = -1;
+            if (s.h == 0 && threadIdx.x % kLanes == 0)
                 atomicOr(p.err, (unsigned)B2PA_DEV_BAD_SLOT);
         }
     }
-    return w;
+    return s;
 }
 
-template <int kLanes, int kRows, typename Idx>
+__device__ __forceinline__ long long place(const long long st[3], const Row& s)
+{
+    return s.page * st[0] + s.h * st[1] + s.slot * st[2];
+}
+
+template <int kChunks, int kLanes>
 __global__ void __launch_bounds__(kThreads) append_scaled_kernel(const __grid_constant__ ScaledKvParams p)
 {
-    const int lane = threadIdx.x % kLanes;
-    const bool mine = 8 * lane < p.D;
-    Row row[kRows];
-    uint4 v[kRows][2];
+    const int lane = threadIdx.x % kLanes, d = 8 * kChunks * lane;
+    const Row s = row_of<kLanes>(p);
+    const bool on = s.on && s.page >= 0, mine = on && d < p.D;  // every lane stays for the shuffles
+    uint4 v[2][kChunks];
 #pragma unroll
-    for (int r = 0; r < kRows; ++r) {
-        row[r] = row_of<kLanes, kRows, Idx>(p, r);
-        row[r].on = row[r].on && row[r].page >= 0;
+    for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            v[r][i] = make_uint4(0u, 0u, 0u, 0u);
-            if (row[r].on && mine)
-                v[r][i] = *reinterpret_cast<const uint4*>(p.x[i] + row[r].n * p.tok[i] + row[r].h * p.head[i] + 8 * lane);
-        }
-    }
-#pragma unroll
-    for (int r = 0; r < kRows; ++r)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            uint32_t top = top8(v[r][i]);
-#pragma unroll
-            for (int o = kLanes / 2; o > 0; o >>= 1)
-                top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-            const int e = scale_exponent(top);
-            if (!row[r].on)
-                continue;
-            const uint2 c = quantise8(v[r][i], __int_as_float((127 - e) << 23));
+        for (int c = 0; c < kChunks; ++c) {
+            v[i][c] = make_uint4(0u, 0u, 0u, 0u);
             if (mine)
-                *reinterpret_cast<uint2*>(p.pool[i] + row[r].page * p.pool_st[i][0] + row[r].h * p.pool_st[i][1] +
-                                          row[r].slot * p.pool_st[i][2] + 8 * lane) = c;
-            if (lane == 0)
-                p.scale[i][row[r].page * p.scale_st[i][0] + row[r].h * p.scale_st[i][1] +
-                           row[r].slot * p.scale_st[i][2]] = __int_as_float((127 + e) << 23);
+                v[i][c] = reinterpret_cast<const uint4*>(p.x[i] + s.n * p.tok[i] + s.h * p.head[i] + d)[c];
         }
+    uint32_t top = top_of<kChunks>(v[0]) | top_of<kChunks>(v[1]) << 16;
+#pragma unroll
+    for (int o = kLanes / 2; o > 0; o >>= 1)
+        top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, o));
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int e = scale_exponent(i ? top >> 16 : top & 0xFFFFu);
+        const float inv = __int_as_float((127 - e) << 23);
+        if (mine) {
+            uint8_t* to = p.pool[i] + place(p.pool_st[i], s) + d;
+            if constexpr (kChunks == 2) {
+                const uint2 a = quantise8(v[i][0], inv), b = quantise8(v[i][1], inv);
+                *reinterpret_cast<uint4*>(to) = make_uint4(a.x, a.y, b.x, b.y);
+            } else {
+                *reinterpret_cast<uint2*>(to) = quantise8(v[i][0], inv);
+            }
+        }
+        if (on && lane == 0)
+            p.scale[i][place(p.scale_st[i], s)] = __int_as_float((127 + e) << 23);
+    }
 }
 
 // Eight codes times a scale, as bf16.
-__device__ __forceinline__ uint4 restore8(uint2 c, float scale)
+__device__ __forceinline__ uint4 restore8(uint32_t c0, uint32_t c1, float scale)
 {
-    const uint32_t w[4] = {c.x & 0xFFFFu, c.x >> 16, c.y & 0xFFFFu, c.y >> 16};
+    const uint32_t w[4] = {c0 & 0xFFFFu, c0 >> 16, c1 & 0xFFFFu, c1 >> 16};
     uint32_t o[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -153,98 +174,100 @@ __device__ __forceinline__ uint4 restore8(uint2 c, float scale)
         asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, h;\n\t}"
             : "=f"(lo), "=f"(hi)
             : "r"(h));
-        o[i] = pack_bf16x2(lo * scale, hi * scale);
+        const float2 y = __fmul2_rn(make_float2(lo, hi), make_float2(scale, scale));
+        o[i] = pack_bf16x2(y.x, y.y);
     }
     return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
-template <int kLanes, int kRows, typename Idx>
+template <int kChunks, int kLanes>
 __global__ void __launch_bounds__(kThreads) read_scaled_kernel(const __grid_constant__ ScaledKvParams p)
 {
-    const int lane = threadIdx.x % kLanes;
-    const bool mine = 8 * lane < p.D;
-    Row row[kRows];
-    uint2 c[kRows][2];
-    float s[kRows][2];
+    const int d = 8 * kChunks * (int)(threadIdx.x % kLanes);
+    const Row s = row_of<kLanes>(p);
+    if (!s.on || d >= p.D)
+        return;
+    uint32_t c[2][2 * kChunks];
+    float unit[2];
 #pragma unroll
-    for (int r = 0; r < kRows; ++r) {
-        row[r] = row_of<kLanes, kRows, Idx>(p, r);
+    for (int i = 0; i < 2; ++i) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            c[r][i] = make_uint2(0u, 0u);  // a slot outside the pool reads as zeros
-            s[r][i] = 1.f;
-            if (row[r].on && mine && row[r].page >= 0) {
-                c[r][i] = *reinterpret_cast<const uint2*>(p.pool[i] + row[r].page * p.pool_st[i][0] +
-                                                          row[r].h * p.pool_st[i][1] + row[r].slot * p.pool_st[i][2] +
-                                                          8 * lane);
-                s[r][i] = p.scale[i][row[r].page * p.scale_st[i][0] + row[r].h * p.scale_st[i][1] +
-                                     row[r].slot * p.scale_st[i][2]];
+        for (int k = 0; k < 2 * kChunks; ++k)
+            c[i][k] = 0u;  // a slot outside the pool reads as zeros
+        unit[i] = 1.f;
+        if (s.page >= 0) {
+            const uint8_t* from = p.pool[i] + place(p.pool_st[i], s) + d;
+            if constexpr (kChunks == 2) {
+                const uint4 x = *reinterpret_cast<const uint4*>(from);
+                c[i][0] = x.x;
+                c[i][1] = x.y;
+                c[i][2] = x.z;
+                c[i][3] = x.w;
+            } else {
+                const uint2 x = *reinterpret_cast<const uint2*>(from);
+                c[i][0] = x.x;
+                c[i][1] = x.y;
             }
+            unit[i] = p.scale[i][place(p.scale_st[i], s)];
         }
     }
 #pragma unroll
-    for (int r = 0; r < kRows; ++r)
+    for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-            if (row[r].on && mine)
-                *reinterpret_cast<uint4*>(p.y[i] + row[r].n * p.tok[i] + row[r].h * p.head[i] + 8 * lane) =
-                    restore8(c[r][i], s[r][i]);
+        for (int k = 0; k < kChunks; ++k)
+            reinterpret_cast<uint4*>(p.y[i] + s.n * p.tok[i] + s.h * p.head[i] + d)[k] =
+                restore8(c[i][2 * k], c[i][2 * k + 1], unit[i]);
 }
 
-template <bool kWrite, int kLanes, int kRows>
-cudaError_t launch_rows(const ScaledKvParams& p, cudaStream_t stream)
+template <bool kWrite, int kChunks, int kLanes>
+cudaError_t launch_lanes(const ScaledKvParams& p, cudaStream_t stream)
 {
-    constexpr long long kPerBlock = (long long)kThreads / kLanes * kRows;
-    const long long rows = (long long)p.T * p.Hkv;
-    const long long blocks = (rows + kPerBlock - 1) / kPerBlock;
+    constexpr int kGroups = kThreads / kLanes;
+    const long long blocks = ((long long)p.T * p.Hkv + kGroups - 1) / kGroups;
     if (blocks > 0x7FFFFFFFLL)
         return cudaErrorInvalidConfiguration;
-    if (rows <= 0x7FFFFFFFLL - kPerBlock) {
-        if (kWrite)
-            append_scaled_kernel<kLanes, kRows, unsigned><<<(unsigned)blocks, kThreads, 0, stream>>>(p);
-        else
-            read_scaled_kernel<kLanes, kRows, unsigned><<<(unsigned)blocks, kThreads, 0, stream>>>(p);
-    } else {
-        if (kWrite)
-            append_scaled_kernel<kLanes, kRows, unsigned long long><<<(unsigned)blocks, kThreads, 0, stream>>>(p);
-        else
-            read_scaled_kernel<kLanes, kRows, unsigned long long><<<(unsigned)blocks, kThreads, 0, stream>>>(p);
-    }
+    if (kWrite)
+        append_scaled_kernel<kChunks, kLanes><<<(unsigned)blocks, kThreads, 0, stream>>>(p);
+    else
+        read_scaled_kernel<kChunks, kLanes><<<(unsigned)blocks, kThreads, 0, stream>>>(p);
     return cudaGetLastError();
 }
 
-template <bool kWrite, int kLanes>
-cudaError_t launch_lanes(const ScaledKvParams& p, int sms, cudaStream_t stream)
-{
-    // several rows per group once one per group would need more than one wave
-    // of blocks (8 blocks of 256 threads per SM)
-    const long long wave = (long long)sms * 8 * (kThreads / kLanes);
-    return (long long)p.T * p.Hkv > wave ? launch_rows<kWrite, kLanes, 4>(p, stream)
-                                         : launch_rows<kWrite, kLanes, 1>(p, stream);
-}
-
 template <bool kWrite>
-cudaError_t launch(const ScaledKvParams& p, int sms, cudaStream_t stream)
+cudaError_t launch(const ScaledKvParams& p, cudaStream_t stream)
 {
     if (p.T == 0)
         return cudaSuccess;
+    // 16 elements per lane where every row of the pools can be taken in 16-byte pieces
+    uintptr_t at = p.D % 16 == 0 ? 0 : 8;
+    for (int i = 0; i < 2; ++i)
+        at |= reinterpret_cast<uintptr_t>(p.pool[i]) | (uintptr_t)p.pool_st[i][0] | (uintptr_t)p.pool_st[i][1] |
+              (uintptr_t)p.pool_st[i][2];
+    if (at % 16 == 0) {
+        const int need = p.D >> 4;
+        if (need <= 4)
+            return launch_lanes<kWrite, 2, 4>(p, stream);
+        if (need <= 8)
+            return launch_lanes<kWrite, 2, 8>(p, stream);
+        return launch_lanes<kWrite, 2, 16>(p, stream);
+    }
     const int need = p.D >> 3;
     if (need <= 8)
-        return launch_lanes<kWrite, 8>(p, sms, stream);
+        return launch_lanes<kWrite, 1, 8>(p, stream);
     if (need <= 16)
-        return launch_lanes<kWrite, 16>(p, sms, stream);
-    return launch_lanes<kWrite, 32>(p, sms, stream);
+        return launch_lanes<kWrite, 1, 16>(p, stream);
+    return launch_lanes<kWrite, 1, 32>(p, stream);
 }
 
 }  // namespace
 
-cudaError_t launch_append_scaled(const ScaledKvParams& p, int sms, cudaStream_t stream)
+cudaError_t launch_append_scaled(const ScaledKvParams& p, cudaStream_t stream)
 {
-    return launch<true>(p, sms, stream);
+    return launch<true>(p, stream);
 }
-cudaError_t launch_read_scaled(const ScaledKvParams& p, int sms, cudaStream_t stream)
+cudaError_t launch_read_scaled(const ScaledKvParams& p, cudaStream_t stream)
 {
-    return launch<false>(p, sms, stream);
+    return launch<false>(p, stream);
 }
 
 }  // namespace b2pa

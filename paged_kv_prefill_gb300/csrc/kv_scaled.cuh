@@ -21,7 +21,7 @@ struct ScaledKvParams {
     unsigned* err;
 };
 
-cudaError_t launch_append_scaled(const ScaledKvParams& p, int sms, cudaStream_t stream);
-cudaError_t launch_read_scaled(const ScaledKvParams& p, int sms, cudaStream_t stream);
+cudaError_t launch_append_scaled(const ScaledKvParams& p, cudaStream_t stream);
+cudaError_t launch_read_scaled(const ScaledKvParams& p, cudaStream_t stream);
 
 }  // namespace b2pa

@@ -148,6 +148,7 @@ int rope_impl(const b2pa_tensor* q, const b2pa_tensor* k, const b2pa_tensor* cos
     p.max_pos = (int)cos_sin->shape[0];
     p.vec_table = half % 4 == 0 && p.cs_stride % 4 == 0 && aligned16(p.cos_sin);
     p.eps = eps;
+    p.inv_d = 1.f / (float)D;
     const cudaError_t e = launch_qk_norm_rope(p, interleaved != 0, di.sms, stream);
     return e == cudaSuccess ? B2PA_OK : cuda_fail(e, "norm and rotation launch");
 }
@@ -235,7 +236,7 @@ int scaled_kv_impl(bool write, const b2pa_tensor* const rows[2], const char* con
     p.D = pr.D;
     p.page_size = pr.P;
     p.num_pages = pr.N;
-    const cudaError_t e = write ? launch_append_scaled(p, di.sms, stream) : launch_read_scaled(p, di.sms, stream);
+    const cudaError_t e = write ? launch_append_scaled(p, stream) : launch_read_scaled(p, stream);
     return e == cudaSuccess ? B2PA_OK : cuda_fail(e, write ? "scaled append launch" : "scaled read launch");
 }
 

@@ -17,8 +17,22 @@
 // sum takes log2(lanes) shuffles.  A lane's two 16-byte chunks are
 // (c, c + R/16) when pairs lie R/2 apart and R/2 is a multiple of 8, and
 // neighbours otherwise; pairs R/2 apart with another R/2 go through a row of
-// shared memory.  A group takes kRows rows of one token, whose cosines and
-// sines it reads once, and issues all their loads first.
+// shared memory.
+//
+// Two kernels.  rope_rows_kernel: one row per group, for calls of about one
+// wave, whose time is latency, and for the rare pairing.  rope_staged_kernel,
+// for the others: the table row must be read before the rotation and its
+// place is known only from the positions, and a group that does this for a few
+// rows at a time keeps too few loads in flight.  So groups loop over sets of
+// kSetRows heads of a token, and each thread copies its own pieces of the rows
+// and of the table into its own places of a ring in shared memory with
+// cp.async, kStages - 1 sets ahead; no thread reads another's pieces, so the
+// ring needs no barrier.  The table goes through L1: read by every set from
+// L2 it was the bound.  11750 tokens x (32 + 8) heads x 128: 75 us with one row
+// per group, 60 us with four in registers, 60 us with the ring and the table
+// from L2, 45.4 us so (5.4 TB/s, 0.80 of the copy rate); 16384 tokens x 72
+// heads with three axes 123 us (5.0 TB/s).  Sets of eight, rings of three
+// stages and smaller blocks were slower (47 to 68 us).
 #include "rope.cuh"
 
 #include "../../include/b2pa.h"
@@ -32,234 +46,482 @@ constexpr int kRopeThreads = 128;
 
 enum RopeMode { kInterleaved, kHalvesInLane, kHalvesInSmem };
 
-__device__ __forceinline__ void unpack8(uint4 v, float* f)
+// Eight consecutive elements as four packed pairs (the packed fp32 operations
+// do two at once).
+__device__ __forceinline__ void unpack8(uint4 v, float2* f)
 {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        f[2 * i] = __uint_as_float(w[i] << 16);
-        f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-    }
+    for (int i = 0; i < 4; ++i)
+        f[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
 }
 
-__device__ __forceinline__ uint4 pack8(const float* f)
+__device__ __forceinline__ uint4 pack8(const float2* f)
 {
-    return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
-                      pack_bf16x2(f[6], f[7]));
+    return make_uint4(pack_bf16x2(f[0].x, f[0].y), pack_bf16x2(f[1].x, f[1].y), pack_bf16x2(f[2].x, f[2].y),
+                      pack_bf16x2(f[3].x, f[3].y));
 }
 
-__device__ __forceinline__ void load_weight8(const RopeTensor& x, int d, float* w)
+__device__ __forceinline__ void load8(const float* p, float2* f)
 {
-    if (x.weight_f32) {
-        const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(x.weight) + d);
-        const float4 a = __ldg(p), b = __ldg(p + 1);
-        w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
-        w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
-    } else {
+    const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+    f[0] = make_float2(a.x, a.y);
+    f[1] = make_float2(a.z, a.w);
+    f[2] = make_float2(b.x, b.y);
+    f[3] = make_float2(b.z, b.w);
+}
+
+__device__ __forceinline__ void load_weight8(const RopeTensor& x, int d, float2* w)
+{
+    if (x.weight_f32)
+        load8(static_cast<const float*>(x.weight) + d, w);
+    else
         unpack8(__ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(x.weight) + d)), w);
-    }
 }
 
-// kLanes: lanes per row, each holding two chunks of 8 elements.
-template <RopeMode kMode, int kLanes, int kRows>
-__global__ void __launch_bounds__(kRopeThreads) qk_norm_rope_kernel(const __grid_constant__ RopeParams p)
+// This lane's two chunks of a row (-1: none) and whether its pairs rotate.
+struct Chunks {
+    int a, b;
+    bool turns;
+};
+
+template <RopeMode kMode>
+__device__ __forceinline__ Chunks chunks_of(const RopeParams& p, int lane)
 {
-    constexpr int kGroups = kRopeThreads / kLanes;
-    __shared__ float pair_rows[kMode == kHalvesInSmem ? kGroups * kLanes * 16 : 1];
-    const int lane = threadIdx.x % kLanes, group = threadIdx.x / kLanes;
-    // sets of kRows rows: those of the queries, then those of the keys
-    const int sets_q = (p.x[0].heads + kRows - 1) / kRows, sets = sets_q + (p.x[1].heads + kRows - 1) / kRows;
-    const unsigned long long id = (unsigned long long)blockIdx.x * kGroups + group;
-    // (a 32-bit division where the number allows it)
-    const long long t = id <= 0xFFFFFFFFull ? (long long)((unsigned)id / (unsigned)sets) : (long long)(id / sets);
-    const bool on = t < p.T;  // every lane stays for the shuffles
-    const int set = (int)((long long)id - t * sets);
-    const bool is_k = set >= sets_q;
-    const RopeTensor& x = p.x[is_k ? 1 : 0];
-    const int h0 = (is_k ? set - sets_q : set) * kRows;
-    const int half = p.R >> 1, chunks = p.D >> 3;
-
-    // this lane's two chunks (-1: none) and whether its pairs rotate
-    int ca = 2 * lane, cb = 2 * lane + 1;
-    bool turns = 8 * ca < p.R;
+    Chunks c{2 * lane, 2 * lane + 1, 16 * lane < p.R};
     if (kMode == kHalvesInLane) {
-        const int hc = half >> 3;  // chunks of one half
-        turns = lane < hc;
-        ca = turns ? lane : 2 * hc + 2 * (lane - hc);
-        cb = turns ? lane + hc : ca + 1;
+        const int hc = p.R >> 4;  // chunks of one half
+        c.turns = lane < hc;
+        c.a = c.turns ? lane : 2 * hc + 2 * (lane - hc);
+        c.b = c.turns ? lane + hc : c.a + 1;
     }
-    if (!on || ca >= chunks)
-        ca = -1;
-    if (!on || cb >= chunks)
-        cb = -1;
+    if (c.a >= p.D >> 3)
+        c.a = -1;
+    if (c.b >= p.D >> 3)
+        c.b = -1;
+    return c;
+}
 
-    uint4 va[kRows], vb[kRows];
-#pragma unroll
-    for (int r = 0; r < kRows; ++r) {
-        va[r] = vb[r] = make_uint4(0u, 0u, 0u, 0u);
-        if (h0 + r < x.heads) {
-            const uint16_t* row = x.in + t * x.in_tok + (long long)(h0 + r) * x.in_head;
-            if (ca >= 0)
-                va[r] = *reinterpret_cast<const uint4*>(row + 8 * ca);
-            if (cb >= 0)
-                vb[r] = *reinterpret_cast<const uint4*>(row + 8 * cb);
-        }
-    }
-
+// A token's positions; ok = false, and the first row of the table, if one is
+// outside it.
+struct Places {
     int pos[kRopeMaxAxes];
-    bool ok = on;
+    bool ok;
+    __device__ __forceinline__ int at(int axis) const
+    {
+        return axis == 0 ? pos[0] : axis == 1 ? pos[1] : axis == 2 ? pos[2] : pos[3];
+    }
+    __device__ __forceinline__ const float* row(const RopeParams& p, int axis) const
+    {
+        return p.cos_sin + (long long)at(axis) * p.cs_stride;
+    }
+};
+
+__device__ __forceinline__ Places places_of(const RopeParams& p, long long t, bool on)
+{
+    Places x;
+    x.ok = on;
 #pragma unroll
     for (int a = 0; a < kRopeMaxAxes; ++a) {
-        pos[a] = 0;
-        if (on && a < p.axes) {
-            pos[a] = p.positions[a * p.pos_stride + t];
-            if (pos[a] < 0 || pos[a] >= p.max_pos)
-                ok = false;
-        }
+        x.pos[a] = 0;
+        if (on && a < p.axes)
+            x.pos[a] = p.positions[a * p.pos_stride + t];
     }
-    if (on && !ok && set == 0 && lane == 0)
-        atomicOr(p.err, (unsigned)B2PA_DEV_BAD_POSITION);
-    if (!ok)
-        pos[0] = pos[1] = pos[2] = pos[3] = 0;
-    auto place = [&](int axis) {
-        return axis == 0 ? pos[0] : axis == 1 ? pos[1] : axis == 2 ? pos[2] : pos[3];
-    };
-    auto entry = [&](int f) { return p.cos_sin + (long long)place(p.axis_of[f]) * p.cs_stride + f; };
+#pragma unroll
+    for (int a = 0; a < kRopeMaxAxes; ++a)
+        if (x.pos[a] < 0 || x.pos[a] >= p.max_pos)
+            x.ok = false;
+    if (!x.ok)
+        x.pos[0] = x.pos[1] = x.pos[2] = x.pos[3] = 0;
+    return x;
+}
 
-    // cosines and sines of this lane's eight frequencies (pairs in one lane)
-    float c[8], s[8];
-    if (kMode != kHalvesInSmem) {
-        const int f0 = 8 * lane;  // interleaved: elements 16 lane ..; halves: elements 8 lane .. of each half
-        const int a8 = turns && f0 + 8 <= half ? p.axis_of8[lane] : 255;
-        if (p.vec_table && a8 != 255) {
-            const float* e = p.cos_sin + (long long)place(a8) * p.cs_stride + f0;
-            const float4 c0 = __ldg(reinterpret_cast<const float4*>(e)), c1 = __ldg(reinterpret_cast<const float4*>(e) + 1);
-            const float4 s0 = __ldg(reinterpret_cast<const float4*>(e + half)), s1 = __ldg(reinterpret_cast<const float4*>(e + half) + 1);
-            c[0] = c0.x; c[1] = c0.y; c[2] = c0.z; c[3] = c0.w; c[4] = c1.x; c[5] = c1.y; c[6] = c1.z; c[7] = c1.w;
-            s[0] = s0.x; s[1] = s0.y; s[2] = s0.z; s[3] = s0.w; s[4] = s1.x; s[5] = s1.y; s[6] = s1.z; s[7] = s1.w;
+__device__ __forceinline__ void load_weights(const RopeTensor& x, const Chunks& ch, float2 (&wa)[4], float2 (&wb)[4])
+{
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        wa[i] = wb[i] = make_float2(1.f, 1.f);
+    if (x.weight != nullptr && ch.a >= 0)
+        load_weight8(x, 8 * ch.a, wa);
+    if (x.weight != nullptr && ch.b >= 0)
+        load_weight8(x, 8 * ch.b, wb);
+}
+
+// x / sqrt(mean(x^2) + eps) over the row that kLanes lanes hold (norm false:
+// x; the lanes of a warp may differ in it, so all take part in the sum).
+template <int kLanes>
+__device__ __forceinline__ void norm_row(const RopeParams& p, bool norm, float2 (&a)[4], float2 (&b)[4])
+{
+    float2 sum2 = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        sum2 = __ffma2_rn(a[i], a[i], __ffma2_rn(b[i], b[i], sum2));
+    float sum = sum2.x + sum2.y;
+#pragma unroll
+    for (int o = kLanes / 2; o > 0; o >>= 1)
+        sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    const float inv = norm ? rsqrtf(fmaf(sum, p.inv_d, p.eps)) : 1.f;
+    const float2 inv2 = make_float2(inv, inv);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        a[i] = __fmul2_rn(a[i], inv2);
+        b[i] = __fmul2_rn(b[i], inv2);
+    }
+}
+
+// Weight and rotation of a lane's 16 elements as one linear map, formed once
+// for all rows that share it:  halves: a' = m0 a + m1 b, b' = m2 b + m3 a with
+// m = (wa c, -wb s, wb c, wa s).  Interleaved, per packed pair (x, y): x' =
+// m.x x + n.x y, y' = m.y y + n.y x with m = (wx c, wy c), n = (-wy s, wx s);
+// m0, n = m1 for a and m2, n = m3 for b.  A pair that does not turn has c = 1,
+// s = 0 and skips the cross terms (an infinity times 0 is no 0).
+struct Turn {
+    float2 m[4][4];
+};
+
+template <RopeMode kMode>
+__device__ __forceinline__ Turn turn_of(const RopeParams& p, int lane, const float2 (&c)[4], const float2 (&s)[4],
+                                        const float2 (&wa)[4], const float2 (&wb)[4])
+{
+    Turn t;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (kMode == kHalvesInLane) {
+            t.m[0][i] = __fmul2_rn(wa[i], c[i]);
+            t.m[1][i] = __fmul2_rn(wb[i], make_float2(-s[i].x, -s[i].y));
+            t.m[2][i] = __fmul2_rn(wb[i], c[i]);
+            t.m[3][i] = __fmul2_rn(wa[i], s[i]);
         } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                c[i] = 1.f;
-                s[i] = 0.f;
-                if (turns && f0 + i < half) {
-                    const float* e = entry(f0 + i);
-                    c[i] = __ldg(e);
-                    s[i] = __ldg(e + half);
-                }
-            }
+            const float ca = i & 1 ? c[i / 2].y : c[i / 2].x, sa = i & 1 ? s[i / 2].y : s[i / 2].x;
+            const float cb = i & 1 ? c[2 + i / 2].y : c[2 + i / 2].x, sb = i & 1 ? s[2 + i / 2].y : s[2 + i / 2].x;
+            t.m[0][i] = __fmul2_rn(wa[i], make_float2(ca, ca));
+            t.m[1][i] = make_float2(-wa[i].y * sa, wa[i].x * sa);
+            t.m[2][i] = __fmul2_rn(wb[i], make_float2(cb, cb));
+            t.m[3][i] = make_float2(-wb[i].y * sb, wb[i].x * sb);
         }
     }
-    const bool norm = x.weight != nullptr;
-    float wa[8], wb[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-        wa[i] = wb[i] = 1.f;
-    if (norm && ca >= 0)
-        load_weight8(x, 8 * ca, wa);
-    if (norm && cb >= 0)
-        load_weight8(x, 8 * cb, wb);
+    return t;
+}
 
+template <RopeMode kMode>
+__device__ __forceinline__ void turn_row(const RopeParams& p, int lane, bool turns, const Turn& t, float2 (&a)[4],
+                                         float2 (&b)[4])
+{
 #pragma unroll
-    for (int r = 0; r < kRows; ++r) {
-        float a[8], b[8];
-        unpack8(va[r], a);
-        unpack8(vb[r], b);
-        if (norm) {
-            float sum = 0.f;
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                sum = fmaf(a[i], a[i], fmaf(b[i], b[i], sum));
-#pragma unroll
-            for (int o = kLanes / 2; o > 0; o >>= 1)
-                sum += __shfl_xor_sync(0xffffffffu, sum, o);
-            const float inv = rsqrtf(sum / (float)p.D + p.eps);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                a[i] *= inv * wa[i];
-                b[i] *= inv * wb[i];
-            }
-        }
+    for (int i = 0; i < 4; ++i) {
+        const float2 u = a[i], v = b[i];
+        a[i] = __fmul2_rn(u, t.m[0][i]);
+        b[i] = __fmul2_rn(v, t.m[2][i]);
         if (kMode == kHalvesInLane) {
             if (turns) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float u = a[i], v = b[i];
-                    a[i] = u * c[i] - v * s[i];
-                    b[i] = v * c[i] + u * s[i];
-                }
-            }
-        } else if (kMode == kInterleaved) {
-            // a pair past R has c = 1, s = 0
-            if (turns) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float u = a[2 * i], v = a[2 * i + 1], y = b[2 * i], z = b[2 * i + 1];
-                    if (16 * lane + 2 * i < p.R) {
-                        a[2 * i] = u * c[i] - v * s[i];
-                        a[2 * i + 1] = v * c[i] + u * s[i];
-                    }
-                    if (16 * lane + 8 + 2 * i < p.R) {
-                        b[2 * i] = y * c[4 + i] - z * s[4 + i];
-                        b[2 * i + 1] = z * c[4 + i] + y * s[4 + i];
-                    }
-                }
+                a[i] = __ffma2_rn(v, t.m[1][i], a[i]);
+                b[i] = __ffma2_rn(u, t.m[3][i], b[i]);
             }
         } else {
-            float* row = pair_rows + group * kLanes * 16;
-            __syncwarp();
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                row[16 * lane + i] = a[i];
-                row[16 * lane + 8 + i] = b[i];
-            }
-            __syncwarp();
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const int e = 16 * lane + i;
-                if (e < p.R && on) {
-                    const int f = e < half ? e : e - half;
-                    const float* cs = entry(f);
-                    const float cc = __ldg(cs), ss = __ldg(cs + half);
-                    const float u = row[e], v = row[e < half ? e + half : e - half];
-                    const float y = e < half ? u * cc - v * ss : u * cc + v * ss;
-                    if (i < 8)
-                        a[i] = y;
-                    else
-                        b[i - 8] = y;
-                }
-            }
-        }
-        if (ok && h0 + r < x.heads) {
-            uint16_t* row = x.out + t * x.out_tok + (long long)(h0 + r) * x.out_head;
-            if (ca >= 0)
-                *reinterpret_cast<uint4*>(row + 8 * ca) = pack8(a);
-            if (cb >= 0)
-                *reinterpret_cast<uint4*>(row + 8 * cb) = pack8(b);
+            if (16 * lane + 2 * i < p.R)
+                a[i] = __ffma2_rn(make_float2(u.y, u.x), t.m[1][i], a[i]);
+            if (16 * lane + 8 + 2 * i < p.R)
+                b[i] = __ffma2_rn(make_float2(v.y, v.x), t.m[3][i], b[i]);
         }
     }
 }
 
-template <RopeMode kMode, int kLanes, int kRows>
-cudaError_t launch_rows(const RopeParams& p, cudaStream_t stream)
+__device__ __forceinline__ void store_row(const RopeTensor& x, long long t, int h, const Chunks& ch, const float2 (&a)[4],
+                                          const float2 (&b)[4])
+{
+    uint16_t* row = x.out + t * x.out_tok + (long long)h * x.out_head;
+    if (ch.a >= 0)
+        *reinterpret_cast<uint4*>(row + 8 * ch.a) = pack8(a);
+    if (ch.b >= 0)
+        *reinterpret_cast<uint4*>(row + 8 * ch.b) = pack8(b);
+}
+
+// The common axis of this lane's eight frequencies if their table entries can
+// be read as float4, else 255.
+__device__ __forceinline__ int vector_axis(const RopeParams& p, int lane)
+{
+    return p.vec_table && 8 * lane + 8 <= p.R >> 1 ? p.axis_of8[lane] : 255;
+}
+
+// kLanes lanes per row, each holding two chunks of 8 elements; one row per group.
+template <RopeMode kMode, int kLanes>
+__global__ void __launch_bounds__(kRopeThreads) rope_rows_kernel(const __grid_constant__ RopeParams p)
 {
     constexpr int kGroups = kRopeThreads / kLanes;
-    const long long sets = (p.x[0].heads + kRows - 1) / kRows + (p.x[1].heads + kRows - 1) / kRows;
-    const long long blocks = (p.T * sets + kGroups - 1) / kGroups;
-    if (blocks > 0x7FFFFFFFLL)
-        return cudaErrorInvalidConfiguration;
-    qk_norm_rope_kernel<kMode, kLanes, kRows><<<(unsigned)blocks, kRopeThreads, 0, stream>>>(p);
-    return cudaGetLastError();
+    __shared__ __align__(16) float pair_rows[kMode == kHalvesInSmem ? kGroups * kLanes * 16 : 1];
+    const int lane = threadIdx.x % kLanes, group = threadIdx.x / kLanes;
+    const unsigned heads = (unsigned)(p.x[0].heads + p.x[1].heads);
+    const unsigned long long id = (unsigned long long)blockIdx.x * kGroups + group;
+    // (a 32-bit division where the number allows it)
+    const long long t = id <= 0xFFFFFFFFull ? (long long)((unsigned)id / heads) : (long long)(id / heads);
+    const bool on = t < p.T;  // every lane stays for the shuffles
+    const int hh = (int)((long long)id - t * heads);
+    const bool is_k = hh >= p.x[0].heads;
+    const RopeTensor& x = p.x[is_k ? 1 : 0];
+    const int h = is_k ? hh - p.x[0].heads : hh;
+    const int half = p.R >> 1;
+    const Chunks ch = chunks_of<kMode>(p, lane);
+
+    uint4 va = make_uint4(0u, 0u, 0u, 0u), vb = va;
+    if (on) {
+        const uint16_t* row = x.in + t * x.in_tok + (long long)h * x.in_head;
+        if (ch.a >= 0)
+            va = *reinterpret_cast<const uint4*>(row + 8 * ch.a);
+        if (ch.b >= 0)
+            vb = *reinterpret_cast<const uint4*>(row + 8 * ch.b);
+    }
+    float2 wa[4], wb[4];
+    load_weights(x, ch, wa, wb);
+    const Places at = places_of(p, t, on);
+    if (on && !at.ok && hh == 0 && lane == 0)
+        atomicOr(p.err, (unsigned)B2PA_DEV_BAD_POSITION);
+
+    float2 c[4], s[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        c[i] = make_float2(1.f, 1.f);
+        s[i] = make_float2(0.f, 0.f);
+    }
+    if (kMode != kHalvesInSmem && ch.turns) {
+        const int f0 = 8 * lane, a8 = vector_axis(p, lane);
+        if (a8 != 255) {
+            load8(at.row(p, a8) + f0, c);
+            load8(at.row(p, a8) + half + f0, s);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                if (f0 + i >= half)
+                    break;
+                const float* e = at.row(p, p.axis_of[f0 + i]) + f0 + i;
+                (i & 1 ? c[i / 2].y : c[i / 2].x) = __ldg(e);
+                (i & 1 ? s[i / 2].y : s[i / 2].x) = __ldg(e + half);
+            }
+        }
+    }
+    float2 a[4], b[4];
+    unpack8(va, a);
+    unpack8(vb, b);
+    norm_row<kLanes>(p, x.weight != nullptr, a, b);
+    if (kMode != kHalvesInSmem) {
+        turn_row<kMode>(p, lane, ch.turns, turn_of<kMode>(p, lane, c, s, wa, wb), a, b);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            a[i] = __fmul2_rn(a[i], wa[i]);
+            b[i] = __fmul2_rn(b[i], wb[i]);
+        }
+        float* row = pair_rows + group * kLanes * 16;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            reinterpret_cast<float2*>(row + 16 * lane)[i] = a[i];
+            reinterpret_cast<float2*>(row + 16 * lane + 8)[i] = b[i];
+        }
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const int e = 16 * lane + i;
+            if (e < p.R) {
+                const int f = e < half ? e : e - half;
+                const float* cs = at.row(p, p.axis_of[f]) + f;
+                const float cc = __ldg(cs), ss = __ldg(cs + half);
+                const float u = row[e], v = row[e < half ? e + half : e - half];
+                const float y = e < half ? u * cc - v * ss : u * cc + v * ss;
+                float2& to = i < 8 ? a[(i & 7) / 2] : b[(i & 7) / 2];
+                (i & 1 ? to.y : to.x) = y;
+            }
+        }
+    }
+    if (at.ok)
+        store_row(x, t, h, ch, a, b);
+}
+
+// ---------------------------------------------------------------- the staged kernel
+
+constexpr int kSetRows = 4;
+constexpr int kStages = 2;
+// a thread's pieces of 16 bytes in one stage: 2 per row, 4 of the table
+constexpr int kPieces = 2 * kSetRows + 4;
+constexpr int kStagedSmem = kStages * kPieces * 16 * kRopeThreads;
+
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+// Through L1: the table's row is the same for all sets of a token, most of
+// which one block has in flight at once.
+__device__ __forceinline__ void copy16_l1(uint32_t dst, const void* src)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy4_l1(uint32_t dst, const void* src)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+
+template <RopeMode kMode, int kLanes>
+__global__ void __launch_bounds__(kRopeThreads) rope_staged_kernel(const __grid_constant__ RopeParams p, unsigned total)
+{
+    extern __shared__ __align__(16) uint8_t ring[];
+    constexpr int kGroups = kRopeThreads / kLanes;
+    const int lane = threadIdx.x % kLanes;
+    const int half = p.R >> 1, f0 = 8 * lane;
+    const Chunks ch = chunks_of<kMode>(p, lane);
+    const int a8 = vector_axis(p, lane);
+    // sets of kSetRows rows of a token: those of the queries, then those of the keys
+    const unsigned sets_q = (unsigned)(p.x[0].heads + kSetRows - 1) / kSetRows;
+    const unsigned sets = sets_q + (unsigned)(p.x[1].heads + kSetRows - 1) / kSetRows;
+    const unsigned first = blockIdx.x * kGroups + threadIdx.x / kLanes, step = gridDim.x * kGroups;
+    const unsigned rounds = (total + step - 1) / step;  // the same for every thread: the shuffles need whole warps
+    const uint32_t mine = smem_u32(ring) + threadIdx.x * 16;
+    auto piece = [&](unsigned stage, int k) { return mine + (stage * kPieces + k) * (kRopeThreads * 16); };
+
+    // a set by its token and its number within the token; the next one of this
+    // group is `step` sets on
+    struct Set {
+        unsigned t, r;
+    };
+    const unsigned step_t = step / sets, step_r = step % sets;
+    auto after = [&](Set z) {
+        z.t += step_t;
+        z.r += step_r;
+        if (z.r >= sets) {
+            z.r -= sets;
+            ++z.t;
+        }
+        return z;
+    };
+    auto on = [&](const Set& z) { return z.t < (unsigned)p.T; };
+    auto is_k = [&](const Set& z) { return z.r >= sets_q; };
+    auto head0 = [&](const Set& z) { return (int)(is_k(z) ? z.r - sets_q : z.r) * kSetRows; };
+    auto start_copies = [&](const Set& z, const Places& at, unsigned stage) {
+        if (on(z)) {
+            const RopeTensor& x = p.x[is_k(z) ? 1 : 0];
+            const int h0 = head0(z);
+            const uint16_t* row = x.in + (long long)z.t * x.in_tok + (long long)h0 * x.in_head;
+#pragma unroll
+            for (int r = 0; r < kSetRows; ++r, row += x.in_head)
+                if (h0 + r < x.heads) {
+                    if (ch.a >= 0)
+                        copy16(piece(stage, 2 * r), row + 8 * ch.a);
+                    if (ch.b >= 0)
+                        copy16(piece(stage, 2 * r + 1), row + 8 * ch.b);
+                }
+            if (ch.turns) {
+                if (a8 != 255) {
+                    const float* e = at.row(p, a8) + f0;
+                    copy16_l1(piece(stage, 2 * kSetRows), e);
+                    copy16_l1(piece(stage, 2 * kSetRows + 1), e + 4);
+                    copy16_l1(piece(stage, 2 * kSetRows + 2), e + half);
+                    copy16_l1(piece(stage, 2 * kSetRows + 3), e + half + 4);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int f = min(f0 + i, half - 1);  // (a frequency past the last one turns no pair)
+                        const float* e = at.row(p, p.axis_of[f]) + f;
+                        copy4_l1(piece(stage, 2 * kSetRows + i / 4) + (i % 4) * 4, e);
+                        copy4_l1(piece(stage, 2 * kSetRows + 2 + i / 4) + (i % 4) * 4, e + half);
+                    }
+                }
+            }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+
+    // `use` is the set whose rows are computed, `copied` the one whose copies
+    // start next and whose positions are in `at`
+    uint32_t ok_bits = 0;  // bit of a stage: its token's positions are inside the table
+    Set use{first / sets, first % sets}, copied = use;
+    Places at = places_of(p, copied.t, on(copied));
+    unsigned to = 0, from = 0;  // stages
+    auto advance = [&] {
+        const Places here = at;
+        const Set z = copied;
+        copied = after(copied);
+        at = places_of(p, copied.t, on(copied));
+        if (on(z) && !here.ok && z.r == 0 && lane == 0)
+            atomicOr(p.err, (unsigned)B2PA_DEV_BAD_POSITION);
+        start_copies(z, here, to);
+        ok_bits = (ok_bits & ~(1u << to)) | ((here.ok ? 1u : 0u) << to);
+        to = to + 1 == kStages ? 0 : to + 1;
+    };
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i)
+        advance();
+    for (unsigned round = 0; round < rounds; ++round) {
+        advance();
+        asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+        const RopeTensor& x = p.x[is_k(use) ? 1 : 0];
+        const int h0 = head0(use);
+        Turn turn;
+        {
+            float2 wa[4], wb[4], c[4], s[4];
+            load_weights(x, ch, wa, wb);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                uint4 u = make_uint4(0x3F800000u, 0x3F800000u, 0x3F800000u, 0x3F800000u), v = make_uint4(0u, 0u, 0u, 0u);
+                if (ch.turns) {
+                    u = ld_shared_v4(piece(from, 2 * kSetRows + i));
+                    v = ld_shared_v4(piece(from, 2 * kSetRows + 2 + i));
+                }
+                c[2 * i] = make_float2(__uint_as_float(u.x), __uint_as_float(u.y));
+                c[2 * i + 1] = make_float2(__uint_as_float(u.z), __uint_as_float(u.w));
+                s[2 * i] = make_float2(__uint_as_float(v.x), __uint_as_float(v.y));
+                s[2 * i + 1] = make_float2(__uint_as_float(v.z), __uint_as_float(v.w));
+            }
+            if (kMode == kInterleaved) {
+                // pairs past R in a lane that turns others keep their value
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (f0 + i >= half)
+                        (i & 1 ? c[i / 2].y : c[i / 2].x) = 1.f;
+            }
+            turn = turn_of<kMode>(p, lane, c, s, wa, wb);
+        }
+        const bool ok = on(use) && (ok_bits >> from & 1u);
+#pragma unroll
+        for (int r = 0; r < kSetRows; ++r) {
+            const bool there = h0 + r < x.heads;
+            uint4 va = make_uint4(0u, 0u, 0u, 0u), vb = va;
+            if (there && ch.a >= 0)
+                va = ld_shared_v4(piece(from, 2 * r));
+            if (there && ch.b >= 0)
+                vb = ld_shared_v4(piece(from, 2 * r + 1));
+            float2 a[4], b[4];
+            unpack8(va, a);
+            unpack8(vb, b);
+            norm_row<kLanes>(p, x.weight != nullptr, a, b);
+            turn_row<kMode>(p, lane, ch.turns, turn, a, b);
+            if (ok && there)
+                store_row(x, use.t, h0 + r, ch, a, b);
+        }
+        use = after(use);
+        from = from + 1 == kStages ? 0 : from + 1;
+    }
 }
 
 template <RopeMode kMode, int kLanes>
 cudaError_t launch_lanes(const RopeParams& p, int sms, cudaStream_t stream)
 {
-    // four rows per group once one row per group would need more than one
-    // wave of blocks (12 blocks of 128 threads fit an SM's registers)
-    const long long groups = (long long)p.T * (p.x[0].heads + p.x[1].heads);
-    const long long wave = (long long)sms * 12 * (kRopeThreads / kLanes);
-    return groups > wave ? launch_rows<kMode, kLanes, 4>(p, stream) : launch_rows<kMode, kLanes, 1>(p, stream);
+    constexpr int kGroups = kRopeThreads / kLanes;
+    const long long rows = (long long)p.T * (p.x[0].heads + p.x[1].heads);
+    if constexpr (kMode != kHalvesInSmem) {
+        // more than one wave of rows_kernel's blocks (7 per SM)
+        const long long sets = (long long)p.T * ((p.x[0].heads + kSetRows - 1) / kSetRows + (p.x[1].heads + kSetRows - 1) / kSetRows);
+        const int grid = sms * 4;  // four rings of 48 KB per SM
+        if (rows > (long long)sms * 7 * kGroups && sets + (long long)grid * kGroups * (kStages + 1) <= 0xFFFFFFFFLL) {
+            auto kern = rope_staged_kernel<kMode, kLanes>;
+            const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kStagedSmem);
+            if (e != cudaSuccess)
+                return e;
+            kern<<<grid, kRopeThreads, kStagedSmem, stream>>>(p, (unsigned)sets);
+            return cudaGetLastError();
+        }
+    }
+    const long long blocks = (rows + kGroups - 1) / kGroups;
+    if (blocks > 0x7FFFFFFFLL)
+        return cudaErrorInvalidConfiguration;
+    rope_rows_kernel<kMode, kLanes><<<(unsigned)blocks, kRopeThreads, 0, stream>>>(p);
+    return cudaGetLastError();
 }
 
 template <RopeMode kMode>

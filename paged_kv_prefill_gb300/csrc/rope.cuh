@@ -28,6 +28,7 @@ struct RopeParams {
     int T, D, R, axes, max_pos;
     int vec_table;           // 1: eight consecutive table entries can be read as two float4
     float eps;
+    float inv_d;             // 1 / D
     unsigned* err;
     uint8_t axis_of[kRopeMaxD / 2];  // axis of each frequency
     // per eight frequencies: their common axis, or 255
