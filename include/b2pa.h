@@ -451,6 +451,56 @@ B2PA_API int b2pa_read_kv_scaled(const b2pa_tensor* k_pool, const b2pa_tensor* v
                                  b2pa_tensor* k_out, b2pa_tensor* v_out, b2pa_stream_t stream);
 
 /*
+ * b2pa_tree_attention -- attention of drafted token trees over a paged cache,
+ * for verifying several continuations of each request at once.  No counterpart
+ * on the pages.
+ *
+ * Request b owns n = cum_q[b+1] - cum_q[b] query rows, the nodes of its tree.
+ * Their keys are the last n of its seq_lens[b] keys, in the same order; the
+ * c = seq_lens[b] - n keys before them are context.  Node i sees
+ *   - context key j if window_left < 0 or j >= pos - window_left, pos being
+ *     positions[row] (its depth's position), not below c nor above
+ *     seq_lens[b] - 1;
+ *   - node j's key if bit j of its mask row is set (bit j % 32 of word j / 32).
+ *     The mask alone decides: a node normally sees itself and its ancestors.
+ *     Bits from n on are ignored.
+ * With s_j = bmm1_scale <q, K_j> over those keys and m their largest:
+ *   out = bmm2_scale * sum_j e^{s_j - m} V_j / (sum_j e^{s_j - m} + [sinks] e^{sinks[h] - m})
+ * and 0 for a row that sees no key.  Keys that a row does not see never touch
+ * it, whatever they hold.  Trees of different sizes, and of none, may share a
+ * batch; a chain is a tree with a triangular mask.
+ *
+ * q, pools, block_tables, seq_lens, cum_q, scales, sinks, layout and out as for
+ * b2pa_context_attention (out's rows must not overlap), and:
+ *  tree_mask     [T, words] int32, stride[1] == 1, words >= ceil(max_q_len / 32).
+ *  positions     contiguous int32 [T]; NULL without a window.
+ *  max_q_len     upper bound on every n: sizes the query tiles.
+ *  max_kv_len    upper bound on every seq_lens[b].
+ *  workspace     device memory of this call, 256-byte aligned, in use until the
+ *                call's kernels are done: calls that may overlap need their own.
+ *                It is written before it is read and keeps nothing.
+ *  bytes_needed  NULL to run the call.  Otherwise nothing runs and it receives
+ *                the bytes of workspace that this call needs (0: workspace may
+ *                be NULL); workspace itself is not looked at.
+ * A request that is malformed (as for b2pa_context_attention) sets
+ * B2PA_DEV_BAD_REQUEST and its rows are not written; a page id outside the pool
+ * sets B2PA_DEV_BAD_PAGE and its keys read as 0.  Page ids of keys that no row
+ * sees (before every window, past the end) are not used.
+ *
+ * e4m3 pools take their scales in bmm1_scale and bmm2_scale.  Shapes that the
+ * tensor-core path does not take (b2pa_query_path) run on CUDA cores.
+ * Asynchronous on `stream`, capturable after one call on the device; allocates
+ * nothing of its own after that.
+ */
+B2PA_API int b2pa_tree_attention(const b2pa_tensor* q, const b2pa_tensor* k_pool, const b2pa_tensor* v_pool,
+                                 const b2pa_tensor* block_tables, const b2pa_tensor* seq_lens,
+                                 const b2pa_tensor* cum_q, const b2pa_tensor* tree_mask, const b2pa_tensor* positions,
+                                 int32_t max_q_len, int32_t max_kv_len, float bmm1_scale, float bmm2_scale,
+                                 int32_t window_left, const b2pa_tensor* sinks, int32_t layout, b2pa_tensor* out,
+                                 void* workspace, uint64_t workspace_bytes, uint64_t* bytes_needed,
+                                 b2pa_stream_t stream);
+
+/*
  * b2pa_get_device_status -- synchronise `stream`, read and clear the device
  * error word of that stream's workspace.  Returns B2PA_OK if it was zero,
  * else B2PA_ERR_DEVICE with the bits (enum b2pa_device_error) in *bits_out

@@ -52,6 +52,7 @@ EXPORTED = [
     "b2pa_append_kv_scaled",
     "b2pa_read_kv_scaled",
     "b2pa_qk_norm_rope",
+    "b2pa_tree_attention",
     "b2pa_get_device_status",
     "b2pa_set_kernel_path",
     "b2pa_query_path",
@@ -126,6 +127,8 @@ def load(path: str = LIB_PATH):
     lib.b2pa_read_kv_scaled.restype = ctypes.c_int
     lib.b2pa_qk_norm_rope.argtypes = [V] * 6 + [F, V, I, V, V, V]
     lib.b2pa_qk_norm_rope.restype = ctypes.c_int
+    lib.b2pa_tree_attention.argtypes = [V] * 8 + [I, I, F, F, I, V, I, V, V, ctypes.c_uint64, V, V]
+    lib.b2pa_tree_attention.restype = ctypes.c_int
     lib.b2pa_get_device_status.argtypes = [ctypes.c_void_p, ctypes.c_void_p]
     lib.b2pa_get_device_status.restype = ctypes.c_int
     lib.b2pa_set_kernel_path.argtypes = [ctypes.c_int32]
@@ -566,6 +569,51 @@ def qk_norm_rope(
                                   1 if interleaved else 0, _packed(q_out), _packed(k_out), _handle(stream, dev))
     _check(st, "b2pa_qk_norm_rope")
     return q_out, k_out
+
+
+def tree_attention(
+    query: torch.Tensor,
+    kv_cache: Union[torch.Tensor, Sequence[torch.Tensor]],
+    block_tables: torch.Tensor,
+    seq_lens: torch.Tensor,
+    tree_mask: torch.Tensor,
+    max_q_len: int,
+    max_kv_len: int,
+    bmm1_scale: float,
+    bmm2_scale: float,
+    cum_seq_lens_q: torch.Tensor,
+    positions: Optional[torch.Tensor] = None,
+    window_left: int = -1,
+    out: Optional[torch.Tensor] = None,
+    kv_layout: str = "HND",
+    sinks: Optional[torch.Tensor] = None,
+    stream=None,
+) -> torch.Tensor:
+    """Attention of drafted token trees over a paged cache (see include/b2pa.h).
+
+    The query rows of request b are its tree's nodes, whose keys are the last ones of its
+    seq_lens[b] keys; each sees the keys before them (with window_left >= 0 those from
+    positions - window_left on) and the nodes whose bit is set in its row of tree_mask, int32
+    [T, words], bit j % 32 of word j / 32 for node j."""
+    k, v = split_kv_cache(kv_cache, kv_layout)
+    tensors = (query, k, v, block_tables, seq_lens, cum_seq_lens_q, tree_mask, positions)
+    dev = _device_of(stream, *tensors, sinks, out)
+    if dev != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return tree_attention(query, kv_cache, block_tables, seq_lens, tree_mask, max_q_len, max_kv_len, bmm1_scale,
+                                  bmm2_scale, cum_seq_lens_q, positions, window_left, out, kv_layout, sinks, stream)
+    if out is None:
+        out = _new(query, query.shape, stream)
+    run = load().b2pa_tree_attention
+    args = (*map(_packed, tensors), int(max_q_len), int(max_kv_len), bmm1_scale, bmm2_scale, int(window_left),
+            _packed(sinks), LAYOUTS[kv_layout], _packed(out))
+    need = ctypes.c_uint64(0)
+    handle = _handle(stream, dev)
+    _check(run(*args, None, 0, ctypes.byref(need), handle), "b2pa_tree_attention")
+    # from torch's allocator, so that every captured graph keeps a workspace of its own
+    workspace = _new(query, (need.value,), stream, torch.uint8) if need.value else None
+    _check(run(*args, workspace.data_ptr() if need.value else None, need.value, None, handle), "b2pa_tree_attention")
+    return out
 
 
 def device_status(stream=None) -> int:

@@ -284,8 +284,7 @@ int parse_pools(const b2pa_tensor* k, const b2pa_tensor* v, int32_t layout, Prob
 int parse_problem(const b2pa_tensor* q, const b2pa_tensor* k_pool, const b2pa_tensor* v_pool,
                   const b2pa_tensor* block_tables, const b2pa_tensor* seq_lens, const b2pa_tensor* cum_q,
                   const b2pa_tensor* cum_kv, const b2pa_tensor* sinks, int32_t layout, const b2pa_tensor* out,
-                  Problem* pr, int32_t q_per_req = 0, const b2pa_tensor* kv_indptr = nullptr,
-                  const b2pa_tensor* last_page_len = nullptr)
+                  Problem* pr, int32_t q_per_req, const b2pa_tensor* kv_indptr, const b2pa_tensor* last_page_len)
 {
     std::memset(pr, 0, sizeof *pr);
     int st = parse_pools(k_pool, v_pool, layout, pr);
@@ -441,10 +440,6 @@ int encode_pool_map(CUtensorMap* m, const Problem& pr, const void* base, const l
     return B2PA_OK;
 }
 
-}  // namespace b2pa
-
-namespace {
-
 int encode_q_map(CUtensorMap* m, const Problem& pr, int rows_per_tile)
 {
     EncodeTiledFn fn = encode_fn();
@@ -467,6 +462,10 @@ int encode_q_map(CUtensorMap* m, const Problem& pr, int rows_per_tile)
         return fail(B2PA_ERR_UNSUPPORTED, "cuTensorMapEncodeTiled(q) failed with %d", (int)r);
     return B2PA_OK;
 }
+
+}  // namespace b2pa
+
+namespace {
 
 // The output as a 3-D (D, H, T) map whose box is one softmax warp's 32 rows
 // (64 columns at a time): {64, min(G, 32), max(1, 32 / G)}.  Only when 32

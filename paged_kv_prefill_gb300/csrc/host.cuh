@@ -57,6 +57,15 @@ struct Problem {
 };
 
 int parse_pools(const b2pa_tensor* k, const b2pa_tensor* v, int32_t layout, Problem* pr);
+int parse_problem(const b2pa_tensor* q, const b2pa_tensor* k_pool, const b2pa_tensor* v_pool,
+                  const b2pa_tensor* block_tables, const b2pa_tensor* seq_lens, const b2pa_tensor* cum_q,
+                  const b2pa_tensor* cum_kv, const b2pa_tensor* sinks, int32_t layout, const b2pa_tensor* out,
+                  Problem* pr, int32_t q_per_req = 0, const b2pa_tensor* kv_indptr = nullptr,
+                  const b2pa_tensor* last_page_len = nullptr);
+// why the tensor-core paths cannot take this problem (nullptr if they can)
+const char* tc_reject(const Problem& pr, const DevInfo& di);
+// box: (64 columns, one kv head's query heads, rows_per_tile tokens)
+int encode_q_map(CUtensorMap* m, const Problem& pr, int rows_per_tile);
 int encode_pool_map(CUtensorMap* m, const Problem& pr, const void* base, const long long st[3]);
 
 }  // namespace b2pa

@@ -1,6 +1,6 @@
 // ops.cu -- host side of the entry points around the attention call: the
-// query/key norm with the rotation, and the write and read of a cache with one
-// scale per row.  Argument checks and launches; nothing here synchronises.
+// query/key norm with the rotation, the write and read of a cache with one
+// scale per row, and the attention of token trees.  Argument checks and launches; nothing here synchronises.
 #include <cmath>
 #include <cstring>
 
@@ -8,6 +8,7 @@
 #include "host.cuh"
 #include "kv_scaled.cuh"
 #include "rope.cuh"
+#include "tree.cuh"
 
 using namespace b2pa;
 
@@ -240,6 +241,141 @@ int scaled_kv_impl(bool write, const b2pa_tensor* const rows[2], const char* con
     return e == cudaSuccess ? B2PA_OK : cuda_fail(e, write ? "scaled append launch" : "scaled read launch");
 }
 
+// How a tree attention call runs: on the tensor cores or not, and what its
+// workspace holds.
+struct TreePlan {
+    bool tc;
+    int tiles;  // query tiles per item
+    size_t off_ml, off_o, bytes;
+};
+
+int plan_tree(const Problem& pr, int max_q_len, const DevInfo& di, TreePlan* out)
+{
+    const char* why = tc_reject(pr, di);
+    const int path = kernel_path();
+    if (path == B2PA_PATH_TCGEN05 && why)
+        return fail(B2PA_ERR_UNSUPPORTED, "tensor-core path: %s", why);
+    TreePlan t{};
+    t.tc = path != B2PA_PATH_GENERIC && !why;
+    if (t.tc) {
+        t.tiles = max_q_len <= tree_rows(pr.H / pr.Hkv).tile_toks ? 1 : 2;
+        const size_t rows = (size_t)di.sms * 2 * t.tiles * kQRows;  // two segments of every CTA
+        t.off_ml = ((size_t)(pr.B + 1) * sizeof(long long) + 255) / 256 * 256;
+        t.off_o = t.off_ml + rows * sizeof(float2);
+        t.bytes = t.off_o + rows * pr.D * sizeof(float);
+    }
+    *out = t;
+    return B2PA_OK;
+}
+
+int tree_impl(const b2pa_tensor* q, const b2pa_tensor* k_pool, const b2pa_tensor* v_pool,
+              const b2pa_tensor* block_tables, const b2pa_tensor* seq_lens, const b2pa_tensor* cum_q,
+              const b2pa_tensor* tree_mask, const b2pa_tensor* positions, int32_t max_q_len, int32_t max_kv_len,
+              float bmm1_scale, float bmm2_scale, int32_t window_left, const b2pa_tensor* sinks, int32_t layout,
+              b2pa_tensor* out, void* workspace, uint64_t workspace_bytes, uint64_t* bytes_needed, cudaStream_t stream)
+{
+    // empty tensors may carry null data pointers
+    b2pa_tensor no_q, no_out;
+    if (q && out && k_pool && q->ndim == 3 && q->shape[0] == 0) {
+        no_q = *q;
+        no_out = *out;
+        no_q.data = no_out.data = k_pool->data;
+        q = &no_q;
+        out = &no_out;
+    }
+    Problem pr;
+    int st = parse_problem(q, k_pool, v_pool, block_tables, seq_lens, cum_q, nullptr, sinks, layout, out, &pr);
+    if (st)
+        return st;
+    if (max_q_len < 0 || max_kv_len < 0)
+        return fail(B2PA_ERR_INVALID_ARG, "max_q_len / max_kv_len must be >= 0");
+    if (!std::isfinite(bmm1_scale) || !(bmm1_scale > 0.f) || !std::isfinite(bmm2_scale))
+        return fail(B2PA_ERR_INVALID_ARG, "bmm1_scale must be finite and > 0, bmm2_scale finite");
+    const int64_t words = ((int64_t)max_q_len + 31) / 32;
+    if (!tree_mask || tree_mask->ndim != 2 || tree_mask->dtype != B2PA_INT32 || tree_mask->shape[0] != pr.T ||
+        tree_mask->shape[1] < words || tree_mask->shape[1] > 0x7FFFFFF ||
+        (tree_mask->shape[1] > 1 && tree_mask->stride[1] != 1) || (pr.T > 0 && words > 0 && !tree_mask->data))
+        return fail(B2PA_ERR_INVALID_ARG,
+                    "tree_mask must be int32 [T, words] with unit column stride and words >= ceil(max_q_len / 32)");
+    const int window = window_left < 0 ? -1 : window_left;
+    if (window >= 0 && pr.T > 0 && !is_vec(positions, B2PA_INT32, pr.T))
+        return fail(B2PA_ERR_INVALID_ARG, "a window needs positions, contiguous int32 [T]");
+    if (pr.T > 0 && ((pr.T > 1 && pr.out_st_tok < pr.D) || (pr.H > 1 && pr.out_st_head < pr.D)))
+        return fail(B2PA_ERR_INVALID_ARG, "out: its rows overlap");
+    if (bytes_needed)
+        *bytes_needed = 0;
+    if (pr.B == 0 || pr.T == 0)
+        return B2PA_OK;
+    int dev;
+    DevInfo di;
+    TreePlan plan;
+    if ((st = device_info(&dev, &di)) || (st = plan_tree(pr, max_q_len, di, &plan)))
+        return st;
+    if (bytes_needed) {
+        *bytes_needed = plan.bytes;
+        return B2PA_OK;
+    }
+    if (plan.tc && (!workspace || workspace_bytes < plan.bytes || (reinterpret_cast<uintptr_t>(workspace) & 255u)))
+        return fail(B2PA_ERR_INVALID_ARG, "workspace: %llu bytes, 256-byte aligned, are needed",
+                    (unsigned long long)plan.bytes);
+    TreeParams p;
+    std::memset(&p, 0, sizeof p);
+    if ((st = status_word(dev, stream, &p.err)))
+        return st;
+    p.rows = tree_rows(pr.H / pr.Hkv);
+    p.q = static_cast<const uint16_t*>(pr.q);
+    p.k = pr.k;
+    p.v = pr.v;
+    p.out = static_cast<uint16_t*>(pr.out);
+    p.q_st_tok = pr.q_st_tok;
+    p.q_st_head = pr.q_st_head;
+    p.out_st_tok = pr.out_st_tok;
+    p.out_st_head = pr.out_st_head;
+    for (int i = 0; i < 3; ++i) {
+        p.k_st[i] = pr.k_st[i];
+        p.v_st[i] = pr.v_st[i];
+    }
+    p.cum_q = pr.cum_q;
+    p.seq_lens = pr.seq;
+    p.block_tables = pr.bt;
+    p.bt_stride = pr.bt_stride;
+    p.mask = static_cast<const unsigned*>(tree_mask->data);
+    p.mask_stride = tree_mask->stride[0];
+    p.mask_words = (int)tree_mask->shape[1];
+    p.positions = window >= 0 ? static_cast<const int*>(positions->data) : nullptr;
+    p.sinks = pr.sinks;
+    p.B = pr.B;
+    p.T = pr.T;
+    p.H = pr.H;
+    p.Hkv = pr.Hkv;
+    p.D = pr.D;
+    p.page_size = pr.P;
+    p.max_pages = pr.max_pages;
+    p.num_pages = pr.N;
+    p.max_q_len = max_q_len;
+    p.max_kv_len = max_kv_len;
+    p.window = window;
+    p.grid = di.sms;
+    p.scale_log2 = (float)((double)bmm1_scale * 1.4426950408889634);
+    p.bmm2 = bmm2_scale;
+    p.wait_limit_ns = wait_limit_ns();
+    p.inject_stall = inject_stall();
+    cudaError_t e;
+    if (plan.tc) {
+        uint8_t* ws = static_cast<uint8_t*>(workspace);
+        p.first_tile = reinterpret_cast<long long*>(ws);
+        p.part_ml = reinterpret_cast<float2*>(ws + plan.off_ml);
+        p.part_o = reinterpret_cast<float*>(ws + plan.off_o);
+        if ((st = encode_q_map(&p.tm_q, pr, p.rows.box_toks)) || (st = encode_pool_map(&p.tm_k, pr, pr.k, pr.k_st)) ||
+            (st = encode_pool_map(&p.tm_v, pr, pr.v, pr.v_st)))
+            return st;
+        e = launch_attention_tree(p, pr.fp8, plan.tiles, stream);
+    } else {
+        e = launch_tree_generic(p, pr.fp8, stream);
+    }
+    return e == cudaSuccess ? B2PA_OK : cuda_fail(e, "tree attention launch");
+}
+
 }  // namespace
 
 // ====================================================================== C ABI
@@ -278,6 +414,20 @@ int b2pa_read_kv_scaled(const b2pa_tensor* k_pool, const b2pa_tensor* v_pool, co
         const char* names[2] = {"k_out", "v_out"};
         return scaled_kv_impl(false, rows, names, k_pool, v_pool, k_scales, v_scales, cache_loc, layout,
                               reinterpret_cast<cudaStream_t>(stream));
+    });
+}
+
+int b2pa_tree_attention(const b2pa_tensor* q, const b2pa_tensor* k_pool, const b2pa_tensor* v_pool,
+                        const b2pa_tensor* block_tables, const b2pa_tensor* seq_lens, const b2pa_tensor* cum_q,
+                        const b2pa_tensor* tree_mask, const b2pa_tensor* positions, int32_t max_q_len,
+                        int32_t max_kv_len, float bmm1_scale, float bmm2_scale, int32_t window_left,
+                        const b2pa_tensor* sinks, int32_t layout, b2pa_tensor* out, void* workspace,
+                        uint64_t workspace_bytes, uint64_t* bytes_needed, b2pa_stream_t stream)
+{
+    return guarded([&] {
+        return tree_impl(q, k_pool, v_pool, block_tables, seq_lens, cum_q, tree_mask, positions, max_q_len, max_kv_len,
+                         bmm1_scale, bmm2_scale, window_left, sinks, layout, out, workspace, workspace_bytes,
+                         bytes_needed, reinterpret_cast<cudaStream_t>(stream));
     });
 }
 

@@ -1,0 +1,133 @@
+// tree.cuh -- parameters and geometry of the tree attention kernels
+// (attn_tree.cu, and tree_generic_kernel in generic.cu), filled in ops.cu.
+//
+// Request b brings n = cum_q[b+1] - cum_q[b] drafted nodes, whose own keys are
+// the last n of its kv_len keys; c = kv_len - n keys before them are context.
+// Node i sees the context keys j >= lo_i and the node keys whose bit is set in
+// its mask row.
+#pragma once
+
+#include "common.cuh"
+
+namespace b2pa {
+
+// How the 128 MMA rows of a query tile are dealt out.  With G <= 32 query heads
+// per kv head, each of the four softmax warps gets whole tokens (box_toks at
+// most, in its first box_toks * G lanes), a tile's tokens being split evenly
+// over the warps so that a small tree still uses all four.  With more heads
+// row = token * G + head.
+struct TreeRows {
+    int G, box_toks, tile_toks, by_warp;
+};
+
+__host__ __device__ inline TreeRows tree_rows(int G)
+{
+    TreeRows r;
+    r.G = G;
+    r.by_warp = G <= 32;
+    r.box_toks = r.by_warp ? 32 / G : kQRows / G;
+    r.tile_toks = r.by_warp ? 4 * r.box_toks : r.box_toks;
+    return r;
+}
+
+struct TreeParams {  // 128-byte aligned through its CUtensorMap members
+    CUtensorMap tm_q;  // 3-D: (D, H, T), box (64, G, box_toks)
+    CUtensorMap tm_k;  // 4-D: (D, P, Hkv, pages), box (64 | 128 bytes, min(P,128), 1, 1)
+    CUtensorMap tm_v;
+    // plain pointers and strides (elements): the generic kernel's, and the slow
+    // path for values that are not finite
+    const uint16_t* q;
+    const void* k;
+    const void* v;
+    uint16_t* out;
+    long long q_st_tok, q_st_head, out_st_tok, out_st_head;
+    long long k_st[3], v_st[3];  // page, head, slot
+    const int* cum_q;
+    const int* seq_lens;
+    const int* block_tables;
+    long long bt_stride;
+    const unsigned* mask;  // [T, words]
+    long long mask_stride;
+    const int* positions;  // null without a window
+    const float* sinks;    // may be null
+    float* part_o;         // [grid * 2][tiles * 128][D] unnormalised partial rows
+    float2* part_ml;       // [grid * 2][tiles * 128] running maximum (log2 units) and sum
+    long long* first_tile;  // [B + 1]: kv tiles of the requests before each
+    unsigned* err;
+    TreeRows rows;
+    int B, T, H, Hkv, D, page_size, max_pages, num_pages, max_q_len, max_kv_len, mask_words, window;
+    int grid;              // CTAs of the attention kernel
+    float scale_log2;      // bmm1_scale * log2(e)
+    float bmm2;
+    unsigned long long wait_limit_ns;
+    int inject_stall;
+};
+
+// A request as the kernels see it.  Its work is items * Hkv units (a unit is
+// a kv head with the nodes of one item) of `tiles` kv tiles each.
+struct TreeReq {
+    int q0, n, kv_len, ctx, lo, items, n_lo, tiles;
+    bool ok;
+    __device__ __forceinline__ long long work(int Hkv) const { return (long long)items * Hkv * tiles; }
+};
+
+__device__ __forceinline__ TreeReq tree_request(const TreeParams& p, int b, int item_toks)
+{
+    const RequestView v = load_request(QStarts{p.cum_q, 0}, p.seq_lens, b, p.max_q_len, p.max_kv_len, p.page_size,
+                                       p.max_pages, p.T);
+    TreeReq r;
+    r.q0 = v.q_start;
+    r.n = v.q_len;
+    r.kv_len = v.kv_len;
+    r.ok = v.ok;
+    r.ctx = v.kv_len - v.q_len;
+    r.lo = p.window < 0 ? 0 : max(0, r.ctx - p.window);  // no row sees an earlier key
+    const bool any = v.ok && v.q_len > 0;
+    r.items = any ? (v.q_len + item_toks - 1) / item_toks : 0;
+    r.n_lo = any ? r.lo / kKvTile : 0;
+    r.tiles = any ? (v.kv_len - 1) / kKvTile - r.n_lo + 1 : 0;
+    return r;
+}
+
+// First context key that a node at position pos sees.
+__device__ __forceinline__ int tree_row_lo(int pos, int ctx, int kv_len, int window)
+{
+    return window < 0 ? 0 : max(0, min(max(pos, ctx), kv_len - 1) - window);
+}
+
+// The CTAs cut all requests' units, laid end to end, into equal runs of kv
+// tiles: CTA i of g takes [start(i), start(i + 1)).
+struct TreeCut {
+    long long total;
+    int g;
+    __device__ __forceinline__ long long start(int i) const { return total * i / g; }
+    __device__ __forceinline__ int owner(long long tile) const
+    {
+        int i = (int)(tile * g / total);
+        while (i + 1 < g && start(i + 1) <= tile)
+            ++i;
+        while (start(i) > tile)
+            --i;
+        return i;
+    }
+};
+
+__device__ __forceinline__ TreeCut tree_cut(long long total, int grid)
+{
+    return TreeCut{total, (int)min((long long)grid, total)};
+}
+
+// The MMA row (0 .. 127) of token `tok` of `toks` in a query tile, head h.
+__device__ __forceinline__ int tree_row(const TreeRows& r, int tok, int toks, int h)
+{
+    if (!r.by_warp)
+        return tok * r.G + h;
+    const int per = (toks + 3) >> 2;
+    return (tok / per) * 32 + (tok % per) * r.G + h;
+}
+
+// tiles: query tiles per item (1 or 2)
+cudaError_t launch_attention_tree(const TreeParams& p, bool fp8, int tiles, cudaStream_t stream);
+cudaError_t launch_tree_generic(const TreeParams& p, bool fp8, cudaStream_t stream);
+
+}  // namespace b2pa
