@@ -79,7 +79,8 @@ enum b2pa_status {
     B2PA_ERR_INVALID_ARG = -1, /* null pointer, bad rank/shape/dtype/stride, H % Hkv != 0, ... */
     B2PA_ERR_UNSUPPORTED = -2, /* valid but not implemented (e.g. a forced kernel path that cannot run the shape) */
     B2PA_ERR_CUDA = -3,        /* a CUDA runtime/driver call failed; see b2pa_last_error_message */
-    B2PA_ERR_DEVICE = -4       /* b2pa_get_device_status: the device error word was non-zero */
+    B2PA_ERR_DEVICE = -4,      /* b2pa_get_device_status: the device error word was non-zero */
+    B2PA_ERR_WORKSPACE = -5    /* b2pa_tree_attention: workspace_bytes is less than *bytes_needed; nothing ran */
 };
 
 /* Bits of the device error word (b2pa_get_device_status). */
@@ -479,9 +480,9 @@ B2PA_API int b2pa_read_kv_scaled(const b2pa_tensor* k_pool, const b2pa_tensor* v
  *  workspace     device memory of this call, 256-byte aligned, in use until the
  *                call's kernels are done: calls that may overlap need their own.
  *                It is written before it is read and keeps nothing.
- *  bytes_needed  NULL to run the call.  Otherwise nothing runs and it receives
- *                the bytes of workspace that this call needs (0: workspace may
- *                be NULL); workspace itself is not looked at.
+ *  bytes_needed  receives the bytes of workspace that the call needs (0:
+ *                workspace may be NULL).  With fewer in workspace_bytes nothing
+ *                runs and the call returns B2PA_ERR_WORKSPACE.
  * A request that is malformed (as for b2pa_context_attention) sets
  * B2PA_DEV_BAD_REQUEST and its rows are not written; a page id outside the pool
  * sets B2PA_DEV_BAD_PAGE and its keys read as 0.  Page ids of keys that no row

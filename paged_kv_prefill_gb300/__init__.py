@@ -28,7 +28,7 @@ B2PA_BF16, B2PA_FP8_E4M3, B2PA_FP32, B2PA_INT32 = 1, 2, 3, 4
 LAYOUTS = {"HND": 0, "NHD": 1}
 PATH_AUTO, PATH_TCGEN05, PATH_GENERIC = 0, 1, 2
 STATUS = {0: "B2PA_OK", -1: "B2PA_ERR_INVALID_ARG", -2: "B2PA_ERR_UNSUPPORTED", -3: "B2PA_ERR_CUDA",
-          -4: "B2PA_ERR_DEVICE"}
+          -4: "B2PA_ERR_DEVICE", -5: "B2PA_ERR_WORKSPACE"}
 DEV_BAD_REQUEST, DEV_BAD_PAGE, DEV_TIMEOUT, DEV_BAD_CUM_KV, DEV_OVERFLOW = 1, 2, 4, 8, 16
 DEV_BAD_SLOT, DEV_BAD_SCALE, DEV_BAD_POSITION = 32, 64, 128
 
@@ -214,11 +214,11 @@ def _handle(stream, dev: int) -> int:
 def _new(like: torch.Tensor, shape, stream, dtype=torch.bfloat16) -> torch.Tensor:
     """A new contiguous tensor on like's device from the memory of the stream that the call runs on."""
     if stream is None:
-        return like.new_empty(shape, dtype=dtype)
+        return torch.empty(shape, dtype=dtype, device=like.device)
     if not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(int(stream), device=like.device)
     with torch.cuda.stream(stream):
-        return like.new_empty(shape, dtype=dtype)
+        return torch.empty(shape, dtype=dtype, device=like.device)
 
 
 def _check(status: int, where: str):
@@ -571,6 +571,9 @@ def qk_norm_rope(
     return q_out, k_out
 
 
+_tree_workspace = {}  # bytes of a tree_attention call's workspace, by its sizes
+
+
 def tree_attention(
     query: torch.Tensor,
     kv_cache: Union[torch.Tensor, Sequence[torch.Tensor]],
@@ -604,15 +607,20 @@ def tree_attention(
                                   bmm2_scale, cum_seq_lens_q, positions, window_left, out, kv_layout, sinks, stream)
     if out is None:
         out = _new(query, query.shape, stream)
-    run = load().b2pa_tree_attention
-    args = (*map(_packed, tensors), int(max_q_len), int(max_kv_len), bmm1_scale, bmm2_scale, int(window_left),
-            _packed(sinks), LAYOUTS[kv_layout], _packed(out))
-    need = ctypes.c_uint64(0)
-    handle = _handle(stream, dev)
-    _check(run(*args, None, 0, ctypes.byref(need), handle), "b2pa_tree_attention")
-    # from torch's allocator, so that every captured graph keeps a workspace of its own
-    workspace = _new(query, (need.value,), stream, torch.uint8) if need.value else None
-    _check(run(*args, workspace.data_ptr() if need.value else None, need.value, None, handle), "b2pa_tree_attention")
+    args = (*map(_packed, tensors), max_q_len, max_kv_len, bmm1_scale, bmm2_scale, window_left, _packed(sinks),
+            LAYOUTS[kv_layout], _packed(out))
+    handle, need = _handle(stream, dev), ctypes.c_uint64(0)
+    # the workspace comes from torch's allocator for this call, so that every captured graph keeps
+    # its own; its size is remembered by the call's sizes
+    sizes = (dev, query.shape[1:], k.shape, max_q_len)
+    size = _tree_workspace.get(sizes, 0)
+    while True:
+        workspace = _new(query, (size,), stream, torch.uint8) if size else None
+        st = load().b2pa_tree_attention(*args, workspace.data_ptr() if size else None, size, ctypes.byref(need), handle)
+        if st != -5 or need.value <= size:
+            break
+        size = _tree_workspace[sizes] = need.value
+    _check(st, "b2pa_tree_attention")
     return out
 
 

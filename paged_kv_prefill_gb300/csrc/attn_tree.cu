@@ -179,6 +179,10 @@ __device__ void tree_producer(const TreeParams& p, const TreeCtx& c, long long p
     bool ok = true;
     TreeReq r = pos < end ? tree_request(p, b, item_toks) : TreeReq{};
     const long long begin = pos;
+    int4* note = p.part_seg + (long long)blockIdx.x * 4;  // of slots 0 and 1
+    if (lane < 2)
+        TreePart{}.write(note + 2 * lane);
+    __syncwarp();
     for (uint32_t n = 0; ok; ++n) {
         const uint32_t slot = n % kTreeSlots;
         if (!wait_bar(&c.it_empty[slot], ((n / kTreeSlots) & 1) ^ 1, c))
@@ -204,6 +208,8 @@ __device__ void tree_producer(const TreeParams& p, const TreeCtx& c, long long p
             s.whole = s.tiles == r.tiles;
             s.slot = pos == begin ? 0 : 1;
             pos += s.tiles;
+            if (!s.whole && lane == 0)
+                TreePart{r.tiles, off, s.tiles, s.q0 + s.tok0, s.toks, s.kvh}.write(note + 2 * s.slot);
         }
         if (lane == 0) {
             post_seg(c.item_slot + slot * 12, s);
@@ -1054,7 +1060,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) attention_tree_kernel(const _
     // Where this CTA's run starts: kv tiles of the requests before each, by a
     // scan over the threads' contiguous shares of the requests (scratch in the
     // ring, which is empty yet).
-    long long* scan = reinterpret_cast<long long*>(smem + C::kOffRing);  // 13 warp sums, then start, end, base, request
+    long long* scan = reinterpret_cast<long long*>(smem + C::kOffRing);  // 12 warp sums; [16] base, [17] request
     const int item_toks = kTiles * p.rows.tile_toks;
     const int share = (p.B + kTreeThreads - 1) / kTreeThreads;
     const int b0 = min(p.B, tid * share), b1 = min(p.B, b0 + share);
@@ -1076,6 +1082,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) attention_tree_kernel(const _
         scan[warp] = before;
     __syncthreads();
     long long total = 0, warps_before = 0;
+#pragma unroll
     for (int w = 0; w < kTreeThreads / 32; ++w) {
         warps_before += w < warp ? scan[w] : 0;
         total += scan[w];
@@ -1087,24 +1094,14 @@ __global__ void __launch_bounds__(kTreeThreads, 1) attention_tree_kernel(const _
     if (works && start >= before && start < before + mine) {
         long long base = before;
         int b = b0;
-        while (true) {
+        for (; b + 1 < b1; ++b) {  // this thread's requests, if it has several
             const long long w = tree_request(p, b, item_toks).work(p.Hkv);
-            if (start < base + w || b + 1 >= b1)
+            if (start < base + w)
                 break;
             base += w;
-            ++b;
         }
         scan[16] = base;
         scan[17] = b;
-    }
-    if (blockIdx.x == 0) {
-        long long base = before;
-        for (int b = b0; b < b1; ++b) {
-            p.first_tile[b] = base;
-            base += tree_request(p, b, item_toks).work(p.Hkv);
-        }
-        if (tid == 0)
-            p.first_tile[p.B] = total;
     }
     __syncthreads();
     const long long base = scan[16];
@@ -1139,99 +1136,129 @@ __global__ void __launch_bounds__(kTreeThreads, 1) attention_tree_kernel(const _
 // The merge of a unit that several CTAs shared: with the segments' (m_c, l_c,
 // O_c) and m = max m_c, w_c = 2^(m_c - m),
 //   out = bmm2 * sum_c w_c O_c / (sum_c w_c l_c + [sinks] 2^(sink log2 e - m)),
-// in the order of the keys.  One warp per output row.
+// in the order of the keys.  Block (i, y) takes the unit whose first segment is
+// CTA i's, if there is one that goes on in the next CTA, and of its rows 8 y ..
+// 8 y + 7, one per warp.  Latency alone: loads that do not depend on each other
+// are issued together.
 // ---------------------------------------------------------------------------
-constexpr int kMergeWarps = 4;
+constexpr int kMergeRows = 8;
 
 template <int D>
-__global__ void __launch_bounds__(kMergeWarps * 32) tree_merge_kernel(const __grid_constant__ TreeParams p, int tiles)
+__global__ void __launch_bounds__(kMergeRows * 32) tree_merge_kernel(const __grid_constant__ TreeParams p, int tiles)
 {
     constexpr float kLog2e = 1.4426950408889634f;
     constexpr int kPer = D / 32;  // dimensions per lane
+    constexpr int kBatch = 8;     // segments whose rows are loaded together
     pdl_wait();
     const int lane = threadIdx.x & 31;
-    const long long id = (long long)blockIdx.x * kMergeWarps + (threadIdx.x >> 5);
-    if (id >= (long long)p.T * p.H)
+    const int first = blockIdx.x, r = (int)blockIdx.y * kMergeRows + (threadIdx.x >> 5);
+    // the segment that opens a unit is the CTA's last; the ones after it are
+    // the first of the CTAs that follow, up to the one that reaches the end
+    const int4* notes = p.part_seg;
+    TreePart x = TreePart::read(notes + (long long)first * 4);
+    const TreePart last = TreePart::read(notes + (long long)first * 4 + 2);
+    TreePart next = TreePart{};
+    if (first + 1 + lane < p.grid)
+        next = TreePart::read(notes + (long long)(first + 1 + lane) * 4);
+    const int slot = last.all != 0 ? 1 : 0;
+    if (slot)
+        x = last;
+    if (x.all == 0 || x.off != 0 || r >= x.toks * p.rows.G)
         return;
-    const int tok = (int)(id / p.H), h = (int)(id % p.H);
-    int lo = 0, hi = p.B - 1;  // the last request that starts at or before tok
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (p.cum_q[mid] <= tok)
-            lo = mid;
-        else
-            hi = mid - 1;
+    int segs = 1;
+    for (int c = first + 1;; c += 32) {
+        if (c > first + 1)
+            next = c + lane < p.grid ? TreePart::read(notes + (long long)(c + lane) * 4) : TreePart{};
+        const unsigned m = __ballot_sync(0xffffffffu, next.off + next.tiles >= next.all);  // (none: 0 >= 0)
+        if (m != 0) {
+            segs += __ffs(m);
+            break;
+        }
+        segs += 32;
     }
-    const int b = lo, item_toks = tiles * p.rows.tile_toks;
-    const TreeReq r = tree_request(p, b, item_toks);
-    const int i = tok - r.q0;
-    if (r.items == 0 || i < 0 || i >= r.n)
-        return;
-    const TreeCut cut = tree_cut(p.first_tile[p.B], p.grid);
-    const int kvh = h / p.rows.G, head = h % p.rows.G, it = i / item_toks;
-    const long long u0 = p.first_tile[b] + ((long long)kvh * r.items + it) * r.tiles;
-    const int c0 = cut.owner(u0), c1 = cut.owner(u0 + r.tiles - 1);
-    if (c0 == c1)
-        return;  // one CTA had it all and wrote the row
-    const int in_item = i - it * item_toks, qt = in_item / p.rows.tile_toks;
-    const int toks = min(p.rows.tile_toks, min(item_toks, r.n - it * item_toks) - qt * p.rows.tile_toks);
-    const int row = tree_row(p.rows, in_item - qt * p.rows.tile_toks, toks, head);
-    // segment c: the first of its CTA's run (slot 0) unless that starts before the unit
+    const int tok = r / p.rows.G, head = r - tok * p.rows.G, h = x.kvh * p.rows.G + head;
+    const int qt = tok / p.rows.tile_toks, in_tile = tok - qt * p.rows.tile_toks;
+    const int row = tree_row(p.rows, in_tile, min(p.rows.tile_toks, x.toks - qt * p.rows.tile_toks), head);
+    // segment c of the unit: slot 0 of CTA first + c, but for its first
     auto part = [&](int c) {
-        const int slot = c > c0 || cut.start(c) == u0 ? 0 : 1;
-        return ((long long)(c * 2 + slot) * tiles + qt) * kQRows + row;
+        return ((long long)((first + c) * 2 + (c == 0 ? slot : 0)) * tiles + qt) * kQRows + row;
     };
-    float m = -INFINITY;
-    for (int c = c0 + lane; c <= c1; c += 32)
-        m = fmaxf(m, p.part_ml[part(c)].x);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    float den = 0.f;
+    const float sink = p.sinks != nullptr ? p.sinks[h] * kLog2e : -INFINITY;
+    // running over groups of 32 segments, each lane holding one's (m, l)
+    float m = -INFINITY, den = 0.f;
     float a[kPer];
 #pragma unroll
     for (int k = 0; k < kPer; ++k)
         a[k] = 0.f;
-#pragma unroll 4
-    for (int c = c0; c <= c1; ++c) {
-        const long long at = part(c);
-        const float2 x = p.part_ml[at];
-        // (a sum that is no number keeps its weight, whatever its maximum)
-        const float w = x.x == -INFINITY && x.y == 0.f ? 0.f : m == -INFINITY ? 1.f : ex2_approx(x.x - m);
-        const float* o = p.part_o + at * D + lane * kPer;
-        float v[kPer];
-        if constexpr (kPer == 4) {
-            const float4 y = *reinterpret_cast<const float4*>(o);
-            v[0] = y.x;
-            v[1] = y.y;
-            v[2] = y.z;
-            v[3] = y.w;
-        } else {
-            const float2 y = *reinterpret_cast<const float2*>(o);
-            v[0] = y.x;
-            v[1] = y.y;
-        }
-        if (w != 0.f) {
-            den = fmaf(w, x.y, den);
+    for (int c0 = 0; c0 < segs; c0 += 32) {
+        const int n = min(32, segs - c0);
+        float2 ml = make_float2(-INFINITY, 0.f);
+        if (lane < n)
+            ml = p.part_ml[part(c0 + lane)];
+        float w = 0.f;
+        for (int b = 0; b < n; b += kBatch) {
+            float v[kBatch][kPer];
 #pragma unroll
-            for (int k = 0; k < kPer; ++k)
-                a[k] = fmaf(w, v[k], a[k]);
+            for (int c = 0; c < kBatch; ++c) {
+                if (b + c >= n)
+                    break;
+                const float* o = p.part_o + part(c0 + b + c) * D + lane * kPer;
+                if constexpr (kPer == 4) {
+                    const float4 y = *reinterpret_cast<const float4*>(o);
+                    v[c][0] = y.x;
+                    v[c][1] = y.y;
+                    v[c][2] = y.z;
+                    v[c][3] = y.w;
+                } else {
+                    const float2 y = *reinterpret_cast<const float2*>(o);
+                    v[c][0] = y.x;
+                    v[c][1] = y.y;
+                }
+            }
+            if (b == 0) {
+                float top = fmaxf(m, ml.x);
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1)
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                const float old = m == -INFINITY ? 1.f : ex2_approx(m - top);  // (no maximum yet: sums of 0 or NaN)
+                // (a sum that is no number keeps its weight, whatever its maximum)
+                w = ml.x == -INFINITY && ml.y == 0.f ? 0.f : top == -INFINITY ? 1.f : ex2_approx(ml.x - top);
+                m = top;
+                float s = w != 0.f ? w * ml.y : 0.f;
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1)
+                    s += __shfl_xor_sync(0xffffffffu, s, o);
+                den = fmaf(den, old, s);
+#pragma unroll
+                for (int k = 0; k < kPer; ++k)
+                    a[k] *= old;
+            }
+#pragma unroll
+            for (int c = 0; c < kBatch; ++c) {
+                const float wc = __shfl_sync(0xffffffffu, w, (b + c) & 31);
+                if (b + c < n && wc != 0.f) {
+#pragma unroll
+                    for (int k = 0; k < kPer; ++k)
+                        a[k] = fmaf(wc, v[c][k], a[k]);
+                }
+            }
         }
     }
-    if (p.sinks != nullptr && m != -INFINITY)
-        den += ex2_approx(fmaf(p.sinks[h], kLog2e, -m));
+    if (m != -INFINITY)
+        den += ex2_approx(sink - m);
     const float f = den == 0.f ? 0.f : p.bmm2 / den;
-    uint16_t* to = p.out + (long long)tok * p.out_st_tok + (long long)h * p.out_st_head + lane * kPer;
-#pragma unroll
-    for (int k = 0; k < kPer; k += 2)
-        *reinterpret_cast<uint32_t*>(to + k) = pack_bf16x2(a[k] * f, a[k + 1] * f);
+    uint16_t* to = p.out + (long long)(x.row0 + tok) * p.out_st_tok + (long long)h * p.out_st_head + lane * kPer;
+    if constexpr (kPer == 4)
+        *reinterpret_cast<uint2*>(to) = make_uint2(pack_bf16x2(a[0] * f, a[1] * f), pack_bf16x2(a[2] * f, a[3] * f));
+    else
+        *reinterpret_cast<uint32_t*>(to) = pack_bf16x2(a[0] * f, a[1] * f);
 }
 
 template <typename Kern, typename... Args>
-cudaError_t launch_pdl(Kern kern, unsigned grid, unsigned threads, size_t smem, cudaStream_t stream, Args... args)
+cudaError_t launch_pdl(Kern kern, dim3 grid, unsigned threads, size_t smem, cudaStream_t stream, const Args&... args)
 {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid);
+    cfg.gridDim = grid;
     cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
@@ -1262,12 +1289,11 @@ cudaError_t launch_tree(const TreeParams& p, cudaStream_t stream)
     });
     if (err[dev] != cudaSuccess)
         return err[dev];
-    if ((e = launch_pdl(kern, (unsigned)p.grid, kTreeThreads, C::kSmemBytes, stream, p)) != cudaSuccess)
+    if ((e = launch_pdl(kern, dim3(p.grid), kTreeThreads, C::kSmemBytes, stream, p)) != cudaSuccess)
         return e;
-    const long long blocks = ((long long)p.T * p.H + kMergeWarps - 1) / kMergeWarps;
-    if (blocks > 0x7FFFFFFFLL)
-        return cudaErrorInvalidConfiguration;
-    return launch_pdl(tree_merge_kernel<D>, (unsigned)blocks, kMergeWarps * 32, 0, stream, p, kTiles);
+    const int rows = min(p.max_q_len, kTiles * p.rows.tile_toks) * p.rows.G;  // of a unit, at most
+    return launch_pdl(tree_merge_kernel<D>, dim3(p.grid, (rows + kMergeRows - 1) / kMergeRows), kMergeRows * 32, 0,
+                      stream, p, kTiles);
 }
 
 }  // namespace

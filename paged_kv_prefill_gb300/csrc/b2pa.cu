@@ -1262,6 +1262,8 @@ const char* b2pa_status_string(int32_t status)
         return "B2PA_ERR_CUDA";
     case B2PA_ERR_DEVICE:
         return "B2PA_ERR_DEVICE";
+    case B2PA_ERR_WORKSPACE:
+        return "B2PA_ERR_WORKSPACE";
     default:
         return "B2PA_UNKNOWN_STATUS";
     }

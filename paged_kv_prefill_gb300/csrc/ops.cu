@@ -260,7 +260,7 @@ int plan_tree(const Problem& pr, int max_q_len, const DevInfo& di, TreePlan* out
     if (t.tc) {
         t.tiles = max_q_len <= tree_rows(pr.H / pr.Hkv).tile_toks ? 1 : 2;
         const size_t rows = (size_t)di.sms * 2 * t.tiles * kQRows;  // two segments of every CTA
-        t.off_ml = ((size_t)(pr.B + 1) * sizeof(long long) + 255) / 256 * 256;
+        t.off_ml = ((size_t)di.sms * 2 * 2 * sizeof(int4) + 255) / 256 * 256;
         t.off_o = t.off_ml + rows * sizeof(float2);
         t.bytes = t.off_o + rows * pr.D * sizeof(float);
     }
@@ -274,6 +274,8 @@ int tree_impl(const b2pa_tensor* q, const b2pa_tensor* k_pool, const b2pa_tensor
               float bmm1_scale, float bmm2_scale, int32_t window_left, const b2pa_tensor* sinks, int32_t layout,
               b2pa_tensor* out, void* workspace, uint64_t workspace_bytes, uint64_t* bytes_needed, cudaStream_t stream)
 {
+    if (!bytes_needed)
+        return fail(B2PA_ERR_INVALID_ARG, "bytes_needed: null");
     // empty tensors may carry null data pointers
     b2pa_tensor no_q, no_out;
     if (q && out && k_pool && q->ndim == 3 && q->shape[0] == 0) {
@@ -302,8 +304,7 @@ int tree_impl(const b2pa_tensor* q, const b2pa_tensor* k_pool, const b2pa_tensor
         return fail(B2PA_ERR_INVALID_ARG, "a window needs positions, contiguous int32 [T]");
     if (pr.T > 0 && ((pr.T > 1 && pr.out_st_tok < pr.D) || (pr.H > 1 && pr.out_st_head < pr.D)))
         return fail(B2PA_ERR_INVALID_ARG, "out: its rows overlap");
-    if (bytes_needed)
-        *bytes_needed = 0;
+    *bytes_needed = 0;
     if (pr.B == 0 || pr.T == 0)
         return B2PA_OK;
     int dev;
@@ -311,13 +312,11 @@ int tree_impl(const b2pa_tensor* q, const b2pa_tensor* k_pool, const b2pa_tensor
     TreePlan plan;
     if ((st = device_info(&dev, &di)) || (st = plan_tree(pr, max_q_len, di, &plan)))
         return st;
-    if (bytes_needed) {
-        *bytes_needed = plan.bytes;
-        return B2PA_OK;
-    }
-    if (plan.tc && (!workspace || workspace_bytes < plan.bytes || (reinterpret_cast<uintptr_t>(workspace) & 255u)))
-        return fail(B2PA_ERR_INVALID_ARG, "workspace: %llu bytes, 256-byte aligned, are needed",
-                    (unsigned long long)plan.bytes);
+    *bytes_needed = plan.bytes;
+    if (workspace_bytes < plan.bytes)
+        return fail(B2PA_ERR_WORKSPACE, "workspace: %llu bytes are needed", (unsigned long long)plan.bytes);
+    if (plan.bytes && (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u)))
+        return fail(B2PA_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
     TreeParams p;
     std::memset(&p, 0, sizeof p);
     if ((st = status_word(dev, stream, &p.err)))
@@ -363,7 +362,7 @@ int tree_impl(const b2pa_tensor* q, const b2pa_tensor* k_pool, const b2pa_tensor
     cudaError_t e;
     if (plan.tc) {
         uint8_t* ws = static_cast<uint8_t*>(workspace);
-        p.first_tile = reinterpret_cast<long long*>(ws);
+        p.part_seg = reinterpret_cast<int4*>(ws);
         p.part_ml = reinterpret_cast<float2*>(ws + plan.off_ml);
         p.part_o = reinterpret_cast<float*>(ws + plan.off_o);
         if ((st = encode_q_map(&p.tm_q, pr, p.rows.box_toks)) || (st = encode_pool_map(&p.tm_k, pr, pr.k, pr.k_st)) ||

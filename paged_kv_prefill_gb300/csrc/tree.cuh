@@ -52,7 +52,7 @@ struct TreeParams {  // 128-byte aligned through its CUtensorMap members
     const float* sinks;    // may be null
     float* part_o;         // [grid * 2][tiles * 128][D] unnormalised partial rows
     float2* part_ml;       // [grid * 2][tiles * 128] running maximum (log2 units) and sum
-    long long* first_tile;  // [B + 1]: kv tiles of the requests before each
+    int4* part_seg;        // [grid * 2][2]: TreePart of each partial segment
     unsigned* err;
     TreeRows rows;
     int B, T, H, Hkv, D, page_size, max_pages, num_pages, max_q_len, max_kv_len, mask_words, window;
@@ -101,21 +101,29 @@ struct TreeCut {
     long long total;
     int g;
     __device__ __forceinline__ long long start(int i) const { return total * i / g; }
-    __device__ __forceinline__ int owner(long long tile) const
-    {
-        int i = (int)(tile * g / total);
-        while (i + 1 < g && start(i + 1) <= tile)
-            ++i;
-        while (start(i) > tile)
-            --i;
-        return i;
-    }
 };
 
 __device__ __forceinline__ TreeCut tree_cut(long long total, int grid)
 {
     return TreeCut{total, (int)min((long long)grid, total)};
 }
+
+// What the merge needs to know of a segment that is part of a unit: kv tiles
+// off .. off + tiles - 1 of the unit's `all`, for the `toks` query rows from
+// row0 and the heads of kv head kvh.  all = 0: there is no such segment.
+struct TreePart {
+    int all, off, tiles, row0, toks, kvh;
+    __device__ __forceinline__ void write(int4* at) const
+    {
+        at[0] = make_int4(all, off, tiles, row0);
+        at[1] = make_int4(toks, kvh, 0, 0);
+    }
+    static __device__ __forceinline__ TreePart read(const int4* at)
+    {
+        const int4 x = at[0], y = at[1];
+        return TreePart{x.x, x.y, x.z, x.w, y.x, y.y};
+    }
+};
 
 // The MMA row (0 .. 127) of token `tok` of `toks` in a query tile, head h.
 __device__ __forceinline__ int tree_row(const TreeRows& r, int tok, int toks, int h)
