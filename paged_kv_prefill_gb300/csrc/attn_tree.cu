@@ -30,20 +30,24 @@
 //
 // kTiles 2 (more than one tile of rows in some request): A and B each have
 // their own query tile, and K/V are read once for both.  kTiles 1: there is
-// one query tile; A takes the even kv tiles of a segment and B the odd ones,
-// each with its own S and O in TMEM, so that the tensor core, the two softmax
-// groups and the loads overlap although there is a single tile of rows; they
-// merge at the end, each writing half of the columns.
+// one query tile; A takes the even kv tiles and B the odd ones, of three S
+// buffers in turn, into one O.  The running maximum of a row goes from one
+// group to the other through shared memory as soon as a tile's own maximum is
+// known, so that tensor core, both groups and loads overlap although there is
+// a single tile of rows; at the end each group writes half of the columns.
+// The MMA issuer takes whatever is ready next, S or P V, and never waits for
+// one while the other could go.
 //
 // e4m3 caches.  K and V go to the tensor core as they are (kind::f8f6f4), so
 // that no thread touches them; what is 16 or 32 bits wide is split instead.
 // A Q row is scaled by a power of two and split into two e4m3 terms whose sum
 // is exact for every element within 2^-9 of the row's largest, and off by at
 // most 2^-17 of the largest below; S = Qh K^T + Ql K^T.  A probability, kept in
-// (0, 2^8] with its row's largest at 2^7 or more, is split into its leading
+// (0, 2^8] with its row's largest at 2^4 or more, is split into its leading
 // four bits and the rest rounded to four: off by at most half a step of bf16
-// (2^-8), down to 2^-17 of the row's largest.  Two 8-bit MMAs take the time of
-// one 16-bit MMA.
+// (2^-8), down to 2^-14 of the row's largest.  (The other four powers of two
+// let a row's maximum grow by that much before O has to be rescaled.)
+// Two 8-bit MMAs take at most the time of one 16-bit MMA.
 //
 // V and keys that some rows of a tile do not see: their P is 0, but 0 times
 // an infinity or NaN is NaN.  Keys before the item's first and past the last
@@ -51,8 +55,9 @@
 // edge) are looked over, and one that is not finite is zeroed and added to the
 // rows that see it in the epilogue, from global memory, in fp32.
 //
-// TMEM (512 columns): S0 [0,128), S1 [128,256), O0 [256,256+D), O1
-// [256+D,256+2D).  P overwrites the first 64 columns of S.
+// TMEM (512 columns).  kTiles 1: S [0,128) [128,256) [256,384), O [384,384+D).
+// kTiles 2: S [0,128) [128,256), O [256,256+D) [256+D,256+2D).  P overwrites the
+// first 64 columns of its S.
 //
 // Every wait is bounded, as in attn_tc.cu.
 #include <mutex>
@@ -81,15 +86,16 @@ struct TreeCfg {
     static constexpr int kEntries = kRing / kKvBytes;       // K and V tiles, alternating
     static constexpr int kOffRing = kQBufs * kTiles * kQBytes;
     static constexpr int kOffBar = kOffRing + kEntries * kKvBytes;
-    static constexpr int kNumBars = 3 * kEntries + 3 * kQBufs + 3 * 2 + 2 + 1 + 2 * kTreeSlots + 1;
+    static constexpr int kSBufs = kTiles == 1 ? 3 : 2;
+    static constexpr int kNumBars = 3 * kEntries + 3 * kQBufs + 2 * kSBufs + 2 + 2 + 8 + 2 + 1 + 2 * kTreeSlots + 1;
     static constexpr int kOffMisc = kOffBar + kNumBars * 8;  // tmem address, abort flag
     static constexpr int kOffItems = kOffMisc + 16;
     static constexpr int kOffBad = kOffItems + kTreeSlots * 12 * 4;
     static constexpr int kOffExp = kOffBad + kBadSlots * 4;  // e4m3: exponent of each Q row (int8)
     static constexpr int kOffMl = (kOffExp + (FP8 ? kQBufs * kTiles * kQRows : 0) + 15) / 16 * 16;
-    static constexpr int kSmemBytes = kOffMl + (kTiles == 1 ? 2 * kQRows * 8 : 0);
+    static constexpr int kSmemBytes = kOffMl + (kTiles == 1 ? 2 * kQRows * 8 : 0);  // ml; its first half: the running maxima
     static constexpr int kTmemCols = 512;
-    static constexpr int kOCol = 2 * kKvTile;
+    static constexpr int kOCol = kSBufs * kKvTile;
     static_assert(D == 64 || D == 128, "head_dim");
     static_assert(!FP8 || D == 128, "e4m3 caches: D = 128");
     static_assert(kEntries >= 5 && kEntries <= 32, "ring");
@@ -99,8 +105,11 @@ struct TreeCfg {
 struct TreeCtx : Ctx {
     uint64_t *kv_full, *kv_empty, *v_ready;  // [kEntries]
     uint64_t *q_full, *q_empty, *q_conv;     // [kQBufs]
-    uint64_t *s_full, *p_full, *o_full;      // [2]
-    uint64_t *met, *left;                    // kTiles 1: both groups posted (m, l); both have read O
+    uint64_t *s_full, *p_full;               // [kSBufs]
+    uint64_t *o_full;                        // [2] (kTiles 1: [0])
+    // kTiles 1: P V of an even / odd tile done; a warp's rows' maxima up to an
+    // even / odd tile posted ([2][4]); both groups posted (m, l); both have read O
+    uint64_t *pv_done, *m_ready, *met, *left;
     uint64_t *drain, *it_full, *it_empty, *never;
 };
 
@@ -178,7 +187,6 @@ __device__ void tree_producer(const TreeParams& p, const TreeCtx& c, long long p
     uint32_t q = 0;  // ring entries filled
     bool ok = true;
     TreeReq r = pos < end ? tree_request(p, b, item_toks) : TreeReq{};
-    const long long begin = pos;
     int4* note = p.part_seg + (long long)blockIdx.x * 4;  // of slots 0 and 1
     if (lane < 2)
         TreePart{}.write(note + 2 * lane);
@@ -188,13 +196,18 @@ __device__ void tree_producer(const TreeParams& p, const TreeCtx& c, long long p
         if (!wait_bar(&c.it_empty[slot], ((n / kTreeSlots) & 1) ^ 1, c))
             break;
         Seg s{};
-        if (pos < end) {
+        while (pos < end && !s.on) {
             while (pos - base >= r.work(p.Hkv) && b + 1 < p.B) {
                 base += r.work(p.Hkv);
                 r = tree_request(p, ++b, item_toks);
             }
-            const long long at = pos - base, unit = at / r.tiles;
-            const int off = (int)(at - unit * r.tiles);
+            const long long unit = (pos - base) / r.unit();
+            const long long u0 = base + unit * r.unit();
+            const int off = max(0, (int)(pos - u0) - kUnitCost);
+            const int to = max(0, (int)min((long long)r.unit(), end - u0) - kUnitCost);
+            pos = min(end, u0 + r.unit());
+            if (to <= off)
+                continue;  // none of its tiles
             const int it = (int)(unit % r.items);
             s.on = 1;
             s.kvh = (int)(unit / r.items);
@@ -204,10 +217,9 @@ __device__ void tree_producer(const TreeParams& p, const TreeCtx& c, long long p
             s.tok0 = it * item_toks;
             s.toks = min(item_toks, r.n - s.tok0);
             s.j0 = r.n_lo + off;
-            s.tiles = (int)min((long long)(r.tiles - off), end - pos);
+            s.tiles = to - off;
             s.whole = s.tiles == r.tiles;
-            s.slot = pos == begin ? 0 : 1;
-            pos += s.tiles;
+            s.slot = n == 0 ? 0 : 1;
             if (!s.whole && lane == 0)
                 TreePart{r.tiles, off, s.tiles, s.q0 + s.tok0, s.toks, s.kvh}.write(note + 2 * s.slot);
         }
@@ -292,10 +304,10 @@ __device__ void tree_mma(const TreeParams& p, const TreeCtx& c)
             }
         }
     };
-    // O of buffer `buf` (+)= P of that buffer times the V in ring entry e
-    auto issue_pv = [&](int buf, uint32_t e, bool acc) {
+    // O number o (+)= P of buffer `buf` times the V in ring entry e
+    auto issue_pv = [&](int o, int buf, uint32_t e, bool acc) {
         const uint32_t b0 = v_lo + e * kEntryW;
-        const uint32_t d = c.tmem + (uint32_t)(C::kOCol + buf * D), a = c.tmem + (uint32_t)(buf * kKvTile);
+        const uint32_t d = c.tmem + (uint32_t)(C::kOCol + o * D), a = c.tmem + (uint32_t)(buf * kKvTile);
         if constexpr (FP8) {
 #pragma unroll
             for (int term = 0; term < 2; ++term)
@@ -310,76 +322,114 @@ __device__ void tree_mma(const TreeParams& p, const TreeCtx& c)
                           issue);
         }
     };
-    uint32_t r0 = 0;           // kv tiles before this segment; tile i's K and V are entries 2 (r0 + i), + 1
-    uint32_t ready_bits = 0;   // parity of each entry's next v_ready phase
-    uint32_t p_cnt[2] = {0, 0};
-    bool ok = true;
-    auto wait_k = [&](int i) {
-        const uint32_t e = 2 * (r0 + i);
-        return wait_bar(&c.kv_full[e % C::kEntries], (e / C::kEntries) & 1, c);
-    };
-    auto entry = [&](int i, int kind) { return (2 * (r0 + i) + kind) % C::kEntries; };
-    auto wait_v = [&](const Seg& s, int i) {
-        const uint32_t q = 2 * (r0 + i) + 1, e = q % C::kEntries;
-        if (!wait_bar(&c.kv_full[e], (q / C::kEntries) & 1, c))
+    // The sequence of kv tiles over all segments: tile g's K and V are ring
+    // entries 2 g and 2 g + 1.
+    auto entry = [](uint32_t g, uint32_t kind) { return (2 * g + kind) % C::kEntries; };
+    auto entry_phase = [](uint32_t g, uint32_t kind) { return ((2 * g + kind) / C::kEntries) & 1u; };
+    uint32_t ready_bits = 0;  // parity of each entry's next v_ready phase
+    // V of tile g of segment s (its first tile being g0), made safe where rows see different keys
+    auto wait_v = [&](const Seg& s, uint32_t g0, uint32_t g) {
+        const uint32_t e = entry(g, 1);
+        if (!wait_bar(&c.kv_full[e], entry_phase(g, 1), c))
             return false;
-        if (!s.mixed(s.j0 + i, p.window))
+        if (!s.mixed(s.j0 + (int)(g - g0), p.window))
             return true;
         const uint32_t parity = ready_bits >> e & 1u;
         ready_bits ^= 1u << e;
         return wait_bar(&c.v_ready[e], parity, c);
     };
-    auto wait_p = [&](int buf) {
-        const bool got = wait_bar(&c.p_full[buf], p_cnt[buf] & 1, c);
-        ++p_cnt[buf];
-        tc_fence_after();
-        return got;
-    };
-
-    if (p.inject_stall && !wait_bar(c.never, 0, c))  // failure-detection tests
-        ok = false;
-    for (uint32_t n = 0; ok; ++n) {
-        Seg s;
-        if (!take_seg(c, n, &s) || !s.on)
-            break;
-        const uint32_t qb = n % C::kQBufs;
-        if (!wait_bar(FP8 ? &c.q_conv[qb] : &c.q_full[qb], (n / C::kQBufs) & 1, c))
-            break;
-        if constexpr (kTiles == 1) {
-            // tile i in buffer i % 2; S runs two tiles ahead
-            auto next_s = [&](int i) {
-                if (!wait_k(i))
-                    return false;
-                issue_s(qb, 0, i & 1, entry(i, 0));
-                mma_commit_p(&c.s_full[i & 1], issue);
-                mma_commit_p(&c.kv_empty[entry(i, 0)], issue);
-                if (i == s.tiles - 1)
-                    mma_commit_p(&c.q_empty[qb], issue);
-                return true;
-            };
-            ok = next_s(0) && (s.tiles < 2 || next_s(1));
-            for (int i = 0; ok && i < s.tiles; ++i) {
-                if (!wait_v(s, i) || !wait_p(i & 1)) {
-                    ok = false;
-                    break;
-                }
-                issue_pv(i & 1, entry(i, 1), i >= 2);
-                mma_commit_p(&c.kv_empty[entry(i, 1)], issue);
-                if (i + 2 >= s.tiles)
-                    mma_commit_p(&c.o_full[i & 1], issue);
-                else
-                    ok = next_s(i + 2);
+    bool ok = !p.inject_stall || wait_bar(c.never, 0, c);  // failure-detection tests
+    if constexpr (kTiles == 1) {
+        // S of tile s_at, P V of tile p_at; S runs up to three tiles ahead, into
+        // the next segment too.  What S needs is looked at without waiting; the
+        // waits are those for P (short, as S may become possible meanwhile) and,
+        // with P there, for V.
+        Seg ss{}, ps{};
+        uint32_t s_n = 0, s_g0 = 0, p_g0 = 0, s_at = 0, p_at = 0;
+        bool q_here = false;  // ss's Q has landed
+        // (decided for the whole warp, which stays converged)
+        auto here = [](uint64_t* bar, uint32_t parity) { return __any_sync(0xffffffffu, mbar_test(bar, parity)) != 0; };
+        ok = ok && take_seg(c, s_n++, &ss);
+        ps = ss;
+        uint64_t idle = 0;  // since when nothing could be done (0: something was)
+        while (ok && ps.on) {
+            // on to the next segment: S (one ahead of P V at most), then P V
+            if (p_at == p_g0 + (uint32_t)ps.tiles && s_g0 != p_g0) {
+                p_g0 = s_g0;
+                ps = ss;
+                continue;
             }
-        } else {
-            // tile t's S for kv tile i + 1 follows its P V for kv tile i
+            bool did = false;
+            if (ss.on && s_at == s_g0 + (uint32_t)ss.tiles && p_g0 == s_g0 &&
+                here(&c.it_full[s_n % kTreeSlots], (s_n / kTreeSlots) & 1)) {
+                s_g0 = s_at;
+                ok = take_seg(c, s_n++, &ss);
+                q_here = false;
+                did = true;
+            }
+            if (ss.on && !q_here) {
+                const uint32_t n = s_n - 1, qb = n % C::kQBufs;
+                q_here = here(FP8 ? &c.q_conv[qb] : &c.q_full[qb], (n / C::kQBufs) & 1);
+            }
+            if (q_here && s_at < s_g0 + (uint32_t)ss.tiles && s_at - p_at < 3 &&
+                here(&c.kv_full[entry(s_at, 0)], entry_phase(s_at, 0))) {
+                const uint32_t qb = (s_n - 1) % C::kQBufs;
+                issue_s(qb, 0, (int)(s_at % 3), entry(s_at, 0));
+                mma_commit_p(&c.s_full[s_at % 3], issue);
+                mma_commit_p(&c.kv_empty[entry(s_at, 0)], issue);
+                if (++s_at == s_g0 + (uint32_t)ss.tiles)
+                    mma_commit_p(&c.q_empty[qb], issue);
+                idle = 0;
+                continue;
+            }
+            if (p_at < p_g0 + (uint32_t)ps.tiles && p_at < s_at &&
+                __any_sync(0xffffffffu, mbar_try_wait_ns(&c.p_full[p_at % 3], (p_at / 3) & 1, 300))) {
+                if (!wait_v(ps, p_g0, p_at))
+                    break;
+                tc_fence_after();
+                issue_pv(0, (int)(p_at % 3), entry(p_at, 1), p_at > p_g0);
+                mma_commit_p(&c.kv_empty[entry(p_at, 1)], issue);
+                mma_commit_p(&c.pv_done[p_at & 1], issue);
+                if (++p_at == p_g0 + (uint32_t)ps.tiles)
+                    mma_commit_p(&c.o_full[0], issue);
+                did = true;
+            }
+            if (did) {
+                idle = 0;
+                continue;
+            }
+            const uint64_t now = global_ns();
+            if (idle == 0)
+                idle = now;
+            const bool timed_out = now - idle > c.wait_limit_ns;
+            if (__any_sync(0xffffffffu, *c.abort_flag != 0 || timed_out)) {
+                if (timed_out && issue) {
+                    *c.abort_flag = 1;
+                    atomicOr(c.err, (unsigned)B2PA_DEV_TIMEOUT);
+                }
+                ok = false;
+            }
+        }
+    } else {
+        // query tile t's S for kv tile i + 1 follows its P V for kv tile i
+        uint32_t g0 = 0;
+        uint32_t p_cnt[2] = {0, 0};
+        for (uint32_t n = 0; ok; ++n) {
+            Seg s;
+            if (!take_seg(c, n, &s) || !s.on)
+                break;
+            const uint32_t qb = n % C::kQBufs;
+            if (!wait_bar(FP8 ? &c.q_conv[qb] : &c.q_full[qb], (n / C::kQBufs) & 1, c))
+                break;
             const int nq = s.toks > p.rows.tile_toks ? 2 : 1;
             auto next_s = [&](int i, int t) {
-                if (t == 0 && !wait_k(i))
+                const uint32_t g = g0 + (uint32_t)i;
+                if (t == 0 && !wait_bar(&c.kv_full[entry(g, 0)], entry_phase(g, 0), c))
                     return false;
-                issue_s(qb, t, t, entry(i, 0));
+                issue_s(qb, t, t, entry(g, 0));
                 mma_commit_p(&c.s_full[t], issue);
                 if (t == nq - 1) {
-                    mma_commit_p(&c.kv_empty[entry(i, 0)], issue);
+                    mma_commit_p(&c.kv_empty[entry(g, 0)], issue);
                     if (i == s.tiles - 1)
                         mma_commit_p(&c.q_empty[qb], issue);
                 }
@@ -388,7 +438,7 @@ __device__ void tree_mma(const TreeParams& p, const TreeCtx& c)
             for (int t = 0; ok && t < nq; ++t)
                 ok = next_s(0, t);
             for (int i = 0; ok && i < s.tiles; ++i) {
-                if (!wait_v(s, i)) {
+                if (!wait_v(s, g0, g0 + (uint32_t)i)) {
                     ok = false;
                     break;
                 }
@@ -396,21 +446,23 @@ __device__ void tree_mma(const TreeParams& p, const TreeCtx& c)
                 for (int t = 0; t < 2; ++t) {
                     if (!ok || t >= nq)
                         break;
-                    if (!wait_p(t)) {
+                    if (!wait_bar(&c.p_full[t], p_cnt[t] & 1, c)) {
                         ok = false;
                         break;
                     }
-                    issue_pv(t, entry(i, 1), i > 0);
+                    ++p_cnt[t];
+                    tc_fence_after();
+                    issue_pv(t, t, entry(g0 + (uint32_t)i, 1), i > 0);
                     if (t == nq - 1)
-                        mma_commit_p(&c.kv_empty[entry(i, 1)], issue);
+                        mma_commit_p(&c.kv_empty[entry(g0 + (uint32_t)i, 1)], issue);
                     if (i == s.tiles - 1)
                         mma_commit_p(&c.o_full[t], issue);
                     else
                         ok = next_s(i + 1, t);
                 }
             }
+            g0 += (uint32_t)s.tiles;
         }
-        r0 += (uint32_t)s.tiles;
     }
     // every MMA this thread issued has completed once the drain barrier flips
     if (issue)
@@ -588,24 +640,38 @@ __device__ void tree_v(const TreeParams& p, const TreeCtx& c)
             }
             uint8_t* v = c.base + C::kOffRing + e * C::kKvBytes + (chunk >> 3) * C::kBlockBytes + (chunk & 7) * 16;
             const int k0 = (s.j0 + i) * kKvTile;
-#pragma unroll 4
-            for (int row = sub; row < kKvTile; row += kRowsAtOnce) {
-                const int key = k0 + row;
-                uint4* at = reinterpret_cast<uint4*>(v + row * 128);
-                const bool out = key < lo || key >= s.kv_len;          // no row sees it (it may never have been loaded)
-                const bool some = !out && (key < lo_all || key >= ctx);  // some rows may not
-                bool zero = out;
-                if (__any_sync(0xffffffffu, some)) {
-                    const bool here = some && not_finite<FP8>(*at);
-                    const uint32_t m = __ballot_sync(0xffffffffu, here);
-                    const bool any = (m >> (sub * kChunks) & (kChunks == 32 ? 0xffffffffu : (1u << kChunks) - 1u)) != 0;
-                    zero = zero || any;
-                    if (m != 0 && lane == 0)
+            auto at = [&](int row) { return reinterpret_cast<uint4*>(v + row * 128); };
+            const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+            // rows that no row of Q sees (they may never have been loaded)
+            const int seen0 = min(max(lo - k0, 0), kKvTile), seen1 = min(s.kv_len - k0, kKvTile);
+            for (int row = sub; row < seen0; row += kRowsAtOnce)
+                *at(row) = zero;
+            for (int row = seen1 + sub; row < kKvTile; row += kRowsAtOnce)
+                *at(row) = zero;
+            // rows that some may not see: before the last window's edge, and the nodes
+            auto look = [&](int r0, int r1) {
+                constexpr int kBatch = 8;  // loads in flight
+                for (int r = r0; r < r1; r += kBatch * kRowsAtOnce) {
+                    uint32_t hit = 0;
+#pragma unroll
+                    for (int k = 0; k < kBatch; ++k) {
+                        const int row = r + k * kRowsAtOnce + sub;
+                        if (row < r1 && not_finite<FP8>(*at(row)))
+                            hit |= 1u << k;
+                    }
+                    if (!__any_sync(0xffffffffu, hit != 0))
+                        continue;
+                    if (lane == 0)
                         bad[n % kBadSlots] = 1;
+                    for (int k = 0; k < kBatch; ++k) {
+                        const uint32_t m = __ballot_sync(0xffffffffu, hit >> k & 1u);
+                        if (m >> (sub * kChunks) & ((1u << kChunks) - 1u))
+                            *at(r + k * kRowsAtOnce + sub) = zero;
+                    }
                 }
-                if (zero)
-                    *at = make_uint4(0u, 0u, 0u, 0u);
-            }
+            };
+            look(seen0, min(max(lo_all - k0, seen0), seen1));
+            look(max(max(ctx, lo_all) - k0, seen0), seen1);
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {
@@ -624,6 +690,22 @@ __device__ __forceinline__ float fmax3(float a, float b, float c)
     float d;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
     return d;
+}
+
+// Two values v in [0, 2^8], given as v 2^-8, into two e4m3 terms each: the
+// codes are the high bytes of the halves of `hi` and `lo`.  In f16, v 2^-8 has
+// e4m3's exponent field, subnormals included (2^-14 against 2^-6), so that a
+// code is the top of the f16 bits: the leading term by cutting, its remainder
+// (exact in f16) by rounding half up.  (The conversion instruction from f32 to
+// e4m3 takes twice the time of an exponential on the same unit, and two of
+// them per pair of values were the bound: 325 us where this takes 160.)
+__device__ __forceinline__ void split_e4m3(float2 v, uint32_t& hi, uint32_t& lo)
+{
+    uint32_t f, r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(f) : "f"(v.y), "f"(v.x));
+    asm("sub.f16x2 %0, %1, %2;" : "=r"(r) : "r"(f), "r"(f & 0x7F807F80u));
+    hi = f << 1;
+    lo = r * 2u + 0x00800080u;
 }
 
 // Bits 0 .. n - 1.
@@ -702,20 +784,23 @@ __device__ void tree_softmax(const TreeParams& p, const TreeCtx& c, int t)
 {
     using C = TreeCfg<D, FP8, kTiles>;
     constexpr float kLog2e = 1.4426950408889634f;
-    // e = 2^(x - m + kBias): e4m3 terms use their range from 2^kBias down.  The
-    // stabiliser is renewed once the row's maximum has grown by kSlack.
-    constexpr float kBias = FP8 ? 7.f : 0.f, kSlack = FP8 ? 1.f : 8.f;
+    // P = 2^(x - m + kBias): e4m3 terms use their range from 2^kBias down.  The
+    // stabiliser is renewed once the row's maximum has grown by kSlack.  The
+    // exponentials that are summed are P 2^-kScale (see split_e4m3).
+    constexpr float kBias = FP8 ? 4.f : 0.f, kSlack = FP8 ? 4.f : 8.f;
+    constexpr float kScale = FP8 ? 8.f : 0.f;
     const int wq = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31, row = wq * 32 + lane;
     const uint32_t lane_off = (uint32_t)(wq * 32) << 16;
-    const uint32_t s_tmem = c.tmem + lane_off + (uint32_t)(t * kKvTile);
-    const uint32_t o_tmem = c.tmem + lane_off + (uint32_t)C::kOCol;  // + buffer * D
+    const uint32_t s0_tmem = c.tmem + lane_off;  // + buffer * kKvTile
+    const uint32_t o_tmem = c.tmem + lane_off + (uint32_t)(C::kOCol + (kTiles == 1 ? 0 : t * D));
     const TreeRows& rows = p.rows;
     const int G = rows.G;
-    const int step = kTiles == 1 ? 2 : 1;
+    volatile float* m_row = reinterpret_cast<volatile float*>(c.base + C::kOffMl) + row;  // kTiles 1: this row's running maximum
     float2* ml = reinterpret_cast<float2*>(c.base + C::kOffMl);
     const volatile int* bad = reinterpret_cast<const volatile int*>(c.base + C::kOffBad);
 
-    uint32_t s_cnt = 0, o_cnt = 0;
+    uint32_t g0 = 0;   // kv tiles before this segment
+    uint32_t s_cnt = 0, o_cnt = 0;  // kTiles 2: S and O of this group awaited so far
     bool ok = true;
     for (uint32_t n = 0; ok; ++n) {
         Seg s;
@@ -741,14 +826,15 @@ __device__ void tree_softmax(const TreeParams& p, const TreeCtx& c, int t)
             ok = false;
             break;
         }
-        if (kTiles == 2 && qt * rows.tile_toks >= s.toks)
+        if (kTiles == 2 && qt * rows.tile_toks >= s.toks) {
+            g0 += (uint32_t)s.tiles;
             continue;
+        }
         const int toks = tile_tokens(rows, s, qt);
-        const int per = (toks + 3) >> 2;
-        const int local = rows.by_warp ? wq * per + lane / G : row / G;
-        const int head = rows.by_warp ? lane % G : row % G;
-        const bool valid = rows.by_warp ? lane < G * per && local < toks : row < G * toks;
-        const int tok = s.q0 + s.tok0 + qt * rows.tile_toks + (valid ? local : 0);
+        const TreeToken mine = tree_token(rows, row, toks);
+        const int head = mine.head;
+        const bool valid = mine.valid;
+        const int tok = s.q0 + s.tok0 + qt * rows.tile_toks + (valid ? mine.tok : 0);
         const bool warp_on = __any_sync(0xffffffffu, valid);
         const float sl2 = p.scale_log2 * q_unscale;
         RowView view;
@@ -759,14 +845,30 @@ __device__ void tree_softmax(const TreeParams& p, const TreeCtx& c, int t)
         view.words = p.mask_words;
 
         float m_used = -INFINITY, l = 0.f;
-        for (int i = kTiles == 1 ? t : 0; i < s.tiles; i += step) {
-            if (!wait_bar(&c.s_full[t], s_cnt & 1, c)) {
+        // kTiles 1: the tiles of this group's parity over all segments
+        for (int i = kTiles == 1 ? (int)((t ^ g0) & 1) : 0; i < s.tiles; i += kTiles == 1 ? 2 : 1) {
+            const uint32_t g = g0 + (uint32_t)i;
+            const int buf = kTiles == 1 ? (int)(g % 3) : t;
+            const uint32_t s_tmem = s0_tmem + (uint32_t)(buf * kKvTile);
+            const int k0 = (s.j0 + i) * kKvTile;
+            // rows that are nobody's count as seeing everything; what they compute
+            // stays in their row.  The mask is read while S is on its way.
+            const bool mixed = !__all_sync(0xffffffffu, !valid || (k0 >= view.lo && k0 + kKvTile <= view.ctx));
+            uint32_t sees[4];
+            if (mixed) {
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    sees[q] = valid ? view.sees(k0 + 32 * q) : 0xffffffffu;
+            }
+            if (!wait_bar(&c.s_full[buf], kTiles == 1 ? (g / 3) & 1 : s_cnt & 1, c)) {
                 ok = false;
                 break;
             }
             ++s_cnt;
             if (!warp_on) {  // no row of this warp is anyone's
-                mbar_arrive_p(&c.p_full[t], lane == 0 ? 1u : 0u);
+                if (kTiles == 1)
+                    mbar_arrive_p(&c.m_ready[(g & 1) * 4 + wq], lane == 0 ? 1u : 0u);
+                mbar_arrive_p(&c.p_full[buf], lane == 0 ? 1u : 0u);
                 continue;
             }
             tc_fence_after();
@@ -783,12 +885,10 @@ __device__ void tree_softmax(const TreeParams& p, const TreeCtx& c, int t)
                 }
                 tmem_wait_ld();
             }
-            const int k0 = (s.j0 + i) * kKvTile;
-            // rows that are nobody's count as seeing everything; what they compute stays in their row
-            if (!__all_sync(0xffffffffu, !valid || (k0 >= view.lo && k0 + kKvTile <= view.ctx))) {
+            if (mixed) {
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
-                    const uint32_t w = valid ? view.sees(k0 + 32 * q) : 0xffffffffu;
+                    const uint32_t w = sees[q];
                     if (__all_sync(0xffffffffu, w == 0xffffffffu))
                         continue;
 #pragma unroll
@@ -806,34 +906,50 @@ __device__ void tree_softmax(const TreeParams& p, const TreeCtx& c, int t)
                 }
             }
             const float m_tile = fmax3(fmax3(mq[0], mq[1], mq[2]), mq[3], -INFINITY) * sl2;
-            const bool need = valid && m_tile > m_used + kSlack;
-            const float alpha = need ? ex2_approx(m_used - m_tile) : 1.f;
-            l *= alpha;
-            m_used = need ? m_tile : m_used;
-            const float neg = m_used == -INFINITY ? 0.f : kBias - m_used;
+            // the maximum up to the tile before: the other group's (kTiles 1), which
+            // posts it as early as this one does
+            float m_old = m_used;
+            if (kTiles == 1 && i > 0) {
+                if (!wait_bar(&c.m_ready[((g - 1) & 1) * 4 + wq], ((g - 1) >> 1) & 1, c)) {
+                    ok = false;
+                    break;
+                }
+                m_old = *m_row;
+            }
+            const bool need = valid && m_tile > m_old + kSlack;
+            const float m_new = need ? m_tile : m_old;
+            if (kTiles == 1) {
+                *m_row = m_new;
+                __syncwarp();
+                mbar_arrive_p(&c.m_ready[(g & 1) * 4 + wq], lane == 0 ? 1u : 0u);
+            }
+            // this group's sum is relative to its own last maximum, O to the last tile's
+            if (m_used != m_new)
+                l *= ex2_approx(m_used - m_new);
+            const float alpha = need ? ex2_approx(m_old - m_new) : 1.f;
+            m_used = m_new;
+            const float neg = m_used == -INFINITY ? 0.f : kBias - kScale - m_used;
             const float2 sc = make_float2(sl2, sl2), ng = make_float2(neg, neg);
             float2 acc[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
                              make_float2(0.f, 0.f)};
-            const bool rescale = __any_sync(0xffffffffu, need) && i >= step;
+            const bool rescale = __any_sync(0xffffffffu, need) && i > 0;
             if constexpr (FP8) {
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {  // 64 keys: 16 columns of each term
                     uint32_t hi[16], lo[16];
 #pragma unroll
                     for (int w = 0; w < 16; ++w) {
-                        hi[w] = lo[w] = 0;
+                        uint32_t a[2], b[2];
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
                             const int k = q * 64 + w * 4 + h * 2;
                             const float2 y = __ffma2_rn(make_float2(x[k], x[k + 1]), sc, ng);
                             const float2 e = make_float2(ex2_approx(y.x), ex2_approx(y.y));
                             acc[w & 3] = __fadd2_rn(acc[w & 3], e);
-                            // leading four bits, and the rest
-                            const float2 f = make_float2(__uint_as_float(__float_as_uint(e.x) & 0xFFF00000u),
-                                                         __uint_as_float(__float_as_uint(e.y) & 0xFFF00000u));
-                            hi[w] |= to_e4m3x2(f.x, f.y) << (16 * h);
-                            lo[w] |= to_e4m3x2(e.x - f.x, e.y - f.y) << (16 * h);
+                            split_e4m3(e, a[h], b[h]);
                         }
+                        hi[w] = __byte_perm(a[0], a[1], 0x7531);
+                        lo[w] = __byte_perm(b[0], b[1], 0x7531);
                     }
                     tmem_st16(s_tmem + (uint32_t)(q * 16), hi);
                     tmem_st16(s_tmem + (uint32_t)(32 + q * 16), lo);
@@ -854,12 +970,18 @@ __device__ void tree_softmax(const TreeParams& p, const TreeCtx& c, int t)
                 }
             }
             if (rescale) {
-                // O holds this group's sum up to its last tile (that P V precedes this S)
+                // O holds the sum up to the tile before, whose P V (kTiles 2: it
+                // precedes this S) has to be done, and whose successor waits for this P
+                if (kTiles == 1 && !wait_bar(&c.pv_done[(g - 1) & 1], ((g - 1) >> 1) & 1, c)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
                 const float2 ff = make_float2(alpha, alpha);
 #pragma unroll 1
                 for (int q = 0; q < D / 16; ++q) {
                     uint32_t o[16];
-                    tmem_ld16(o_tmem + (uint32_t)(t * D + q * 16), o);
+                    tmem_ld16(o_tmem + (uint32_t)(q * 16), o);
                     tmem_wait_ld();
 #pragma unroll
                     for (int k = 0; k < 16; k += 2) {
@@ -867,32 +989,31 @@ __device__ void tree_softmax(const TreeParams& p, const TreeCtx& c, int t)
                         o[k] = __float_as_uint(v.x);
                         o[k + 1] = __float_as_uint(v.y);
                     }
-                    tmem_st16(o_tmem + (uint32_t)(t * D + q * 16), o);
+                    tmem_st16(o_tmem + (uint32_t)(q * 16), o);
                 }
             }
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
-            mbar_arrive_p(&c.p_full[t], lane == 0 ? 1u : 0u);
+            mbar_arrive_p(&c.p_full[buf], lane == 0 ? 1u : 0u);
             const float2 a01 = __fadd2_rn(acc[0], acc[1]), a23 = __fadd2_rn(acc[2], acc[3]);
             const float2 a = __fadd2_rn(a01, a23);
             l += a.x + a.y;
         }
+        if (FP8)
+            l *= 256.f;  // 2^kScale
+        g0 += (uint32_t)s.tiles;
         if (!ok)
             break;
-        const bool had = kTiles == 2 || t < s.tiles;
-        if (had) {
-            if (!wait_bar(&c.o_full[t], o_cnt & 1, c)) {
-                ok = false;
-                break;
-            }
-            ++o_cnt;
+        // the last P V of the segment (kTiles 1: one O, one wait per segment)
+        if (!wait_bar(&c.o_full[kTiles == 1 ? 0 : t], kTiles == 1 ? n & 1 : o_cnt & 1, c)) {
+            ok = false;
+            break;
         }
-        // from here on the stabiliser of l and O is m
-        float m = m_used == -INFINITY ? m_used : m_used - kBias;
-        float w0 = 1.f, w1 = 0.f;  // weights of the O buffers (kTiles 1: of A and B)
+        ++o_cnt;
         if constexpr (kTiles == 1) {
-            ml[t * kQRows + row] = make_float2(m, l);
+            // both groups' sums, relative to the last tile's maximum (the larger one)
+            ml[t * kQRows + row] = make_float2(m_used, l);
             __syncwarp();
             mbar_arrive_p(c.met, lane == 0 ? 1u : 0u);
             if (!wait_bar(c.met, n & 1, c)) {
@@ -900,12 +1021,13 @@ __device__ void tree_softmax(const TreeParams& p, const TreeCtx& c, int t)
                 break;
             }
             const float2 x0 = ml[row], x1 = ml[kQRows + row];
-            m = fmaxf(x0.x, x1.x);
-            // (a sum that is no number keeps its weight, whatever its maximum)
-            w0 = x0.x == -INFINITY && x0.y == 0.f ? 0.f : m == -INFINITY ? 1.f : ex2_approx(x0.x - m);
-            w1 = x1.x == -INFINITY && x1.y == 0.f ? 0.f : m == -INFINITY ? 1.f : ex2_approx(x1.x - m);
-            l = (w0 != 0.f ? w0 * x0.y : 0.f) + (w1 != 0.f ? w1 * x1.y : 0.f);
+            m_used = fmaxf(x0.x, x1.x);
+            // (a sum of no keys has weight 0; one that is no number keeps its weight)
+            l = (x0.x == m_used || x0.y == 0.f ? x0.y : x0.y * ex2_approx(x0.x - m_used)) +
+                (x1.x == m_used || x1.y == 0.f ? x1.y : x1.y * ex2_approx(x1.x - m_used));
         }
+        // from here on the stabiliser of l and O is m
+        const float m = m_used == -INFINITY ? m_used : m_used - kBias;
         tc_fence_after();
         const int h = s.kvh * G + head;
         float out_scale = 1.f;
@@ -917,25 +1039,14 @@ __device__ void tree_softmax(const TreeParams& p, const TreeCtx& c, int t)
         }
         const int d0 = kTiles == 1 ? t * (D / 2) : 0, d1 = kTiles == 1 ? d0 + D / 2 : D;
         const bool any_bad = bad[n % kBadSlots] != 0;
-        const long long part = ((long long)(blockIdx.x * 2 + s.slot) * kTiles + qt) * kQRows + row;
+        const long long part = (long long)(blockIdx.x * 2 + s.slot) * kTiles + qt;
         uint16_t* orow = p.out + (long long)tok * p.out_st_tok + (long long)h * p.out_st_head;
         if (warp_on) {
 #pragma unroll 1
             for (int d = d0; d < d1; d += 32) {
                 uint32_t o[32];
-                if constexpr (kTiles == 1) {
-                    uint32_t o1[32];
-                    tmem_ld32(o_tmem + (uint32_t)d, o);
-                    tmem_ld32(o_tmem + (uint32_t)(D + d), o1);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int k = 0; k < 32; ++k)  // a buffer without weight may hold anything
-                        o[k] = __float_as_uint((w0 != 0.f ? w0 * __uint_as_float(o[k]) : 0.f) +
-                                               (w1 != 0.f ? w1 * __uint_as_float(o1[k]) : 0.f));
-                } else {
-                    tmem_ld32(o_tmem + (uint32_t)(t * D + d), o);
-                    tmem_wait_ld();
-                }
+                tmem_ld32(o_tmem + (uint32_t)d, o);
+                tmem_wait_ld();
                 if (any_bad && valid) {
                     const int* pages = p.block_tables;  // the request's row: found from its first token
                     int b = 0;
@@ -964,15 +1075,15 @@ __device__ void tree_softmax(const TreeParams& p, const TreeCtx& c, int t)
                         *reinterpret_cast<uint4*>(orow + d + 8 * v) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
                     }
                 } else if (valid) {
-                    float4* to = reinterpret_cast<float4*>(p.part_o + part * D + d);
+                    float4* to = p.part_o + (part * (D / 4) + d / 4) * kQRows + row;
 #pragma unroll
                     for (int v = 0; v < 8; ++v)
-                        to[v] = make_float4(__uint_as_float(o[4 * v]), __uint_as_float(o[4 * v + 1]),
-                                            __uint_as_float(o[4 * v + 2]), __uint_as_float(o[4 * v + 3]));
+                        to[v * kQRows] = make_float4(__uint_as_float(o[4 * v]), __uint_as_float(o[4 * v + 1]),
+                                                     __uint_as_float(o[4 * v + 2]), __uint_as_float(o[4 * v + 3]));
                 }
             }
             if (valid && !s.whole && (kTiles == 2 || t == 0))
-                p.part_ml[part] = make_float2(m, l);
+                p.part_ml[part * kQRows + row] = make_float2(m, l);
         }
         tc_fence_before();
         if constexpr (kTiles == 1) {
@@ -1000,9 +1111,11 @@ __global__ void __launch_bounds__(kTreeThreads, 1) attention_tree_kernel(const _
     c.q_empty = c.q_full + C::kQBufs;
     c.q_conv = c.q_empty + C::kQBufs;
     c.s_full = c.q_conv + C::kQBufs;
-    c.p_full = c.s_full + 2;
-    c.o_full = c.p_full + 2;
-    c.met = c.o_full + 2;
+    c.p_full = c.s_full + C::kSBufs;
+    c.o_full = c.p_full + C::kSBufs;
+    c.pv_done = c.o_full + 2;
+    c.m_ready = c.pv_done + 2;
+    c.met = c.m_ready + 8;
     c.left = c.met + 1;
     c.drain = c.left + 1;
     c.it_full = c.drain + 1;
@@ -1025,11 +1138,16 @@ __global__ void __launch_bounds__(kTreeThreads, 1) attention_tree_kernel(const _
             mbar_init(&c.q_empty[b], FP8 ? 9 : 1);  // the MMAs that read it; e4m3: and the softmax warps
             mbar_init(&c.q_conv[b], 1);
         }
-        for (int t = 0; t < 2; ++t) {
-            mbar_init(&c.s_full[t], 1);
-            mbar_init(&c.p_full[t], 4);
-            mbar_init(&c.o_full[t], 1);
+        for (int k = 0; k < C::kSBufs; ++k) {
+            mbar_init(&c.s_full[k], 1);
+            mbar_init(&c.p_full[k], 4);
         }
+        for (int k = 0; k < 2; ++k) {
+            mbar_init(&c.o_full[k], 1);
+            mbar_init(&c.pv_done[k], 1);
+        }
+        for (int k = 0; k < 8; ++k)
+            mbar_init(&c.m_ready[k], 1);
         mbar_init(c.met, 8);
         mbar_init(c.left, 8);
         mbar_init(c.drain, 1);
@@ -1137,21 +1255,20 @@ __global__ void __launch_bounds__(kTreeThreads, 1) attention_tree_kernel(const _
 // O_c) and m = max m_c, w_c = 2^(m_c - m),
 //   out = bmm2 * sum_c w_c O_c / (sum_c w_c l_c + [sinks] 2^(sink log2 e - m)),
 // in the order of the keys.  Block (i, y) takes the unit whose first segment is
-// CTA i's, if there is one that goes on in the next CTA, and of its rows 8 y ..
-// 8 y + 7, one per warp.  Latency alone: loads that do not depend on each other
-// are issued together.
+// CTA i's, if there is one that goes on in the next CTA, and of its query tile
+// y / 4 the 32 MMA rows of quadrant y % 4: a lane per row, so that the partial
+// rows, four columns of all 128 rows together, are read and were written in
+// whole lines.  Each warp takes kCols4 groups of four columns.  Latency alone:
+// loads that do not depend on each other are issued together.
 // ---------------------------------------------------------------------------
-constexpr int kMergeRows = 8;
-
 template <int D>
-__global__ void __launch_bounds__(kMergeRows * 32) tree_merge_kernel(const __grid_constant__ TreeParams p, int tiles)
+__global__ void __launch_bounds__(D * 2) tree_merge_kernel(const __grid_constant__ TreeParams p, int tiles)
 {
     constexpr float kLog2e = 1.4426950408889634f;
-    constexpr int kPer = D / 32;  // dimensions per lane
-    constexpr int kBatch = 8;     // segments whose rows are loaded together
+    constexpr int kCols4 = 4;  // D / 16 warps
     pdl_wait();
-    const int lane = threadIdx.x & 31;
-    const int first = blockIdx.x, r = (int)blockIdx.y * kMergeRows + (threadIdx.x >> 5);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int first = blockIdx.x, qt = blockIdx.y >> 2, row = (blockIdx.y & 3) * 32 + lane;
     // the segment that opens a unit is the CTA's last; the ones after it are
     // the first of the CTAs that follow, up to the one that reaches the end
     const int4* notes = p.part_seg;
@@ -1163,7 +1280,8 @@ __global__ void __launch_bounds__(kMergeRows * 32) tree_merge_kernel(const __gri
     const int slot = last.all != 0 ? 1 : 0;
     if (slot)
         x = last;
-    if (x.all == 0 || x.off != 0 || r >= x.toks * p.rows.G)
+    const int toks = min(p.rows.tile_toks, x.toks - qt * p.rows.tile_toks);
+    if (x.all == 0 || x.off != 0 || toks <= 0)
         return;
     int segs = 1;
     for (int c = first + 1;; c += 32) {
@@ -1176,82 +1294,71 @@ __global__ void __launch_bounds__(kMergeRows * 32) tree_merge_kernel(const __gri
         }
         segs += 32;
     }
-    const int tok = r / p.rows.G, head = r - tok * p.rows.G, h = x.kvh * p.rows.G + head;
-    const int qt = tok / p.rows.tile_toks, in_tile = tok - qt * p.rows.tile_toks;
-    const int row = tree_row(p.rows, in_tile, min(p.rows.tile_toks, x.toks - qt * p.rows.tile_toks), head);
+    const TreeToken at = tree_token(p.rows, row, toks);
+    if (!__any_sync(0xffffffffu, at.valid))
+        return;
     // segment c of the unit: slot 0 of CTA first + c, but for its first
-    auto part = [&](int c) {
-        return ((long long)((first + c) * 2 + (c == 0 ? slot : 0)) * tiles + qt) * kQRows + row;
-    };
-    const float sink = p.sinks != nullptr ? p.sinks[h] * kLog2e : -INFINITY;
-    // running over groups of 32 segments, each lane holding one's (m, l)
+    auto part = [&](int c) { return (long long)((first + c) * 2 + (c == 0 ? slot : 0)) * tiles + qt; };
+    const int h = x.kvh * p.rows.G + at.head;
+    const float sink = p.sinks != nullptr && at.valid ? p.sinks[h] * kLog2e : -INFINITY;
     float m = -INFINITY, den = 0.f;
-    float a[kPer];
+    float4 a[kCols4];
 #pragma unroll
-    for (int k = 0; k < kPer; ++k)
-        a[k] = 0.f;
-    for (int c0 = 0; c0 < segs; c0 += 32) {
-        const int n = min(32, segs - c0);
-        float2 ml = make_float2(-INFINITY, 0.f);
-        if (lane < n)
-            ml = p.part_ml[part(c0 + lane)];
-        float w = 0.f;
-        for (int b = 0; b < n; b += kBatch) {
-            float v[kBatch][kPer];
+    for (int k = 0; k < kCols4; ++k)
+        a[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+    constexpr int kBatch = 4;  // segments loaded together
+    for (int c0 = 0; c0 < segs; c0 += kBatch) {
+        float2 ml[kBatch];
+        float4 v[kBatch][kCols4];
 #pragma unroll
-            for (int c = 0; c < kBatch; ++c) {
-                if (b + c >= n)
-                    break;
-                const float* o = p.part_o + part(c0 + b + c) * D + lane * kPer;
-                if constexpr (kPer == 4) {
-                    const float4 y = *reinterpret_cast<const float4*>(o);
-                    v[c][0] = y.x;
-                    v[c][1] = y.y;
-                    v[c][2] = y.z;
-                    v[c][3] = y.w;
-                } else {
-                    const float2 y = *reinterpret_cast<const float2*>(o);
-                    v[c][0] = y.x;
-                    v[c][1] = y.y;
-                }
+        for (int c = 0; c < kBatch; ++c) {
+            ml[c] = make_float2(-INFINITY, 0.f);
+            if (c0 + c < segs && at.valid) {
+                const long long q = part(c0 + c);
+                ml[c] = p.part_ml[q * kQRows + row];
+#pragma unroll
+                for (int k = 0; k < kCols4; ++k)
+                    v[c][k] = p.part_o[(q * (D / 4) + warp * kCols4 + k) * kQRows + row];
             }
-            if (b == 0) {
-                float top = fmaxf(m, ml.x);
+        }
+        float top = m;
 #pragma unroll
-                for (int o = 16; o > 0; o >>= 1)
-                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-                const float old = m == -INFINITY ? 1.f : ex2_approx(m - top);  // (no maximum yet: sums of 0 or NaN)
-                // (a sum that is no number keeps its weight, whatever its maximum)
-                w = ml.x == -INFINITY && ml.y == 0.f ? 0.f : top == -INFINITY ? 1.f : ex2_approx(ml.x - top);
-                m = top;
-                float s = w != 0.f ? w * ml.y : 0.f;
+        for (int c = 0; c < kBatch; ++c)
+            top = fmaxf(top, ml[c].x);
+        const float old = m == top ? 1.f : ex2_approx(m - top);  // (no maximum yet: sums of 0 or NaN)
+        m = top;
+        den *= old;
 #pragma unroll
-                for (int o = 16; o > 0; o >>= 1)
-                    s += __shfl_xor_sync(0xffffffffu, s, o);
-                den = fmaf(den, old, s);
+        for (int k = 0; k < kCols4; ++k)
+            a[k] = make_float4(a[k].x * old, a[k].y * old, a[k].z * old, a[k].w * old);
 #pragma unroll
-                for (int k = 0; k < kPer; ++k)
-                    a[k] *= old;
-            }
+        for (int c = 0; c < kBatch; ++c) {
+            // (a sum that is no number keeps its weight, whatever its maximum)
+            const float w = ml[c].x == -INFINITY && ml[c].y == 0.f ? 0.f : top == -INFINITY ? 1.f : ex2_approx(ml[c].x - top);
+            if (w != 0.f) {
+                den = fmaf(w, ml[c].y, den);
 #pragma unroll
-            for (int c = 0; c < kBatch; ++c) {
-                const float wc = __shfl_sync(0xffffffffu, w, (b + c) & 31);
-                if (b + c < n && wc != 0.f) {
-#pragma unroll
-                    for (int k = 0; k < kPer; ++k)
-                        a[k] = fmaf(wc, v[c][k], a[k]);
+                for (int k = 0; k < kCols4; ++k) {
+                    a[k].x = fmaf(w, v[c][k].x, a[k].x);
+                    a[k].y = fmaf(w, v[c][k].y, a[k].y);
+                    a[k].z = fmaf(w, v[c][k].z, a[k].z);
+                    a[k].w = fmaf(w, v[c][k].w, a[k].w);
                 }
             }
         }
     }
+    if (!at.valid)
+        return;
     if (m != -INFINITY)
         den += ex2_approx(sink - m);
     const float f = den == 0.f ? 0.f : p.bmm2 / den;
-    uint16_t* to = p.out + (long long)(x.row0 + tok) * p.out_st_tok + (long long)h * p.out_st_head + lane * kPer;
-    if constexpr (kPer == 4)
-        *reinterpret_cast<uint2*>(to) = make_uint2(pack_bf16x2(a[0] * f, a[1] * f), pack_bf16x2(a[2] * f, a[3] * f));
-    else
-        *reinterpret_cast<uint32_t*>(to) = pack_bf16x2(a[0] * f, a[1] * f);
+    const int tok = x.row0 + qt * p.rows.tile_toks + at.tok;
+    uint16_t* to = p.out + (long long)tok * p.out_st_tok + (long long)h * p.out_st_head + warp * kCols4 * 4;
+#pragma unroll
+    for (int k = 0; k < kCols4; k += 2)
+        *reinterpret_cast<uint4*>(to + 4 * k) =
+            make_uint4(pack_bf16x2(a[k].x * f, a[k].y * f), pack_bf16x2(a[k].z * f, a[k].w * f),
+                       pack_bf16x2(a[k + 1].x * f, a[k + 1].y * f), pack_bf16x2(a[k + 1].z * f, a[k + 1].w * f));
 }
 
 template <typename Kern, typename... Args>
@@ -1291,9 +1398,7 @@ cudaError_t launch_tree(const TreeParams& p, cudaStream_t stream)
         return err[dev];
     if ((e = launch_pdl(kern, dim3(p.grid), kTreeThreads, C::kSmemBytes, stream, p)) != cudaSuccess)
         return e;
-    const int rows = min(p.max_q_len, kTiles * p.rows.tile_toks) * p.rows.G;  // of a unit, at most
-    return launch_pdl(tree_merge_kernel<D>, dim3(p.grid, (rows + kMergeRows - 1) / kMergeRows), kMergeRows * 32, 0,
-                      stream, p, kTiles);
+    return launch_pdl(tree_merge_kernel<D>, dim3(p.grid, 4 * kTiles), D * 2, 0, stream, p, kTiles);
 }
 
 }  // namespace

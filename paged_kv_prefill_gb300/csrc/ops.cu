@@ -364,7 +364,7 @@ int tree_impl(const b2pa_tensor* q, const b2pa_tensor* k_pool, const b2pa_tensor
         uint8_t* ws = static_cast<uint8_t*>(workspace);
         p.part_seg = reinterpret_cast<int4*>(ws);
         p.part_ml = reinterpret_cast<float2*>(ws + plan.off_ml);
-        p.part_o = reinterpret_cast<float*>(ws + plan.off_o);
+        p.part_o = reinterpret_cast<float4*>(ws + plan.off_o);
         if ((st = encode_q_map(&p.tm_q, pr, p.rows.box_toks)) || (st = encode_pool_map(&p.tm_k, pr, pr.k, pr.k_st)) ||
             (st = encode_pool_map(&p.tm_v, pr, pr.v, pr.v_st)))
             return st;

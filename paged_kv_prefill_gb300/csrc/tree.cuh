@@ -50,7 +50,7 @@ struct TreeParams {  // 128-byte aligned through its CUtensorMap members
     long long mask_stride;
     const int* positions;  // null without a window
     const float* sinks;    // may be null
-    float* part_o;         // [grid * 2][tiles * 128][D] unnormalised partial rows
+    float4* part_o;        // [grid * 2][tiles][D / 4][128] unnormalised partial rows, four columns at a time
     float2* part_ml;       // [grid * 2][tiles * 128] running maximum (log2 units) and sum
     int4* part_seg;        // [grid * 2][2]: TreePart of each partial segment
     unsigned* err;
@@ -63,12 +63,17 @@ struct TreeParams {  // 128-byte aligned through its CUtensorMap members
     int inject_stall;
 };
 
+// What a unit costs beyond its kv tiles, in kv tiles: its Q, the first scores,
+// the tree's own tile and the rows' way out.
+constexpr int kUnitCost = 2;
+
 // A request as the kernels see it.  Its work is items * Hkv units (a unit is
 // a kv head with the nodes of one item) of `tiles` kv tiles each.
 struct TreeReq {
     int q0, n, kv_len, ctx, lo, items, n_lo, tiles;
     bool ok;
-    __device__ __forceinline__ long long work(int Hkv) const { return (long long)items * Hkv * tiles; }
+    __device__ __forceinline__ int unit() const { return tiles + kUnitCost; }
+    __device__ __forceinline__ long long work(int Hkv) const { return (long long)items * Hkv * unit(); }
 };
 
 __device__ __forceinline__ TreeReq tree_request(const TreeParams& p, int b, int item_toks)
@@ -95,8 +100,9 @@ __device__ __forceinline__ int tree_row_lo(int pos, int ctx, int kv_len, int win
     return window < 0 ? 0 : max(0, min(max(pos, ctx), kv_len - 1) - window);
 }
 
-// The CTAs cut all requests' units, laid end to end, into equal runs of kv
-// tiles: CTA i of g takes [start(i), start(i + 1)).
+// The CTAs cut all requests' units, laid end to end, into equal runs: CTA i of
+// g takes [start(i), start(i + 1)).  Of a unit, the first kUnitCost steps are
+// no tiles: a run that ends there leaves the whole unit to the next.
 struct TreeCut {
     long long total;
     int g;
@@ -125,13 +131,27 @@ struct TreePart {
     }
 };
 
-// The MMA row (0 .. 127) of token `tok` of `toks` in a query tile, head h.
-__device__ __forceinline__ int tree_row(const TreeRows& r, int tok, int toks, int h)
+// Which of the `toks` tokens of a query tile, and which head, an MMA row (0 ..
+// 127) is; not valid: nobody's.
+struct TreeToken {
+    int tok, head;
+    bool valid;
+};
+
+__device__ __forceinline__ TreeToken tree_token(const TreeRows& r, int row, int toks)
 {
-    if (!r.by_warp)
-        return tok * r.G + h;
-    const int per = (toks + 3) >> 2;
-    return (tok / per) * 32 + (tok % per) * r.G + h;
+    TreeToken t;
+    if (r.by_warp) {
+        const int per = (toks + 3) >> 2, lane = row & 31, in = lane / r.G;
+        t.tok = (row >> 5) * per + in;
+        t.head = lane - in * r.G;
+        t.valid = in < per && t.tok < toks;
+    } else {
+        t.tok = row / r.G;
+        t.head = row - t.tok * r.G;
+        t.valid = t.tok < toks;
+    }
+    return t;
 }
 
 // tiles: query tiles per item (1 or 2)
