@@ -22,10 +22,14 @@
 //   warp 0   producer: walks the run, posts each segment's description to the
 //            other roles, and loads K/V pages (one TMA box per page and
 //            128-byte column block) into a ring of K and V entries.
-//   warp 1   MMA issuer; owns TMEM.
-//   warp 2   loads Q (a TMA box per softmax warp's tokens and column block);
-//            e4m3 caches: splits it into two e4m3 terms.
-//   warp 3   makes V safe where rows see different keys (see below).
+//   warp 1   issues S = Q K^T; owns TMEM.
+//   warp 2   issues O += P V.  Two issuers, since what an MMA waits for takes a
+//            few hundred cycles to look at, and one warp that looked at K, P, V
+//            and free buffers in turn left the tensor core idle meanwhile
+//            (e4m3 batch: 3000 cycles per kv tile with one).
+//   warp 3   loads Q (a TMA box per softmax warp's tokens and column block; e4m3
+//            caches: splits it into two e4m3 terms), and makes V safe where
+//            rows see different keys (see below).
 //   warps 4-7, 8-11   softmax A and B: one thread per MMA row.
 //
 // kTiles 2 (more than one tile of rows in some request): A and B each have
@@ -35,8 +39,6 @@
 // group to the other through shared memory as soon as a tile's own maximum is
 // known, so that tensor core, both groups and loads overlap although there is
 // a single tile of rows; at the end each group writes half of the columns.
-// The MMA issuer takes whatever is ready next, S or P V, and never waits for
-// one while the other could go.
 //
 // e4m3 caches.  K and V go to the tensor core as they are (kind::f8f6f4), so
 // that no thread touches them; what is 16 or 32 bits wide is split instead.
@@ -71,8 +73,8 @@ namespace {
 
 constexpr int kTreeThreads = 384;
 constexpr int kTreeSlots = 4;     // posted segments in flight
-constexpr int kTreeConsumers = 11;  // warps that read a posted segment
-constexpr int kBadSlots = 8;
+constexpr int kTreeConsumers = 12;  // reads of a posted segment: warps 1 and 2, twice by warp 3, the softmax warps
+constexpr int kBadSlots = 16;     // segments whose V was found not to be finite: a bit each
 
 template <int D, bool FP8, int kTiles>
 struct TreeCfg {
@@ -87,11 +89,11 @@ struct TreeCfg {
     static constexpr int kOffRing = kQBufs * kTiles * kQBytes;
     static constexpr int kOffBar = kOffRing + kEntries * kKvBytes;
     static constexpr int kSBufs = kTiles == 1 ? 3 : 2;
-    static constexpr int kNumBars = 3 * kEntries + 3 * kQBufs + 2 * kSBufs + 2 + 2 + 8 + 2 + 1 + 2 * kTreeSlots + 1;
+    static constexpr int kNumBars = 3 * kEntries + 3 * kQBufs + 3 * kSBufs + 2 + 8 + 2 + 2 + 2 * kTreeSlots + 1;
     static constexpr int kOffMisc = kOffBar + kNumBars * 8;  // tmem address, abort flag
     static constexpr int kOffItems = kOffMisc + 16;
     static constexpr int kOffBad = kOffItems + kTreeSlots * 12 * 4;
-    static constexpr int kOffExp = kOffBad + kBadSlots * 4;  // e4m3: exponent of each Q row (int8)
+    static constexpr int kOffExp = kOffBad + 4;  // e4m3: exponent of each Q row (int8)
     static constexpr int kOffMl = (kOffExp + (FP8 ? kQBufs * kTiles * kQRows : 0) + 15) / 16 * 16;
     static constexpr int kSmemBytes = kOffMl + (kTiles == 1 ? 2 * kQRows * 8 : 0);  // ml; its first half: the running maxima
     static constexpr int kTmemCols = 512;
@@ -105,12 +107,12 @@ struct TreeCfg {
 struct TreeCtx : Ctx {
     uint64_t *kv_full, *kv_empty, *v_ready;  // [kEntries]
     uint64_t *q_full, *q_empty, *q_conv;     // [kQBufs]
-    uint64_t *s_full, *p_full;               // [kSBufs]
+    uint64_t *s_full, *p_full, *s_free;      // [kSBufs]: S there, P there, P V done
     uint64_t *o_full;                        // [2] (kTiles 1: [0])
-    // kTiles 1: P V of an even / odd tile done; a warp's rows' maxima up to an
-    // even / odd tile posted ([2][4]); both groups posted (m, l); both have read O
-    uint64_t *pv_done, *m_ready, *met, *left;
-    uint64_t *drain, *it_full, *it_empty, *never;
+    // kTiles 1: a warp's rows' maxima up to an even / odd tile posted ([2][4]);
+    // both groups posted (m, l); both have read O
+    uint64_t *m_ready, *met, *left;
+    uint64_t *drain /* [2] */, *it_full, *it_empty, *never;
 };
 
 // A segment: kv tiles j0 .. j0 + tiles - 1 of a unit.
@@ -266,213 +268,169 @@ __device__ void tree_producer(const TreeParams& p, const TreeCtx& c, long long p
 }
 
 // ---------------------------------------------------------------------------
-// warp 1.  The whole warp waits and runs the issue code; MMAs and commits are
-// predicated on lane 0.
+// warps 1 and 2.  The whole warp waits and runs the issue code; MMAs and
+// commits are predicated on lane 0.
 // ---------------------------------------------------------------------------
+// f32 accumulators; bf16 operands (format 1 of kind::f16) or e4m3 (format 0 of
+// kind::f8f6f4); b_mn: B is MN-major (V).
+__device__ __forceinline__ constexpr uint32_t tree_idesc(bool fp8, int n, bool b_mn)
+{
+    const uint32_t fmt = fp8 ? 0u : 1u;
+    return (1u << 4) | (fmt << 7) | (fmt << 10) | ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) |
+           ((uint32_t)(kQRows >> 4) << 24);
+}
+constexpr uint32_t kTreeDescHi = sdesc_hi_sw128(1024);  // 8 rows x 128 B per core group
+
+// The sequence of kv tiles over all segments: tile g's K and V are ring entries
+// 2 g and 2 g + 1.
+template <typename C>
+__device__ __forceinline__ uint32_t ring_entry(uint32_t g, uint32_t kind)
+{
+    return (2 * g + kind) % C::kEntries;
+}
+template <typename C>
+__device__ __forceinline__ uint32_t ring_phase(uint32_t g, uint32_t kind)
+{
+    return ((2 * g + kind) / C::kEntries) & 1u;
+}
+
 template <int D, bool FP8, int kTiles>
-__device__ void tree_mma(const TreeParams& p, const TreeCtx& c)
+__device__ void tree_s(const TreeParams& p, const TreeCtx& c)
 {
     using C = TreeCfg<D, FP8, kTiles>;
-    // f32 accumulators; bf16 operands (format 1 of kind::f16) or e4m3 (format 0 of kind::f8f6f4)
-    constexpr uint32_t kFmt = FP8 ? 0u : 1u;
-    constexpr uint32_t kIdescS = (1u << 4) | (kFmt << 7) | (kFmt << 10) | ((uint32_t)(kKvTile >> 3) << 17) |
-                                 ((uint32_t)(kQRows >> 4) << 24);
-    constexpr uint32_t kIdescO = (1u << 4) | (kFmt << 7) | (kFmt << 10) | (1u << 16) | ((uint32_t)(D >> 3) << 17) |
-                                 ((uint32_t)(kQRows >> 4) << 24);
+    constexpr uint32_t kIdesc = tree_idesc(FP8, kKvTile, false);
     const uint32_t issue = (threadIdx.x & 31) == 0 ? 1u : 0u;
-    constexpr uint32_t kHi = sdesc_hi_sw128(1024);  // 8 rows x 128 B per core group
-    const uint32_t q_lo = sdesc_lo(smem_u32(c.base), 16);                                   // K-major: LBO unused
+    const uint32_t q_lo = sdesc_lo(smem_u32(c.base), 16);                    // K-major: LBO unused
     const uint32_t k_lo = sdesc_lo(smem_u32(c.base + C::kOffRing), 16);
-    const uint32_t v_lo = sdesc_lo(smem_u32(c.base + C::kOffRing), C::kBlockBytes);         // MN-major: next column block
     constexpr uint32_t kEntryW = C::kKvBytes >> 4, kQTileW = C::kQBytes >> 4, kBlockW = C::kBlockBytes >> 4;
-
-    // S of buffer `buf` = query tile t of Q buffer qb times the K in ring entry e
-    auto issue_s = [&](uint32_t qb, int t, int buf, uint32_t e) {
-        const uint32_t a0 = q_lo + (qb * kTiles + t) * kQTileW, b0 = k_lo + e * kEntryW;
-        const uint32_t d = c.tmem + (uint32_t)(buf * kKvTile);
-        if constexpr (FP8) {
-#pragma unroll
-            for (int term = 0; term < 2; ++term)
-#pragma unroll
-                for (int k = 0; k < D / 32; ++k)  // 32 elements = 32 B
-                    mma8_ss_wp(d, a0 + term * kBlockW + k * 2, b0 + k * 2, kHi, kIdescS, term + k > 0 ? 1u : 0u, issue);
-        } else {
-#pragma unroll
-            for (int k = 0; k < D / 16; ++k) {  // 16 elements = 32 B
-                const uint32_t off = (uint32_t)((k / 4) * kBlockW + (k % 4) * 2);
-                mma_ss_wp(d, a0 + off, b0 + off, kHi, kIdescS, k > 0 ? 1u : 0u, issue);
-            }
-        }
-    };
-    // O number o (+)= P of buffer `buf` times the V in ring entry e
-    auto issue_pv = [&](int o, int buf, uint32_t e, bool acc) {
-        const uint32_t b0 = v_lo + e * kEntryW;
-        const uint32_t d = c.tmem + (uint32_t)(C::kOCol + o * D), a = c.tmem + (uint32_t)(buf * kKvTile);
-        if constexpr (FP8) {
-#pragma unroll
-            for (int term = 0; term < 2; ++term)
-#pragma unroll
-                for (int k = 0; k < kKvTile / 32; ++k)  // 32 keys: 8 columns of P, 32 rows of 128 B
-                    mma8_ts_wp(d, a + (uint32_t)(term * 32 + k * 8), b0 + (uint32_t)(k * 256), kHi, kIdescO,
-                               (acc || term + k > 0) ? 1u : 0u, issue);
-        } else {
-#pragma unroll
-            for (int k = 0; k < kKvTile / 16; ++k)  // 16 keys: 8 columns of P, 16 rows of 128 B
-                mma_ts_wp(d, a + (uint32_t)(k * 8), b0 + (uint32_t)(k * 128), kHi, kIdescO, (acc || k > 0) ? 1u : 0u,
-                          issue);
-        }
-    };
-    // The sequence of kv tiles over all segments: tile g's K and V are ring
-    // entries 2 g and 2 g + 1.
-    auto entry = [](uint32_t g, uint32_t kind) { return (2 * g + kind) % C::kEntries; };
-    auto entry_phase = [](uint32_t g, uint32_t kind) { return ((2 * g + kind) / C::kEntries) & 1u; };
-    uint32_t ready_bits = 0;  // parity of each entry's next v_ready phase
-    // V of tile g of segment s (its first tile being g0), made safe where rows see different keys
-    auto wait_v = [&](const Seg& s, uint32_t g0, uint32_t g) {
-        const uint32_t e = entry(g, 1);
-        if (!wait_bar(&c.kv_full[e], entry_phase(g, 1), c))
-            return false;
-        if (!s.mixed(s.j0 + (int)(g - g0), p.window))
-            return true;
-        const uint32_t parity = ready_bits >> e & 1u;
-        ready_bits ^= 1u << e;
-        return wait_bar(&c.v_ready[e], parity, c);
-    };
+    uint32_t g = 0, used[2] = {0, 0};  // kv tiles; kTiles 2: S of each query tile so far
     bool ok = !p.inject_stall || wait_bar(c.never, 0, c);  // failure-detection tests
-    if constexpr (kTiles == 1) {
-        // S of tile s_at, P V of tile p_at; S runs up to three tiles ahead, into
-        // the next segment too.  What S needs is looked at without waiting; the
-        // waits are those for P (short, as S may become possible meanwhile) and,
-        // with P there, for V.
-        Seg ss{}, ps{};
-        uint32_t s_n = 0, s_g0 = 0, p_g0 = 0, s_at = 0, p_at = 0;
-        bool q_here = false;  // ss's Q has landed
-        // (decided for the whole warp, which stays converged)
-        auto here = [](uint64_t* bar, uint32_t parity) { return __any_sync(0xffffffffu, mbar_test(bar, parity)) != 0; };
-        ok = ok && take_seg(c, s_n++, &ss);
-        ps = ss;
-        uint64_t idle = 0;  // since when nothing could be done (0: something was)
-        while (ok && ps.on) {
-            // on to the next segment: S (one ahead of P V at most), then P V
-            if (p_at == p_g0 + (uint32_t)ps.tiles && s_g0 != p_g0) {
-                p_g0 = s_g0;
-                ps = ss;
-                continue;
-            }
-            bool did = false;
-            if (ss.on && s_at == s_g0 + (uint32_t)ss.tiles && p_g0 == s_g0 &&
-                here(&c.it_full[s_n % kTreeSlots], (s_n / kTreeSlots) & 1)) {
-                s_g0 = s_at;
-                ok = take_seg(c, s_n++, &ss);
-                q_here = false;
-                did = true;
-            }
-            if (ss.on && !q_here) {
-                const uint32_t n = s_n - 1, qb = n % C::kQBufs;
-                q_here = here(FP8 ? &c.q_conv[qb] : &c.q_full[qb], (n / C::kQBufs) & 1);
-            }
-            if (q_here && s_at < s_g0 + (uint32_t)ss.tiles && s_at - p_at < 3 &&
-                here(&c.kv_full[entry(s_at, 0)], entry_phase(s_at, 0))) {
-                const uint32_t qb = (s_n - 1) % C::kQBufs;
-                issue_s(qb, 0, (int)(s_at % 3), entry(s_at, 0));
-                mma_commit_p(&c.s_full[s_at % 3], issue);
-                mma_commit_p(&c.kv_empty[entry(s_at, 0)], issue);
-                if (++s_at == s_g0 + (uint32_t)ss.tiles)
-                    mma_commit_p(&c.q_empty[qb], issue);
-                idle = 0;
-                continue;
-            }
-            if (p_at < p_g0 + (uint32_t)ps.tiles && p_at < s_at &&
-                __any_sync(0xffffffffu, mbar_try_wait_ns(&c.p_full[p_at % 3], (p_at / 3) & 1, 300))) {
-                if (!wait_v(ps, p_g0, p_at))
-                    break;
-                tc_fence_after();
-                issue_pv(0, (int)(p_at % 3), entry(p_at, 1), p_at > p_g0);
-                mma_commit_p(&c.kv_empty[entry(p_at, 1)], issue);
-                mma_commit_p(&c.pv_done[p_at & 1], issue);
-                if (++p_at == p_g0 + (uint32_t)ps.tiles)
-                    mma_commit_p(&c.o_full[0], issue);
-                did = true;
-            }
-            if (did) {
-                idle = 0;
-                continue;
-            }
-            const uint64_t now = global_ns();
-            if (idle == 0)
-                idle = now;
-            const bool timed_out = now - idle > c.wait_limit_ns;
-            if (__any_sync(0xffffffffu, *c.abort_flag != 0 || timed_out)) {
-                if (timed_out && issue) {
-                    *c.abort_flag = 1;
-                    atomicOr(c.err, (unsigned)B2PA_DEV_TIMEOUT);
-                }
+    for (uint32_t n = 0; ok; ++n) {
+        Seg s;
+        if (!take_seg(c, n, &s) || !s.on)
+            break;
+        const uint32_t qb = n % C::kQBufs;
+        if (!wait_bar(FP8 ? &c.q_conv[qb] : &c.q_full[qb], (n / C::kQBufs) & 1, c))
+            break;
+        const int nq = kTiles == 2 && s.toks > p.rows.tile_toks ? 2 : 1;
+        for (int i = 0; ok && i < s.tiles; ++i, ++g) {
+            const uint32_t e = ring_entry<C>(g, 0);
+            if (!wait_bar(&c.kv_full[e], ring_phase<C>(g, 0), c)) {
                 ok = false;
+                break;
             }
-        }
-    } else {
-        // query tile t's S for kv tile i + 1 follows its P V for kv tile i
-        uint32_t g0 = 0;
-        uint32_t p_cnt[2] = {0, 0};
-        for (uint32_t n = 0; ok; ++n) {
-            Seg s;
-            if (!take_seg(c, n, &s) || !s.on)
-                break;
-            const uint32_t qb = n % C::kQBufs;
-            if (!wait_bar(FP8 ? &c.q_conv[qb] : &c.q_full[qb], (n / C::kQBufs) & 1, c))
-                break;
-            const int nq = s.toks > p.rows.tile_toks ? 2 : 1;
-            auto next_s = [&](int i, int t) {
-                const uint32_t g = g0 + (uint32_t)i;
-                if (t == 0 && !wait_bar(&c.kv_full[entry(g, 0)], entry_phase(g, 0), c))
-                    return false;
-                issue_s(qb, t, t, entry(g, 0));
-                mma_commit_p(&c.s_full[t], issue);
-                if (t == nq - 1) {
-                    mma_commit_p(&c.kv_empty[entry(g, 0)], issue);
-                    if (i == s.tiles - 1)
-                        mma_commit_p(&c.q_empty[qb], issue);
-                }
-                return true;
-            };
-            for (int t = 0; ok && t < nq; ++t)
-                ok = next_s(0, t);
-            for (int i = 0; ok && i < s.tiles; ++i) {
-                if (!wait_v(s, g0, g0 + (uint32_t)i)) {
+#pragma unroll
+            for (int t = 0; t < kTiles; ++t) {
+                if (t >= nq)
+                    break;
+                // the buffer's last P has been used
+                const int buf = kTiles == 1 ? (int)(g % 3) : t;
+                const uint32_t use = kTiles == 1 ? g / 3 : used[t];
+                if (use > 0 && !wait_bar(&c.s_free[buf], (use - 1) & 1, c)) {
                     ok = false;
                     break;
                 }
+                ++used[t];
+                tc_fence_after();
+                const uint32_t a0 = q_lo + (qb * kTiles + t) * kQTileW, b0 = k_lo + e * kEntryW;
+                const uint32_t d = c.tmem + (uint32_t)(buf * kKvTile);
+                if constexpr (FP8) {
 #pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    if (!ok || t >= nq)
-                        break;
-                    if (!wait_bar(&c.p_full[t], p_cnt[t] & 1, c)) {
-                        ok = false;
-                        break;
+                    for (int term = 0; term < 2; ++term)
+#pragma unroll
+                        for (int k = 0; k < D / 32; ++k)  // 32 elements = 32 B
+                            mma8_ss_wp(d, a0 + term * kBlockW + k * 2, b0 + k * 2, kTreeDescHi, kIdesc,
+                                       term + k > 0 ? 1u : 0u, issue);
+                } else {
+#pragma unroll
+                    for (int k = 0; k < D / 16; ++k) {  // 16 elements = 32 B
+                        const uint32_t off = (uint32_t)((k / 4) * kBlockW + (k % 4) * 2);
+                        mma_ss_wp(d, a0 + off, b0 + off, kTreeDescHi, kIdesc, k > 0 ? 1u : 0u, issue);
                     }
-                    ++p_cnt[t];
-                    tc_fence_after();
-                    issue_pv(t, t, entry(g0 + (uint32_t)i, 1), i > 0);
-                    if (t == nq - 1)
-                        mma_commit_p(&c.kv_empty[entry(g0 + (uint32_t)i, 1)], issue);
+                }
+                mma_commit_p(&c.s_full[buf], issue);
+                if (t == nq - 1) {
+                    mma_commit_p(&c.kv_empty[e], issue);
                     if (i == s.tiles - 1)
-                        mma_commit_p(&c.o_full[t], issue);
-                    else
-                        ok = next_s(i + 1, t);
+                        mma_commit_p(&c.q_empty[qb], issue);
                 }
             }
-            g0 += (uint32_t)s.tiles;
         }
     }
     // every MMA this thread issued has completed once the drain barrier flips
     if (issue)
-        mma_commit(c.drain);
+        mma_commit(&c.drain[0]);
     __syncwarp();
-    drain_wait(c.drain, 0);
+    drain_wait(&c.drain[0], 0);
+}
+
+template <int D, bool FP8, int kTiles>
+__device__ void tree_pv(const TreeParams& p, const TreeCtx& c)
+{
+    using C = TreeCfg<D, FP8, kTiles>;
+    constexpr uint32_t kIdesc = tree_idesc(FP8, D, true);
+    const uint32_t issue = (threadIdx.x & 31) == 0 ? 1u : 0u;
+    const uint32_t v_lo = sdesc_lo(smem_u32(c.base + C::kOffRing), C::kBlockBytes);  // MN-major: LBO = next column block
+    constexpr uint32_t kEntryW = C::kKvBytes >> 4;
+    uint32_t g = 0, used[2] = {0, 0};
+    uint32_t ready_bits = 0;  // parity of each entry's next v_ready phase
+    bool ok = true;
+    for (uint32_t n = 0; ok; ++n) {
+        Seg s;
+        if (!take_seg(c, n, &s) || !s.on)
+            break;
+        const int nq = kTiles == 2 && s.toks > p.rows.tile_toks ? 2 : 1;
+        for (int i = 0; ok && i < s.tiles; ++i, ++g) {
+            const uint32_t e = ring_entry<C>(g, 1);
+            // V, made safe where rows see different keys
+            ok = wait_bar(&c.kv_full[e], ring_phase<C>(g, 1), c);
+            if (ok && s.mixed(s.j0 + i, p.window)) {
+                ok = wait_bar(&c.v_ready[e], ready_bits >> e & 1u, c);
+                ready_bits ^= 1u << e;
+            }
+#pragma unroll
+            for (int t = 0; t < kTiles; ++t) {
+                if (!ok || t >= nq)
+                    break;
+                const int buf = kTiles == 1 ? (int)(g % 3) : t;
+                if (!wait_bar(&c.p_full[buf], (kTiles == 1 ? g / 3 : used[t]) & 1, c)) {
+                    ok = false;
+                    break;
+                }
+                ++used[t];
+                tc_fence_after();
+                const uint32_t b0 = v_lo + e * kEntryW, a = c.tmem + (uint32_t)(buf * kKvTile);
+                const uint32_t d = c.tmem + (uint32_t)(C::kOCol + (kTiles == 1 ? 0 : t * D));
+                const bool acc = i > 0;
+                if constexpr (FP8) {
+#pragma unroll
+                    for (int term = 0; term < 2; ++term)
+#pragma unroll
+                        for (int k = 0; k < kKvTile / 32; ++k)  // 32 keys: 8 columns of each term, 32 rows of 128 B
+                            mma8_ts_wp(d, a + (uint32_t)(k * 16 + term * 8), b0 + (uint32_t)(k * 256), kTreeDescHi,
+                                       kIdesc, (acc || term + k > 0) ? 1u : 0u, issue);
+                } else {
+#pragma unroll
+                    for (int k = 0; k < kKvTile / 16; ++k)  // 16 keys: 8 columns of P, 16 rows of 128 B
+                        mma_ts_wp(d, a + (uint32_t)(k * 8), b0 + (uint32_t)(k * 128), kTreeDescHi, kIdesc,
+                                  (acc || k > 0) ? 1u : 0u, issue);
+                }
+                mma_commit_p(&c.s_free[buf], issue);
+                if (t == nq - 1)
+                    mma_commit_p(&c.kv_empty[e], issue);
+                if (i == s.tiles - 1)
+                    mma_commit_p(&c.o_full[kTiles == 1 ? 0 : t], issue);
+            }
+        }
+    }
+    if (issue)
+        mma_commit(&c.drain[1]);
+    __syncwarp();
+    drain_wait(&c.drain[1], 0);
 }
 
 // ---------------------------------------------------------------------------
-// warp 2: Q
+// warp 3: Q, and V of tiles with keys that not every row sees
 // ---------------------------------------------------------------------------
 // Two floats -> two e4m3 codes (`lo` in the low byte), and back.
 __device__ __forceinline__ uint32_t to_e4m3x2(float lo, float hi)
@@ -538,59 +496,6 @@ __device__ __forceinline__ int split_q_row(uint8_t* row, int sw, int block_bytes
     return e;
 }
 
-template <int D, bool FP8, int kTiles>
-__device__ void tree_q(const TreeParams& p, const TreeCtx& c)
-{
-    using C = TreeCfg<D, FP8, kTiles>;
-    const int lane = threadIdx.x & 31;
-    const TreeRows& r = p.rows;
-    uint32_t loads = 0;
-    for (uint32_t n = 0;; ++n) {
-        Seg s;
-        if (!take_seg(c, n, &s) || !s.on)
-            break;
-        const uint32_t qb = n % C::kQBufs, ph = (n / C::kQBufs) & 1;
-        if (!wait_bar(&c.q_empty[qb], ph ^ 1, c))
-            break;
-        // lane = (tile, warp's tokens, column block): one box each
-        const int t = lane / (4 * C::kQHalves), w = lane / C::kQHalves % 4, h = lane % C::kQHalves;
-        const int toks = t < kTiles ? tile_tokens(r, s, t) : 0;
-        const int per = r.by_warp ? (toks + 3) >> 2 : r.tile_toks;
-        const bool box = toks > 0 && w * per < toks && (r.by_warp || w == 0);
-        const uint32_t boxes = __popc(__ballot_sync(0xffffffffu, box));
-        mbar_arrive_expect_tx_p(&c.q_full[qb], boxes * (uint32_t)(r.G * r.box_toks * 128), lane == 0 ? 1u : 0u);
-        __syncwarp();
-        if (box)
-            tma_load_3d(smem_u32(c.base) + (qb * kTiles + t) * C::kQBytes + h * C::kBlockBytes + w * 32 * 128, &p.tm_q,
-                        &c.q_full[qb], h * 64, s.kvh * r.G, s.q0 + s.tok0 + t * r.tile_toks + w * per);
-        loads = n + 1;
-        __syncwarp();
-        if constexpr (FP8) {
-            if (!wait_bar(&c.q_full[qb], ph, c))
-                break;
-            int8_t* exps = reinterpret_cast<int8_t*>(c.base + C::kOffExp) + qb * kTiles * kQRows;
-#pragma unroll 1
-            for (int k = 0; k < kTiles * 4; ++k) {
-                const int row = (k & 3) * 32 + lane;
-                exps[(k >> 2) * kQRows + row] = (int8_t)split_q_row(
-                    c.base + (qb * kTiles + (k >> 2)) * C::kQBytes + row * 128, row & 7, C::kBlockBytes);
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0)
-                mbar_arrive(&c.q_conv[qb]);
-        }
-    }
-    if (*c.abort_flag) {
-        const uint32_t first = loads > (uint32_t)C::kQBufs ? loads - C::kQBufs : 0;
-        for (uint32_t k = first; k < loads; ++k)
-            drain_wait(&c.q_full[k % C::kQBufs], (k / C::kQBufs) & 1);
-    }
-}
-
-// ---------------------------------------------------------------------------
-// warp 3: V of tiles with keys that not every row sees
-// ---------------------------------------------------------------------------
 template <bool FP8>
 __device__ __forceinline__ bool not_finite(uint4 v)
 {
@@ -606,79 +511,181 @@ __device__ __forceinline__ bool not_finite(uint4 v)
     return bad;
 }
 
+// The Q tiles of a segment, into buffer qb.
 template <int D, bool FP8, int kTiles>
-__device__ void tree_v(const TreeParams& p, const TreeCtx& c)
+__device__ __forceinline__ void load_q(const TreeParams& p, const TreeCtx& c, const Seg& s, uint32_t qb)
 {
     using C = TreeCfg<D, FP8, kTiles>;
-    constexpr int kChunks = 8 * C::kHalves;      // 16-byte pieces of a V row
+    const int lane = threadIdx.x & 31;
+    const TreeRows& r = p.rows;
+    // lane = (tile, warp's tokens, column block): one box each
+    const int t = lane / (4 * C::kQHalves), w = lane / C::kQHalves % 4, h = lane % C::kQHalves;
+    const int toks = t < kTiles ? tile_tokens(r, s, t) : 0;
+    const int per = r.by_warp ? (toks + 3) >> 2 : r.tile_toks;
+    const bool box = toks > 0 && w * per < toks && (r.by_warp || w == 0);
+    const uint32_t boxes = __popc(__ballot_sync(0xffffffffu, box));
+    mbar_arrive_expect_tx_p(&c.q_full[qb], boxes * (uint32_t)(r.G * r.box_toks * 128), lane == 0 ? 1u : 0u);
+    __syncwarp();
+    if (box)
+        tma_load_3d(smem_u32(c.base) + (qb * kTiles + t) * C::kQBytes + h * C::kBlockBytes + w * 32 * 128, &p.tm_q,
+                    &c.q_full[qb], h * 64, s.kvh * r.G, s.q0 + s.tok0 + t * r.tile_toks + w * per);
+    __syncwarp();
+}
+
+// V entry e, kv tile j of segment s (its n-th): keys that no row sees become
+// 0, and so do keys that some rows may not see and that are not finite.
+template <int D, bool FP8, int kTiles>
+__device__ __forceinline__ void safe_v(const TreeParams& p, const TreeCtx& c, const Seg& s, uint32_t n, int j, uint32_t e)
+{
+    using C = TreeCfg<D, FP8, kTiles>;
+    constexpr int kChunks = 8 * C::kHalves;  // 16-byte pieces of a V row
     constexpr int kRowsAtOnce = 32 / kChunks;
     const int lane = threadIdx.x & 31;
     const int sub = lane / kChunks, chunk = lane % kChunks;
     volatile int* bad = reinterpret_cast<volatile int*>(c.base + C::kOffBad);
-    uint32_t q = 0;  // ring entries seen
-    bool ok = true;
-    for (uint32_t n = 0; ok; ++n) {
-        Seg s;
-        if (!take_seg(c, n, &s) || !s.on)
-            break;
-        if (lane == 0)
-            bad[n % kBadSlots] = 0;
-        __syncwarp();
-        const int lo = s.lo(p.window), lo_all = s.lo_all(p.window), ctx = s.ctx();
-        // every entry is awaited and released in order, so that this warp never
-        // lags a barrier by more than one phase
-        for (int k = 0; k < 2 * s.tiles; ++k, ++q) {
-            const uint32_t e = q % C::kEntries;
-            const int i = k >> 1;
-            if (!wait_bar(&c.kv_full[e], (q / C::kEntries) & 1, c)) {
-                ok = false;
-                break;
-            }
-            if (!(k & 1) || !s.mixed(s.j0 + i, p.window)) {
-                mbar_arrive_p(&c.kv_empty[e], lane == 0 ? 1u : 0u);
-                continue;
-            }
-            uint8_t* v = c.base + C::kOffRing + e * C::kKvBytes + (chunk >> 3) * C::kBlockBytes + (chunk & 7) * 16;
-            const int k0 = (s.j0 + i) * kKvTile;
-            auto at = [&](int row) { return reinterpret_cast<uint4*>(v + row * 128); };
-            const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-            // rows that no row of Q sees (they may never have been loaded)
-            const int seen0 = min(max(lo - k0, 0), kKvTile), seen1 = min(s.kv_len - k0, kKvTile);
-            for (int row = sub; row < seen0; row += kRowsAtOnce)
-                *at(row) = zero;
-            for (int row = seen1 + sub; row < kKvTile; row += kRowsAtOnce)
-                *at(row) = zero;
-            // rows that some may not see: before the last window's edge, and the nodes
-            auto look = [&](int r0, int r1) {
-                constexpr int kBatch = 8;  // loads in flight
-                for (int r = r0; r < r1; r += kBatch * kRowsAtOnce) {
-                    uint32_t hit = 0;
+    const int lo = s.lo(p.window), lo_all = s.lo_all(p.window), ctx = s.ctx();
+    uint8_t* v = c.base + C::kOffRing + e * C::kKvBytes + (chunk >> 3) * C::kBlockBytes + (chunk & 7) * 16;
+    const int k0 = j * kKvTile;
+    auto at = [&](int row) { return reinterpret_cast<uint4*>(v + row * 128); };
+    const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+    // rows that no row of Q sees (they may never have been loaded)
+    const int seen0 = min(max(lo - k0, 0), kKvTile), seen1 = min(s.kv_len - k0, kKvTile);
+    for (int row = sub; row < seen0; row += kRowsAtOnce)
+        *at(row) = zero;
+    for (int row = seen1 + sub; row < kKvTile; row += kRowsAtOnce)
+        *at(row) = zero;
+    // rows that some may not see: before the last window's edge, and the nodes
+    auto look = [&](int r0, int r1) {
+        constexpr int kBatch = 8;  // loads in flight
+        for (int r = r0; r < r1; r += kBatch * kRowsAtOnce) {
+            uint32_t hit = 0;
 #pragma unroll
-                    for (int k = 0; k < kBatch; ++k) {
-                        const int row = r + k * kRowsAtOnce + sub;
-                        if (row < r1 && not_finite<FP8>(*at(row)))
-                            hit |= 1u << k;
-                    }
-                    if (!__any_sync(0xffffffffu, hit != 0))
-                        continue;
-                    if (lane == 0)
-                        bad[n % kBadSlots] = 1;
-                    for (int k = 0; k < kBatch; ++k) {
-                        const uint32_t m = __ballot_sync(0xffffffffu, hit >> k & 1u);
-                        if (m >> (sub * kChunks) & ((1u << kChunks) - 1u))
-                            *at(r + k * kRowsAtOnce + sub) = zero;
-                    }
-                }
-            };
-            look(seen0, min(max(lo_all - k0, seen0), seen1));
-            look(max(max(ctx, lo_all) - k0, seen0), seen1);
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(&c.v_ready[e]);
-                mbar_arrive(&c.kv_empty[e]);
+            for (int k = 0; k < kBatch; ++k) {
+                const int row = r + k * kRowsAtOnce + sub;
+                if (row < r1 && not_finite<FP8>(*at(row)))
+                    hit |= 1u << k;
+            }
+            if (!__any_sync(0xffffffffu, hit != 0))
+                continue;
+            if (lane == 0)
+                *bad = *bad | 1 << n % kBadSlots;
+            for (int k = 0; k < kBatch; ++k) {
+                const uint32_t m = __ballot_sync(0xffffffffu, hit >> k & 1u);
+                if (m >> (sub * kChunks) & ((1u << kChunks) - 1u))
+                    *at(r + k * kRowsAtOnce + sub) = zero;
             }
         }
+    };
+    look(seen0, min(max(lo_all - k0, seen0), seen1));
+    look(max(max(ctx, lo_all) - k0, seen0), seen1);
+    fence_proxy_async_smem();
+    __syncwarp();
+}
+
+// Q runs up to a segment (and a buffer) ahead of V; what is possible next is
+// done, and this warp waits for neither while the other could go.
+template <int D, bool FP8, int kTiles>
+__device__ void tree_feed(const TreeParams& p, const TreeCtx& c)
+{
+    using C = TreeCfg<D, FP8, kTiles>;
+    const int lane = threadIdx.x & 31;
+    volatile int* bad = reinterpret_cast<volatile int*>(c.base + C::kOffBad);
+    // (decided for the whole warp, which stays converged)
+    auto here = [](uint64_t* bar, uint32_t parity) { return __any_sync(0xffffffffu, mbar_test(bar, parity)) != 0; };
+    Seg qs{}, vs{};
+    uint32_t qn = 0, vn = 0;  // segments taken
+    enum { kNext, kEmpty, kLanded, kNone } q_at = kNext;  // what Q needs next: a segment, a buffer, its copies, nothing more
+    uint32_t loads = 0;       // segments whose Q copies were started
+    uint32_t q = 0, q_end = 0;  // ring entries seen, and those of the segments taken
+    bool v_more = true, ok = true;
+    uint64_t idle = 0;  // since when nothing could be done (0: something was)
+    while (ok && (q_at != kNone || v_more)) {
+        bool did = false;
+        if (q_at == kNext && here(&c.it_full[qn % kTreeSlots], (qn / kTreeSlots) & 1)) {
+            ok = take_seg(c, qn++, &qs);
+            q_at = qs.on ? kEmpty : kNone;
+            did = true;
+        }
+        const uint32_t qb = (qn - 1) % C::kQBufs, ph = ((qn - 1) / C::kQBufs) & 1;
+        if (q_at == kEmpty && here(&c.q_empty[qb], ph ^ 1)) {
+            load_q<D, FP8, kTiles>(p, c, qs, qb);
+            loads = qn;
+            q_at = FP8 ? kLanded : kNext;
+            did = true;
+        }
+        if (FP8 && q_at == kLanded && here(&c.q_full[qb], ph)) {
+            int8_t* exps = reinterpret_cast<int8_t*>(c.base + C::kOffExp) + qb * kTiles * kQRows;
+#pragma unroll 1
+            for (int k = 0; k < kTiles * 4; ++k) {
+                const int row = (k & 3) * 32 + lane;
+                exps[(k >> 2) * kQRows + row] = (int8_t)split_q_row(
+                    c.base + (qb * kTiles + (k >> 2)) * C::kQBytes + row * 128, row & 7, C::kBlockBytes);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&c.q_conv[qb]);
+            q_at = kNext;
+            did = true;
+        }
+        // every ring entry is seen and released in order, so that this warp never
+        // lags a barrier by more than one phase
+        uint64_t* bar = nullptr;
+        uint32_t parity = 0;
+        if (v_more && q == q_end) {
+            bar = &c.it_full[vn % kTreeSlots];
+            parity = (vn / kTreeSlots) & 1;
+            if (here(bar, parity)) {
+                ok = ok && take_seg(c, vn++, &vs);
+                v_more = vs.on != 0;
+                q_end += 2 * (uint32_t)vs.tiles;
+                if (lane == 0)
+                    *bad = *bad & ~(1 << (vn - 1) % kBadSlots);
+                __syncwarp();
+                did = true;
+            }
+        } else if (v_more) {
+            const uint32_t e = q % C::kEntries;
+            bar = &c.kv_full[e];
+            parity = (q / C::kEntries) & 1;
+            if (here(bar, parity)) {
+                const int j = vs.j0 + vs.tiles - (int)((q_end - q + 1) >> 1);
+                const bool mixed = (q & 1) && vs.mixed(j, p.window);
+                if (mixed)
+                    safe_v<D, FP8, kTiles>(p, c, vs, vn - 1, j, e);
+                if (lane == 0) {
+                    if (mixed)
+                        mbar_arrive(&c.v_ready[e]);
+                    mbar_arrive(&c.kv_empty[e]);
+                }
+                __syncwarp();
+                ++q;
+                did = true;
+            }
+        }
+        if (did) {
+            idle = 0;
+            continue;
+        }
+        if (bar != nullptr)
+            mbar_try_wait_ns(bar, parity, 100);
+        const uint64_t now = global_ns();
+        if (idle == 0)
+            idle = now;
+        const bool timed_out = now - idle > c.wait_limit_ns;
+        if (__any_sync(0xffffffffu, *c.abort_flag != 0 || timed_out)) {
+            if (timed_out && lane == 0) {
+                *c.abort_flag = 1;
+                atomicOr(c.err, (unsigned)B2PA_DEV_TIMEOUT);
+            }
+            ok = false;
+        }
+    }
+    __syncwarp();
+    if (*c.abort_flag) {
+        const uint32_t first = loads > (uint32_t)C::kQBufs ? loads - C::kQBufs : 0;
+        for (uint32_t k = first; k < loads; ++k)
+            drain_wait(&c.q_full[k % C::kQBufs], (k / C::kQBufs) & 1);
     }
 }
 
@@ -872,40 +879,34 @@ __device__ void tree_softmax(const TreeParams& p, const TreeCtx& c, int t)
                 continue;
             }
             tc_fence_after();
-            float x[kKvTile];
-            float mq[4];  // maxima of the four 32-key loads
-            {
+            // The scores are read twice, once for the maximum and once for the
+            // exponentials, in loops that are not unrolled: held in 128 registers,
+            // with everything unrolled over them, the code of the roles did not
+            // fit the instruction caches, and waits for instructions were the
+            // largest stall of every kernel here (e4m3 batch: 295 us).
+            float mx;
+            if (!mixed) {
                 uint32_t r[32];
+                float mq[4];  // maxima of the four 32-key loads
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
+                for (int q = 0; q < 4; ++q)
                     tmem_ld32_max(s_tmem + (uint32_t)(q * 32), r, &mq[q]);
-#pragma unroll
-                    for (int k = 0; k < 32; ++k)
-                        x[q * 32 + k] = __uint_as_float(r[k]);
-                }
                 tmem_wait_ld();
-            }
-            if (mixed) {
-#pragma unroll
+                mx = fmax3(fmax3(mq[0], mq[1], mq[2]), mq[3], -INFINITY);
+            } else {
+                mx = -INFINITY;
+#pragma unroll 1
                 for (int q = 0; q < 4; ++q) {
-                    const uint32_t w = sees[q];
-                    if (__all_sync(0xffffffffu, w == 0xffffffffu))
-                        continue;
+                    const uint32_t w = q == 0 ? sees[0] : q == 1 ? sees[1] : q == 2 ? sees[2] : sees[3];
+                    uint32_t r[32];
+                    tmem_ld32(s_tmem + (uint32_t)(q * 32), r);
+                    tmem_wait_ld();
 #pragma unroll
                     for (int k = 0; k < 32; ++k)
-                        if (!(w >> k & 1u))
-                            x[32 * q + k] = -INFINITY;
-                    float m0 = fmax3(x[32 * q], x[32 * q + 1], x[32 * q + 2]);
-                    float m1 = fmax3(x[32 * q + 16], x[32 * q + 17], x[32 * q + 18]);
-#pragma unroll
-                    for (int k = 3; k < 15; k += 2) {
-                        m0 = fmax3(m0, x[32 * q + k], x[32 * q + k + 1]);
-                        m1 = fmax3(m1, x[32 * q + 16 + k], x[32 * q + 16 + k + 1]);
-                    }
-                    mq[q] = fmax3(m0, m1, fmaxf(x[32 * q + 15], x[32 * q + 31]));
+                        mx = w >> k & 1u ? fmaxf(mx, __uint_as_float(r[k])) : mx;
                 }
             }
-            const float m_tile = fmax3(fmax3(mq[0], mq[1], mq[2]), mq[3], -INFINITY) * sl2;
+            const float m_tile = mx * sl2;
             // the maximum up to the tile before: the other group's (kTiles 1), which
             // posts it as early as this one does
             float m_old = m_used;
@@ -933,46 +934,50 @@ __device__ void tree_softmax(const TreeParams& p, const TreeCtx& c, int t)
             float2 acc[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
                              make_float2(0.f, 0.f)};
             const bool rescale = __any_sync(0xffffffffu, need) && i > 0;
-            if constexpr (FP8) {
+#pragma unroll 1
+            for (int q = 0; q < 4; ++q) {  // 32 keys: 16 columns of P, over scores already read
+                uint32_t r[32];
+                tmem_ld32(s_tmem + (uint32_t)(q * 32), r);
+                tmem_wait_ld();
+                if (mixed) {
+                    const uint32_t w = q == 0 ? sees[0] : q == 1 ? sees[1] : q == 2 ? sees[2] : sees[3];
 #pragma unroll
-                for (int q = 0; q < 2; ++q) {  // 64 keys: 16 columns of each term
-                    uint32_t hi[16], lo[16];
+                    for (int k = 0; k < 32; ++k)
+                        r[k] = w >> k & 1u ? r[k] : 0xFF800000u;  // -inf
+                }
+                uint32_t pk[16];
+                if constexpr (FP8) {  // eight columns of the leading terms, eight of the others
 #pragma unroll
-                    for (int w = 0; w < 16; ++w) {
+                    for (int w = 0; w < 8; ++w) {
                         uint32_t a[2], b[2];
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
-                            const int k = q * 64 + w * 4 + h * 2;
-                            const float2 y = __ffma2_rn(make_float2(x[k], x[k + 1]), sc, ng);
+                            const int k = w * 4 + h * 2;
+                            const float2 y =
+                                __ffma2_rn(make_float2(__uint_as_float(r[k]), __uint_as_float(r[k + 1])), sc, ng);
                             const float2 e = make_float2(ex2_approx(y.x), ex2_approx(y.y));
                             acc[w & 3] = __fadd2_rn(acc[w & 3], e);
                             split_e4m3(e, a[h], b[h]);
                         }
-                        hi[w] = __byte_perm(a[0], a[1], 0x7531);
-                        lo[w] = __byte_perm(b[0], b[1], 0x7531);
+                        pk[w] = __byte_perm(a[0], a[1], 0x7531);
+                        pk[8 + w] = __byte_perm(b[0], b[1], 0x7531);
                     }
-                    tmem_st16(s_tmem + (uint32_t)(q * 16), hi);
-                    tmem_st16(s_tmem + (uint32_t)(32 + q * 16), lo);
-                }
-            } else {
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {  // 32 keys: 16 columns
-                    uint32_t pk[16];
+                } else {
 #pragma unroll
                     for (int w = 0; w < 16; ++w) {
-                        const int k = q * 32 + w * 2;
-                        const float2 y = __ffma2_rn(make_float2(x[k], x[k + 1]), sc, ng);
+                        const float2 y = __ffma2_rn(
+                            make_float2(__uint_as_float(r[2 * w]), __uint_as_float(r[2 * w + 1])), sc, ng);
                         const float2 e = make_float2(ex2_approx(y.x), ex2_approx(y.y));
                         acc[w & 3] = __fadd2_rn(acc[w & 3], e);
                         pk[w] = pack_bf16x2(e.x, e.y);
                     }
-                    tmem_st16(s_tmem + (uint32_t)(q * 16), pk);
                 }
+                tmem_st16(s_tmem + (uint32_t)(q * 16), pk);
             }
             if (rescale) {
                 // O holds the sum up to the tile before, whose P V (kTiles 2: it
                 // precedes this S) has to be done, and whose successor waits for this P
-                if (kTiles == 1 && !wait_bar(&c.pv_done[(g - 1) & 1], ((g - 1) >> 1) & 1, c)) {
+                if (kTiles == 1 && !wait_bar(&c.s_free[(g - 1) % 3], ((g - 1) / 3) & 1, c)) {
                     ok = false;
                     break;
                 }
@@ -1038,28 +1043,32 @@ __device__ void tree_softmax(const TreeParams& p, const TreeCtx& c, int t)
             out_scale = total == 0.f ? 0.f : p.bmm2 / total;
         }
         const int d0 = kTiles == 1 ? t * (D / 2) : 0, d1 = kTiles == 1 ? d0 + D / 2 : D;
-        const bool any_bad = bad[n % kBadSlots] != 0;
+        const bool any_bad = *bad >> n % kBadSlots & 1;
         const long long part = (long long)(blockIdx.x * 2 + s.slot) * kTiles + qt;
         uint16_t* orow = p.out + (long long)tok * p.out_st_tok + (long long)h * p.out_st_head;
+        if (any_bad && warp_on) {
+            // values of V that are not finite, for the rows that see them
+            int b = 0;
+            while (b + 1 < p.B && p.cum_q[b + 1] <= tok)
+                ++b;
+#pragma unroll 1
+            for (int d = d0; d < d1; ++d) {
+                float o = __uint_as_float(tmem_ld1(o_tmem + (uint32_t)d));
+                tmem_wait_ld();
+                if (valid)
+                    o += tree_bad_column<FP8>(p, p.block_tables + (long long)b * p.bt_stride, view, s.lo_all(p.window),
+                                              s.j0 * kKvTile, (s.j0 + s.tiles) * kKvTile, tok, h, s.kvh, p.scale_log2, m, d);
+                __syncwarp();
+                tmem_st1(o_tmem + (uint32_t)d, __float_as_uint(o));
+            }
+            tmem_wait_st();
+        }
         if (warp_on) {
 #pragma unroll 1
             for (int d = d0; d < d1; d += 32) {
                 uint32_t o[32];
                 tmem_ld32(o_tmem + (uint32_t)d, o);
                 tmem_wait_ld();
-                if (any_bad && valid) {
-                    const int* pages = p.block_tables;  // the request's row: found from its first token
-                    int b = 0;
-                    while (b + 1 < p.B && p.cum_q[b + 1] <= tok)
-                        ++b;
-                    pages += (long long)b * p.bt_stride;
-                    const float raw = FP8 ? p.scale_log2 : sl2;
-#pragma unroll
-                    for (int k = 0; k < 32; ++k)
-                        o[k] = __float_as_uint(__uint_as_float(o[k]) +
-                                               tree_bad_column<FP8>(p, pages, view, s.lo_all(p.window), s.j0 * kKvTile,
-                                                                    (s.j0 + s.tiles) * kKvTile, tok, h, s.kvh, raw, m, d + k));
-                }
                 if (valid && s.whole) {
                     const float2 f = make_float2(out_scale, out_scale);
 #pragma unroll
@@ -1112,13 +1121,13 @@ __global__ void __launch_bounds__(kTreeThreads, 1) attention_tree_kernel(const _
     c.q_conv = c.q_empty + C::kQBufs;
     c.s_full = c.q_conv + C::kQBufs;
     c.p_full = c.s_full + C::kSBufs;
-    c.o_full = c.p_full + C::kSBufs;
-    c.pv_done = c.o_full + 2;
-    c.m_ready = c.pv_done + 2;
+    c.s_free = c.p_full + C::kSBufs;
+    c.o_full = c.s_free + C::kSBufs;
+    c.m_ready = c.o_full + 2;
     c.met = c.m_ready + 8;
     c.left = c.met + 1;
     c.drain = c.left + 1;
-    c.it_full = c.drain + 1;
+    c.it_full = c.drain + 2;
     c.it_empty = c.it_full + kTreeSlots;
     c.never = c.it_empty + kTreeSlots;
     uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
@@ -1141,22 +1150,23 @@ __global__ void __launch_bounds__(kTreeThreads, 1) attention_tree_kernel(const _
         for (int k = 0; k < C::kSBufs; ++k) {
             mbar_init(&c.s_full[k], 1);
             mbar_init(&c.p_full[k], 4);
+            mbar_init(&c.s_free[k], 1);
         }
         for (int k = 0; k < 2; ++k) {
             mbar_init(&c.o_full[k], 1);
-            mbar_init(&c.pv_done[k], 1);
+            mbar_init(&c.drain[k], 1);
         }
         for (int k = 0; k < 8; ++k)
             mbar_init(&c.m_ready[k], 1);
         mbar_init(c.met, 8);
         mbar_init(c.left, 8);
-        mbar_init(c.drain, 1);
         for (int s = 0; s < kTreeSlots; ++s) {
             mbar_init(&c.it_full[s], 1);
             mbar_init(&c.it_empty[s], kTreeConsumers);
         }
         mbar_init(c.never, 1);
         *c.abort_flag = 0;
+        *reinterpret_cast<volatile int*>(smem + C::kOffBad) = 0;
         fence_mbar_init();
     }
     if (tid == 32) {
@@ -1233,11 +1243,11 @@ __global__ void __launch_bounds__(kTreeThreads, 1) attention_tree_kernel(const _
         if (warp == 0)
             tree_producer<D, FP8, kTiles>(p, c, start, end, first_b, base);
         else if (warp == 1)
-            tree_mma<D, FP8, kTiles>(p, c);
+            tree_s<D, FP8, kTiles>(p, c);
         else if (warp == 2)
-            tree_q<D, FP8, kTiles>(p, c);
+            tree_pv<D, FP8, kTiles>(p, c);
         else
-            tree_v<D, FP8, kTiles>(p, c);
+            tree_feed<D, FP8, kTiles>(p, c);
     } else {
         regs_inc<200>();
         tree_softmax<D, FP8, kTiles>(p, c, (warp - 4) >> 2);
