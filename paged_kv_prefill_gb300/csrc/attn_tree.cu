@@ -203,11 +203,11 @@ __device__ void tree_producer(const TreeParams& p, const TreeCtx& c, long long p
                 base += r.work(p.Hkv);
                 r = tree_request(p, ++b, item_toks);
             }
-            const long long unit = (pos - base) / r.unit();
-            const long long u0 = base + unit * r.unit();
-            const int off = max(0, (int)(pos - u0) - kUnitCost);
-            const int to = max(0, (int)min((long long)r.unit(), end - u0) - kUnitCost);
-            pos = min(end, u0 + r.unit());
+            const long long unit = (pos - base) / r.unit;
+            const long long u0 = base + unit * r.unit;
+            const int off = max(0, (int)(pos - u0) - p.unit_cost);
+            const int to = max(0, (int)min((long long)r.unit, end - u0) - p.unit_cost);
+            pos = min(end, u0 + r.unit);
             if (to <= off)
                 continue;  // none of its tiles
             const int it = (int)(unit % r.items);
@@ -334,19 +334,16 @@ __device__ void tree_s(const TreeParams& p, const TreeCtx& c)
                 tc_fence_after();
                 const uint32_t a0 = q_lo + (qb * kTiles + t) * kQTileW, b0 = k_lo + e * kEntryW;
                 const uint32_t d = c.tmem + (uint32_t)(buf * kKvTile);
-                if constexpr (FP8) {
-#pragma unroll
-                    for (int term = 0; term < 2; ++term)
-#pragma unroll
-                        for (int k = 0; k < D / 32; ++k)  // 32 elements = 32 B
-                            mma8_ss_wp(d, a0 + term * kBlockW + k * 2, b0 + k * 2, kTreeDescHi, kIdesc,
-                                       term + k > 0 ? 1u : 0u, issue);
-                } else {
-#pragma unroll
-                    for (int k = 0; k < D / 16; ++k) {  // 16 elements = 32 B
-                        const uint32_t off = (uint32_t)((k / 4) * kBlockW + (k % 4) * 2);
-                        mma_ss_wp(d, a0 + off, b0 + off, kTreeDescHi, kIdesc, k > 0 ? 1u : 0u, issue);
-                    }
+                // a step is 32 bytes of a row: 32 e4m3 elements or 16 of 16 bits; four
+                // steps are a column block (e4m3: of Q's first, then second term).
+                // Rolled: instructions cost more here than loops (see tree_softmax).
+#pragma unroll 1
+                for (int k = 0; k < (FP8 ? 8 : D / 16); ++k) {
+                    const uint32_t step = (uint32_t)((k & 3) * 2), block = (uint32_t)(k >> 2) * kBlockW;
+                    if constexpr (FP8)
+                        mma8_ss_wp(d, a0 + block + step, b0 + step, kTreeDescHi, kIdesc, k > 0 ? 1u : 0u, issue);
+                    else
+                        mma_ss_wp(d, a0 + block + step, b0 + block + step, kTreeDescHi, kIdesc, k > 0 ? 1u : 0u, issue);
                 }
                 mma_commit_p(&c.s_full[buf], issue);
                 if (t == nq - 1) {
@@ -401,19 +398,17 @@ __device__ void tree_pv(const TreeParams& p, const TreeCtx& c)
                 tc_fence_after();
                 const uint32_t b0 = v_lo + e * kEntryW, a = c.tmem + (uint32_t)(buf * kKvTile);
                 const uint32_t d = c.tmem + (uint32_t)(C::kOCol + (kTiles == 1 ? 0 : t * D));
-                const bool acc = i > 0;
-                if constexpr (FP8) {
-#pragma unroll
-                    for (int term = 0; term < 2; ++term)
-#pragma unroll
-                        for (int k = 0; k < kKvTile / 32; ++k)  // 32 keys: 8 columns of each term, 32 rows of 128 B
-                            mma8_ts_wp(d, a + (uint32_t)(k * 16 + term * 8), b0 + (uint32_t)(k * 256), kTreeDescHi,
-                                       kIdesc, (acc || term + k > 0) ? 1u : 0u, issue);
-                } else {
-#pragma unroll
-                    for (int k = 0; k < kKvTile / 16; ++k)  // 16 keys: 8 columns of P, 16 rows of 128 B
-                        mma_ts_wp(d, a + (uint32_t)(k * 8), b0 + (uint32_t)(k * 128), kTreeDescHi, kIdesc,
-                                  (acc || k > 0) ? 1u : 0u, issue);
+                // a step is 8 columns of P: 16 keys (16 rows of V), or 32 of one e4m3
+                // term; keys behind the last are left out in whole steps
+                const int keys = min(kKvTile, s.kv_len - (s.j0 + i) * kKvTile);
+                const int steps = FP8 ? (keys + 31) / 32 * 2 : (keys + 15) / 16;
+#pragma unroll 1
+                for (int k = 0; k < steps; ++k) {
+                    const uint32_t acc = i > 0 || k > 0 ? 1u : 0u;
+                    if constexpr (FP8)
+                        mma8_ts_wp(d, a + (uint32_t)(k * 8), b0 + (uint32_t)((k >> 1) * 256), kTreeDescHi, kIdesc, acc, issue);
+                    else
+                        mma_ts_wp(d, a + (uint32_t)(k * 8), b0 + (uint32_t)(k * 128), kTreeDescHi, kIdesc, acc, issue);
                 }
                 mma_commit_p(&c.s_free[buf], issue);
                 if (t == nq - 1)
@@ -432,13 +427,7 @@ __device__ void tree_pv(const TreeParams& p, const TreeCtx& c)
 // ---------------------------------------------------------------------------
 // warp 3: Q, and V of tiles with keys that not every row sees
 // ---------------------------------------------------------------------------
-// Two floats -> two e4m3 codes (`lo` in the low byte), and back.
-__device__ __forceinline__ uint32_t to_e4m3x2(float lo, float hi)
-{
-    uint16_t r;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
-    return r;
-}
+// Two e4m3 codes -> two floats.
 __device__ __forceinline__ float2 from_e4m3x2(uint32_t two)
 {
     uint32_t h;
@@ -450,50 +439,76 @@ __device__ __forceinline__ float2 from_e4m3x2(uint32_t two)
     return f;
 }
 
-// One Q row of 128 bf16 values in shared memory (two column blocks of 128
-// bytes, 16-byte chunks swizzled by row % 8) becomes its two e4m3 terms, in
-// place: the high one in the first block, the low one in the second.  Returns
-// the power of two it was scaled by, which brings its largest value to
-// [2^7, 2^8).  A row that is not finite becomes NaN, which is what every score
-// of it makes of the softmax.
-__device__ __forceinline__ int split_q_row(uint8_t* row, int sw, int block_bytes)
+// Two values |v| < 2^8, given as v 2^-8, into two e4m3 terms each: the codes
+// are the high bytes of the halves of `hi` and `lo`.  In f16, v 2^-8 has e4m3's
+// exponent field, subnormals included (2^-14 against 2^-6), so that a code is
+// the top of the f16 bits: the leading term by cutting, its remainder (exact in
+// f16) by rounding half up.  (The conversion instruction from f32 to e4m3 runs
+// at half the rate of an exponential on the same unit: with two of them per
+// pair of probabilities they were the bound.)
+template <bool kSigned>
+__device__ __forceinline__ void split_e4m3(float2 v, uint32_t& hi, uint32_t& lo)
 {
-    uint4 x[16];
-    uint32_t mx = 0;
-#pragma unroll
-    for (int k = 0; k < 16; ++k) {  // eight elements each
-        x[k] = *reinterpret_cast<const uint4*>(row + (k >> 3) * block_bytes + (((k & 7) ^ sw) << 4));
-        const uint32_t m = __vmaxu2(__vmaxu2(x[k].x & 0x7FFF7FFFu, x[k].y & 0x7FFF7FFFu),
-                                    __vmaxu2(x[k].z & 0x7FFF7FFFu, x[k].w & 0x7FFF7FFFu));
-        mx = max(mx, max(m & 0xFFFFu, m >> 16));
+    uint32_t f, r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(f) : "f"(v.y), "f"(v.x));
+    const uint32_t sign = kSigned ? f & 0x80008000u : 0u;
+    const uint32_t mag = kSigned ? f & 0x7FFF7FFFu : f;
+    asm("sub.f16x2 %0, %1, %2;" : "=r"(r) : "r"(mag), "r"(mag & 0x7F807F80u));
+    hi = mag << 1 | sign;
+    lo = r * 2u + 0x00800080u | sign;
+}
+
+// `count` Q rows of 128 bf16 values from row0 (a multiple of 32; at most 32) in
+// shared memory (two column blocks of 128 bytes, 16-byte chunks swizzled by row
+// % 8) become their two e4m3 terms, in place: the high one in the first block,
+// the low one in the second.  exps[row] is the power of two a row was scaled
+// by, which brings its largest value to [2^7, 2^8).  A row that is not finite
+// becomes NaN, which is what every score of it makes of the softmax.
+__device__ __forceinline__ void split_q_rows(uint8_t* tile, int block_bytes, int row0, int count, int8_t* exps)
+{
+    const int lane = threadIdx.x & 31;
+    // a row's maximum by one lane
+    uint32_t m = 0;
+    if (lane < count) {
+        const uint8_t* row = tile + (row0 + lane) * 128;
+#pragma unroll 4
+        for (int k = 0; k < 16; ++k) {
+            const uint4 x = *reinterpret_cast<const uint4*>(row + (k >> 3) * block_bytes + (((k & 7) ^ (lane & 7)) << 4));
+            m = __vmaxu2(m, __vmaxu2(__vmaxu2(x.x & 0x7FFF7FFFu, x.y & 0x7FFF7FFFu),
+                                     __vmaxu2(x.z & 0x7FFF7FFFu, x.w & 0x7FFF7FFFu)));
+        }
     }
-    const int e = mx == 0 || mx >= 0x7F80u ? 0 : min(120, max(-120, 7 - ((int)(mx >> 7) - 127)));
-    const float sc = __int_as_float((127 + e) << 23);
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {  // sixteen elements each
+    m = max(m & 0xFFFFu, m >> 16);
+    const int mine = m == 0 || m >= 0x7F80u ? 0 : min(120, max(-110, 7 - ((int)(m >> 7) - 127)));
+    if (lane < count)
+        exps[row0 + lane] = (int8_t)mine;
+    __syncwarp();
+    // two rows at a time, eight elements per lane
+    const int c = lane & 15;
+#pragma unroll 2
+    for (int k = 0; k < count; k += 2) {
+        const int r = k + (lane >> 4), sw = r & 7;
+        const bool on = r < count;
+        const int e = __shfl_sync(0xffffffffu, mine, r & 31);
+        const bool nan = __shfl_sync(0xffffffffu, m, r & 31) >= 0x7F80u;
+        const float sc = __int_as_float((127 - 8 + e) << 23);
+        uint8_t* row = tile + (row0 + (on ? r : k)) * 128;
+        const uint4 x = *reinterpret_cast<const uint4*>(row + (c >> 3) * block_bytes + (((c & 7) ^ sw) << 4));
+        const uint32_t u[4] = {x.x, x.y, x.z, x.w};
         uint32_t hi[4], lo[4];
 #pragma unroll
-        for (int w = 0; w < 4; ++w) {
-            hi[w] = lo[w] = 0;
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const uint4 v = x[2 * k + w / 2];
-                const int word = (w % 2) * 2 + i;
-                const uint32_t u = word == 0 ? v.x : word == 1 ? v.y : word == 2 ? v.z : v.w;
-                const float a = __uint_as_float(u << 16) * sc, b = __uint_as_float(u & 0xFFFF0000u) * sc;
-                const uint32_t h = to_e4m3x2(a, b);
-                const float2 f = from_e4m3x2(h);
-                hi[w] |= h << (16 * i);
-                lo[w] |= to_e4m3x2(a - f.x, b - f.y) << (16 * i);
-            }
-            if (mx >= 0x7F80u)
-                hi[w] = 0x7F7F7F7Fu;
+        for (int i = 0; i < 4; ++i)
+            split_e4m3<true>(make_float2(__uint_as_float(u[i] << 16) * sc, __uint_as_float(u[i] & 0xFFFF0000u) * sc), hi[i], lo[i]);
+        __syncwarp();  // the whole row is read
+        if (on) {
+            uint8_t* to = row + (((c >> 1) ^ sw) << 4) + (c & 1) * 8;
+            const uint2 h = make_uint2(__byte_perm(hi[0], hi[1], 0x7531), __byte_perm(hi[2], hi[3], 0x7531));
+            *reinterpret_cast<uint2*>(to) = nan ? make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu) : h;
+            *reinterpret_cast<uint2*>(to + block_bytes) =
+                make_uint2(__byte_perm(lo[0], lo[1], 0x7531), __byte_perm(lo[2], lo[3], 0x7531));
         }
-        uint8_t* to = row + ((k ^ sw) << 4);
-        *reinterpret_cast<uint4*>(to) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-        *reinterpret_cast<uint4*>(to + block_bytes) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
     }
-    return e;
+    __syncwarp();
 }
 
 template <bool FP8>
@@ -549,10 +564,11 @@ __device__ __forceinline__ void safe_v(const TreeParams& p, const TreeCtx& c, co
     auto at = [&](int row) { return reinterpret_cast<uint4*>(v + row * 128); };
     const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
     // rows that no row of Q sees (they may never have been loaded)
+    constexpr int kStep = FP8 ? 32 : 16;  // keys of an MMA: the steps after the last key are not issued
     const int seen0 = min(max(lo - k0, 0), kKvTile), seen1 = min(s.kv_len - k0, kKvTile);
     for (int row = sub; row < seen0; row += kRowsAtOnce)
         *at(row) = zero;
-    for (int row = seen1 + sub; row < kKvTile; row += kRowsAtOnce)
+    for (int row = seen1 + sub; row < (seen1 + kStep - 1) / kStep * kStep; row += kRowsAtOnce)
         *at(row) = zero;
     // rows that some may not see: before the last window's edge, and the nodes
     auto look = [&](int r0, int r1) {
@@ -594,7 +610,9 @@ __device__ void tree_feed(const TreeParams& p, const TreeCtx& c)
     auto here = [](uint64_t* bar, uint32_t parity) { return __any_sync(0xffffffffu, mbar_test(bar, parity)) != 0; };
     Seg qs{}, vs{};
     uint32_t qn = 0, vn = 0;  // segments taken
-    enum { kNext, kEmpty, kLanded, kNone } q_at = kNext;  // what Q needs next: a segment, a buffer, its copies, nothing more
+    // what Q needs next: a segment, a buffer, its copies, its split, nothing more
+    enum { kNext, kEmpty, kLanded, kSplit, kNone } q_at = kNext;
+    int q_tile = 0, q_quad = 0;  // where its split has come to
     uint32_t loads = 0;       // segments whose Q copies were started
     uint32_t q = 0, q_end = 0;  // ring entries seen, and those of the segments taken
     bool v_more = true, ok = true;
@@ -613,19 +631,28 @@ __device__ void tree_feed(const TreeParams& p, const TreeCtx& c)
             q_at = FP8 ? kLanded : kNext;
             did = true;
         }
-        if (FP8 && q_at == kLanded && here(&c.q_full[qb], ph)) {
-            int8_t* exps = reinterpret_cast<int8_t*>(c.base + C::kOffExp) + qb * kTiles * kQRows;
-#pragma unroll 1
-            for (int k = 0; k < kTiles * 4; ++k) {
-                const int row = (k & 3) * 32 + lane;
-                exps[(k >> 2) * kQRows + row] = (int8_t)split_q_row(
-                    c.base + (qb * kTiles + (k >> 2)) * C::kQBytes + row * 128, row & 7, C::kBlockBytes);
+        if (FP8 && q_at == kLanded && here(&c.q_full[qb], ph))
+            q_at = kSplit;
+        if (FP8 && q_at == kSplit) {
+            // 32 rows at a time, so that the ring does not wait for all of them
+            const int toks = tile_tokens(p.rows, qs, q_tile);
+            const int per = (toks + 3) >> 2;  // tokens of a quadrant
+            const int count = p.rows.by_warp ? (q_quad * per < toks ? p.rows.G * per : 0) : min(32, p.rows.G * toks - q_quad * 32);
+            const uint32_t at = qb * kTiles + (uint32_t)q_tile;
+            if (count > 0)
+                split_q_rows(c.base + at * C::kQBytes, C::kBlockBytes, q_quad * 32, count,
+                             reinterpret_cast<int8_t*>(c.base + C::kOffExp) + at * kQRows);
+            if (++q_quad == 4 || count <= 0) {
+                q_quad = 0;
+                if (++q_tile == kTiles || tile_tokens(p.rows, qs, q_tile) <= 0) {
+                    q_tile = 0;
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(&c.q_conv[qb]);
+                    q_at = kNext;
+                }
             }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0)
-                mbar_arrive(&c.q_conv[qb]);
-            q_at = kNext;
             did = true;
         }
         // every ring entry is seen and released in order, so that this warp never
@@ -699,22 +726,6 @@ __device__ __forceinline__ float fmax3(float a, float b, float c)
     return d;
 }
 
-// Two values v in [0, 2^8], given as v 2^-8, into two e4m3 terms each: the
-// codes are the high bytes of the halves of `hi` and `lo`.  In f16, v 2^-8 has
-// e4m3's exponent field, subnormals included (2^-14 against 2^-6), so that a
-// code is the top of the f16 bits: the leading term by cutting, its remainder
-// (exact in f16) by rounding half up.  (The conversion instruction from f32 to
-// e4m3 takes twice the time of an exponential on the same unit, and two of
-// them per pair of values were the bound: 325 us where this takes 160.)
-__device__ __forceinline__ void split_e4m3(float2 v, uint32_t& hi, uint32_t& lo)
-{
-    uint32_t f, r;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(f) : "f"(v.y), "f"(v.x));
-    asm("sub.f16x2 %0, %1, %2;" : "=r"(r) : "r"(f), "r"(f & 0x7F807F80u));
-    hi = f << 1;
-    lo = r * 2u + 0x00800080u;
-}
-
 // Bits 0 .. n - 1.
 __device__ __forceinline__ uint32_t low_bits(int n) { return n >= 32 ? 0xffffffffu : (1u << max(n, 0)) - 1u; }
 
@@ -744,6 +755,32 @@ struct RowView {
         return w;
     }
 };
+
+// The scores of the keys k0 .. k0 + 127 that a row does not see become -inf, in TMEM.
+__device__ __noinline__ void hide_keys(uint32_t s_tmem, const RowView view, int k0, bool valid)
+{
+#pragma unroll 1
+    for (int q = 0; q < 4; ++q) {
+        const uint32_t w = valid ? view.sees(k0 + 32 * q) : 0xffffffffu;
+        if (__all_sync(0xffffffffu, w == 0xffffffffu))
+            continue;
+        uint32_t r[32];
+        tmem_ld32(s_tmem + (uint32_t)(q * 32), r);
+        tmem_wait_ld();
+#pragma unroll
+        for (int k = 0; k < 32; ++k)
+            r[k] = w >> k & 1u ? r[k] : 0xFF800000u;
+        uint32_t a[16], b[16];
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+            a[k] = r[k];
+            b[k] = r[16 + k];
+        }
+        tmem_st16(s_tmem + (uint32_t)(q * 32), a);
+        tmem_st16(s_tmem + (uint32_t)(q * 32 + 16), b);
+    }
+    tmem_wait_st();
+}
 
 template <bool FP8>
 __device__ __forceinline__ float kv_elem(const void* base, long long at)
@@ -796,6 +833,8 @@ __device__ void tree_softmax(const TreeParams& p, const TreeCtx& c, int t)
     // exponentials that are summed are P 2^-kScale (see split_e4m3).
     constexpr float kBias = FP8 ? 4.f : 0.f, kSlack = FP8 ? 4.f : 8.f;
     constexpr float kScale = FP8 ? 8.f : 0.f;
+    // 32-key steps of the exponentials that are unrolled (see below)
+    constexpr int kUnroll = kTiles == 2 && !FP8 ? 4 : 1;
     const int wq = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31, row = wq * 32 + lane;
     const uint32_t lane_off = (uint32_t)(wq * 32) << 16;
     const uint32_t s0_tmem = c.tmem + lane_off;  // + buffer * kKvTile
@@ -859,14 +898,10 @@ __device__ void tree_softmax(const TreeParams& p, const TreeCtx& c, int t)
             const uint32_t s_tmem = s0_tmem + (uint32_t)(buf * kKvTile);
             const int k0 = (s.j0 + i) * kKvTile;
             // rows that are nobody's count as seeing everything; what they compute
-            // stays in their row.  The mask is read while S is on its way.
+            // stays in their row
             const bool mixed = !__all_sync(0xffffffffu, !valid || (k0 >= view.lo && k0 + kKvTile <= view.ctx));
-            uint32_t sees[4];
-            if (mixed) {
-#pragma unroll
-                for (int q = 0; q < 4; ++q)
-                    sees[q] = valid ? view.sees(k0 + 32 * q) : 0xffffffffu;
-            }
+            if (mixed)  // the mask row, while S is on its way
+                asm volatile("prefetch.global.L1 [%0];" ::"l"(view.mask + min(max(k0 - view.ctx, 0) >> 5, view.words - 1)));
             if (!wait_bar(&c.s_full[buf], kTiles == 1 ? (g / 3) & 1 : s_cnt & 1, c)) {
                 ok = false;
                 break;
@@ -879,32 +914,23 @@ __device__ void tree_softmax(const TreeParams& p, const TreeCtx& c, int t)
                 continue;
             }
             tc_fence_after();
-            // The scores are read twice, once for the maximum and once for the
-            // exponentials, in loops that are not unrolled: held in 128 registers,
-            // with everything unrolled over them, the code of the roles did not
-            // fit the instruction caches, and waits for instructions were the
-            // largest stall of every kernel here (e4m3 batch: 295 us).
+            // Keys that a row does not see become -inf in place.  Then the scores
+            // are read twice, once for the maximum and once for the exponentials, 32
+            // keys at a time in a loop.  All this keeps the code short: with the 128
+            // scores of a row in registers and everything unrolled over them, the
+            // roles' code did not fit the instruction caches, and waits for
+            // instructions were the largest stall of every kernel here.
+            if (mixed)
+                hide_keys(s_tmem, view, k0, valid);
+            uint32_t ra[32];  // 32 scores; at first of the keys 0 .. 31
             float mx;
-            if (!mixed) {
-                uint32_t r[32];
-                float mq[4];  // maxima of the four 32-key loads
+            {
+                float mq[4];  // maxima of the four loads
 #pragma unroll
-                for (int q = 0; q < 4; ++q)
-                    tmem_ld32_max(s_tmem + (uint32_t)(q * 32), r, &mq[q]);
+                for (int q = 3; q >= 0; --q)
+                    tmem_ld32_max(s_tmem + (uint32_t)(q * 32), ra, &mq[q]);
                 tmem_wait_ld();
                 mx = fmax3(fmax3(mq[0], mq[1], mq[2]), mq[3], -INFINITY);
-            } else {
-                mx = -INFINITY;
-#pragma unroll 1
-                for (int q = 0; q < 4; ++q) {
-                    const uint32_t w = q == 0 ? sees[0] : q == 1 ? sees[1] : q == 2 ? sees[2] : sees[3];
-                    uint32_t r[32];
-                    tmem_ld32(s_tmem + (uint32_t)(q * 32), r);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int k = 0; k < 32; ++k)
-                        mx = w >> k & 1u ? fmaxf(mx, __uint_as_float(r[k])) : mx;
-                }
             }
             const float m_tile = mx * sl2;
             // the maximum up to the tile before: the other group's (kTiles 1), which
@@ -934,17 +960,13 @@ __device__ void tree_softmax(const TreeParams& p, const TreeCtx& c, int t)
             float2 acc[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
                              make_float2(0.f, 0.f)};
             const bool rescale = __any_sync(0xffffffffu, need) && i > 0;
-#pragma unroll 1
-            for (int q = 0; q < 4; ++q) {  // 32 keys: 16 columns of P, over scores already read
-                uint32_t r[32];
-                tmem_ld32(s_tmem + (uint32_t)(q * 32), r);
-                tmem_wait_ld();
-                if (mixed) {
-                    const uint32_t w = q == 0 ? sees[0] : q == 1 ? sees[1] : q == 2 ? sees[2] : sees[3];
-#pragma unroll
-                    for (int k = 0; k < 32; ++k)
-                        r[k] = w >> k & 1u ? r[k] : 0xFF800000u;  // -inf
-                }
+#pragma unroll(kUnroll)
+            for (int q = 0; q < 4; ++q) {
+                // 32 keys' P are 16 columns, over scores already read; the next 32
+                // scores are loaded behind their exponentials
+                uint32_t rb[32];
+                if (q < 3)
+                    tmem_ld32(s_tmem + (uint32_t)(q * 32 + 32), rb);
                 uint32_t pk[16];
                 if constexpr (FP8) {  // eight columns of the leading terms, eight of the others
 #pragma unroll
@@ -954,10 +976,10 @@ __device__ void tree_softmax(const TreeParams& p, const TreeCtx& c, int t)
                         for (int h = 0; h < 2; ++h) {
                             const int k = w * 4 + h * 2;
                             const float2 y =
-                                __ffma2_rn(make_float2(__uint_as_float(r[k]), __uint_as_float(r[k + 1])), sc, ng);
+                                __ffma2_rn(make_float2(__uint_as_float(ra[k]), __uint_as_float(ra[k + 1])), sc, ng);
                             const float2 e = make_float2(ex2_approx(y.x), ex2_approx(y.y));
                             acc[w & 3] = __fadd2_rn(acc[w & 3], e);
-                            split_e4m3(e, a[h], b[h]);
+                            split_e4m3<false>(e, a[h], b[h]);
                         }
                         pk[w] = __byte_perm(a[0], a[1], 0x7531);
                         pk[8 + w] = __byte_perm(b[0], b[1], 0x7531);
@@ -966,13 +988,17 @@ __device__ void tree_softmax(const TreeParams& p, const TreeCtx& c, int t)
 #pragma unroll
                     for (int w = 0; w < 16; ++w) {
                         const float2 y = __ffma2_rn(
-                            make_float2(__uint_as_float(r[2 * w]), __uint_as_float(r[2 * w + 1])), sc, ng);
+                            make_float2(__uint_as_float(ra[2 * w]), __uint_as_float(ra[2 * w + 1])), sc, ng);
                         const float2 e = make_float2(ex2_approx(y.x), ex2_approx(y.y));
                         acc[w & 3] = __fadd2_rn(acc[w & 3], e);
                         pk[w] = pack_bf16x2(e.x, e.y);
                     }
                 }
                 tmem_st16(s_tmem + (uint32_t)(q * 16), pk);
+                tmem_wait_ld();
+#pragma unroll
+                for (int k = 0; k < 32; ++k)
+                    ra[k] = rb[k];
             }
             if (rescale) {
                 // O holds the sum up to the tile before, whose P V (kTiles 2: it

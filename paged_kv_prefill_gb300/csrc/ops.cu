@@ -355,6 +355,7 @@ int tree_impl(const b2pa_tensor* q, const b2pa_tensor* k_pool, const b2pa_tensor
     p.max_kv_len = max_kv_len;
     p.window = window;
     p.grid = di.sms;
+    p.unit_cost = pr.fp8 ? 6 : 3;
     p.scale_log2 = (float)((double)bmm1_scale * 1.4426950408889634);
     p.bmm2 = bmm2_scale;
     p.wait_limit_ns = wait_limit_ns();
