@@ -2,8 +2,10 @@
 
 Argument marshalling only.  Every step of the computation runs in the CUDA
 kernels behind the C ABI declared in include/b2pa.h; this module turns torch
-tensors into b2pa_tensor descriptors and calls it.  There is no fallback:
-if the library is missing, load() raises.
+tensors into b2pa_tensor descriptors and calls it, through ctypes or, for the
+calls around the attention whose host time counts, through the small _native
+module.  There is no fallback: if the library or the module is missing, load()
+or native() raises.
 
 The call mirrors flashinfer.prefill.trtllm_batch_context_with_kv_cache
 (FlashInfer API reference, parameter list): ``query``, ``kv_cache`` (a
@@ -15,6 +17,7 @@ The call mirrors flashinfer.prefill.trtllm_batch_context_with_kv_cache
 from __future__ import annotations
 
 import ctypes
+import importlib
 import os
 import struct
 from typing import Optional, Sequence, Tuple, Union
@@ -120,14 +123,16 @@ def load(path: str = LIB_PATH):
     lib.b2pa_debug_gather.argtypes = [P, P, P, P, P, ctypes.c_int32, P, P, ctypes.c_void_p]
     lib.b2pa_debug_gather.restype = ctypes.c_int
     lib.b2pa_append_kv.argtypes = [P, P, P, P, P, ctypes.c_float, ctypes.c_float, ctypes.c_int32, ctypes.c_void_p]
-    V, I, F = ctypes.c_void_p, ctypes.c_int32, ctypes.c_float  # (tensors as bytes: _packed)
-    lib.b2pa_append_kv_scaled.argtypes = [V] * 7 + [I, V]
+    # (their Python functions call them through the _native module)
+    V, I, F = ctypes.c_void_p, ctypes.c_int32, ctypes.c_float
+    lib.b2pa_append_kv_scaled.argtypes = [P] * 7 + [I, V]
     lib.b2pa_append_kv_scaled.restype = ctypes.c_int
-    lib.b2pa_read_kv_scaled.argtypes = [V] * 5 + [I, V, V, V]
+    lib.b2pa_read_kv_scaled.argtypes = [P] * 5 + [I, P, P, V]
     lib.b2pa_read_kv_scaled.restype = ctypes.c_int
-    lib.b2pa_qk_norm_rope.argtypes = [V] * 6 + [F, V, I, V, V, V]
+    lib.b2pa_qk_norm_rope.argtypes = [P] * 6 + [F, ctypes.POINTER(I), I, P, P, V]
     lib.b2pa_qk_norm_rope.restype = ctypes.c_int
-    lib.b2pa_tree_attention.argtypes = [V] * 8 + [I, I, F, F, I, V, I, V, V, ctypes.c_uint64, V, V]
+    lib.b2pa_tree_attention.argtypes = [P] * 8 + [I, I, F, F, I, P, I, P, V, ctypes.c_uint64,
+                                                  ctypes.POINTER(ctypes.c_uint64), V]
     lib.b2pa_tree_attention.restype = ctypes.c_int
     lib.b2pa_get_device_status.argtypes = [ctypes.c_void_p, ctypes.c_void_p]
     lib.b2pa_get_device_status.restype = ctypes.c_int
@@ -153,6 +158,18 @@ def load(path: str = LIB_PATH):
     return lib
 
 
+_calls = None
+
+
+def native():
+    """The module of direct bindings (csrc/native.cpp, built with the library); raises if it is missing."""
+    global _calls
+    if _calls is None:
+        load()
+        _calls = importlib.import_module("._native", __name__)  # links to the library loaded above
+    return _calls
+
+
 def desc(t: Optional[torch.Tensor]) -> Optional[B2paTensor]:
     """b2pa_tensor describing a torch tensor (strides in elements)."""
     if t is None:
@@ -176,49 +193,45 @@ def _stream_handle(stream) -> int:
     return int(stream)
 
 
-# a b2pa_tensor of each rank as bytes: pointer, dtype, rank, shape[5], stride[5]
-_PACK = [struct.Struct(f"Pii{n}q{8 * (5 - n)}x{n}q{8 * (5 - n)}x").pack for n in range(6)]
+class _On:
+    """Makes a call's device current and, where the caller named a stream, that stream too (new
+    tensors then come from its memory); `handle` is the stream's."""
+
+    def __init__(self, first: torch.Tensor, stream):
+        dev = first.get_device()
+        if dev < 0:
+            raise ValueError(f"tensors on {first.device}: CUDA tensors are needed")
+        if stream is not None and not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(int(stream), device=first.device)
+        if stream is not None and stream.device != first.device:
+            raise ValueError(f"a stream of {stream.device} for tensors on {first.device}")
+        # (torch.cuda.stream makes its stream's device current)
+        self.guard = torch.cuda.stream(stream) if stream is not None else torch.cuda.device(dev)
+        self.dev = dev
+
+    def __enter__(self) -> int:
+        self.guard.__enter__()
+        return torch.cuda.current_stream(self.dev).cuda_stream
+
+    def __exit__(self, *exc):
+        return self.guard.__exit__(*exc)
 
 
-def _packed(t: Optional[torch.Tensor]) -> Optional[bytes]:
-    """b2pa_tensor describing a torch tensor, as bytes (a quarter of desc()'s time, which small calls feel)."""
-    if t is None:
-        return None
-    n = t.dim()
-    if n > 5:
-        raise ValueError("rank > 5")
-    code = _DTYPES.get(t.dtype)
-    if code is None:
-        raise TypeError(f"unsupported dtype {t.dtype}")
-    return _PACK[n](t.data_ptr(), code, n, *t.shape, *t.stride())
-
-
-def _device_of(stream, *tensors) -> int:
-    """The one CUDA device that a call's tensors (None: not given) and its stream are on."""
-    dev = tensors[0].get_device()
-    for t in tensors:
-        if t is not None and t.get_device() != dev:
-            raise ValueError(f"tensors on {tensors[0].device} and {t.device}: one device per call")
-    if dev < 0:
-        raise ValueError(f"tensors on {tensors[0].device}: CUDA tensors are needed")
-    if isinstance(stream, torch.cuda.Stream) and stream.device.index != dev:
-        raise ValueError(f"a stream of {stream.device} for tensors on {tensors[0].device}")
-    return dev
-
-
-def _handle(stream, dev: int) -> int:
-    """The stream's handle; None: the current stream of device dev, which is current."""
-    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream_handle(stream)
-
-
-def _new(like: torch.Tensor, shape, stream, dtype=torch.bfloat16) -> torch.Tensor:
-    """A new contiguous tensor on like's device from the memory of the stream that the call runs on."""
+def _here(first: torch.Tensor, stream) -> int:
+    """The current stream's handle if a call can run as things are (its device is current, and it
+    names no stream), else -1: the call is made inside _On."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=like.device)
-    if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(int(stream), device=like.device)
-    with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=like.device)
+        dev = first.get_device()
+        if dev >= 0 and dev == torch.cuda.current_device():
+            return torch._C._cuda_getCurrentRawStream(dev)  # (current_stream() makes an object first)
+    return -1
+
+
+def _done(result, where: str):
+    """The outputs of a native call, or the error that its status stands for."""
+    if isinstance(result, int):
+        _check(result, where)
+    return result
 
 
 def _check(status: int, where: str):
@@ -494,14 +507,16 @@ def append_kv_scaled(k_new: torch.Tensor, v_new: torch.Tensor, kv_cache, kv_scal
     kv_scales is (k_scales, v_scales), fp32 with the pools' shape without head_dim.  Each row gets
     the smallest power of two that brings its largest value to 448 at most, and its values
     divided by that, rounded to the nearest e4m3 value (see include/b2pa.h)."""
+    call = native().append_kv_scaled
     k, v = split_kv_cache(kv_cache, kv_layout)
     ks, vs = _two(kv_scales, "kv_scales")
-    args = (k_new, v_new, k, v, ks, vs, cache_loc)
-    dev = _device_of(stream, *args)
-    if dev != torch.cuda.current_device():
-        with torch.cuda.device(dev):
-            return append_kv_scaled(k_new, v_new, kv_cache, kv_scales, cache_loc, kv_layout, stream)
-    st = load().b2pa_append_kv_scaled(*map(_packed, args), LAYOUTS[kv_layout], _handle(stream, dev))
+    args = (k_new, v_new, k, v, ks, vs, cache_loc, LAYOUTS[kv_layout])
+    handle = _here(k_new, stream)
+    if handle >= 0:
+        st = call(handle, *args)
+    else:
+        with _On(k_new, stream) as handle:
+            st = call(handle, *args)
     _check(st, "b2pa_append_kv_scaled")
 
 
@@ -512,22 +527,15 @@ def read_kv_scaled(kv_cache, kv_scales, cache_loc: torch.Tensor, k_out: Optional
 
     k_out and v_out may be given, as views of bf16 pools for example.  A slot outside the pool
     reads as zeros and is flagged in device_status()."""
+    call = native().read_kv_scaled
     k, v = split_kv_cache(kv_cache, kv_layout)
     ks, vs = _two(kv_scales, "kv_scales")
-    dev = _device_of(stream, k, v, ks, vs, cache_loc, k_out, v_out)
-    if dev != torch.cuda.current_device():
-        with torch.cuda.device(dev):
-            return read_kv_scaled(kv_cache, kv_scales, cache_loc, k_out, v_out, kv_layout, stream)
-    layout = LAYOUTS[kv_layout]
-    shape = (cache_loc.numel(), k.shape[1 + layout], k.shape[3]) if k.dim() == 4 else (0, 0, 0)
-    if k_out is None:
-        k_out = _new(k, shape, stream)
-    if v_out is None:
-        v_out = _new(k, shape, stream)
-    st = load().b2pa_read_kv_scaled(*map(_packed, (k, v, ks, vs, cache_loc)), layout, _packed(k_out), _packed(v_out),
-                                    _handle(stream, dev))
-    _check(st, "b2pa_read_kv_scaled")
-    return k_out, v_out
+    args = (k, v, ks, vs, cache_loc, LAYOUTS[kv_layout], k_out, v_out)
+    handle = _here(k, stream)
+    if handle >= 0:
+        return _done(call(handle, *args), "b2pa_read_kv_scaled")
+    with _On(k, stream) as handle:
+        return _done(call(handle, *args), "b2pa_read_kv_scaled")
 
 
 def qk_norm_rope(
@@ -551,27 +559,18 @@ def qk_norm_rope(
     may be query / key themselves.  cos_sin [max_position, R] fp32 holds R / 2 cosines and R / 2
     sines per position.  positions is int32 [T], or [axes, T] with axis_of naming the axis of
     each of the R / 2 frequencies."""
-    dev = _device_of(stream, query, key, cos_sin, positions, q_weight, k_weight, q_out, k_out)
-    if dev != torch.cuda.current_device():
-        with torch.cuda.device(dev):
-            return qk_norm_rope(query, key, cos_sin, positions, q_weight, k_weight, eps, axis_of, interleaved, q_out,
-                                k_out, stream)
+    call = native().qk_norm_rope
     axes = None
     if axis_of is not None:
         if len(axis_of) != cos_sin.shape[-1] // 2:
             raise ValueError(f"axis_of: one axis for each of the {cos_sin.shape[-1] // 2} frequencies")
         axes = struct.pack(f"{len(axis_of)}i", *axis_of)
-    if q_out is None:
-        q_out = _new(query, query.shape, stream)
-    if k_out is None:
-        k_out = _new(key, key.shape, stream)
-    st = load().b2pa_qk_norm_rope(*map(_packed, (query, key, cos_sin, positions, q_weight, k_weight)), eps, axes,
-                                  1 if interleaved else 0, _packed(q_out), _packed(k_out), _handle(stream, dev))
-    _check(st, "b2pa_qk_norm_rope")
-    return q_out, k_out
-
-
-_tree_workspace = {}  # bytes of a tree_attention call's workspace, by its sizes
+    args = (query, key, cos_sin, positions, q_weight, k_weight, eps, axes, 1 if interleaved else 0, q_out, k_out)
+    handle = _here(query, stream)
+    if handle >= 0:
+        return _done(call(handle, *args), "b2pa_qk_norm_rope")
+    with _On(query, stream) as handle:
+        return _done(call(handle, *args), "b2pa_qk_norm_rope")
 
 
 def tree_attention(
@@ -597,31 +596,21 @@ def tree_attention(
     The query rows of request b are its tree's nodes, whose keys are the last ones of its
     seq_lens[b] keys; each sees the keys before them (with window_left >= 0 those from
     positions - window_left on) and the nodes whose bit is set in its row of tree_mask, int32
-    [T, words], bit j % 32 of word j / 32 for node j."""
+    [T, words], bit j % 32 of word j / 32 for node j.  The call's workspace comes from torch's
+    allocator."""
+    call = native().tree_attention
     k, v = split_kv_cache(kv_cache, kv_layout)
-    tensors = (query, k, v, block_tables, seq_lens, cum_seq_lens_q, tree_mask, positions)
-    dev = _device_of(stream, *tensors, sinks, out)
-    if dev != torch.cuda.current_device():
-        with torch.cuda.device(dev):
-            return tree_attention(query, kv_cache, block_tables, seq_lens, tree_mask, max_q_len, max_kv_len, bmm1_scale,
-                                  bmm2_scale, cum_seq_lens_q, positions, window_left, out, kv_layout, sinks, stream)
-    if out is None:
-        out = _new(query, query.shape, stream)
-    args = (*map(_packed, tensors), max_q_len, max_kv_len, bmm1_scale, bmm2_scale, window_left, _packed(sinks),
-            LAYOUTS[kv_layout], _packed(out))
-    handle, need = _handle(stream, dev), ctypes.c_uint64(0)
-    # the workspace comes from torch's allocator for this call, so that every captured graph keeps
-    # its own; its size is remembered by the call's sizes
-    sizes = (dev, query.shape[1:], k.shape, max_q_len)
-    size = _tree_workspace.get(sizes, 0)
-    while True:
-        workspace = _new(query, (size,), stream, torch.uint8) if size else None
-        st = load().b2pa_tree_attention(*args, workspace.data_ptr() if size else None, size, ctypes.byref(need), handle)
-        if st != -5 or need.value <= size:
-            break
-        size = _tree_workspace[sizes] = need.value
-    _check(st, "b2pa_tree_attention")
-    return out
+    if isinstance(sinks, (list, tuple)):
+        if len(sinks) != 1:
+            raise ValueError("sinks: one fp32 [num_heads] tensor")
+        sinks = sinks[0]
+    args = (query, k, v, block_tables, seq_lens, cum_seq_lens_q, tree_mask, positions, max_q_len, max_kv_len, bmm1_scale,
+            bmm2_scale, window_left, sinks, LAYOUTS[kv_layout], out)
+    handle = _here(query, stream)
+    if handle >= 0:
+        return _done(call(handle, *args), "b2pa_tree_attention")
+    with _On(query, stream) as handle:
+        return _done(call(handle, *args), "b2pa_tree_attention")
 
 
 def device_status(stream=None) -> int:

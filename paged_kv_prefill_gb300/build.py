@@ -2,7 +2,8 @@
 
 Each .cu file under csrc/ is compiled in parallel to _build/, then linked
 into paged_kv_prefill_gb300/libb2pa.so with the CUDA runtime linked
-statically.  The driver API is reached at run time through
+statically.  csrc/native.cpp, the Python module of direct bindings, is compiled
+with g++ against this machine's Python and torch headers to _native.so.  The driver API is reached at run time through
 cudaGetDriverEntryPointByVersion, so nothing links against libcuda.
 """
 from __future__ import annotations
@@ -12,11 +13,13 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libb2pa.so")
+NATIVE = os.path.join(HERE, "_native.so")
 SOURCES = ["b2pa.cu", "attn_tc.cu", "attn_win.cu", "sched_gather.cu", "generic.cu", "append.cu", "decode.cu",
            "ops.cu", "rope.cu", "kv_scaled.cu", "attn_tree.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -42,9 +45,26 @@ def _deps_mtime() -> float:
     return m
 
 
+def _native_commands(tmp: str) -> list:
+    """Compile and link commands of _native.so (to tmp)."""
+    import torch
+
+    root = os.path.dirname(torch.__file__)
+    inc = [sysconfig.get_paths()["include"], os.path.join(root, "include"),
+           os.path.join(root, "include", "torch", "csrc", "api", "include")]
+    obj = os.path.join(BUILD, "native.o")
+    cxx = ["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
+    return [
+        cxx + [x for i in inc for x in ("-isystem", i)] + ["-c", os.path.join(CSRC, "native.cpp"), "-o", obj],
+        ["g++", "-shared", "-o", tmp, obj, "-L", HERE, "-l:libb2pa.so", "-Wl,-rpath,$ORIGIN",
+         "-L", os.path.join(root, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10"],
+    ]
+
+
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
     """Compile and link libb2pa.so if any source is newer; return its path."""
-    if not force and os.path.exists(LIB) and os.path.getmtime(LIB) >= _deps_mtime():
+    if not force and all(os.path.exists(f) and os.path.getmtime(f) >= _deps_mtime() for f in (LIB, NATIVE)):
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     nvcc = _nvcc()
@@ -59,14 +79,23 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
             sys.stderr.write(r.stdout + r.stderr)
         return obj
 
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    def run(cmd: list, what: str) -> None:
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"{what} failed:\n{r.stdout}\n{r.stderr}")
+
+    native_tmp = NATIVE + f".tmp{os.getpid()}"
+    compile_native, link_native = _native_commands(native_tmp)
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        native = ex.submit(run, compile_native, "compiling native.cpp")
         objs = list(ex.map(one, SOURCES))
+        native.result()
     tmp = LIB + f".tmp{os.getpid()}"
-    cmd = [nvcc] + ARCH + ["-shared", "-o", tmp] + objs + ["-cudart", "static", "-Xcompiler", "-fPIC"]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+    run([nvcc] + ARCH + ["-shared", "-o", tmp] + objs + ["-cudart", "static", "-Xcompiler", "-fPIC",
+                                                        "-Xlinker", "-soname=libb2pa.so"], "link")
     os.replace(tmp, LIB)
+    run(link_native, "linking native.o")
+    os.replace(native_tmp, NATIVE)
     return LIB
 
 
