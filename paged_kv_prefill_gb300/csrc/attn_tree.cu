@@ -834,7 +834,7 @@ __device__ void tree_softmax(const TreeParams& p, const TreeCtx& c, int t)
     constexpr float kBias = FP8 ? 4.f : 0.f, kSlack = FP8 ? 4.f : 8.f;
     constexpr float kScale = FP8 ? 8.f : 0.f;
     // 32-key steps of the exponentials that are unrolled (see below)
-    constexpr int kUnroll = kTiles == 2 && !FP8 ? 4 : 1;
+    constexpr int kUnroll = kTiles == 2 && !FP8 ? 4 : 2;
     const int wq = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31, row = wq * 32 + lane;
     const uint32_t lane_off = (uint32_t)(wq * 32) << 16;
     const uint32_t s0_tmem = c.tmem + lane_off;  // + buffer * kKvTile

@@ -16,9 +16,10 @@
 // the maxima of the two rows ride in the two halves of one word, through one
 // chain of log2(lanes) shuffles.  More rows per group, with their loads issued
 // together, were slower: the registers they take cost more loads in flight
-// than they add (write of 32768 tokens x 8 heads x 128: 34.8 us with one row,
-// 36.9 with two, 37.1 with four, 47.3 with eight; read of 131072 x 8 x 64:
-// 67.7, 72.2, 78.1, 82.5).
+// than they add (write of 32768 tokens x 8 heads x 128: 35 us with one row, 37
+// with two or four, 47 with eight; read of 131072 x 8 x 64: 68, 72, 78, 83).
+// Blocks of 128 threads: 35.6 and 68.7 us (5.7 and 6.0 TB/s, 0.84 and 0.88 of
+// the copy rate); of 256: 36.8 and 70.9.
 #include "kv_scaled.cuh"
 
 #include "../../include/b2pa.h"
@@ -28,7 +29,7 @@ namespace b2pa {
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 
 __device__ __forceinline__ uint32_t two_e4m3(float lo, float hi)
 {

@@ -115,11 +115,11 @@ int rope_impl(const b2pa_tensor* q, const b2pa_tensor* k, const b2pa_tensor* cos
     }
     if (T == 0)
         return B2PA_OK;
-    for (int g = 0; g < (half + 7) / 8; ++g) {
-        p.axis_of8[g] = p.axis_of[8 * g];
-        for (int i = 8 * g; i < 8 * g + 8 && i < half; ++i)
-            if (p.axis_of[i] != p.axis_of[8 * g])
-                p.axis_of8[g] = 255;
+    for (int g = 0; g < (half + 3) / 4; ++g) {
+        p.axis_of4[g] = 4 * g + 4 <= half ? p.axis_of[4 * g] : 255;
+        for (int i = 4 * g; i < 4 * g + 4 && i < half; ++i)
+            if (p.axis_of[i] != p.axis_of[4 * g])
+                p.axis_of4[g] = 255;
     }
     int dev;
     DevInfo di;

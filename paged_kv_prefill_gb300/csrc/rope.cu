@@ -32,7 +32,8 @@
 // per group, 60 us with four in registers, 60 us with the ring and the table
 // from L2, 45.4 us so (5.4 TB/s, 0.80 of the copy rate); 16384 tokens x 72
 // heads with three axes 123 us (5.0 TB/s).  Sets of eight, rings of three
-// stages and smaller blocks were slower (47 to 68 us).
+// stages and smaller blocks were slower (47 to 68 us), blocks of 256 threads the
+// same.
 #include "rope.cuh"
 
 #include "../../include/b2pa.h"
@@ -62,20 +63,19 @@ __device__ __forceinline__ uint4 pack8(const float2* f)
                       pack_bf16x2(f[3].x, f[3].y));
 }
 
-__device__ __forceinline__ void load8(const float* p, float2* f)
+__device__ __forceinline__ void load4(const float* p, float2* f)
 {
-    const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+    const float4 a = __ldg(reinterpret_cast<const float4*>(p));
     f[0] = make_float2(a.x, a.y);
     f[1] = make_float2(a.z, a.w);
-    f[2] = make_float2(b.x, b.y);
-    f[3] = make_float2(b.z, b.w);
 }
 
 __device__ __forceinline__ void load_weight8(const RopeTensor& x, int d, float2* w)
 {
-    if (x.weight_f32)
-        load8(static_cast<const float*>(x.weight) + d, w);
-    else
+    if (x.weight_f32) {
+        load4(static_cast<const float*>(x.weight) + d, w);
+        load4(static_cast<const float*>(x.weight) + d + 4, w + 2);
+    } else
         unpack8(__ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(x.weight) + d)), w);
 }
 
@@ -236,11 +236,11 @@ __device__ __forceinline__ void store_row(const RopeTensor& x, long long t, int 
         *reinterpret_cast<uint4*>(row + 8 * ch.b) = pack8(b);
 }
 
-// The common axis of this lane's eight frequencies if their table entries can
-// be read as float4, else 255.
-__device__ __forceinline__ int vector_axis(const RopeParams& p, int lane)
+// The common axis of the frequencies 4 g .. 4 g + 3 if their table entries can
+// be read as a float4, else 255.
+__device__ __forceinline__ int vector_axis(const RopeParams& p, int g)
 {
-    return p.vec_table && 8 * lane + 8 <= p.R >> 1 ? p.axis_of8[lane] : 255;
+    return p.vec_table && 4 * g < p.R >> 1 ? p.axis_of4[g] : 255;
 }
 
 // kLanes lanes per row, each holding two chunks of 8 elements; one row per group.
@@ -283,18 +283,21 @@ __global__ void __launch_bounds__(kRopeThreads) rope_rows_kernel(const __grid_co
         s[i] = make_float2(0.f, 0.f);
     }
     if (kMode != kHalvesInSmem && ch.turns) {
-        const int f0 = 8 * lane, a8 = vector_axis(p, lane);
-        if (a8 != 255) {
-            load8(at.row(p, a8) + f0, c);
-            load8(at.row(p, a8) + half + f0, s);
-        } else {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                if (f0 + i >= half)
-                    break;
-                const float* e = at.row(p, p.axis_of[f0 + i]) + f0 + i;
-                (i & 1 ? c[i / 2].y : c[i / 2].x) = __ldg(e);
-                (i & 1 ? s[i / 2].y : s[i / 2].x) = __ldg(e + half);
+        for (int v = 0; v < 2; ++v) {  // four of its eight frequencies
+            const int f = 8 * lane + 4 * v, axis = vector_axis(p, 2 * lane + v);
+            if (axis != 255) {
+                load4(at.row(p, axis) + f, &c[2 * v]);
+                load4(at.row(p, axis) + half + f, &s[2 * v]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    if (f + i >= half)
+                        break;
+                    const float* e = at.row(p, p.axis_of[f + i]) + f + i;
+                    (i & 1 ? c[2 * v + i / 2].y : c[2 * v + i / 2].x) = __ldg(e);
+                    (i & 1 ? s[2 * v + i / 2].y : s[2 * v + i / 2].x) = __ldg(e + half);
+                }
             }
         }
     }
@@ -366,7 +369,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_staged_kernel(const __grid_
     const int lane = threadIdx.x % kLanes;
     const int half = p.R >> 1, f0 = 8 * lane;
     const Chunks ch = chunks_of<kMode>(p, lane);
-    const int a8 = vector_axis(p, lane);
+    const int axis0 = vector_axis(p, 2 * lane), axis1 = vector_axis(p, 2 * lane + 1);
     // sets of kSetRows rows of a token: those of the queries, then those of the keys
     const unsigned sets_q = (unsigned)(p.x[0].heads + kSetRows - 1) / kSetRows;
     const unsigned sets = sets_q + (unsigned)(p.x[1].heads + kSetRows - 1) / kSetRows;
@@ -407,19 +410,22 @@ __global__ void __launch_bounds__(kRopeThreads) rope_staged_kernel(const __grid_
                         copy16(piece(stage, 2 * r + 1), row + 8 * ch.b);
                 }
             if (ch.turns) {
-                if (a8 != 255) {
-                    const float* e = at.row(p, a8) + f0;
-                    copy16_l1(piece(stage, 2 * kSetRows), e);
-                    copy16_l1(piece(stage, 2 * kSetRows + 1), e + 4);
-                    copy16_l1(piece(stage, 2 * kSetRows + 2), e + half);
-                    copy16_l1(piece(stage, 2 * kSetRows + 3), e + half + 4);
-                } else {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const int f = min(f0 + i, half - 1);  // (a frequency past the last one turns no pair)
-                        const float* e = at.row(p, p.axis_of[f]) + f;
-                        copy4_l1(piece(stage, 2 * kSetRows + i / 4) + (i % 4) * 4, e);
-                        copy4_l1(piece(stage, 2 * kSetRows + 2 + i / 4) + (i % 4) * 4, e + half);
+                for (int v = 0; v < 2; ++v) {
+                    const int axis = v ? axis1 : axis0, f = f0 + 4 * v;
+                    const uint32_t cos = piece(stage, 2 * kSetRows + v), sin = piece(stage, 2 * kSetRows + 2 + v);
+                    if (axis != 255) {
+                        const float* e = at.row(p, axis) + f;
+                        copy16_l1(cos, e);
+                        copy16_l1(sin, e + half);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int fi = min(f + i, half - 1);  // (a frequency past the last one turns no pair)
+                            const float* e = at.row(p, p.axis_of[fi]) + fi;
+                            copy4_l1(cos + 4 * i, e);
+                            copy4_l1(sin + 4 * i, e + half);
+                        }
                     }
                 }
             }

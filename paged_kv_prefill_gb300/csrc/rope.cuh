@@ -26,13 +26,13 @@ struct RopeParams {
     const int* positions;    // [axes, T]
     long long pos_stride;    // between axes
     int T, D, R, axes, max_pos;
-    int vec_table;           // 1: eight consecutive table entries can be read as two float4
+    int vec_table;           // 1: four consecutive table entries can be read as one float4
     float eps;
     float inv_d;             // 1 / D
     unsigned* err;
     uint8_t axis_of[kRopeMaxD / 2];  // axis of each frequency
-    // per eight frequencies: their common axis, or 255
-    uint8_t axis_of8[kRopeMaxD / 16];
+    // per four frequencies: their common axis, or 255
+    uint8_t axis_of4[kRopeMaxD / 8];
 };
 
 // interleaved: element pairs (2i, 2i + 1) rotate; else (i, i + R / 2)

@@ -111,7 +111,9 @@ struct TreeCut {
 
 __device__ __forceinline__ TreeCut tree_cut(long long total, int grid)
 {
-    return TreeCut{total, (int)min((long long)grid, total)};
+    // two steps per CTA at least: fewer partial rows to merge where there is little
+    // work (8 nodes, 2048 keys: 16.6 us with one, 15.1 with two or three)
+    return TreeCut{total, (int)min((long long)grid, (total + 1) / 2)};
 }
 
 // What the merge needs to know of a segment that is part of a unit: kv tiles
