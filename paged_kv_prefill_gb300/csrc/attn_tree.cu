@@ -27,10 +27,11 @@
 //            few hundred cycles to look at, and one warp that looked at K, P, V
 //            and free buffers in turn left the tensor core idle meanwhile
 //            (e4m3 batch: 3000 cycles per kv tile with one).
-//   warp 3   loads Q (a TMA box per softmax warp's tokens and column block; e4m3
-//            caches: splits it into two e4m3 terms), and makes V safe where
-//            rows see different keys (see below).
-//   warps 4-7, 8-11   softmax A and B: one thread per MMA row.
+//   warp 3   loads Q (a TMA box per softmax warp's tokens and column block), and
+//            makes V safe where rows see different keys (see below).
+//   warps 4-7, 8-11   softmax A and B: one thread per MMA row.  e4m3 caches:
+//            they split the next segment's Q into two e4m3 terms while a segment's
+//            last P V runs (e4m3 batch: 146 us, 164 with warp 3 alone).
 //
 // kTiles 2 (more than one tile of rows in some request): A and B each have
 // their own query tile, and K/V are read once for both.  kTiles 1: there is
@@ -49,7 +50,12 @@
 // four bits and the rest rounded to four: off by at most half a step of bf16
 // (2^-8), down to 2^-14 of the row's largest.  (The other four powers of two
 // let a row's maximum grow by that much before O has to be rescaled.)
-// Two 8-bit MMAs take at most the time of one 16-bit MMA.
+// With two MMAs for every one of a 16-bit cache, and 128 cycles for each P V
+// MMA of 32 keys, where one of 16 keys takes 80, these would be bound by the
+// tensor core.  So a tile of at most 64 rows is stacked: its rows are in it
+// twice, one copy's P holding the leading terms and the other's the rest, and
+// one set of P V MMAs does both; the copies' O are added at the end, through
+// shared memory (e4m3 batch of 8 nodes x 4 heads: 173 us, stacked 165).
 //
 // V and keys that some rows of a tile do not see: their P is 0, but 0 times
 // an infinity or NaN is NaN.  Keys before the item's first and past the last
@@ -76,7 +82,7 @@ constexpr int kTreeSlots = 4;     // posted segments in flight
 constexpr int kTreeConsumers = 12;  // reads of a posted segment: warps 1 and 2, twice by warp 3, the softmax warps
 constexpr int kBadSlots = 16;     // segments whose V was found not to be finite: a bit each
 
-template <int D, bool FP8, int kTiles>
+template <int D, bool FP8, int kTiles, bool kStack>
 struct TreeCfg {
     static constexpr int kBlockBytes = kQRows * 128;        // 128 rows of one 128-byte column block
     static constexpr int kHalves = FP8 ? 1 : D / 64;        // column blocks of a K/V row
@@ -84,12 +90,14 @@ struct TreeCfg {
     static constexpr int kKvBytes = kHalves * kBlockBytes;
     static constexpr int kQBytes = kQHalves * kBlockBytes;
     static constexpr int kQBufs = D == 128 && !FP8 ? 1 : 2;
-    static constexpr int kRing = 224 * 1024 - kQBufs * kTiles * kQBytes;
+    static constexpr int kAddBytes = kStack ? 2 * 64 * 128 : 0;  // per group: 64 rows x 32 columns of O's second copy
+    static constexpr int kRing = 224 * 1024 - kQBufs * kTiles * kQBytes - kAddBytes;
     static constexpr int kEntries = kRing / kKvBytes;       // K and V tiles, alternating
     static constexpr int kOffRing = kQBufs * kTiles * kQBytes;
-    static constexpr int kOffBar = kOffRing + kEntries * kKvBytes;
+    static constexpr int kOffAdd = kOffRing + kEntries * kKvBytes;
+    static constexpr int kOffBar = kOffAdd + kAddBytes;
     static constexpr int kSBufs = kTiles == 1 ? 3 : 2;
-    static constexpr int kNumBars = 3 * kEntries + 3 * kQBufs + 3 * kSBufs + 2 + 8 + 2 + 2 + 2 * kTreeSlots + 1;
+    static constexpr int kNumBars = 3 * kEntries + 3 * kQBufs + 3 * kSBufs + 2 + 8 + 2 + 2 + 2 * kTreeSlots + 1 + (kStack ? 4 : 0);
     static constexpr int kOffMisc = kOffBar + kNumBars * 8;  // tmem address, abort flag
     static constexpr int kOffItems = kOffMisc + 16;
     static constexpr int kOffBad = kOffItems + kTreeSlots * 12 * 4;
@@ -100,6 +108,7 @@ struct TreeCfg {
     static constexpr int kOCol = kSBufs * kKvTile;
     static_assert(D == 64 || D == 128, "head_dim");
     static_assert(!FP8 || D == 128, "e4m3 caches: D = 128");
+    static_assert(!kStack || (FP8 && kTiles == 1), "stacked tiles: e4m3 caches");
     static_assert(kEntries >= 5 && kEntries <= 32, "ring");
     static_assert(kSmemBytes <= 232448, "shared memory");
 };
@@ -112,6 +121,7 @@ struct TreeCtx : Ctx {
     // kTiles 1: a warp's rows' maxima up to an even / odd tile posted ([2][4]);
     // both groups posted (m, l); both have read O
     uint64_t *m_ready, *met, *left;
+    uint64_t *add_full, *add_free;           // kStack, [2]: 32 columns of O's second copy posted, added
     uint64_t *drain /* [2] */, *it_full, *it_empty, *never;
 };
 
@@ -177,10 +187,10 @@ __device__ __forceinline__ int tile_tokens(const TreeRows& r, const Seg& s, int 
 // ---------------------------------------------------------------------------
 // warp 0
 // ---------------------------------------------------------------------------
-template <int D, bool FP8, int kTiles>
+template <int D, bool FP8, int kTiles, bool kStack>
 __device__ void tree_producer(const TreeParams& p, const TreeCtx& c, long long pos, long long end, int b, long long base)
 {
-    using C = TreeCfg<D, FP8, kTiles>;
+    using C = TreeCfg<D, FP8, kTiles, kStack>;
     const int lane = threadIdx.x & 31;
     const uint32_t ring = smem_u32(c.base + C::kOffRing);
     const int P = p.page_size, log2_p = 31 - __clz(P);  // the tensor-core path takes powers of two only
@@ -281,29 +291,63 @@ __device__ __forceinline__ constexpr uint32_t tree_idesc(bool fp8, int n, bool b
 }
 constexpr uint32_t kTreeDescHi = sdesc_hi_sw128(1024);  // 8 rows x 128 B per core group
 
-// The sequence of kv tiles over all segments: tile g's K and V are ring entries
-// 2 g and 2 g + 1.
-template <typename C>
-__device__ __forceinline__ uint32_t ring_entry(uint32_t g, uint32_t kind)
+// The issuers share their schedulers (and instruction caches) with two softmax
+// warps each, so that every instruction of theirs costs tens of cycles: their
+// loops step through ring and buffers by adding, keep barrier addresses, and
+// leave the waits that take long to a call.
+__device__ __noinline__ bool wait_long(uint32_t bar, uint32_t parity, volatile int* abort_flag, unsigned* err,
+                                       unsigned long long limit)
 {
-    return (2 * g + kind) % C::kEntries;
-}
-template <typename C>
-__device__ __forceinline__ uint32_t ring_phase(uint32_t g, uint32_t kind)
-{
-    return ((2 * g + kind) / C::kEntries) & 1u;
+    const uint64_t t0 = global_ns();
+    while (!mbar_try_wait(bar, parity)) {
+        const bool timed_out = global_ns() - t0 > limit;
+        if (__any_sync(0xffffffffu, *abort_flag != 0 || timed_out)) {
+            if (timed_out && (threadIdx.x & 31) == 0) {
+                *abort_flag = 1;
+                atomicOr(err, (unsigned)B2PA_DEV_TIMEOUT);
+            }
+            __syncwarp();
+            return false;
+        }
+    }
+    return true;
 }
 
-template <int D, bool FP8, int kTiles>
+// wait_bar for a barrier given by its address.
+__device__ __forceinline__ bool wait_at(uint32_t bar, uint32_t parity, const TreeCtx& c)
+{
+    return mbar_try_wait(bar, parity) || wait_long(bar, parity, c.abort_flag, c.err, c.wait_limit_ns);
+}
+
+// The K (kind 0) or V (1) entries of the ring, in the order of the kv tiles:
+// tile g's are entries 2 g and 2 g + 1.
+template <int kEntries>
+struct RingPos {
+    uint32_t e, phase;
+    __device__ __forceinline__ explicit RingPos(uint32_t kind) : e(kind), phase(0) {}
+    __device__ __forceinline__ void next()
+    {
+        e += 2;
+        if (e >= kEntries) {
+            e -= kEntries;
+            phase ^= 1;
+        }
+    }
+};
+
+template <int D, bool FP8, int kTiles, bool kStack>
 __device__ void tree_s(const TreeParams& p, const TreeCtx& c)
 {
-    using C = TreeCfg<D, FP8, kTiles>;
+    using C = TreeCfg<D, FP8, kTiles, kStack>;
     constexpr uint32_t kIdesc = tree_idesc(FP8, kKvTile, false);
     const uint32_t issue = (threadIdx.x & 31) == 0 ? 1u : 0u;
     const uint32_t q_lo = sdesc_lo(smem_u32(c.base), 16);                    // K-major: LBO unused
     const uint32_t k_lo = sdesc_lo(smem_u32(c.base + C::kOffRing), 16);
     constexpr uint32_t kEntryW = C::kKvBytes >> 4, kQTileW = C::kQBytes >> 4, kBlockW = C::kBlockBytes >> 4;
-    uint32_t g = 0, used[2] = {0, 0};  // kv tiles; kTiles 2: S of each query tile so far
+    const uint32_t kv_full = smem_u32(c.kv_full), kv_empty = smem_u32(c.kv_empty);
+    const uint32_t s_full = smem_u32(c.s_full), s_free = smem_u32(c.s_free);
+    RingPos<C::kEntries> at(0);
+    uint32_t buf = 0, turn[2] = {0, 0};  // kTiles 1: the next S buffer; the buffers' (kTiles 2: each one's) turn
     bool ok = !p.inject_stall || wait_bar(c.never, 0, c);  // failure-detection tests
     for (uint32_t n = 0; ok; ++n) {
         Seg s;
@@ -312,32 +356,23 @@ __device__ void tree_s(const TreeParams& p, const TreeCtx& c)
         const uint32_t qb = n % C::kQBufs;
         if (!wait_bar(FP8 ? &c.q_conv[qb] : &c.q_full[qb], (n / C::kQBufs) & 1, c))
             break;
-        const int nq = kTiles == 2 && s.toks > p.rows.tile_toks ? 2 : 1;
-        for (int i = 0; ok && i < s.tiles; ++i, ++g) {
-            const uint32_t e = ring_entry<C>(g, 0);
-            if (!wait_bar(&c.kv_full[e], ring_phase<C>(g, 0), c)) {
-                ok = false;
-                break;
-            }
+        const bool two = kTiles == 2 && s.toks > p.rows.tile_toks;
+        for (int i = s.tiles; ok && i > 0; --i) {
+            ok = wait_at(kv_full + at.e * 8, at.phase, c);
 #pragma unroll
             for (int t = 0; t < kTiles; ++t) {
-                if (t >= nq)
+                if (t == 1 && !two)
                     break;
-                // the buffer's last P has been used
-                const int buf = kTiles == 1 ? (int)(g % 3) : t;
-                const uint32_t use = kTiles == 1 ? g / 3 : used[t];
-                if (use > 0 && !wait_bar(&c.s_free[buf], (use - 1) & 1, c)) {
-                    ok = false;
+                const uint32_t to = kTiles == 1 ? buf : (uint32_t)t;
+                ok = ok && wait_at(s_free + to * 8, turn[t] ^ 1, c);  // the buffer's last P has been used
+                if (!ok)
                     break;
-                }
-                ++used[t];
                 tc_fence_after();
-                const uint32_t a0 = q_lo + (qb * kTiles + t) * kQTileW, b0 = k_lo + e * kEntryW;
-                const uint32_t d = c.tmem + (uint32_t)(buf * kKvTile);
+                const uint32_t a0 = q_lo + (qb * kTiles + t) * kQTileW, b0 = k_lo + at.e * kEntryW;
+                const uint32_t d = c.tmem + to * kKvTile;
                 // a step is 32 bytes of a row: 32 e4m3 elements or 16 of 16 bits; four
-                // steps are a column block (e4m3: of Q's first, then second term).
-                // Rolled: instructions cost more here than loops (see tree_softmax).
-#pragma unroll 1
+                // steps are a column block (e4m3: of Q's first, then second term)
+#pragma unroll
                 for (int k = 0; k < (FP8 ? 8 : D / 16); ++k) {
                     const uint32_t step = (uint32_t)((k & 3) * 2), block = (uint32_t)(k >> 2) * kBlockW;
                     if constexpr (FP8)
@@ -345,14 +380,21 @@ __device__ void tree_s(const TreeParams& p, const TreeCtx& c)
                     else
                         mma_ss_wp(d, a0 + block + step, b0 + block + step, kTreeDescHi, kIdesc, k > 0 ? 1u : 0u, issue);
                 }
-                mma_commit_p(&c.s_full[buf], issue);
-                if (t == nq - 1) {
-                    mma_commit_p(&c.kv_empty[e], issue);
-                    if (i == s.tiles - 1)
-                        mma_commit_p(&c.q_empty[qb], issue);
-                }
+                mma_commit_at(s_full + to * 8, issue);
+                if (kTiles == 2)
+                    turn[t] ^= 1;
+            }
+            if (!ok)
+                break;
+            mma_commit_at(kv_empty + at.e * 8, issue);
+            at.next();
+            if (kTiles == 1 && ++buf == 3) {
+                buf = 0;
+                turn[0] ^= 1;
             }
         }
+        if (ok)
+            mma_commit_p(&c.q_empty[qb], issue);
     }
     // every MMA this thread issued has completed once the drain barrier flips
     if (issue)
@@ -361,60 +403,76 @@ __device__ void tree_s(const TreeParams& p, const TreeCtx& c)
     drain_wait(&c.drain[0], 0);
 }
 
-template <int D, bool FP8, int kTiles>
+template <int D, bool FP8, int kTiles, bool kStack>
 __device__ void tree_pv(const TreeParams& p, const TreeCtx& c)
 {
-    using C = TreeCfg<D, FP8, kTiles>;
+    using C = TreeCfg<D, FP8, kTiles, kStack>;
     constexpr uint32_t kIdesc = tree_idesc(FP8, D, true);
     const uint32_t issue = (threadIdx.x & 31) == 0 ? 1u : 0u;
     const uint32_t v_lo = sdesc_lo(smem_u32(c.base + C::kOffRing), C::kBlockBytes);  // MN-major: LBO = next column block
     constexpr uint32_t kEntryW = C::kKvBytes >> 4;
-    uint32_t g = 0, used[2] = {0, 0};
+    // A step is 8 columns of P: 16 keys (16 rows of V), or 32 of one e4m3 term
+    // (both, stacked); kSteps of them are a tile.  Of a request's last tile the
+    // steps behind the last key are left out.
+    constexpr int kStepsAtKeys = FP8 && !kStack ? 2 : 1, kKeys = FP8 ? 32 : 16, kSteps = kKvTile / kKeys * kStepsAtKeys;
+    const uint32_t kv_full = smem_u32(c.kv_full), kv_empty = smem_u32(c.kv_empty), v_ready = smem_u32(c.v_ready);
+    const uint32_t p_full = smem_u32(c.p_full), s_free = smem_u32(c.s_free);
+    RingPos<C::kEntries> at(1);
+    uint32_t buf = 0, turn[2] = {0, 0};  // as in tree_s
     uint32_t ready_bits = 0;  // parity of each entry's next v_ready phase
     bool ok = true;
     for (uint32_t n = 0; ok; ++n) {
         Seg s;
         if (!take_seg(c, n, &s) || !s.on)
             break;
-        const int nq = kTiles == 2 && s.toks > p.rows.tile_toks ? 2 : 1;
-        for (int i = 0; ok && i < s.tiles; ++i, ++g) {
-            const uint32_t e = ring_entry<C>(g, 1);
-            // V, made safe where rows see different keys
-            ok = wait_bar(&c.kv_full[e], ring_phase<C>(g, 1), c);
-            if (ok && s.mixed(s.j0 + i, p.window)) {
-                ok = wait_bar(&c.v_ready[e], ready_bits >> e & 1u, c);
-                ready_bits ^= 1u << e;
+        const bool two = kTiles == 2 && s.toks > p.rows.tile_toks;
+        // tiles [0, mixed0) and [mixed1, ...) have keys that not every row sees
+        const int mixed0 = (s.lo_all(p.window) + kKvTile - 1) / kKvTile - s.j0, mixed1 = s.ctx() / kKvTile - s.j0;
+        for (int i = 0; ok && i < s.tiles; ++i) {
+            ok = wait_at(kv_full + at.e * 8, at.phase, c);
+            if (ok && (i < mixed0 || i >= mixed1)) {  // V, made safe
+                ok = wait_at(v_ready + at.e * 8, ready_bits >> at.e & 1u, c);
+                ready_bits ^= 1u << at.e;
             }
 #pragma unroll
             for (int t = 0; t < kTiles; ++t) {
-                if (!ok || t >= nq)
+                if (t == 1 && !two)
                     break;
-                const int buf = kTiles == 1 ? (int)(g % 3) : t;
-                if (!wait_bar(&c.p_full[buf], (kTiles == 1 ? g / 3 : used[t]) & 1, c)) {
-                    ok = false;
+                const uint32_t from = kTiles == 1 ? buf : (uint32_t)t;
+                ok = ok && wait_at(p_full + from * 8, turn[t], c);
+                if (!ok)
                     break;
-                }
-                ++used[t];
                 tc_fence_after();
-                const uint32_t b0 = v_lo + e * kEntryW, a = c.tmem + (uint32_t)(buf * kKvTile);
+                const uint32_t b0 = v_lo + at.e * kEntryW, a = c.tmem + from * kKvTile;
                 const uint32_t d = c.tmem + (uint32_t)(C::kOCol + (kTiles == 1 ? 0 : t * D));
-                // a step is 8 columns of P: 16 keys (16 rows of V), or 32 of one e4m3
-                // term; keys behind the last are left out in whole steps
-                const int keys = min(kKvTile, s.kv_len - (s.j0 + i) * kKvTile);
-                const int steps = FP8 ? (keys + 31) / 32 * 2 : (keys + 15) / 16;
+                const int keys = s.kv_len - (s.j0 + i) * kKvTile;
+                const int steps = keys >= kKvTile ? kSteps : (keys + kKeys - 1) / kKeys * kStepsAtKeys;
+                uint32_t acc = i > 0 ? 1u : 0u;
 #pragma unroll 1
-                for (int k = 0; k < steps; ++k) {
-                    const uint32_t acc = i > 0 || k > 0 ? 1u : 0u;
-                    if constexpr (FP8)
-                        mma8_ts_wp(d, a + (uint32_t)(k * 8), b0 + (uint32_t)((k >> 1) * 256), kTreeDescHi, kIdesc, acc, issue);
-                    else
-                        mma_ts_wp(d, a + (uint32_t)(k * 8), b0 + (uint32_t)(k * 128), kTreeDescHi, kIdesc, acc, issue);
+                for (int k = 0; k < steps; k += kStepsAtKeys) {
+#pragma unroll
+                    for (int h = 0; h < kStepsAtKeys; ++h) {
+                        const uint32_t ak = a + (uint32_t)((k + h) * 8), bk = b0 + (uint32_t)(k / kStepsAtKeys * kKeys * 8);
+                        if constexpr (FP8)
+                            mma8_ts_wp(d, ak, bk, kTreeDescHi, kIdesc, acc, issue);
+                        else
+                            mma_ts_wp(d, ak, bk, kTreeDescHi, kIdesc, acc, issue);
+                        acc = 1;
+                    }
                 }
-                mma_commit_p(&c.s_free[buf], issue);
-                if (t == nq - 1)
-                    mma_commit_p(&c.kv_empty[e], issue);
+                mma_commit_at(s_free + from * 8, issue);
                 if (i == s.tiles - 1)
                     mma_commit_p(&c.o_full[kTiles == 1 ? 0 : t], issue);
+                if (kTiles == 2)
+                    turn[t] ^= 1;
+            }
+            if (!ok)
+                break;
+            mma_commit_at(kv_empty + at.e * 8, issue);
+            at.next();
+            if (kTiles == 1 && ++buf == 3) {
+                buf = 0;
+                turn[0] ^= 1;
             }
         }
     }
@@ -458,26 +516,37 @@ __device__ __forceinline__ void split_e4m3(float2 v, uint32_t& hi, uint32_t& lo)
     lo = r * 2u + 0x00800080u | sign;
 }
 
-// `count` Q rows of 128 bf16 values from row0 (a multiple of 32; at most 32) in
+// One of those terms of two values: the leading one with cut = half = 0, the
+// other with split_e4m3's masks.
+__device__ __forceinline__ uint32_t term_e4m3(float2 v, uint32_t cut, uint32_t half)
+{
+    uint32_t f, r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(f) : "f"(v.y), "f"(v.x));
+    asm("sub.f16x2 %0, %1, %2;" : "=r"(r) : "r"(f), "r"(f & cut));
+    return r * 2u + half;
+}
+
+// `count` Q rows of 128 bf16 values from row0 (a multiple of 16; at most 16) in
 // shared memory (two column blocks of 128 bytes, 16-byte chunks swizzled by row
 // % 8) become their two e4m3 terms, in place: the high one in the first block,
 // the low one in the second.  exps[row] is the power of two a row was scaled
 // by, which brings its largest value to [2^7, 2^8).  A row that is not finite
 // becomes NaN, which is what every score of it makes of the softmax.
-__device__ __forceinline__ void split_q_rows(uint8_t* tile, int block_bytes, int row0, int count, int8_t* exps)
+__device__ __noinline__ void split_q_rows(uint8_t* tile, int block_bytes, int row0, int count, int8_t* exps)
 {
     const int lane = threadIdx.x & 31;
-    // a row's maximum by one lane
+    // a row's maximum by two lanes, a block each
     uint32_t m = 0;
-    if (lane < count) {
-        const uint8_t* row = tile + (row0 + lane) * 128;
-#pragma unroll 4
-        for (int k = 0; k < 16; ++k) {
-            const uint4 x = *reinterpret_cast<const uint4*>(row + (k >> 3) * block_bytes + (((k & 7) ^ (lane & 7)) << 4));
+    if ((lane & 15) < count) {
+        const uint8_t* row = tile + (row0 + (lane & 15)) * 128 + (lane >> 4) * block_bytes;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const uint4 x = *reinterpret_cast<const uint4*>(row + ((k ^ (lane & 7)) << 4));
             m = __vmaxu2(m, __vmaxu2(__vmaxu2(x.x & 0x7FFF7FFFu, x.y & 0x7FFF7FFFu),
                                      __vmaxu2(x.z & 0x7FFF7FFFu, x.w & 0x7FFF7FFFu)));
         }
     }
+    m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 16));
     m = max(m & 0xFFFFu, m >> 16);
     const int mine = m == 0 || m >= 0x7F80u ? 0 : min(120, max(-110, 7 - ((int)(m >> 7) - 127)));
     if (lane < count)
@@ -489,8 +558,8 @@ __device__ __forceinline__ void split_q_rows(uint8_t* tile, int block_bytes, int
     for (int k = 0; k < count; k += 2) {
         const int r = k + (lane >> 4), sw = r & 7;
         const bool on = r < count;
-        const int e = __shfl_sync(0xffffffffu, mine, r & 31);
-        const bool nan = __shfl_sync(0xffffffffu, m, r & 31) >= 0x7F80u;
+        const int e = __shfl_sync(0xffffffffu, mine, r & 15);
+        const bool nan = __shfl_sync(0xffffffffu, m, r & 15) >= 0x7F80u;
         const float sc = __int_as_float((127 - 8 + e) << 23);
         uint8_t* row = tile + (row0 + (on ? r : k)) * 128;
         const uint4 x = *reinterpret_cast<const uint4*>(row + (c >> 3) * block_bytes + (((c & 7) ^ sw) << 4));
@@ -527,32 +596,33 @@ __device__ __forceinline__ bool not_finite(uint4 v)
 }
 
 // The Q tiles of a segment, into buffer qb.
-template <int D, bool FP8, int kTiles>
+template <int D, bool FP8, int kTiles, bool kStack>
 __device__ __forceinline__ void load_q(const TreeParams& p, const TreeCtx& c, const Seg& s, uint32_t qb)
 {
-    using C = TreeCfg<D, FP8, kTiles>;
+    using C = TreeCfg<D, FP8, kTiles, kStack>;
     const int lane = threadIdx.x & 31;
     const TreeRows& r = p.rows;
     // lane = (tile, warp's tokens, column block): one box each
     const int t = lane / (4 * C::kQHalves), w = lane / C::kQHalves % 4, h = lane % C::kQHalves;
     const int toks = t < kTiles ? tile_tokens(r, s, t) : 0;
-    const int per = r.by_warp ? (toks + 3) >> 2 : r.tile_toks;
-    const bool box = toks > 0 && w * per < toks && (r.by_warp || w == 0);
+    const int per = r.by_warp ? (toks + r.warps - 1) / r.warps : r.tile_toks;
+    const int first = w % r.warps * per;  // this warp's first token
+    const bool box = toks > 0 && first < toks && (r.by_warp || w == 0);
     const uint32_t boxes = __popc(__ballot_sync(0xffffffffu, box));
     mbar_arrive_expect_tx_p(&c.q_full[qb], boxes * (uint32_t)(r.G * r.box_toks * 128), lane == 0 ? 1u : 0u);
     __syncwarp();
     if (box)
         tma_load_3d(smem_u32(c.base) + (qb * kTiles + t) * C::kQBytes + h * C::kBlockBytes + w * 32 * 128, &p.tm_q,
-                    &c.q_full[qb], h * 64, s.kvh * r.G, s.q0 + s.tok0 + t * r.tile_toks + w * per);
+                    &c.q_full[qb], h * 64, s.kvh * r.G, s.q0 + s.tok0 + t * r.tile_toks + first);
     __syncwarp();
 }
 
 // V entry e, kv tile j of segment s (its n-th): keys that no row sees become
 // 0, and so do keys that some rows may not see and that are not finite.
-template <int D, bool FP8, int kTiles>
+template <int D, bool FP8, int kTiles, bool kStack>
 __device__ __forceinline__ void safe_v(const TreeParams& p, const TreeCtx& c, const Seg& s, uint32_t n, int j, uint32_t e)
 {
-    using C = TreeCfg<D, FP8, kTiles>;
+    using C = TreeCfg<D, FP8, kTiles, kStack>;
     constexpr int kChunks = 8 * C::kHalves;  // 16-byte pieces of a V row
     constexpr int kRowsAtOnce = 32 / kChunks;
     const int lane = threadIdx.x & 31;
@@ -600,19 +670,17 @@ __device__ __forceinline__ void safe_v(const TreeParams& p, const TreeCtx& c, co
 
 // Q runs up to a segment (and a buffer) ahead of V; what is possible next is
 // done, and this warp waits for neither while the other could go.
-template <int D, bool FP8, int kTiles>
+template <int D, bool FP8, int kTiles, bool kStack>
 __device__ void tree_feed(const TreeParams& p, const TreeCtx& c)
 {
-    using C = TreeCfg<D, FP8, kTiles>;
+    using C = TreeCfg<D, FP8, kTiles, kStack>;
     const int lane = threadIdx.x & 31;
     volatile int* bad = reinterpret_cast<volatile int*>(c.base + C::kOffBad);
     // (decided for the whole warp, which stays converged)
     auto here = [](uint64_t* bar, uint32_t parity) { return __any_sync(0xffffffffu, mbar_test(bar, parity)) != 0; };
     Seg qs{}, vs{};
     uint32_t qn = 0, vn = 0;  // segments taken
-    // what Q needs next: a segment, a buffer, its copies, its split, nothing more
-    enum { kNext, kEmpty, kLanded, kSplit, kNone } q_at = kNext;
-    int q_tile = 0, q_quad = 0;  // where its split has come to
+    enum { kNext, kEmpty, kNone } q_at = kNext;  // what Q needs next: a segment, a buffer, nothing more
     uint32_t loads = 0;       // segments whose Q copies were started
     uint32_t q = 0, q_end = 0;  // ring entries seen, and those of the segments taken
     bool v_more = true, ok = true;
@@ -626,33 +694,9 @@ __device__ void tree_feed(const TreeParams& p, const TreeCtx& c)
         }
         const uint32_t qb = (qn - 1) % C::kQBufs, ph = ((qn - 1) / C::kQBufs) & 1;
         if (q_at == kEmpty && here(&c.q_empty[qb], ph ^ 1)) {
-            load_q<D, FP8, kTiles>(p, c, qs, qb);
+            load_q<D, FP8, kTiles, kStack>(p, c, qs, qb);
             loads = qn;
-            q_at = FP8 ? kLanded : kNext;
-            did = true;
-        }
-        if (FP8 && q_at == kLanded && here(&c.q_full[qb], ph))
-            q_at = kSplit;
-        if (FP8 && q_at == kSplit) {
-            // 32 rows at a time, so that the ring does not wait for all of them
-            const int toks = tile_tokens(p.rows, qs, q_tile);
-            const int per = (toks + 3) >> 2;  // tokens of a quadrant
-            const int count = p.rows.by_warp ? (q_quad * per < toks ? p.rows.G * per : 0) : min(32, p.rows.G * toks - q_quad * 32);
-            const uint32_t at = qb * kTiles + (uint32_t)q_tile;
-            if (count > 0)
-                split_q_rows(c.base + at * C::kQBytes, C::kBlockBytes, q_quad * 32, count,
-                             reinterpret_cast<int8_t*>(c.base + C::kOffExp) + at * kQRows);
-            if (++q_quad == 4 || count <= 0) {
-                q_quad = 0;
-                if (++q_tile == kTiles || tile_tokens(p.rows, qs, q_tile) <= 0) {
-                    q_tile = 0;
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0)
-                        mbar_arrive(&c.q_conv[qb]);
-                    q_at = kNext;
-                }
-            }
+            q_at = kNext;
             did = true;
         }
         // every ring entry is seen and released in order, so that this warp never
@@ -679,7 +723,7 @@ __device__ void tree_feed(const TreeParams& p, const TreeCtx& c)
                 const int j = vs.j0 + vs.tiles - (int)((q_end - q + 1) >> 1);
                 const bool mixed = (q & 1) && vs.mixed(j, p.window);
                 if (mixed)
-                    safe_v<D, FP8, kTiles>(p, c, vs, vn - 1, j, e);
+                    safe_v<D, FP8, kTiles, kStack>(p, c, vs, vn - 1, j, e);
                 if (lane == 0) {
                     if (mixed)
                         mbar_arrive(&c.v_ready[e]);
@@ -823,10 +867,42 @@ __device__ __noinline__ float tree_bad_column(const TreeParams& p, const int* ro
     return sum;
 }
 
-template <int D, bool FP8, int kTiles>
+// e4m3: this warp's share of the n-th segment's Q becomes e4m3 terms (each group
+// its own tile, or half of the one tile's rows), if there is such a segment.
+template <typename C, int kTiles>
+__device__ __forceinline__ bool split_q(const TreeParams& p, const TreeCtx& c, uint32_t n, int t)
+{
+    const int wq = (threadIdx.x >> 5) & 3;
+    const uint32_t slot = n % kTreeSlots, qb = n % C::kQBufs;
+    if (!wait_bar(&c.it_full[slot], (n / kTreeSlots) & 1, c))
+        return false;
+    const volatile int* rec = c.item_slot + slot * 12;  // (taken, and released, later)
+    if (rec[0] == 0)
+        return true;
+    const int qt = kTiles == 1 ? 0 : t;
+    const int toks = min(p.rows.tile_toks, rec[6] - qt * p.rows.tile_toks);
+    if (!wait_bar(&c.q_full[qb], (n / C::kQBufs) & 1, c))
+        return false;
+    const int per = (toks + p.rows.warps - 1) / p.rows.warps;  // tokens of a quadrant
+    const int count = !p.rows.by_warp                      ? min(32, p.rows.G * toks - wq * 32)
+                      : wq % p.rows.warps * per < toks ? p.rows.G * per
+                                                           : 0;
+    uint8_t* tile = c.base + (qb * kTiles + qt) * C::kQBytes;
+    int8_t* exps = reinterpret_cast<int8_t*>(c.base + C::kOffExp) + (qb * kTiles + qt) * kQRows;
+#pragma unroll 1
+    for (int h = kTiles == 1 ? t : 0; h < (kTiles == 1 ? t + 1 : 2); ++h)
+        if (count > h * 16)
+            split_q_rows(tile, C::kBlockBytes, wq * 32 + h * 16, min(16, count - h * 16), exps);
+    fence_proxy_async_smem();
+    __syncwarp();
+    mbar_arrive_p(&c.q_conv[qb], (threadIdx.x & 31) == 0 ? 1u : 0u);
+    return true;
+}
+
+template <int D, bool FP8, int kTiles, bool kStack>
 __device__ void tree_softmax(const TreeParams& p, const TreeCtx& c, int t)
 {
-    using C = TreeCfg<D, FP8, kTiles>;
+    using C = TreeCfg<D, FP8, kTiles, kStack>;
     constexpr float kLog2e = 1.4426950408889634f;
     // P = 2^(x - m + kBias): e4m3 terms use their range from 2^kBias down.  The
     // stabiliser is renewed once the row's maximum has grown by kSlack.  The
@@ -845,9 +921,13 @@ __device__ void tree_softmax(const TreeParams& p, const TreeCtx& c, int t)
     float2* ml = reinterpret_cast<float2*>(c.base + C::kOffMl);
     const volatile int* bad = reinterpret_cast<const volatile int*>(c.base + C::kOffBad);
 
+    // kStack: the term of P that this warp's copy of the rows holds
+    const bool second = kStack && wq >= 2;
+    const uint32_t term_cut = second ? 0x7F807F80u : 0u, term_half = second ? 0x00800080u : 0u;
+    uint32_t adds = 0;  // kStack: column groups that the copies have added
     uint32_t g0 = 0;   // kv tiles before this segment
     uint32_t s_cnt = 0, o_cnt = 0;  // kTiles 2: S and O of this group awaited so far
-    bool ok = true;
+    bool ok = !FP8 || split_q<C, kTiles>(p, c, 0, t);
     for (uint32_t n = 0; ok; ++n) {
         Seg s;
         if (!take_seg(c, n, &s) || !s.on)
@@ -874,6 +954,7 @@ __device__ void tree_softmax(const TreeParams& p, const TreeCtx& c, int t)
         }
         if (kTiles == 2 && qt * rows.tile_toks >= s.toks) {
             g0 += (uint32_t)s.tiles;
+            ok = !FP8 || split_q<C, kTiles>(p, c, n + 1, t);
             continue;
         }
         const int toks = tile_tokens(rows, s, qt);
@@ -968,7 +1049,27 @@ __device__ void tree_softmax(const TreeParams& p, const TreeCtx& c, int t)
                 if (q < 3)
                     tmem_ld32(s_tmem + (uint32_t)(q * 32 + 32), rb);
                 uint32_t pk[16];
-                if constexpr (FP8) {  // eight columns of the leading terms, eight of the others
+                if constexpr (kStack) {  // eight columns of this copy's term
+#pragma unroll
+                    for (int w = 0; w < 8; ++w) {
+                        uint32_t a[2];
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const int k = w * 4 + h * 2;
+                            const float2 y =
+                                __ffma2_rn(make_float2(__uint_as_float(ra[k]), __uint_as_float(ra[k + 1])), sc, ng);
+                            const float2 e = make_float2(ex2_approx(y.x), ex2_approx(y.y));
+                            acc[w & 3] = __fadd2_rn(acc[w & 3], e);
+                            a[h] = term_e4m3(e, term_cut, term_half);
+                        }
+                        pk[w] = __byte_perm(a[0], a[1], 0x7531);
+                    }
+                    uint32_t p8[8];
+#pragma unroll
+                    for (int w = 0; w < 8; ++w)
+                        p8[w] = pk[w];
+                    tmem_st8(s_tmem + (uint32_t)(q * 8), p8);
+                } else if constexpr (FP8) {  // eight columns of the leading terms, eight of the others
 #pragma unroll
                     for (int w = 0; w < 8; ++w) {
                         uint32_t a[2], b[2];
@@ -994,7 +1095,8 @@ __device__ void tree_softmax(const TreeParams& p, const TreeCtx& c, int t)
                         pk[w] = pack_bf16x2(e.x, e.y);
                     }
                 }
-                tmem_st16(s_tmem + (uint32_t)(q * 16), pk);
+                if constexpr (!kStack)
+                    tmem_st16(s_tmem + (uint32_t)(q * 16), pk);
                 tmem_wait_ld();
 #pragma unroll
                 for (int k = 0; k < 32; ++k)
@@ -1034,6 +1136,9 @@ __device__ void tree_softmax(const TreeParams& p, const TreeCtx& c, int t)
         if (FP8)
             l *= 256.f;  // 2^kScale
         g0 += (uint32_t)s.tiles;
+        // the next segment's Q, while the last P V runs
+        if (FP8)
+            ok = ok && split_q<C, kTiles>(p, c, n + 1, t);
         if (!ok)
             break;
         // the last P V of the segment (kTiles 1: one O, one wait per segment)
@@ -1081,7 +1186,7 @@ __device__ void tree_softmax(const TreeParams& p, const TreeCtx& c, int t)
             for (int d = d0; d < d1; ++d) {
                 float o = __uint_as_float(tmem_ld1(o_tmem + (uint32_t)d));
                 tmem_wait_ld();
-                if (valid)
+                if (valid && !second)
                     o += tree_bad_column<FP8>(p, p.block_tables + (long long)b * p.bt_stride, view, s.lo_all(p.window),
                                               s.j0 * kKvTile, (s.j0 + s.tiles) * kKvTile, tok, h, s.kvh, p.scale_log2, m, d);
                 __syncwarp();
@@ -1089,12 +1194,39 @@ __device__ void tree_softmax(const TreeParams& p, const TreeCtx& c, int t)
             }
             tmem_wait_st();
         }
-        if (warp_on) {
+        if (warp_on || kStack) {
 #pragma unroll 1
             for (int d = d0; d < d1; d += 32) {
                 uint32_t o[32];
                 tmem_ld32(o_tmem + (uint32_t)d, o);
                 tmem_wait_ld();
+                if constexpr (kStack) {
+                    // the second copy's columns by way of shared memory: four columns of all rows together
+                    float4* add = reinterpret_cast<float4*>(c.base + C::kOffAdd) + t * (64 * 8) + (row & 63);
+                    uint64_t* bar = second ? &c.add_free[t] : &c.add_full[t];
+                    if (!(second && adds == 0) && !wait_bar(bar, (second ? adds - 1 : adds) & 1, c)) {
+                        ok = false;
+                        break;
+                    }
+                    ++adds;
+#pragma unroll
+                    for (int v = 0; v < 8; ++v) {
+                        if (second) {
+                            add[v * 64] = make_float4(__uint_as_float(o[4 * v]), __uint_as_float(o[4 * v + 1]),
+                                                      __uint_as_float(o[4 * v + 2]), __uint_as_float(o[4 * v + 3]));
+                        } else {
+                            const float4 y = add[v * 64];
+                            o[4 * v] = __float_as_uint(__uint_as_float(o[4 * v]) + y.x);
+                            o[4 * v + 1] = __float_as_uint(__uint_as_float(o[4 * v + 1]) + y.y);
+                            o[4 * v + 2] = __float_as_uint(__uint_as_float(o[4 * v + 2]) + y.z);
+                            o[4 * v + 3] = __float_as_uint(__uint_as_float(o[4 * v + 3]) + y.w);
+                        }
+                    }
+                    __syncwarp();
+                    mbar_arrive_p(second ? &c.add_full[t] : &c.add_free[t], lane == 0 ? 1u : 0u);
+                    if (second)
+                        continue;
+                }
                 if (valid && s.whole) {
                     const float2 f = make_float2(out_scale, out_scale);
 #pragma unroll
@@ -1117,9 +1249,11 @@ __device__ void tree_softmax(const TreeParams& p, const TreeCtx& c, int t)
                                                      __uint_as_float(o[4 * v + 2]), __uint_as_float(o[4 * v + 3]));
                 }
             }
-            if (valid && !s.whole && (kTiles == 2 || t == 0))
+            if (valid && !second && !s.whole && (kTiles == 2 || t == 0))
                 p.part_ml[part * kQRows + row] = make_float2(m, l);
         }
+        if (!ok)
+            break;
         tc_fence_before();
         if constexpr (kTiles == 1) {
             __syncwarp();
@@ -1131,10 +1265,10 @@ __device__ void tree_softmax(const TreeParams& p, const TreeCtx& c, int t)
 
 // ---------------------------------------------------------------------------
 
-template <int D, bool FP8, int kTiles>
+template <int D, bool FP8, int kTiles, bool kStack>
 __global__ void __launch_bounds__(kTreeThreads, 1) attention_tree_kernel(const __grid_constant__ TreeParams p)
 {
-    using C = TreeCfg<D, FP8, kTiles>;
+    using C = TreeCfg<D, FP8, kTiles, kStack>;
     extern __shared__ __align__(1024) uint8_t smem[];
     TreeCtx c;
     c.base = smem;
@@ -1156,6 +1290,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1) attention_tree_kernel(const _
     c.it_full = c.drain + 2;
     c.it_empty = c.it_full + kTreeSlots;
     c.never = c.it_empty + kTreeSlots;
+    c.add_full = c.never + 1;  // (kStack)
+    c.add_free = c.add_full + 2;
     uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
     c.abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 4);
     c.err = p.err;
@@ -1171,7 +1307,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) attention_tree_kernel(const _
         for (int b = 0; b < C::kQBufs; ++b) {
             mbar_init(&c.q_full[b], 1);
             mbar_init(&c.q_empty[b], FP8 ? 9 : 1);  // the MMAs that read it; e4m3: and the softmax warps
-            mbar_init(&c.q_conv[b], 1);
+            mbar_init(&c.q_conv[b], 8);
         }
         for (int k = 0; k < C::kSBufs; ++k) {
             mbar_init(&c.s_full[k], 1);
@@ -1181,6 +1317,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1) attention_tree_kernel(const _
         for (int k = 0; k < 2; ++k) {
             mbar_init(&c.o_full[k], 1);
             mbar_init(&c.drain[k], 1);
+            if (kStack) {
+                mbar_init(&c.add_full[k], 2);
+                mbar_init(&c.add_free[k], 2);
+            }
         }
         for (int k = 0; k < 8; ++k)
             mbar_init(&c.m_ready[k], 1);
@@ -1267,16 +1407,16 @@ __global__ void __launch_bounds__(kTreeThreads, 1) attention_tree_kernel(const _
     if (warp < 4) {
         regs_dec<104>();
         if (warp == 0)
-            tree_producer<D, FP8, kTiles>(p, c, start, end, first_b, base);
+            tree_producer<D, FP8, kTiles, kStack>(p, c, start, end, first_b, base);
         else if (warp == 1)
-            tree_s<D, FP8, kTiles>(p, c);
+            tree_s<D, FP8, kTiles, kStack>(p, c);
         else if (warp == 2)
-            tree_pv<D, FP8, kTiles>(p, c);
+            tree_pv<D, FP8, kTiles, kStack>(p, c);
         else
-            tree_feed<D, FP8, kTiles>(p, c);
+            tree_feed<D, FP8, kTiles, kStack>(p, c);
     } else {
         regs_inc<200>();
-        tree_softmax<D, FP8, kTiles>(p, c, (warp - 4) >> 2);
+        tree_softmax<D, FP8, kTiles, kStack>(p, c, (warp - 4) >> 2);
     }
     tc_fence_before();
     __syncthreads();
@@ -1292,7 +1432,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) attention_tree_kernel(const _
 //   out = bmm2 * sum_c w_c O_c / (sum_c w_c l_c + [sinks] 2^(sink log2 e - m)),
 // in the order of the keys.  Block (i, y) takes the unit whose first segment is
 // CTA i's, if there is one that goes on in the next CTA, and of its query tile
-// y / 4 the 32 MMA rows of quadrant y % 4: a lane per row, so that the partial
+// y / 4 the 32 MMA rows of quadrant y % 4 (2 for stacked tiles): a lane per row, so that the partial
 // rows, four columns of all 128 rows together, are read and were written in
 // whole lines.  Each warp takes kCols4 groups of four columns.  Latency alone:
 // loads that do not depend on each other are issued together.
@@ -1304,7 +1444,7 @@ __global__ void __launch_bounds__(D * 2) tree_merge_kernel(const __grid_constant
     constexpr int kCols4 = 4;  // D / 16 warps
     pdl_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int first = blockIdx.x, qt = blockIdx.y >> 2, row = (blockIdx.y & 3) * 32 + lane;
+    const int first = blockIdx.x, qt = (int)blockIdx.y / p.rows.warps, row = (int)blockIdx.y % p.rows.warps * 32 + lane;
     // the segment that opens a unit is the CTA's last; the ones after it are
     // the first of the CTAs that follow, up to the one that reaches the end
     const int4* notes = p.part_seg;
@@ -1413,11 +1553,11 @@ cudaError_t launch_pdl(Kern kern, dim3 grid, unsigned threads, size_t smem, cuda
     return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
-template <int D, bool FP8, int kTiles>
+template <int D, bool FP8, int kTiles, bool kStack>
 cudaError_t launch_tree(const TreeParams& p, cudaStream_t stream)
 {
-    using C = TreeCfg<D, FP8, kTiles>;
-    auto kern = attention_tree_kernel<D, FP8, kTiles>;
+    using C = TreeCfg<D, FP8, kTiles, kStack>;
+    auto kern = attention_tree_kernel<D, FP8, kTiles, kStack>;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess)
@@ -1434,20 +1574,22 @@ cudaError_t launch_tree(const TreeParams& p, cudaStream_t stream)
         return err[dev];
     if ((e = launch_pdl(kern, dim3(p.grid), kTreeThreads, C::kSmemBytes, stream, p)) != cudaSuccess)
         return e;
-    return launch_pdl(tree_merge_kernel<D>, dim3(p.grid, 4 * kTiles), D * 2, 0, stream, p, kTiles);
+    return launch_pdl(tree_merge_kernel<D>, dim3(p.grid, p.rows.warps * kTiles), D * 2, 0, stream, p, kTiles);
 }
 
 }  // namespace
 
-cudaError_t launch_attention_tree(const TreeParams& p, bool fp8, int tiles, cudaStream_t stream)
+cudaError_t launch_attention_tree(const TreeParams& p, bool fp8, int tiles, bool stacked, cudaStream_t stream)
 {
     if (fp8)
-        return p.D != 128 ? cudaErrorInvalidValue
-                          : tiles == 1 ? launch_tree<128, true, 1>(p, stream) : launch_tree<128, true, 2>(p, stream);
+        return p.D != 128  ? cudaErrorInvalidValue
+               : stacked   ? launch_tree<128, true, 1, true>(p, stream)
+               : tiles == 1 ? launch_tree<128, true, 1, false>(p, stream)
+                            : launch_tree<128, true, 2, false>(p, stream);
     if (p.D == 128)
-        return tiles == 1 ? launch_tree<128, false, 1>(p, stream) : launch_tree<128, false, 2>(p, stream);
+        return tiles == 1 ? launch_tree<128, false, 1, false>(p, stream) : launch_tree<128, false, 2, false>(p, stream);
     if (p.D == 64)
-        return tiles == 1 ? launch_tree<64, false, 1>(p, stream) : launch_tree<64, false, 2>(p, stream);
+        return tiles == 1 ? launch_tree<64, false, 1, false>(p, stream) : launch_tree<64, false, 2, false>(p, stream);
     return cudaErrorInvalidValue;
 }
 

@@ -245,7 +245,8 @@ int scaled_kv_impl(bool write, const b2pa_tensor* const rows[2], const char* con
 // workspace holds.
 struct TreePlan {
     bool tc;
-    int tiles;  // query tiles per item
+    int tiles;     // query tiles per item
+    bool stacked;  // e4m3 rows twice in one tile
     size_t off_ml, off_o, bytes;
 };
 
@@ -258,7 +259,9 @@ int plan_tree(const Problem& pr, int max_q_len, const DevInfo& di, TreePlan* out
     TreePlan t{};
     t.tc = path != B2PA_PATH_GENERIC && !why;
     if (t.tc) {
-        t.tiles = max_q_len <= tree_rows(pr.H / pr.Hkv).tile_toks ? 1 : 2;
+        const int G = pr.H / pr.Hkv;
+        t.tiles = max_q_len <= tree_rows(G, false).tile_toks ? 1 : 2;
+        t.stacked = pr.fp8 && G <= 32 && max_q_len <= tree_rows(G, true).tile_toks;
         const size_t rows = (size_t)di.sms * 2 * t.tiles * kQRows;  // two segments of every CTA
         t.off_ml = ((size_t)di.sms * 2 * 2 * sizeof(int4) + 255) / 256 * 256;
         t.off_o = t.off_ml + rows * sizeof(float2);
@@ -321,7 +324,7 @@ int tree_impl(const b2pa_tensor* q, const b2pa_tensor* k_pool, const b2pa_tensor
     std::memset(&p, 0, sizeof p);
     if ((st = status_word(dev, stream, &p.err)))
         return st;
-    p.rows = tree_rows(pr.H / pr.Hkv);
+    p.rows = tree_rows(pr.H / pr.Hkv, plan.stacked);
     p.q = static_cast<const uint16_t*>(pr.q);
     p.k = pr.k;
     p.v = pr.v;
@@ -369,7 +372,7 @@ int tree_impl(const b2pa_tensor* q, const b2pa_tensor* k_pool, const b2pa_tensor
         if ((st = encode_q_map(&p.tm_q, pr, p.rows.box_toks)) || (st = encode_pool_map(&p.tm_k, pr, pr.k, pr.k_st)) ||
             (st = encode_pool_map(&p.tm_v, pr, pr.v, pr.v_st)))
             return st;
-        e = launch_attention_tree(p, pr.fp8, plan.tiles, stream);
+        e = launch_attention_tree(p, pr.fp8, plan.tiles, plan.stacked, stream);
     } else {
         e = launch_tree_generic(p, pr.fp8, stream);
     }

@@ -276,6 +276,13 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16])
         : "r"(taddr));
 }
 
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8])
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]),
+                 "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
+
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16])
 {
     asm volatile(
@@ -371,14 +378,15 @@ __device__ __forceinline__ void mma8_ts_wp(uint32_t d_tmem, uint32_t a_tmem, uin
         : "memory");
 }
 
-__device__ __forceinline__ void mma_commit_p(uint64_t* bar, uint32_t issue)
+__device__ __forceinline__ void mma_commit_at(uint32_t bar, uint32_t issue)
 {
     asm volatile(
         "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
-        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)),
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar),
         "r"(issue)
         : "memory");
 }
+__device__ __forceinline__ void mma_commit_p(uint64_t* bar, uint32_t issue) { mma_commit_at(smem_u32(bar), issue); }
 
 // Instruction descriptor for kind::f16 (PTX ISA: tcgen05 "Instruction descriptor"):
 // bits 4-5 D format (1 = f32), 7-9 A format (1 = bf16), 10-12 B format

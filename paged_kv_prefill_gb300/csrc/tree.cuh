@@ -15,18 +15,21 @@ namespace b2pa {
 // per kv head, each of the four softmax warps gets whole tokens (box_toks at
 // most, in its first box_toks * G lanes), a tile's tokens being split evenly
 // over the warps so that a small tree still uses all four.  With more heads
-// row = token * G + head.
+// row = token * G + head.  Stacked tiles (attn_tree.cu) hold their tokens in two
+// warps, and the same rows again in the other two.
 struct TreeRows {
     int G, box_toks, tile_toks, by_warp;
+    int warps;  // warps that the tokens are split over (by_warp)
 };
 
-__host__ __device__ inline TreeRows tree_rows(int G)
+__host__ __device__ inline TreeRows tree_rows(int G, bool stacked)
 {
     TreeRows r;
     r.G = G;
     r.by_warp = G <= 32;
+    r.warps = stacked ? 2 : 4;
     r.box_toks = r.by_warp ? 32 / G : kQRows / G;
-    r.tile_toks = r.by_warp ? 4 * r.box_toks : r.box_toks;
+    r.tile_toks = r.by_warp ? r.warps * r.box_toks : r.box_toks;
     return r;
 }
 
@@ -144,8 +147,8 @@ __device__ __forceinline__ TreeToken tree_token(const TreeRows& r, int row, int 
 {
     TreeToken t;
     if (r.by_warp) {
-        const int per = (toks + 3) >> 2, lane = row & 31, in = lane / r.G;
-        t.tok = (row >> 5) * per + in;
+        const int per = (toks + r.warps - 1) / r.warps, lane = row & 31, in = lane / r.G;
+        t.tok = (row >> 5) % r.warps * per + in;
         t.head = lane - in * r.G;
         t.valid = in < per && t.tok < toks;
     } else {
@@ -156,8 +159,8 @@ __device__ __forceinline__ TreeToken tree_token(const TreeRows& r, int row, int 
     return t;
 }
 
-// tiles: query tiles per item (1 or 2)
-cudaError_t launch_attention_tree(const TreeParams& p, bool fp8, int tiles, cudaStream_t stream);
+// tiles: query tiles per item (1 or 2); stacked: see tree_rows
+cudaError_t launch_attention_tree(const TreeParams& p, bool fp8, int tiles, bool stacked, cudaStream_t stream);
 cudaError_t launch_tree_generic(const TreeParams& p, bool fp8, cudaStream_t stream);
 
 }  // namespace b2pa
