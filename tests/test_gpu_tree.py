@@ -204,6 +204,16 @@ def test_against_the_formula(cuda_lib, name):
     t.check(out)
 
 
+@pytest.mark.parametrize("G,n", [(1, 1), (1, 64), (1, 65), (1, 128), (1, 129), (3, 20), (3, 21), (3, 41), (4, 1), (4, 2), (4, 16),
+                                 (4, 17), (5, 12), (5, 13), (31, 2), (31, 3), (32, 1), (32, 2), (32, 3), (32, 5), (33, 1),
+                                 (33, 4), (64, 2), (100, 1)])
+def test_e4m3_tiles_at_their_edges(cuda_lib, G, n):
+    """Row counts around those at which a tile holds its rows twice, once, and in two tiles."""
+    t = Batch([n, max(1, n - 1), 1], [1500, 130, 700], 2 * G, 2, 128, 16, cache="e4m3", sinks=G % 2 == 0, seed=G + n)
+    t.check(cuda_lib.tree_attention(**t.dev()))
+    assert cuda_lib.device_status() == 0
+
+
 @pytest.mark.parametrize("name", ["ragged", "window", "two_tiles", "e4m3"])
 def test_generic_path_and_padding_rows(cuda_lib, name):
     """The CUDA-core path on tensor-core shapes; rows behind the last request stay as they were."""
