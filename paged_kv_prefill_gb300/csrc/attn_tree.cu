@@ -121,6 +121,7 @@ struct TreeCtx : Ctx {
     // kTiles 1: a warp's rows' maxima up to an even / odd tile posted ([2][4]);
     // both groups posted (m, l); both have read O
     uint64_t *m_ready, *met, *left;
+    uint64_t* turn;                          // kTiles 2, [2]: this tile's MMAs next (m_ready's place)
     uint64_t *add_full, *add_free;           // kStack, [2]: 32 columns of O's second copy posted, added
     uint64_t *drain /* [2] */, *it_full, *it_empty, *never;
 };
@@ -137,6 +138,9 @@ struct Seg {
     {
         return j * kKvTile + kKvTile > ctx() || j * kKvTile < lo_all(window);
     }
+    // the same of the segment's i-th: i < mixed0 or i >= mixed1
+    __device__ __forceinline__ int mixed0(int window) const { return (lo_all(window) + kKvTile - 1) / kKvTile - j0; }
+    __device__ __forceinline__ int mixed1() const { return ctx() / kKvTile - j0; }
 };
 
 __device__ __forceinline__ void post_seg(volatile int* rec, const Seg& s)
@@ -335,19 +339,87 @@ struct RingPos {
     }
 };
 
+// The MMAs of one query tile and kv tile.
 template <int D, bool FP8, int kTiles, bool kStack>
+struct TreeMma {
+    using C = TreeCfg<D, FP8, kTiles, kStack>;
+    static constexpr uint32_t kIdescS = tree_idesc(FP8, kKvTile, false), kIdescO = tree_idesc(FP8, D, true);
+    static constexpr uint32_t kEntryW = C::kKvBytes >> 4, kQTileW = C::kQBytes >> 4, kBlockW = C::kBlockBytes >> 4;
+    // A step of P V is 8 columns of P: 16 keys (16 rows of V), or 32 of one e4m3
+    // term (both, stacked); kSteps of them are a tile.  Of a request's last tile
+    // the steps behind the last key are left out.
+    static constexpr int kStepsAtKeys = FP8 && !kStack ? 2 : 1, kKeys = FP8 ? 32 : 16;
+    static constexpr int kSteps = kKvTile / kKeys * kStepsAtKeys;
+    uint32_t tmem, q_lo, k_lo, v_lo, issue;
+    __device__ __forceinline__ explicit TreeMma(const TreeCtx& c)
+        : tmem(c.tmem),
+          q_lo(sdesc_lo(smem_u32(c.base), 16)),                           // K-major: LBO unused
+          k_lo(sdesc_lo(smem_u32(c.base + C::kOffRing), 16)),
+          v_lo(sdesc_lo(smem_u32(c.base + C::kOffRing), C::kBlockBytes)),  // MN-major: LBO = next column block
+          issue((threadIdx.x & 31) == 0 ? 1u : 0u)
+    {
+    }
+    // S (buffer s) = Q tile q (of all buffers') times K (ring entry e)
+    __device__ __forceinline__ void scores(uint32_t s, uint32_t q, uint32_t e) const
+    {
+        const uint32_t a0 = q_lo + q * kQTileW, b0 = k_lo + e * kEntryW, d = tmem + s * kKvTile;
+        // a step is 32 bytes of a row: 32 e4m3 elements or 16 of 16 bits; four
+        // steps are a column block (e4m3: of Q's first, then second term)
+#pragma unroll
+        for (int k = 0; k < (FP8 ? 8 : D / 16); ++k) {
+            const uint32_t step = (uint32_t)((k & 3) * 2), block = (uint32_t)(k >> 2) * kBlockW;
+            if constexpr (FP8)
+                mma8_ss_wp(d, a0 + block + step, b0 + step, kTreeDescHi, kIdescS, k > 0 ? 1u : 0u, issue);
+            else
+                mma_ss_wp(d, a0 + block + step, b0 + block + step, kTreeDescHi, kIdescS, k > 0 ? 1u : 0u, issue);
+        }
+    }
+    // O (tile t) += P (buffer s) times V (ring entry e), of which `keys` are the request's
+    __device__ __forceinline__ void values(uint32_t t, uint32_t s, uint32_t e, int keys, bool first) const
+    {
+        const uint32_t b0 = v_lo + e * kEntryW, a = tmem + s * kKvTile, d = tmem + (uint32_t)C::kOCol + t * D;
+        auto step = [&](int k, uint32_t acc) {
+            const uint32_t ak = a + (uint32_t)(k * 8), bk = b0 + (uint32_t)(k / kStepsAtKeys * kKeys * 8);
+            if constexpr (FP8)
+                mma8_ts_wp(d, ak, bk, kTreeDescHi, kIdescO, acc, issue);
+            else
+                mma_ts_wp(d, ak, bk, kTreeDescHi, kIdescO, acc, issue);
+        };
+        step(0, first ? 0u : 1u);
+        if (keys >= kKvTile) {
+#pragma unroll
+            for (int k = 1; k < kSteps; ++k)
+                step(k, 1u);
+        } else {
+            const int steps = (keys + kKeys - 1) / kKeys * kStepsAtKeys;
+#pragma unroll 1
+            for (int k = 1; k < steps; ++k)
+                step(k, 1u);
+        }
+    }
+};
+
+// V of tile i of a segment there, and made safe where not every row sees its keys.
+template <typename Ring>
+__device__ __forceinline__ bool wait_v(const TreeCtx& c, const Ring& at, bool mixed, uint32_t& ready_bits)
+{
+    bool ok = wait_at(smem_u32(c.kv_full) + at.e * 8, at.phase, c);
+    if (ok && mixed) {
+        ok = wait_at(smem_u32(c.v_ready) + at.e * 8, ready_bits >> at.e & 1u, c);
+        ready_bits ^= 1u << at.e;
+    }
+    return ok;
+}
+
+// kTiles 1, warp 1: S of every kv tile, three buffers in turn.
+template <int D, bool FP8, bool kStack>
 __device__ void tree_s(const TreeParams& p, const TreeCtx& c)
 {
-    using C = TreeCfg<D, FP8, kTiles, kStack>;
-    constexpr uint32_t kIdesc = tree_idesc(FP8, kKvTile, false);
-    const uint32_t issue = (threadIdx.x & 31) == 0 ? 1u : 0u;
-    const uint32_t q_lo = sdesc_lo(smem_u32(c.base), 16);                    // K-major: LBO unused
-    const uint32_t k_lo = sdesc_lo(smem_u32(c.base + C::kOffRing), 16);
-    constexpr uint32_t kEntryW = C::kKvBytes >> 4, kQTileW = C::kQBytes >> 4, kBlockW = C::kBlockBytes >> 4;
-    const uint32_t kv_full = smem_u32(c.kv_full), kv_empty = smem_u32(c.kv_empty);
-    const uint32_t s_full = smem_u32(c.s_full), s_free = smem_u32(c.s_free);
+    using C = TreeCfg<D, FP8, 1, kStack>;
+    const TreeMma<D, FP8, 1, kStack> mma(c);
+    const uint32_t kv_full = smem_u32(c.kv_full), s_full = smem_u32(c.s_full), s_free = smem_u32(c.s_free);
     RingPos<C::kEntries> at(0);
-    uint32_t buf = 0, turn[2] = {0, 0};  // kTiles 1: the next S buffer; the buffers' (kTiles 2: each one's) turn
+    uint32_t buf = 0, turn = 0;
     bool ok = !p.inject_stall || wait_bar(c.never, 0, c);  // failure-detection tests
     for (uint32_t n = 0; ok; ++n) {
         Seg s;
@@ -356,130 +428,143 @@ __device__ void tree_s(const TreeParams& p, const TreeCtx& c)
         const uint32_t qb = n % C::kQBufs;
         if (!wait_bar(FP8 ? &c.q_conv[qb] : &c.q_full[qb], (n / C::kQBufs) & 1, c))
             break;
-        const bool two = kTiles == 2 && s.toks > p.rows.tile_toks;
-        for (int i = s.tiles; ok && i > 0; --i) {
-            ok = wait_at(kv_full + at.e * 8, at.phase, c);
-#pragma unroll
-            for (int t = 0; t < kTiles; ++t) {
-                if (t == 1 && !two)
-                    break;
-                const uint32_t to = kTiles == 1 ? buf : (uint32_t)t;
-                ok = ok && wait_at(s_free + to * 8, turn[t] ^ 1, c);  // the buffer's last P has been used
-                if (!ok)
-                    break;
-                tc_fence_after();
-                const uint32_t a0 = q_lo + (qb * kTiles + t) * kQTileW, b0 = k_lo + at.e * kEntryW;
-                const uint32_t d = c.tmem + to * kKvTile;
-                // a step is 32 bytes of a row: 32 e4m3 elements or 16 of 16 bits; four
-                // steps are a column block (e4m3: of Q's first, then second term)
-#pragma unroll
-                for (int k = 0; k < (FP8 ? 8 : D / 16); ++k) {
-                    const uint32_t step = (uint32_t)((k & 3) * 2), block = (uint32_t)(k >> 2) * kBlockW;
-                    if constexpr (FP8)
-                        mma8_ss_wp(d, a0 + block + step, b0 + step, kTreeDescHi, kIdesc, k > 0 ? 1u : 0u, issue);
-                    else
-                        mma_ss_wp(d, a0 + block + step, b0 + block + step, kTreeDescHi, kIdesc, k > 0 ? 1u : 0u, issue);
-                }
-                mma_commit_at(s_full + to * 8, issue);
-                if (kTiles == 2)
-                    turn[t] ^= 1;
-            }
+        for (int i = s.tiles; i > 0; --i) {
+            // K, and the buffer's last P used
+            ok = wait_at(kv_full + at.e * 8, at.phase, c) && wait_at(s_free + buf * 8, turn ^ 1, c);
             if (!ok)
                 break;
-            mma_commit_at(kv_empty + at.e * 8, issue);
+            tc_fence_after();
+            mma.scores(buf, qb, at.e);
+            mma_commit_at(s_full + buf * 8, mma.issue);  // (the softmax group releases K)
             at.next();
-            if (kTiles == 1 && ++buf == 3) {
+            if (++buf == 3) {
                 buf = 0;
-                turn[0] ^= 1;
+                turn ^= 1;
             }
         }
         if (ok)
-            mma_commit_p(&c.q_empty[qb], issue);
+            mma_commit_p(&c.q_empty[qb], mma.issue);
     }
     // every MMA this thread issued has completed once the drain barrier flips
-    if (issue)
+    if (mma.issue)
         mma_commit(&c.drain[0]);
     __syncwarp();
     drain_wait(&c.drain[0], 0);
 }
 
-template <int D, bool FP8, int kTiles, bool kStack>
+// kTiles 1, warp 2: O += P V.
+template <int D, bool FP8, bool kStack>
 __device__ void tree_pv(const TreeParams& p, const TreeCtx& c)
 {
-    using C = TreeCfg<D, FP8, kTiles, kStack>;
-    constexpr uint32_t kIdesc = tree_idesc(FP8, D, true);
-    const uint32_t issue = (threadIdx.x & 31) == 0 ? 1u : 0u;
-    const uint32_t v_lo = sdesc_lo(smem_u32(c.base + C::kOffRing), C::kBlockBytes);  // MN-major: LBO = next column block
-    constexpr uint32_t kEntryW = C::kKvBytes >> 4;
-    // A step is 8 columns of P: 16 keys (16 rows of V), or 32 of one e4m3 term
-    // (both, stacked); kSteps of them are a tile.  Of a request's last tile the
-    // steps behind the last key are left out.
-    constexpr int kStepsAtKeys = FP8 && !kStack ? 2 : 1, kKeys = FP8 ? 32 : 16, kSteps = kKvTile / kKeys * kStepsAtKeys;
-    const uint32_t kv_full = smem_u32(c.kv_full), kv_empty = smem_u32(c.kv_empty), v_ready = smem_u32(c.v_ready);
-    const uint32_t p_full = smem_u32(c.p_full), s_free = smem_u32(c.s_free);
+    using C = TreeCfg<D, FP8, 1, kStack>;
+    const TreeMma<D, FP8, 1, kStack> mma(c);
+    const uint32_t kv_empty = smem_u32(c.kv_empty), p_full = smem_u32(c.p_full), s_free = smem_u32(c.s_free);
     RingPos<C::kEntries> at(1);
-    uint32_t buf = 0, turn[2] = {0, 0};  // as in tree_s
+    uint32_t buf = 0, turn = 0;
     uint32_t ready_bits = 0;  // parity of each entry's next v_ready phase
     bool ok = true;
     for (uint32_t n = 0; ok; ++n) {
         Seg s;
         if (!take_seg(c, n, &s) || !s.on)
             break;
-        const bool two = kTiles == 2 && s.toks > p.rows.tile_toks;
-        // tiles [0, mixed0) and [mixed1, ...) have keys that not every row sees
-        const int mixed0 = (s.lo_all(p.window) + kKvTile - 1) / kKvTile - s.j0, mixed1 = s.ctx() / kKvTile - s.j0;
-        for (int i = 0; ok && i < s.tiles; ++i) {
-            ok = wait_at(kv_full + at.e * 8, at.phase, c);
-            if (ok && (i < mixed0 || i >= mixed1)) {  // V, made safe
-                ok = wait_at(v_ready + at.e * 8, ready_bits >> at.e & 1u, c);
-                ready_bits ^= 1u << at.e;
-            }
-#pragma unroll
-            for (int t = 0; t < kTiles; ++t) {
-                if (t == 1 && !two)
-                    break;
-                const uint32_t from = kTiles == 1 ? buf : (uint32_t)t;
-                ok = ok && wait_at(p_full + from * 8, turn[t], c);
-                if (!ok)
-                    break;
-                tc_fence_after();
-                const uint32_t b0 = v_lo + at.e * kEntryW, a = c.tmem + from * kKvTile;
-                const uint32_t d = c.tmem + (uint32_t)(C::kOCol + (kTiles == 1 ? 0 : t * D));
-                const int keys = s.kv_len - (s.j0 + i) * kKvTile;
-                const int steps = keys >= kKvTile ? kSteps : (keys + kKeys - 1) / kKeys * kStepsAtKeys;
-                uint32_t acc = i > 0 ? 1u : 0u;
-#pragma unroll 1
-                for (int k = 0; k < steps; k += kStepsAtKeys) {
-#pragma unroll
-                    for (int h = 0; h < kStepsAtKeys; ++h) {
-                        const uint32_t ak = a + (uint32_t)((k + h) * 8), bk = b0 + (uint32_t)(k / kStepsAtKeys * kKeys * 8);
-                        if constexpr (FP8)
-                            mma8_ts_wp(d, ak, bk, kTreeDescHi, kIdesc, acc, issue);
-                        else
-                            mma_ts_wp(d, ak, bk, kTreeDescHi, kIdesc, acc, issue);
-                        acc = 1;
-                    }
-                }
-                mma_commit_at(s_free + from * 8, issue);
-                if (i == s.tiles - 1)
-                    mma_commit_p(&c.o_full[kTiles == 1 ? 0 : t], issue);
-                if (kTiles == 2)
-                    turn[t] ^= 1;
-            }
+        const int mixed0 = s.mixed0(p.window), mixed1 = s.mixed1();
+        for (int i = 0; i < s.tiles; ++i) {
+            ok = wait_v(c, at, i < mixed0 || i >= mixed1, ready_bits) && wait_at(p_full + buf * 8, turn, c);
             if (!ok)
                 break;
-            mma_commit_at(kv_empty + at.e * 8, issue);
+            tc_fence_after();
+            mma.values(0, buf, at.e, s.kv_len - (s.j0 + i) * kKvTile, i == 0);
+            mma_commit_at(s_free + buf * 8, mma.issue);
+            mma_commit_at(kv_empty + at.e * 8, mma.issue);
             at.next();
-            if (kTiles == 1 && ++buf == 3) {
+            if (++buf == 3) {
                 buf = 0;
-                turn[0] ^= 1;
+                turn ^= 1;
             }
         }
+        if (ok)
+            mma_commit_p(&c.o_full[0], mma.issue);
     }
-    if (issue)
+    if (mma.issue)
         mma_commit(&c.drain[1]);
     __syncwarp();
     drain_wait(&c.drain[1], 0);
+}
+
+// kTiles 2, warps 1 and 2: all MMAs of a query tile each.  P V of a kv tile and
+// right behind it S of the next one into the same buffer, which is in order for
+// it is one thread's, with no wait between them.  The two warps take turns, so
+// that one tile's MMAs run, undivided, during the other's softmax; left alone
+// they fall into step, and tensor core and softmax wait for one another (wide
+// trees of 512 rows: xx us in turns, 127 without, 119 with all S from one warp
+// and all P V from the other).
+template <int D, bool FP8>
+__device__ void tree_tile(const TreeParams& p, const TreeCtx& c, int t)
+{
+    using C = TreeCfg<D, FP8, 2, false>;
+    const TreeMma<D, FP8, 2, false> mma(c);
+    const uint32_t kv_full = smem_u32(c.kv_full), kv_empty = smem_u32(c.kv_empty);
+    const uint32_t p_full = smem_u32(c.p_full) + t * 8, s_full = smem_u32(c.s_full) + t * 8;
+    const uint32_t my_turn = smem_u32(c.turn) + t * 8, your_turn = smem_u32(c.turn) + (t ^ 1) * 8;
+    RingPos<C::kEntries> at_k(0), at_v(1);
+    uint32_t p_phase = 0, turn_phase = t ^ 1;  // (tile 0 goes first)
+    uint32_t ready_bits = 0;  // parity of each entry's next v_ready phase
+    bool ok = t != 0 || !p.inject_stall || wait_bar(c.never, 0, c);  // failure-detection tests
+    for (uint32_t n = 0; ok; ++n) {
+        Seg s;
+        if (!take_seg(c, n, &s) || !s.on)
+            break;
+        const uint32_t qb = n % C::kQBufs;
+        // (a segment of one query tile: the other's warp only passes the ring on)
+        const bool two = s.toks > p.rows.tile_toks, mine = two || t == 0;
+        const int mixed0 = s.mixed0(p.window), mixed1 = s.mixed1();
+        ok = wait_bar(FP8 ? &c.q_conv[qb] : &c.q_full[qb], (n / C::kQBufs) & 1, c);
+        for (int i = -1; i < s.tiles; ++i) {  // P V of tile i, S of tile i + 1
+            const bool pv = i >= 0, sc = i + 1 < s.tiles;
+            if (pv) {
+                ok = ok && wait_v(c, at_v, i < mixed0 || i >= mixed1, ready_bits);
+                if (mine) {
+                    ok = ok && wait_at(p_full, p_phase, c);
+                    p_phase ^= 1;
+                }
+            }
+            if (sc)
+                ok = ok && wait_at(kv_full + at_k.e * 8, at_k.phase, c);
+            if (two) {
+                ok = ok && wait_at(my_turn, turn_phase, c);
+                turn_phase ^= 1;
+            }
+            if (!ok)
+                break;
+            tc_fence_after();
+            if (mine && pv)
+                mma.values(t, t, at_v.e, s.kv_len - (s.j0 + i) * kKvTile, i == 0);
+            if (mine && sc)
+                mma.scores(t, qb * 2 + t, at_k.e);
+            // before the commit, which waits for room among the MMAs
+            mbar_arrive_at(your_turn, two ? mma.issue : 0u);
+            if (mine && sc)
+                mma_commit_at(s_full, mma.issue);
+            // K and V are released by the softmax group, which hears of it all the same
+            if (pv) {
+                mbar_arrive_at(kv_empty + at_v.e * 8, mine ? 0u : mma.issue);
+                at_v.next();
+            }
+            if (sc) {
+                mbar_arrive_at(kv_empty + at_k.e * 8, mine ? 0u : mma.issue);
+                at_k.next();
+            }
+        }
+        if (ok) {
+            if (mine)
+                mma_commit_p(&c.o_full[t], mma.issue);
+            mma_commit_p(&c.q_empty[qb], mma.issue);
+        }
+    }
+    if (mma.issue)
+        mma_commit(&c.drain[t]);
+    __syncwarp();
+    drain_wait(&c.drain[t], 0);
 }
 
 // ---------------------------------------------------------------------------
@@ -988,6 +1073,12 @@ __device__ void tree_softmax(const TreeParams& p, const TreeCtx& c, int t)
                 break;
             }
             ++s_cnt;
+            if (wq == 0) {  // K has been read; kTiles 2: and V of the tile before
+                const uint32_t lane0 = lane == 0 ? 1u : 0u;
+                mbar_arrive_p(&c.kv_empty[2 * g % C::kEntries], lane0);
+                if (kTiles == 2 && i > 0)
+                    mbar_arrive_p(&c.kv_empty[(2 * g - 1) % C::kEntries], lane0);
+            }
             if (!warp_on) {  // no row of this warp is anyone's
                 if (kTiles == 1)
                     mbar_arrive_p(&c.m_ready[(g & 1) * 4 + wq], lane == 0 ? 1u : 0u);
@@ -1147,6 +1238,8 @@ __device__ void tree_softmax(const TreeParams& p, const TreeCtx& c, int t)
             break;
         }
         ++o_cnt;
+        if (kTiles == 2 && wq == 0)
+            mbar_arrive_p(&c.kv_empty[(2 * g0 - 1) % C::kEntries], lane == 0 ? 1u : 0u);  // (g0: the next segment's)
         if constexpr (kTiles == 1) {
             // both groups' sums, relative to the last tile's maximum (the larger one)
             ml[t * kQRows + row] = make_float2(m_used, l);
@@ -1284,6 +1377,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) attention_tree_kernel(const _
     c.s_free = c.p_full + C::kSBufs;
     c.o_full = c.s_free + C::kSBufs;
     c.m_ready = c.o_full + 2;
+    c.turn = c.m_ready;
     c.met = c.m_ready + 8;
     c.left = c.met + 1;
     c.drain = c.left + 1;
@@ -1301,12 +1395,12 @@ __global__ void __launch_bounds__(kTreeThreads, 1) attention_tree_kernel(const _
     if (tid == 0) {
         for (int e = 0; e < C::kEntries; ++e) {
             mbar_init(&c.kv_full[e], 1);
-            mbar_init(&c.kv_empty[e], 2);  // the MMAs that read it, and warp 3
+            mbar_init(&c.kv_empty[e], 1 + kTiles);  // its MMAs (kTiles 2: two tiles'), and warp 3
             mbar_init(&c.v_ready[e], 1);
         }
         for (int b = 0; b < C::kQBufs; ++b) {
             mbar_init(&c.q_full[b], 1);
-            mbar_init(&c.q_empty[b], FP8 ? 9 : 1);  // the MMAs that read it; e4m3: and the softmax warps
+            mbar_init(&c.q_empty[b], (FP8 ? 8 : 0) + kTiles);  // the MMAs that read it; e4m3: and the softmax warps
             mbar_init(&c.q_conv[b], 8);
         }
         for (int k = 0; k < C::kSBufs; ++k) {
@@ -1408,12 +1502,14 @@ __global__ void __launch_bounds__(kTreeThreads, 1) attention_tree_kernel(const _
         regs_dec<104>();
         if (warp == 0)
             tree_producer<D, FP8, kTiles, kStack>(p, c, start, end, first_b, base);
-        else if (warp == 1)
-            tree_s<D, FP8, kTiles, kStack>(p, c);
-        else if (warp == 2)
-            tree_pv<D, FP8, kTiles, kStack>(p, c);
-        else
+        else if (warp == 3)
             tree_feed<D, FP8, kTiles, kStack>(p, c);
+        else if constexpr (kTiles == 2)
+            tree_tile<D, FP8>(p, c, warp - 1);
+        else if (warp == 1)
+            tree_s<D, FP8, kStack>(p, c);
+        else
+            tree_pv<D, FP8, kStack>(p, c);
     } else {
         regs_inc<200>();
         tree_softmax<D, FP8, kTiles, kStack>(p, c, (warp - 4) >> 2);

@@ -35,13 +35,14 @@ __device__ __forceinline__ void mbar_arrive(uint64_t* bar)
 }
 
 // mbar_arrive executed by a whole warp, arriving only from lanes with issue != 0.
-__device__ __forceinline__ void mbar_arrive_p(uint64_t* bar, uint32_t issue)
+__device__ __forceinline__ void mbar_arrive_at(uint32_t bar, uint32_t issue)
 {
     asm volatile("{\n\t.reg .b64 st;\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
-                 "@q mbarrier.arrive.shared::cta.b64 st, [%0];\n\t}" ::"r"(smem_u32(bar)),
+                 "@q mbarrier.arrive.shared::cta.b64 st, [%0];\n\t}" ::"r"(bar),
                  "r"(issue)
                  : "memory");
 }
+__device__ __forceinline__ void mbar_arrive_p(uint64_t* bar, uint32_t issue) { mbar_arrive_at(smem_u32(bar), issue); }
 
 __device__ __forceinline__ void mbar_arrive_expect_tx(uint64_t* bar, uint32_t bytes)
 {
