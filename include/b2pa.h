@@ -22,9 +22,11 @@
  * 内部", section "句柄到偏移的物理含义": the table holds page ids and the
  * kernel adds id x page stride to the pool base).
  *
- * The library also does the step that precedes the attention in a serving
- * engine: writing the new tokens' K and V into the pools (b2pa_append_kv,
- * quantising to e4m3 for an FP8 cache).
+ * The library also does the steps around the attention in a serving engine:
+ * the heads' norms and rotary rotation (b2pa_qk_norm_rope), writing the new
+ * tokens' K and V into the pools (b2pa_append_kv, quantising to e4m3 for an FP8
+ * cache; b2pa_append_kv_scaled with a scale per row, b2pa_read_kv_scaled back),
+ * and the attention that verifies trees of drafted tokens (b2pa_tree_attention).
  *
  * Conventions for every entry point:
  *  - All tensors are described by b2pa_tensor: a pointer, a dtype, a rank,
@@ -442,8 +444,9 @@ B2PA_API int b2pa_append_kv_scaled(const b2pa_tensor* k_new, const b2pa_tensor* 
  * b2pa_read_kv_scaled -- read rows of such a cache back as bf16: row n of k_out
  * and v_out is code * scale of slot cache_loc[n] (any order, repeats allowed),
  * the binary32 product rounded to bf16 (exact for rows that
- * b2pa_append_kv_scaled wrote, down to bf16's smallest values).  For code that needs 16-bit K and V of a cached
- * prefix: k_out and v_out may be views of bf16 pools that the attention reads.
+ * b2pa_append_kv_scaled wrote, down to bf16's smallest values).  For code that
+ * needs 16-bit K and V of a cached prefix: k_out and v_out may be views of bf16
+ * pools that the attention reads.
  * A slot outside the pool reads as zeros and sets B2PA_DEV_BAD_SLOT.  The
  * outputs' rows must not overlap.  Otherwise as b2pa_append_kv_scaled.
  */
@@ -472,11 +475,12 @@ B2PA_API int b2pa_read_kv_scaled(const b2pa_tensor* k_pool, const b2pa_tensor* v
  * batch; a chain is a tree with a triangular mask.
  *
  * q, pools, block_tables, seq_lens, cum_q, scales, sinks, layout and out as for
- * b2pa_context_attention (out's rows must not overlap), and:
+ * b2pa_context_attention (out must not overlap any input, nor its rows one
+ * another), and:
  *  tree_mask     [T, words] int32, stride[1] == 1, words >= ceil(max_q_len / 32).
  *  positions     contiguous int32 [T]; NULL without a window.
  *  max_q_len     upper bound on every n: sizes the query tiles.
- *  max_kv_len    upper bound on every seq_lens[b].
+ *  max_kv_len    upper bound on every seq_lens[b]; at most 2^31 - 257.
  *  workspace     device memory of this call, 256-byte aligned, in use until the
  *                call's kernels are done: calls that may overlap need their own.
  *                It is written before it is read and keeps nothing.

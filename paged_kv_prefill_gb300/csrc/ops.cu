@@ -294,6 +294,8 @@ int tree_impl(const b2pa_tensor* q, const b2pa_tensor* k_pool, const b2pa_tensor
         return st;
     if (max_q_len < 0 || max_kv_len < 0)
         return fail(B2PA_ERR_INVALID_ARG, "max_q_len / max_kv_len must be >= 0");
+    if (max_kv_len > 0x7FFFFFFF - 2 * kKvTile)  // (a tile behind the last key is an int still)
+        return fail(B2PA_ERR_UNSUPPORTED, "max_kv_len must be at most 2^31 - 257");
     if (!std::isfinite(bmm1_scale) || !(bmm1_scale > 0.f) || !std::isfinite(bmm2_scale))
         return fail(B2PA_ERR_INVALID_ARG, "bmm1_scale must be finite and > 0, bmm2_scale finite");
     const int64_t words = ((int64_t)max_q_len + 31) / 32;
@@ -307,6 +309,8 @@ int tree_impl(const b2pa_tensor* q, const b2pa_tensor* k_pool, const b2pa_tensor
         return fail(B2PA_ERR_INVALID_ARG, "a window needs positions, contiguous int32 [T]");
     if (pr.T > 0 && ((pr.T > 1 && pr.out_st_tok < pr.D) || (pr.H > 1 && pr.out_st_head < pr.D)))
         return fail(B2PA_ERR_INVALID_ARG, "out: its rows overlap");
+    if (pr.T > 0 && pr.out == pr.q)
+        return fail(B2PA_ERR_INVALID_ARG, "out must not be q: rows are read by several blocks");
     *bytes_needed = 0;
     if (pr.B == 0 || pr.T == 0)
         return B2PA_OK;

@@ -202,6 +202,15 @@ def test_tree(lib, change, status):
     assert lib.b2pa_last_error_message()
 
 
+def test_tree_in_place_and_too_long(lib):
+    q = fake([9, 4, 128], BF, base=1 << 20)
+    out = fake([9, 4, 128], BF, base=2 << 20)
+    assert tree(lib, q=q, out=fake([9, 4, 128], BF, base=1 << 20)) == INVALID
+    assert b"out must not be q" in lib.b2pa_last_error_message()
+    assert tree(lib, q=q, out=out, max_kv=2**31 - 256) == UNSUPPORTED
+    assert b"max_kv_len" in lib.b2pa_last_error_message()
+
+
 def test_tree_of_nothing(lib):
     none = dict(q=fake([0, 4, 128], BF, base=0), out=fake([0, 4, 128], BF, base=0), mask=fake([0, 2], I32, base=0))
     assert tree(lib, **none) == OK
