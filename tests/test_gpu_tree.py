@@ -267,8 +267,9 @@ def test_a_chain_is_the_decode_batch(cuda_lib):
 
 
 @pytest.mark.parametrize("cfg", [dict(H=8, Hkv=2, D=128, P=16), dict(H=32, Hkv=8, D=64, P=8, window=50),
-                                 dict(H=16, Hkv=2, D=128, P=32, cache="e4m3"), dict(H=2, Hkv=1, D=48, P=8, window=50)],
-                         ids=["bf16", "d64_window", "e4m3", "generic"])
+                                 dict(H=16, Hkv=2, D=128, P=32, cache="e4m3"), dict(H=2, Hkv=1, D=48, P=8, window=50),
+                                 dict(H=4, Hkv=2, D=128, P=32, cache="e4m3", window=50)],
+                         ids=["bf16", "d64_window", "e4m3", "generic", "e4m3_rows_twice"])
 @pytest.mark.parametrize("sinks", [False, True])
 def test_rows_that_see_nothing(cuda_lib, cfg, sinks):
     t = Batch([12, 20], [12, 400], sinks=sinks, **cfg)
@@ -283,8 +284,11 @@ def test_rows_that_see_nothing(cuda_lib, cfg, sinks):
 
 @pytest.mark.parametrize("cfg", [dict(H=8, Hkv=2, D=128, P=16), dict(H=8, Hkv=2, D=64, P=16, window=40),
                                  dict(H=8, Hkv=2, D=128, P=16, cache="e4m3"), dict(H=16, Hkv=1, D=128, P=128),
-                                 dict(H=4, Hkv=2, D=48, P=8, window=40)],
-                         ids=["bf16", "d64_window", "e4m3", "two_tiles", "generic"])
+                                 dict(H=4, Hkv=2, D=48, P=8, window=40), dict(H=4, Hkv=2, D=128, P=16, cache="e4m3"),
+                                 dict(H=4, Hkv=2, D=128, P=16, cache="e4m3", window=40),
+                                 dict(H=16, Hkv=1, D=128, P=128, cache="e4m3")],
+                         ids=["bf16", "d64_window", "e4m3", "two_tiles", "generic", "e4m3_rows_twice",
+                              "e4m3_rows_twice_window", "e4m3_two_tiles"])
 @pytest.mark.parametrize("kv", [40, 260])
 def test_what_unseen_keys_hold_does_not_matter(cuda_lib, cfg, kv):
     """NaN and infinities in V (and NaN in K) of sibling nodes, of page tails, of pages nobody uses and before a window."""
@@ -440,7 +444,7 @@ def test_streams_and_two_graphs_at_once(cuda_lib):
 
 def test_wait_limit(cuda_lib):
     """A wait that nothing completes runs out: an error bit, and the next call is fine."""
-    for name in ("ragged", "two_tiles", "e4m3"):
+    for name in ("ragged", "two_tiles", "e4m3", "e4m3_two_tiles"):
         t = Batch(**CASES[name])
         d = t.dev()
         ref = cuda_lib.tree_attention(**d)
