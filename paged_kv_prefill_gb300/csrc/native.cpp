@@ -12,6 +12,7 @@
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <exception>
+#include <utility>
 
 #include "../../include/b2pa.h"
 
@@ -114,12 +115,31 @@ public:
     {
         return none(i) ? at::empty(shape, at::TensorOptions().device(device_).dtype(at::kBFloat16)) : tensor(i);
     }
+    // Two of them.  New ones share one allocation, the second behind the first
+    // (16-byte aligned: its rows are multiples of 8 elements): an allocation and
+    // its release cost about as much as the launch of a small kernel.
+    std::pair<at::Tensor, at::Tensor> outputs(int i, at::IntArrayRef a, int j, at::IntArrayRef b)
+    {
+        if (!none(i) || !none(j))
+            return {output(i, a), output(j, b)};
+        const int64_t n = c10::multiply_integers(a), m = c10::multiply_integers(b);
+        const at::Tensor both = at::empty({n + m}, at::TensorOptions().device(device_).dtype(at::kBFloat16));
+        return {part(both, 0, a), part(both, n, b)};
+    }
     at::Tensor bytes(uint64_t n) const
     {
         return at::empty({(int64_t)n}, at::TensorOptions().device(device_).dtype(at::kByte));
     }
 
 private:
+    // a contiguous tensor over `all`'s memory from element `at` on, with a version of its own
+    static at::Tensor part(const at::Tensor& all, int64_t at, at::IntArrayRef shape)
+    {
+        at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(all.storage()), all.key_set(), all.dtype());
+        t.unsafeGetTensorImpl()->set_sizes_contiguous(shape);
+        t.unsafeGetTensorImpl()->set_storage_offset(at);
+        return t;
+    }
     PyObject* const* args_;
     at::Device device_ = at::kCPU;
     int used_ = 0;
@@ -167,7 +187,7 @@ PyObject* qk_norm_rope(PyObject*, PyObject* const* args, Py_ssize_t n)
                 throw Refused{};
             axes = reinterpret_cast<const int32_t*>(bytes);
         }
-        const at::Tensor qo = a.output(10, a.tensor(1).sizes()), ko = a.output(11, a.tensor(2).sizes());
+        const auto [qo, ko] = a.outputs(10, a.tensor(1).sizes(), 11, a.tensor(2).sizes());
         // (the outputs' descriptors are read only)
         return two(b2pa_qk_norm_rope(q, k, cs, pos, qw, kw, a.number(7), axes, a.int32(9),
                                      const_cast<b2pa_tensor*>(a.describe(qo)), const_cast<b2pa_tensor*>(a.describe(ko)),
@@ -201,7 +221,7 @@ PyObject* read_kv_scaled(PyObject*, PyObject* const* args, Py_ssize_t n)
         const bool ok = d[0]->ndim == 4 && d[4]->ndim == 1;
         const int64_t shape[3] = {ok ? d[4]->shape[0] : 0, ok ? d[0]->shape[layout == B2PA_HND ? 1 : 2] : 0,
                                   ok ? d[0]->shape[3] : 0};
-        const at::Tensor ko = a.output(7, shape), vo = a.output(8, shape);
+        const auto [ko, vo] = a.outputs(7, shape, 8, shape);
         return two(b2pa_read_kv_scaled(d[0], d[1], d[2], d[3], d[4], layout, const_cast<b2pa_tensor*>(a.describe(ko)),
                                        const_cast<b2pa_tensor*>(a.describe(vo)), a.stream()),
                    ko, vo);
