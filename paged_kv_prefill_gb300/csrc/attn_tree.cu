@@ -8,7 +8,11 @@
 // What bounds it.  A tree has few rows (nodes x G per kv head) against a long
 // context, so K and V are read once for all of them: up to about 280 rows per
 // kv head the time is that of the K/V stream from HBM, beyond that of the
-// tensor cores and the exponentials.
+// tensor cores and the exponentials.  Measured: 32 requests of 512 to 8192 keys,
+// 9 to 16 nodes x 4 heads, D = 128: 104 us, 5.6 TB/s (0.83 of the copy rate);
+// the same with e4m3, up to 16384 keys and 8 nodes: 145 us, 4.5 TB/s (0.66);
+// 8 requests of up to 16384 keys, 64 nodes x 8 heads: 112 us, 940 TFLOP/s (0.49 of
+// the bf16 rate); one request, 8 nodes, 2048 keys: 14.5 us, latency.
 //
 // Work.  A unit is (request, kv head, up to kTiles query tiles of 128 rows);
 // all units' kv tiles of 128 keys, laid end to end, are cut into equal runs,
@@ -22,16 +26,16 @@
 //   warp 0   producer: walks the run, posts each segment's description to the
 //            other roles, and loads K/V pages (one TMA box per page and
 //            128-byte column block) into a ring of K and V entries.
-//   warp 1   issues S = Q K^T; owns TMEM.
-//   warp 2   issues O += P V.  Two issuers, since what an MMA waits for takes a
-//            few hundred cycles to look at, and one warp that looked at K, P, V
-//            and free buffers in turn left the tensor core idle meanwhile
-//            (e4m3 batch: 3000 cycles per kv tile with one).
+//   warps 1, 2   issue the MMAs; warp 1 owns TMEM.  Two issuers, since what an
+//            MMA waits for takes a few hundred cycles to look at, and one warp
+//            that did all of it left the tensor core idle meanwhile (512 rows per
+//            kv head: 126 us with one).  kTiles 1: S = Q K^T and O += P V.
+//            kTiles 2: a query tile each, in turns.
 //   warp 3   loads Q (a TMA box per softmax warp's tokens and column block), and
 //            makes V safe where rows see different keys (see below).
 //   warps 4-7, 8-11   softmax A and B: one thread per MMA row.  e4m3 caches:
 //            they split the next segment's Q into two e4m3 terms while a segment's
-//            last P V runs (e4m3 batch: 146 us, 164 with warp 3 alone).
+//            last P V runs (e4m3 batch: 146 us, 164 with warp 3 doing it).
 //
 // kTiles 2 (more than one tile of rows in some request): A and B each have
 // their own query tile, and K/V are read once for both.  kTiles 1: there is
@@ -219,8 +223,8 @@ __device__ void tree_producer(const TreeParams& p, const TreeCtx& c, long long p
             }
             const long long unit = (pos - base) / r.unit;
             const long long u0 = base + unit * r.unit;
-            const int off = max(0, (int)(pos - u0) - p.unit_cost);
-            const int to = max(0, (int)min((long long)r.unit, end - u0) - p.unit_cost);
+            const int off = max(0, (int)(pos - u0) - kTreeUnitCost);
+            const int to = max(0, (int)min((long long)r.unit, end - u0) - kTreeUnitCost);
             pos = min(end, u0 + r.unit);
             if (to <= off)
                 continue;  // none of its tiles
@@ -496,7 +500,7 @@ __device__ void tree_pv(const TreeParams& p, const TreeCtx& c)
 // it is one thread's, with no wait between them.  The two warps take turns, so
 // that one tile's MMAs run, undivided, during the other's softmax; left alone
 // they fall into step, and tensor core and softmax wait for one another (wide
-// trees of 512 rows: xx us in turns, 127 without, 119 with all S from one warp
+// trees of 512 rows: 111 us in turns, 127 without, 118 with all S from one warp
 // and all P V from the other).
 template <int D, bool FP8>
 __device__ void tree_tile(const TreeParams& p, const TreeCtx& c, int t)

@@ -60,14 +60,17 @@ struct TreeParams {  // 128-byte aligned through its CUtensorMap members
     TreeRows rows;
     int B, T, H, Hkv, D, page_size, max_pages, num_pages, max_q_len, max_kv_len, mask_words, window;
     int grid;              // CTAs of the attention kernel
-    // What a unit costs beyond its kv tiles, in kv tiles: its Q, the first scores,
-    // the tree's own tile and the rows' way out.
-    int unit_cost;
     float scale_log2;      // bmm1_scale * log2(e)
     float bmm2;
     unsigned long long wait_limit_ns;
     int inject_stall;
 };
+
+// What a unit costs beyond its kv tiles, in kv tiles: its Q, the first scores,
+// the tree's own tile and the rows' way out.  (bf16 batch 114 us with 0, 105
+// with 2, 104.5 with 4, 105 with 6; e4m3 batch 154, 149, 146 and 147; 512 rows per
+// kv head 125, 118, 114.6 and 116.)
+constexpr int kTreeUnitCost = 4;
 
 // A request as the kernels see it.  Its work is items * Hkv units (a unit is
 // a kv head with the nodes of one item) of `tiles` kv tiles each.
@@ -93,7 +96,7 @@ __device__ __forceinline__ TreeReq tree_request(const TreeParams& p, int b, int 
     r.items = any ? (v.q_len + item_toks - 1) / item_toks : 0;
     r.n_lo = any ? r.lo / kKvTile : 0;
     r.tiles = any ? (v.kv_len - 1) / kKvTile - r.n_lo + 1 : 0;
-    r.unit = r.tiles + p.unit_cost;
+    r.unit = r.tiles + kTreeUnitCost;
     return r;
 }
 
@@ -104,7 +107,7 @@ __device__ __forceinline__ int tree_row_lo(int pos, int ctx, int kv_len, int win
 }
 
 // The CTAs cut all requests' units, laid end to end, into equal runs: CTA i of
-// g takes [start(i), start(i + 1)).  Of a unit, the first unit_cost steps are
+// g takes [start(i), start(i + 1)).  Of a unit, the first kTreeUnitCost steps are
 // no tiles: a run that ends there leaves the whole unit to the next.
 struct TreeCut {
     long long total;
