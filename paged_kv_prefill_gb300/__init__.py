@@ -217,13 +217,18 @@ class _On:
         return self.guard.__exit__(*exc)
 
 
+# what torch.cuda.current_device() and current_stream() ask, without their Python around it
+_current_device = getattr(torch._C, "_cuda_getDevice", None)
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _here(first: torch.Tensor, stream) -> int:
     """The current stream's handle if a call can run as things are (its device is current, and it
     names no stream), else -1: the call is made inside _On."""
     if stream is None:
         dev = first.get_device()
-        if dev >= 0 and dev == torch.cuda.current_device():
-            return torch._C._cuda_getCurrentRawStream(dev)  # (current_stream() makes an object first)
+        if dev >= 0 and dev == _current_device():  # (a tensor on a GPU: torch is initialised)
+            return _current_stream(dev)
     return -1
 
 
@@ -507,7 +512,7 @@ def append_kv_scaled(k_new: torch.Tensor, v_new: torch.Tensor, kv_cache, kv_scal
     kv_scales is (k_scales, v_scales), fp32 with the pools' shape without head_dim.  Each row gets
     the smallest power of two that brings its largest value to 448 at most, and its values
     divided by that, rounded to the nearest e4m3 value (see include/b2pa.h)."""
-    call = native().append_kv_scaled
+    call = (_calls or native()).append_kv_scaled
     k, v = split_kv_cache(kv_cache, kv_layout)
     ks, vs = _two(kv_scales, "kv_scales")
     args = (k_new, v_new, k, v, ks, vs, cache_loc, LAYOUTS[kv_layout])
@@ -527,7 +532,7 @@ def read_kv_scaled(kv_cache, kv_scales, cache_loc: torch.Tensor, k_out: Optional
 
     k_out and v_out may be given, as views of bf16 pools for example.  A slot outside the pool
     reads as zeros and is flagged in device_status()."""
-    call = native().read_kv_scaled
+    call = (_calls or native()).read_kv_scaled
     k, v = split_kv_cache(kv_cache, kv_layout)
     ks, vs = _two(kv_scales, "kv_scales")
     args = (k, v, ks, vs, cache_loc, LAYOUTS[kv_layout], k_out, v_out)
@@ -559,7 +564,7 @@ def qk_norm_rope(
     may be query / key themselves.  cos_sin [max_position, R] fp32 holds R / 2 cosines and R / 2
     sines per position.  positions is int32 [T], or [axes, T] with axis_of naming the axis of
     each of the R / 2 frequencies."""
-    call = native().qk_norm_rope
+    call = (_calls or native()).qk_norm_rope
     axes = None
     if axis_of is not None:
         if len(axis_of) != cos_sin.shape[-1] // 2:
@@ -598,7 +603,7 @@ def tree_attention(
     positions - window_left on) and the nodes whose bit is set in its row of tree_mask, int32
     [T, words], bit j % 32 of word j / 32 for node j.  The call's workspace comes from torch's
     allocator."""
-    call = native().tree_attention
+    call = (_calls or native()).tree_attention
     k, v = split_kv_cache(kv_cache, kv_layout)
     if isinstance(sinks, (list, tuple)):
         if len(sinks) != 1:
