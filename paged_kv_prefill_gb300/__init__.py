@@ -530,8 +530,8 @@ def read_kv_scaled(kv_cache, kv_scales, cache_loc: torch.Tensor, k_out: Optional
                    stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
     """K and V rows (bf16 [T, Hkv, D]) of slots cache_loc of a cache that append_kv_scaled wrote.
 
-    k_out and v_out may be given, as views of bf16 pools for example.  A slot outside the pool
-    reads as zeros and is flagged in device_status()."""
+    k_out and v_out may be given, as views of bf16 pools for example; two new ones share one
+    allocation.  A slot outside the pool reads as zeros and is flagged in device_status()."""
     call = (_calls or native()).read_kv_scaled
     k, v = split_kv_cache(kv_cache, kv_layout)
     ks, vs = _two(kv_scales, "kv_scales")
@@ -561,7 +561,7 @@ def qk_norm_rope(
     one pass; returns (q_out, k_out), bf16 (see include/b2pa.h).
 
     query [T, H, D] and key [T, Hkv, D] may be views of one projection's output, and q_out / k_out
-    may be query / key themselves.  cos_sin [max_position, R] fp32 holds R / 2 cosines and R / 2
+    may be query / key themselves; two new ones share one allocation.  cos_sin [max_position, R] fp32 holds R / 2 cosines and R / 2
     sines per position.  positions is int32 [T], or [axes, T] with axis_of naming the axis of
     each of the R / 2 frequencies."""
     call = (_calls or native()).qk_norm_rope
