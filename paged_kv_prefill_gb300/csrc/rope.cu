@@ -19,21 +19,23 @@
 // neighbours otherwise; pairs R/2 apart with another R/2 go through a row of
 // shared memory.
 //
-// Two kernels.  rope_rows_kernel: one row per group, for calls of about one
-// wave, whose time is latency, and for the rare pairing.  rope_staged_kernel,
+// Two kernels.  rope_rows_kernel: one row per group, for calls of one or
+// two waves, whose time is latency, and for the rare pairing.  rope_staged_kernel,
 // for the others: the table row must be read before the rotation and its
 // place is known only from the positions, and a group that does this for a few
-// rows at a time keeps too few loads in flight.  So groups loop over sets of
-// kSetRows heads of a token, and each thread copies its own pieces of the rows
-// and of the table into its own places of a ring in shared memory with
-// cp.async, kStages - 1 sets ahead; no thread reads another's pieces, so the
-// ring needs no barrier.  The table goes through L1: read by every set from
-// L2 it was the bound.  11750 tokens x (32 + 8) heads x 128: 75 us with one row
-// per group, 60 us with four in registers, 60 us with the ring and the table
-// from L2, 45.4 us so (5.4 TB/s, 0.80 of the copy rate); 16384 tokens x 72
-// heads with three axes 123 us (5.0 TB/s).  Sets of eight, rings of three
-// stages and smaller blocks were slower (47 to 68 us), blocks of 256 threads the
-// same.
+// rows at a time keeps too few loads in flight.  So all tokens' rows, laid end
+// to end in sets of kSetRows heads, are cut into equal runs, one per group, and
+// each thread copies its own pieces of the rows and of the table into its own
+// places of a ring in shared memory with cp.async, kStages - 1 sets ahead; no
+// thread reads another's pieces, so the ring needs no barrier.  A run goes
+// through a token's heads one after the other, so that positions, table row
+// and the weights times the table are taken once per token and tensor and not
+// once per set, which was most of the instructions.  11750 tokens x (32 + 8)
+// heads x 128: 75 us with one row per group, 60 us with four in registers,
+// 45.4 us so (5.4 TB/s, 0.80 of the copy rate); 16384 tokens x 72 heads with
+// three axes 101 us (6.0 TB/s, 0.89; 123 with the table per set).  Sets of one and
+// three rows 103 and 104 us, of four and eight 115; three blocks of 128 threads
+// per SM 112, five 112, six 123; eight of 64 the same as four of 128.
 #include "rope.cuh"
 
 #include "../../include/b2pa.h"
@@ -340,11 +342,10 @@ __global__ void __launch_bounds__(kRopeThreads) rope_rows_kernel(const __grid_co
 
 // ---------------------------------------------------------------- the staged kernel
 
-constexpr int kSetRows = 4;
+constexpr int kSetRows = 2;
 constexpr int kStages = 2;
-// a thread's pieces of 16 bytes in one stage: 2 per row, 4 of the table
-constexpr int kPieces = 2 * kSetRows + 4;
-constexpr int kStagedSmem = kStages * kPieces * 16 * kRopeThreads;
+// a thread's pieces of 16 bytes: 2 per row, 4 of a table row
+constexpr int kStagedSmem = (kStages * 2 * kSetRows + 2 * 4) * 16 * kRopeThreads;  // rows; two tokens' table rows
 
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src)
 {
@@ -370,104 +371,107 @@ __global__ void __launch_bounds__(kRopeThreads) rope_staged_kernel(const __grid_
     const int half = p.R >> 1, f0 = 8 * lane;
     const Chunks ch = chunks_of<kMode>(p, lane);
     const int axis0 = vector_axis(p, 2 * lane), axis1 = vector_axis(p, 2 * lane + 1);
-    // sets of kSetRows rows of a token: those of the queries, then those of the keys
+    // sets of kSetRows rows of a token: those of the queries, then those of the
+    // keys; all tokens' sets, one after the other, are cut into equal runs
     const unsigned sets_q = (unsigned)(p.x[0].heads + kSetRows - 1) / kSetRows;
     const unsigned sets = sets_q + (unsigned)(p.x[1].heads + kSetRows - 1) / kSetRows;
-    const unsigned first = blockIdx.x * kGroups + threadIdx.x / kLanes, step = gridDim.x * kGroups;
-    const unsigned rounds = (total + step - 1) / step;  // the same for every thread: the shuffles need whole warps
+    const unsigned groups = gridDim.x * kGroups, me = blockIdx.x * kGroups + threadIdx.x / kLanes;
+    const unsigned share = total / groups, more = total % groups;
+    const unsigned first = me * share + min(me, more), count = share + (me < more ? 1 : 0);
+    const unsigned rounds = share + (more > 0 ? 1 : 0);  // the same for every thread: the shuffles need whole warps
     const uint32_t mine = smem_u32(ring) + threadIdx.x * 16;
-    auto piece = [&](unsigned stage, int k) { return mine + (stage * kPieces + k) * (kRopeThreads * 16); };
+    // this thread's pieces of a set's rows and of a token's table row
+    auto piece = [&](unsigned stage, int k) { return mine + (stage * 2 * kSetRows + k) * (kRopeThreads * 16); };
+    auto table = [&](unsigned which, int k) { return mine + ((kStages * kSetRows + which * 2) * 2 + k) * (kRopeThreads * 16); };
 
-    // a set by its token and its number within the token; the next one of this
-    // group is `step` sets on
     struct Set {
-        unsigned t, r;
+        unsigned n;     // of this group's
+        unsigned t, r;  // token, set of the token
+        unsigned tab;   // where the token's table row is
+        bool opens;     // the group's first set of this token
     };
-    const unsigned step_t = step / sets, step_r = step % sets;
-    auto after = [&](Set z) {
-        z.t += step_t;
-        z.r += step_r;
-        if (z.r >= sets) {
-            z.r -= sets;
+    auto next = [&](Set& z) {
+        ++z.n;
+        z.opens = ++z.r == sets;
+        if (z.opens) {
+            z.r = 0;
             ++z.t;
+            z.tab ^= 1;
         }
-        return z;
     };
-    auto on = [&](const Set& z) { return z.t < (unsigned)p.T; };
     auto is_k = [&](const Set& z) { return z.r >= sets_q; };
     auto head0 = [&](const Set& z) { return (int)(is_k(z) ? z.r - sets_q : z.r) * kSetRows; };
-    auto start_copies = [&](const Set& z, const Places& at, unsigned stage) {
-        if (on(z)) {
-            const RopeTensor& x = p.x[is_k(z) ? 1 : 0];
-            const int h0 = head0(z);
-            const uint16_t* row = x.in + (long long)z.t * x.in_tok + (long long)h0 * x.in_head;
+
+    // `use` is the set whose rows are computed, `copied` the one whose copies
+    // start next; `at` are the positions of the token it opens next
+    Set use{0, first / sets, first % sets, 0, true}, copied = use;
+    Places at = places_of(p, copied.t, count > 0);
+    uint32_t ok_bits = 0;  // bit of a table row: its token's positions are inside the table
+    unsigned to = 0, from = 0;  // stages
+    auto advance = [&] {
+        if (copied.n < count) {
+            const RopeTensor& x = p.x[is_k(copied) ? 1 : 0];
+            const int h0 = head0(copied);
+            const uint16_t* row = x.in + (long long)copied.t * x.in_tok + (long long)h0 * x.in_head;
 #pragma unroll
             for (int r = 0; r < kSetRows; ++r, row += x.in_head)
                 if (h0 + r < x.heads) {
                     if (ch.a >= 0)
-                        copy16(piece(stage, 2 * r), row + 8 * ch.a);
+                        copy16(piece(to, 2 * r), row + 8 * ch.a);
                     if (ch.b >= 0)
-                        copy16(piece(stage, 2 * r + 1), row + 8 * ch.b);
+                        copy16(piece(to, 2 * r + 1), row + 8 * ch.b);
                 }
-            if (ch.turns) {
+            if (copied.opens) {  // (behind the rows, which need no position)
+                if (!at.ok && lane == 0)
+                    atomicOr(p.err, (unsigned)B2PA_DEV_BAD_POSITION);
+                ok_bits = (ok_bits & ~(1u << copied.tab)) | ((at.ok ? 1u : 0u) << copied.tab);
+                if (ch.turns) {
 #pragma unroll
-                for (int v = 0; v < 2; ++v) {
-                    const int axis = v ? axis1 : axis0, f = f0 + 4 * v;
-                    const uint32_t cos = piece(stage, 2 * kSetRows + v), sin = piece(stage, 2 * kSetRows + 2 + v);
-                    if (axis != 255) {
-                        const float* e = at.row(p, axis) + f;
-                        copy16_l1(cos, e);
-                        copy16_l1(sin, e + half);
-                    } else {
+                    for (int v = 0; v < 2; ++v) {
+                        const int axis = v ? axis1 : axis0, f = f0 + 4 * v;
+                        const uint32_t cos = table(copied.tab, v), sin = table(copied.tab, 2 + v);
+                        if (axis != 255) {
+                            const float* e = at.row(p, axis) + f;
+                            copy16_l1(cos, e);
+                            copy16_l1(sin, e + half);
+                        } else {
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const int fi = min(f + i, half - 1);  // (a frequency past the last one turns no pair)
-                            const float* e = at.row(p, p.axis_of[fi]) + fi;
-                            copy4_l1(cos + 4 * i, e);
-                            copy4_l1(sin + 4 * i, e + half);
+                            for (int i = 0; i < 4; ++i) {
+                                const int fi = min(f + i, half - 1);  // (a frequency past the last one turns no pair)
+                                const float* e = at.row(p, p.axis_of[fi]) + fi;
+                                copy4_l1(cos + 4 * i, e);
+                                copy4_l1(sin + 4 * i, e + half);
+                            }
                         }
                     }
                 }
+                at = places_of(p, copied.t + 1, copied.t + 1 < (unsigned)p.T);
             }
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
-    };
-
-    // `use` is the set whose rows are computed, `copied` the one whose copies
-    // start next and whose positions are in `at`
-    uint32_t ok_bits = 0;  // bit of a stage: its token's positions are inside the table
-    Set use{first / sets, first % sets}, copied = use;
-    Places at = places_of(p, copied.t, on(copied));
-    unsigned to = 0, from = 0;  // stages
-    auto advance = [&] {
-        const Places here = at;
-        const Set z = copied;
-        copied = after(copied);
-        at = places_of(p, copied.t, on(copied));
-        if (on(z) && !here.ok && z.r == 0 && lane == 0)
-            atomicOr(p.err, (unsigned)B2PA_DEV_BAD_POSITION);
-        start_copies(z, here, to);
-        ok_bits = (ok_bits & ~(1u << to)) | ((here.ok ? 1u : 0u) << to);
+        next(copied);
         to = to + 1 == kStages ? 0 : to + 1;
     };
 #pragma unroll
     for (int i = 0; i < kStages - 1; ++i)
         advance();
+    Turn turn;
     for (unsigned round = 0; round < rounds; ++round) {
         advance();
         asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
         const RopeTensor& x = p.x[is_k(use) ? 1 : 0];
         const int h0 = head0(use);
-        Turn turn;
-        {
+        // another token, or its keys after its queries (for the whole warp: what a
+        // group has already it forms again)
+        if (__any_sync(0xffffffffu, use.opens || use.r == sets_q)) {
             float2 wa[4], wb[4], c[4], s[4];
             load_weights(x, ch, wa, wb);
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 uint4 u = make_uint4(0x3F800000u, 0x3F800000u, 0x3F800000u, 0x3F800000u), v = make_uint4(0u, 0u, 0u, 0u);
                 if (ch.turns) {
-                    u = ld_shared_v4(piece(from, 2 * kSetRows + i));
-                    v = ld_shared_v4(piece(from, 2 * kSetRows + 2 + i));
+                    u = ld_shared_v4(table(use.tab, i));
+                    v = ld_shared_v4(table(use.tab, 2 + i));
                 }
                 c[2 * i] = make_float2(__uint_as_float(u.x), __uint_as_float(u.y));
                 c[2 * i + 1] = make_float2(__uint_as_float(u.z), __uint_as_float(u.w));
@@ -483,7 +487,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_staged_kernel(const __grid_
             }
             turn = turn_of<kMode>(p, lane, c, s, wa, wb);
         }
-        const bool ok = on(use) && (ok_bits >> from & 1u);
+        const bool ok = use.n < count && (ok_bits >> use.tab & 1u);
 #pragma unroll
         for (int r = 0; r < kSetRows; ++r) {
             const bool there = h0 + r < x.heads;
@@ -500,7 +504,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_staged_kernel(const __grid_
             if (ok && there)
                 store_row(x, use.t, h0 + r, ch, a, b);
         }
-        use = after(use);
+        next(use);
         from = from + 1 == kStages ? 0 : from + 1;
     }
 }
@@ -511,10 +515,11 @@ cudaError_t launch_lanes(const RopeParams& p, int sms, cudaStream_t stream)
     constexpr int kGroups = kRopeThreads / kLanes;
     const long long rows = (long long)p.T * (p.x[0].heads + p.x[1].heads);
     if constexpr (kMode != kHalvesInSmem) {
-        // more than one wave of rows_kernel's blocks (7 per SM)
+        // Where the copies ahead pay: 40 heads x 128, 430 tokens 3.9 us by rows and 4.2
+        // staged, 600 tokens 5.4 and 5.5, 900 tokens 6.8 and 6.4, 3000 tokens 17.8 and 15.
         const long long sets = (long long)p.T * ((p.x[0].heads + kSetRows - 1) / kSetRows + (p.x[1].heads + kSetRows - 1) / kSetRows);
-        const int grid = sms * 4;  // four rings of 48 KB per SM
-        if (rows > (long long)sms * 7 * kGroups && sets + (long long)grid * kGroups * (kStages + 1) <= 0xFFFFFFFFLL) {
+        const int grid = sms * 4;  // (see the top)
+        if (rows > (long long)sms * 10 * kGroups && sets + (long long)grid * kGroups * (kStages + 1) <= 0xFFFFFFFFLL) {
             auto kern = rope_staged_kernel<kMode, kLanes>;
             const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kStagedSmem);
             if (e != cudaSuccess)

@@ -101,6 +101,38 @@ def test_against_the_formula(cuda_lib, case):
     assert torch.equal(d[:, (H + K) * D :].cpu(), qkv[:, (H + K) * D :])
 
 
+@pytest.mark.parametrize("case", [
+    (13000, 1, 1, 128, 128, 1, False, "bf16"),  # two sets per token
+    (6100, 3, 1, 128, 64, 3, False, "fp32"),    # axes in blocks, partial rotation
+    (9000, 5, 1, 64, 64, 2, True, "none"),      # axes in turn
+    (4000, 4, 3, 128, 50, 1, True, "bf16"),     # pairs that end inside a lane
+    (2500, 6, 2, 256, 256, 4, False, "fp32"),
+    (1, 20000, 9000, 128, 128, 1, False, "bf16"),  # one token for all
+], ids=lambda c: "-".join(map(str, c)))
+def test_many_rows(cuda_lib, case):
+    """Enough rows for the kernel that goes through them in runs; some positions are outside the table."""
+    T, H, K, D, R, axes, inter, weights = case
+    g = torch.Generator().manual_seed(T)
+    q, k = torch.randn((T, H, D), generator=g).to(BF), torch.randn((T, K, D), generator=g).to(BF)
+    w = [None, None]
+    if weights != "none":
+        w = [(1 + torch.randn(D, generator=g) * 0.3).to(BF if weights == "bf16" else torch.float32) for _ in w]
+    cs = table(300, R)
+    pos = torch.randint(0, 300, (axes, T), generator=g, dtype=torch.int32)
+    axis_of = None if axes == 1 else [i % axes if inter else min(axes - 1, i * axes // (R // 2)) for i in range(R // 2)]
+    bad = torch.zeros(T, dtype=torch.bool)
+    for t in range(5, T, 97):
+        pos[t % axes, t] = -1 if t % 2 else 300
+        bad[t] = True
+    out = torch.full((T, H, D), 5.0, dtype=BF, device=DEV), torch.full((T, K, D), 5.0, dtype=BF, device=DEV)
+    cuda_lib.qk_norm_rope(q.to(DEV), k.to(DEV), cs.to(DEV), pos.to(DEV), *[None if x is None else x.to(DEV) for x in w],
+                          axis_of=axis_of, interleaved=inter, q_out=out[0], k_out=out[1])
+    assert cuda_lib.device_status() == (cuda_lib.DEV_BAD_POSITION if bad.any() else 0)
+    for x, y, wx in ((q, out[0], w[0]), (k, out[1], w[1])):
+        check(y[~bad.to(DEV)], want(x[~bad], wx, cs, pos[:, ~bad], axis_of, inter, 1e-6))
+        assert (y[bad.to(DEV)] == 5).all()
+
+
 def test_rows_by_head_and_a_padded_table(cuda_lib):
     """[heads, T, D] storage on both sides; a table whose rows are not 16-byte aligned."""
     T, H, K, D, R = 19, 6, 2, 64, 64
