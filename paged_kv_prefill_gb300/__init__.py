@@ -515,14 +515,15 @@ def append_kv_scaled(k_new: torch.Tensor, v_new: torch.Tensor, kv_cache, kv_scal
     call = (_calls or native()).append_kv_scaled
     k, v = split_kv_cache(kv_cache, kv_layout)
     ks, vs = _two(kv_scales, "kv_scales")
-    args = (k_new, v_new, k, v, ks, vs, cache_loc, LAYOUTS[kv_layout])
+    layout = LAYOUTS[kv_layout]
     handle = _here(k_new, stream)
     if handle >= 0:
-        st = call(handle, *args)
+        st = call(handle, k_new, v_new, k, v, ks, vs, cache_loc, layout)
     else:
         with _On(k_new, stream) as handle:
-            st = call(handle, *args)
-    _check(st, "b2pa_append_kv_scaled")
+            st = call(handle, k_new, v_new, k, v, ks, vs, cache_loc, layout)
+    if st != 0:
+        _check(st, "b2pa_append_kv_scaled")
 
 
 def read_kv_scaled(kv_cache, kv_scales, cache_loc: torch.Tensor, k_out: Optional[torch.Tensor] = None,
@@ -535,12 +536,12 @@ def read_kv_scaled(kv_cache, kv_scales, cache_loc: torch.Tensor, k_out: Optional
     call = (_calls or native()).read_kv_scaled
     k, v = split_kv_cache(kv_cache, kv_layout)
     ks, vs = _two(kv_scales, "kv_scales")
-    args = (k, v, ks, vs, cache_loc, LAYOUTS[kv_layout], k_out, v_out)
+    layout = LAYOUTS[kv_layout]
     handle = _here(k, stream)
     if handle >= 0:
-        return _done(call(handle, *args), "b2pa_read_kv_scaled")
+        return _done(call(handle, k, v, ks, vs, cache_loc, layout, k_out, v_out), "b2pa_read_kv_scaled")
     with _On(k, stream) as handle:
-        return _done(call(handle, *args), "b2pa_read_kv_scaled")
+        return _done(call(handle, k, v, ks, vs, cache_loc, layout, k_out, v_out), "b2pa_read_kv_scaled")
 
 
 def qk_norm_rope(
@@ -570,12 +571,14 @@ def qk_norm_rope(
         if len(axis_of) != cos_sin.shape[-1] // 2:
             raise ValueError(f"axis_of: one axis for each of the {cos_sin.shape[-1] // 2} frequencies")
         axes = struct.pack(f"{len(axis_of)}i", *axis_of)
-    args = (query, key, cos_sin, positions, q_weight, k_weight, eps, axes, 1 if interleaved else 0, q_out, k_out)
+    pairs = 1 if interleaved else 0
     handle = _here(query, stream)
     if handle >= 0:
-        return _done(call(handle, *args), "b2pa_qk_norm_rope")
+        return _done(call(handle, query, key, cos_sin, positions, q_weight, k_weight, eps, axes, pairs, q_out, k_out),
+                     "b2pa_qk_norm_rope")
     with _On(query, stream) as handle:
-        return _done(call(handle, *args), "b2pa_qk_norm_rope")
+        return _done(call(handle, query, key, cos_sin, positions, q_weight, k_weight, eps, axes, pairs, q_out, k_out),
+                     "b2pa_qk_norm_rope")
 
 
 def tree_attention(

@@ -51,14 +51,15 @@ def _native_commands(tmp: str) -> list:
 
     root = os.path.dirname(torch.__file__)
     inc = [sysconfig.get_paths()["include"], os.path.join(root, "include"),
-           os.path.join(root, "include", "torch", "csrc", "api", "include")]
+           os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(_nvcc()))), "include")]
     obj = os.path.join(BUILD, "native.o")
     cxx = ["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
     return [
         cxx + [x for i in inc for x in ("-isystem", i)] + ["-c", os.path.join(CSRC, "native.cpp"), "-o", obj],
         ["g++", "-shared", "-o", tmp, obj, "-L", HERE, "-l:libb2pa.so", "-Wl,-rpath,$ORIGIN",
-         "-L", os.path.join(root, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10"],
+         "-L", os.path.join(root, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"],
     ]
 
 

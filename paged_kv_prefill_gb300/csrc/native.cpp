@@ -8,7 +8,8 @@
 // to both).  They return their output, or the status of a call that failed.
 #include <Python.h>
 
-#include <ATen/ops/empty.h>
+#include <ATen/core/Tensor.h>
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <exception>
@@ -113,7 +114,9 @@ public:
     // the tensor given, or a new contiguous bf16 one
     at::Tensor output(int i, at::IntArrayRef shape)
     {
-        return none(i) ? at::empty(shape, at::TensorOptions().device(device_).dtype(at::kBFloat16)) : tensor(i);
+        if (!none(i))
+            return tensor(i);
+        return part(memory(c10::multiply_integers(shape)), 0, shape);
     }
     // Two of them.  New ones share one allocation, the second behind the first
     // (16-byte aligned: its rows are multiples of 8 elements): an allocation and
@@ -122,20 +125,25 @@ public:
     {
         if (!none(i) || !none(j))
             return {output(i, a), output(j, b)};
-        const int64_t n = c10::multiply_integers(a), m = c10::multiply_integers(b);
-        const at::Tensor both = at::empty({n + m}, at::TensorOptions().device(device_).dtype(at::kBFloat16));
+        const int64_t n = c10::multiply_integers(a);
+        const c10::Storage both = memory(n + c10::multiply_integers(b));
         return {part(both, 0, a), part(both, n, b)};
-    }
-    at::Tensor bytes(uint64_t n) const
-    {
-        return at::empty({(int64_t)n}, at::TensorOptions().device(device_).dtype(at::kByte));
     }
 
 private:
-    // a contiguous tensor over `all`'s memory from element `at` on, with a version of its own
-    static at::Tensor part(const at::Tensor& all, int64_t at, at::IntArrayRef shape)
+    // What at::empty takes too, from the same allocator, without its dispatch and
+    // device guard (the device is current).
+    static c10::Storage memory(int64_t elements)
     {
-        at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(all.storage()), all.key_set(), all.dtype());
+        c10::Allocator* const from = c10::cuda::CUDACachingAllocator::get();
+        const size_t bytes = (size_t)elements * sizeof(at::BFloat16);
+        return c10::Storage(c10::Storage::use_byte_size_t(), bytes, from->allocate(bytes), from, true);
+    }
+    // a contiguous bf16 tensor over memory from element `at` on
+    static at::Tensor part(c10::Storage all, int64_t at, at::IntArrayRef shape)
+    {
+        at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(
+            std::move(all), c10::DispatchKeySet(c10::DispatchKey::CUDA), caffe2::TypeMeta::Make<at::BFloat16>());
         t.unsafeGetTensorImpl()->set_sizes_contiguous(shape);
         t.unsafeGetTensorImpl()->set_storage_offset(at);
         return t;
@@ -247,8 +255,8 @@ PyObject* tree_attention(PyObject*, PyObject* const* args, Py_ssize_t n)
         int st = call(nullptr, 0);
         if (st == B2PA_ERR_WORKSPACE) {
             // from torch's allocator for this call, so that every captured graph keeps its own
-            const at::Tensor workspace = a.bytes(need);
-            st = call(workspace.data_ptr(), need);
+            const c10::DataPtr workspace = c10::cuda::CUDACachingAllocator::get()->allocate(need);
+            st = call(workspace.get(), need);
         }
         return st == B2PA_OK ? THPVariable_Wrap(out) : PyLong_FromLong(st);
     });
