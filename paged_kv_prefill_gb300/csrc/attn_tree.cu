@@ -12,11 +12,11 @@
 // 9 to 16 nodes x 4 heads, D = 128: 104 us, 5.6 TB/s (0.83 of the copy rate);
 // the same with e4m3, up to 16384 keys and 8 nodes: 145 us, 4.5 TB/s (0.66);
 // 8 requests of up to 16384 keys, 64 nodes x 8 heads: 112 us, 940 TFLOP/s (0.49 of
-// the bf16 rate); one request, 8 nodes, 2048 keys: 14.5 us, latency.
+// the bf16 rate); one request, 8 nodes, 2048 keys: 14.4 us, latency.
 //
 // Work.  A unit is (request, kv head, up to kTiles query tiles of 128 rows);
 // all units' kv tiles of 128 keys, laid end to end, are cut into equal runs,
-// one per CTA, one CTA per SM (TreeCut).  Every CTA finds its run from the
+// one per CTA, one CTA per SM (TreeCut; small units stay whole, tree_snap).  Every CTA finds its run from the
 // lengths alone: no list, no counters, nothing that two launches or two graphs
 // could share, and equal shares whatever the lengths.  A CTA thus has at most
 // two segments that are parts of a unit, the first and the last of its run;
@@ -1449,57 +1449,88 @@ __global__ void __launch_bounds__(kTreeThreads, 1) attention_tree_kernel(const _
 
     pdl_wait();  // inputs may come from the kernel this launch follows
 
-    // Where this CTA's run starts: kv tiles of the requests before each, by a
-    // scan over the threads' contiguous shares of the requests (scratch in the
-    // ring, which is empty yet).
-    long long* scan = reinterpret_cast<long long*>(smem + C::kOffRing);  // 12 warp sums; [16] base, [17] request
+    // Where this CTA's run starts: the first request whose work, with that of the
+    // requests before it, passes the run's start.  warp 0 alone needs to know; for
+    // more than a request per lane all threads add up.
     const int item_toks = kTiles * p.rows.tile_toks;
-    const int share = (p.B + kTreeThreads - 1) / kTreeThreads;
-    const int b0 = min(p.B, tid * share), b1 = min(p.B, b0 + share);
-    long long mine = 0;
-    for (int b = b0; b < b1; ++b) {
-        const TreeReq r = tree_request(p, b, item_toks);
-        if (!r.ok && blockIdx.x == 0)
-            atomicOr(p.err, (unsigned)B2PA_DEV_BAD_REQUEST);
-        mine += r.work(p.Hkv);
-    }
-    long long before = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const long long y = __shfl_up_sync(0xffffffffu, before, o);
-        if (lane >= o)
-            before += y;
-    }
-    if (lane == 31)
-        scan[warp] = before;
-    __syncthreads();
-    long long total = 0, warps_before = 0;
-#pragma unroll
-    for (int w = 0; w < kTreeThreads / 32; ++w) {
-        warps_before += w < warp ? scan[w] : 0;
-        total += scan[w];
-    }
-    before += warps_before - mine;
-    const TreeCut cut = tree_cut(total, gridDim.x);
-    const bool works = (int)blockIdx.x < cut.g;
-    const long long start = works ? cut.start(blockIdx.x) : 0, end = works ? cut.start(blockIdx.x + 1) : 0;
-    if (works && start >= before && start < before + mine) {
-        long long base = before;
-        int b = b0;
-        for (; b + 1 < b1; ++b) {  // this thread's requests, if it has several
-            const long long w = tree_request(p, b, item_toks).work(p.Hkv);
-            if (start < base + w)
-                break;
-            base += w;
+    const bool by_all = p.B > 32;  // (of the whole grid)
+    long long start = 0, end = 0, base = 0;
+    int first_b = 0;
+    if (by_all || warp == 0) {
+        long long* scan = reinterpret_cast<long long*>(smem + C::kOffRing);  // (empty yet) 12 warp sums; [16 ..] the run
+        const int threads = by_all ? kTreeThreads : 32, share = (p.B + threads - 1) / threads;
+        const int b0 = min(p.B, tid * share), b1 = min(p.B, b0 + share);
+        long long mine = 0;
+        for (int b = b0; b < b1; ++b) {
+            const TreeReq r = tree_request(p, b, item_toks);
+            if (!r.ok && blockIdx.x == 0)
+                atomicOr(p.err, (unsigned)B2PA_DEV_BAD_REQUEST);
+            mine += r.work(p.Hkv);
         }
-        scan[16] = base;
-        scan[17] = b;
+        long long before = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long y = __shfl_up_sync(0xffffffffu, before, o);
+            if (lane >= o)
+                before += y;
+        }
+        long long total = 0, warps_before = 0;
+        if (by_all) {
+            if (lane == 31)
+                scan[warp] = before;
+            __syncthreads();
+#pragma unroll
+            for (int w = 0; w < kTreeThreads / 32; ++w) {
+                warps_before += w < warp ? scan[w] : 0;
+                total += scan[w];
+            }
+        } else {
+            total = __shfl_sync(0xffffffffu, before, 31);
+        }
+        before += warps_before - mine;
+        const TreeCut cut = tree_cut(total, gridDim.x);
+        const bool works = (int)blockIdx.x < cut.g;
+        start = works ? cut.start(blockIdx.x) : 0;
+        end = works ? cut.start(blockIdx.x + 1) : 0;
+        // the run's ends, moved off units that are not cut, by the threads whose
+        // requests they are in
+        const bool has_start = start >= before && start < before + mine, has_end = end >= before && end < before + mine;
+        if (!by_all) {  // a request per lane
+            const TreeReq r = tree_request(p, min(b0, p.B - 1), item_toks);
+            const long long s0 = has_start ? tree_snap(start, before, r, cut) : 0, e0 = has_end ? tree_snap(end, before, r, cut) : 0;
+            const unsigned ws = __ballot_sync(0xffffffffu, has_start), we = __ballot_sync(0xffffffffu, has_end);
+            first_b = ws != 0 ? __ffs(ws) - 1 : 0;
+            base = __shfl_sync(0xffffffffu, before, first_b);
+            start = __shfl_sync(0xffffffffu, s0, first_b);
+            const long long e1 = __shfl_sync(0xffffffffu, e0, we != 0 ? __ffs(we) - 1 : 0);
+            end = we != 0 ? e1 : end;  // (none: it is the last)
+        } else {
+            for (int k = 0; k < 2; ++k) {
+                if (!(k ? has_end : has_start))
+                    continue;
+                const long long x = k ? end : start;
+                long long from = before;
+                int b = b0;
+                TreeReq r = tree_request(p, b, item_toks);
+                for (; b + 1 < b1 && x >= from + r.work(p.Hkv); r = tree_request(p, ++b, item_toks))
+                    from += r.work(p.Hkv);
+                scan[16 + k] = tree_snap(x, from, r, cut);
+                if (k == 0) {
+                    scan[18] = from;
+                    scan[19] = b;
+                }
+            }
+            __syncthreads();
+            if (works) {
+                start = scan[16];
+                end = end < total ? scan[17] : end;
+                base = scan[18];
+                first_b = (int)scan[19];
+            }
+            fence_proxy_async_smem();  // the ring's next writes come through the async proxy
+            __syncthreads();
+        }
     }
-    __syncthreads();
-    const long long base = scan[16];
-    const int first_b = works ? (int)scan[17] : 0;
-    fence_proxy_async_smem();  // the ring's next writes come through the async proxy
-    __syncthreads();
 
     // 384 threads launch with 168 registers each (104 + 200 + 200 = 504 = 3 x 168)
     if (warp < 4) {

@@ -246,6 +246,19 @@ def test_long_context_cut_over_all_sms(cuda_lib, cache, kv):
     assert cuda_lib.device_status() == 0
 
 
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+@pytest.mark.parametrize("kvs", [[512] * 24, [513] * 24, [1024] * 8, [1025] * 16, [640] * 33, [300] * 60, [4] * 40,
+                                 [100, 500, 1000, 1100, 9000, 4] * 3, [100, 500, 1000, 1100, 9000, 4] * 9],
+                         ids=lambda k: f"{len(k)}x{k[0]}")
+def test_units_whole_and_cut(cuda_lib, cache, kvs):
+    """Requests around the sizes up to which no CTA's share ends inside one, alone and among others."""
+    t = Batch([4] * len(kvs), kvs, 16, 4, 128, 32, cache=cache, seed=len(kvs) + kvs[0])
+    out = cuda_lib.tree_attention(**t.dev())
+    assert cuda_lib.device_status() == 0
+    t.check(out)
+    assert torch.equal(out, cuda_lib.tree_attention(**t.dev()))
+
+
 def test_many_requests(cuda_lib):
     r = random.Random(1)
     ns = [r.choice([0, 1, 2, 3, 5, 8]) for _ in range(900)]
