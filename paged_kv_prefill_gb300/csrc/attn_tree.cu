@@ -208,7 +208,7 @@ __device__ void tree_producer(const TreeParams& p, const TreeCtx& c, long long p
     bool ok = true;
     TreeReq r = pos < end ? tree_request(p, b, item_toks) : TreeReq{};
     int4* note = p.part_seg + (long long)blockIdx.x * 4;  // of slots 0 and 1
-    if (lane < 2)
+    if (lane < 2 && !p.whole)
         TreePart{}.write(note + 2 * lane);
     __syncwarp();
     for (uint32_t n = 0; ok; ++n) {
@@ -1497,7 +1497,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) attention_tree_kernel(const _
         const bool has_start = start >= before && start < before + mine, has_end = end >= before && end < before + mine;
         if (!by_all) {  // a request per lane
             const TreeReq r = tree_request(p, min(b0, p.B - 1), item_toks);
-            const long long s0 = has_start ? tree_snap(start, before, r, cut) : 0, e0 = has_end ? tree_snap(end, before, r, cut) : 0;
+            const long long s0 = has_start ? tree_snap(start, before, r, cut, p.whole) : 0, e0 = has_end ? tree_snap(end, before, r, cut, p.whole) : 0;
             const unsigned ws = __ballot_sync(0xffffffffu, has_start), we = __ballot_sync(0xffffffffu, has_end);
             first_b = ws != 0 ? __ffs(ws) - 1 : 0;
             base = __shfl_sync(0xffffffffu, before, first_b);
@@ -1514,7 +1514,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) attention_tree_kernel(const _
                 TreeReq r = tree_request(p, b, item_toks);
                 for (; b + 1 < b1 && x >= from + r.work(p.Hkv); r = tree_request(p, ++b, item_toks))
                     from += r.work(p.Hkv);
-                scan[16 + k] = tree_snap(x, from, r, cut);
+                scan[16 + k] = tree_snap(x, from, r, cut, p.whole);
                 if (k == 0) {
                     scan[18] = from;
                     scan[19] = b;
@@ -1705,6 +1705,8 @@ cudaError_t launch_tree(const TreeParams& p, cudaStream_t stream)
         return err[dev];
     if ((e = launch_pdl(kern, dim3(p.grid), kTreeThreads, C::kSmemBytes, stream, p)) != cudaSuccess)
         return e;
+    if (p.whole)
+        return cudaSuccess;
     return launch_pdl(tree_merge_kernel<D>, dim3(p.grid, p.rows.warps * kTiles), D * 2, 0, stream, p, kTiles);
 }
 

@@ -1,6 +1,7 @@
 // ops.cu -- host side of the entry points around the attention call: the
 // query/key norm with the rotation, the write and read of a cache with one
 // scale per row, and the attention of token trees.  Argument checks and launches; nothing here synchronises.
+#include <algorithm>
 #include <cmath>
 #include <cstring>
 
@@ -246,11 +247,12 @@ int scaled_kv_impl(bool write, const b2pa_tensor* const rows[2], const char* con
 struct TreePlan {
     bool tc;
     int tiles;     // query tiles per item
+    bool whole;    // no unit is cut
     bool stacked;  // e4m3 rows twice in one tile
     size_t off_ml, off_o, bytes;
 };
 
-int plan_tree(const Problem& pr, int max_q_len, const DevInfo& di, TreePlan* out)
+int plan_tree(const Problem& pr, int max_q_len, int max_kv_len, int window, const DevInfo& di, TreePlan* out)
 {
     const char* why = tc_reject(pr, di);
     const int path = kernel_path();
@@ -266,10 +268,15 @@ int plan_tree(const Problem& pr, int max_q_len, const DevInfo& di, TreePlan* out
         t.tiles = max_q_len <= tree_rows(G, false).tile_toks ? 1 : 2;
         // e4m3 rows twice where they fit (146 us; once 161)
         t.stacked = pr.fp8 && G <= 32 && max_q_len <= tree_rows(G, true).tile_toks;
+        // kv tiles of a unit at most: its keys start at 0, or anywhere with a window
+        const long long all = ((long long)max_kv_len + kKvTile - 1) / kKvTile;
+        const long long seen = ((long long)window + max_q_len + kKvTile - 2) / kKvTile + 1;
+        const long long kv_tiles = window >= 0 ? std::min(all, seen) : all;
+        t.whole = kv_tiles <= kTreeWholeTiles;
         const size_t rows = (size_t)di.sms * 2 * t.tiles * kQRows;  // two segments of every CTA
         t.off_ml = ((size_t)di.sms * 2 * 2 * sizeof(int4) + 255) / 256 * 256;
         t.off_o = t.off_ml + rows * sizeof(float2);
-        t.bytes = t.off_o + rows * pr.D * sizeof(float);
+        t.bytes = t.whole ? 0 : t.off_o + rows * pr.D * sizeof(float);
     }
     *out = t;
     return B2PA_OK;
@@ -321,7 +328,7 @@ int tree_impl(const b2pa_tensor* q, const b2pa_tensor* k_pool, const b2pa_tensor
     int dev;
     DevInfo di;
     TreePlan plan;
-    if ((st = device_info(&dev, &di)) || (st = plan_tree(pr, max_q_len, di, &plan)))
+    if ((st = device_info(&dev, &di)) || (st = plan_tree(pr, max_q_len, max_kv_len, window, di, &plan)))
         return st;
     *bytes_needed = plan.bytes;
     if (workspace_bytes < plan.bytes)
@@ -372,10 +379,13 @@ int tree_impl(const b2pa_tensor* q, const b2pa_tensor* k_pool, const b2pa_tensor
     p.inject_stall = inject_stall();
     cudaError_t e;
     if (plan.tc) {
-        uint8_t* ws = static_cast<uint8_t*>(workspace);
-        p.part_seg = reinterpret_cast<int4*>(ws);
-        p.part_ml = reinterpret_cast<float2*>(ws + plan.off_ml);
-        p.part_o = reinterpret_cast<float4*>(ws + plan.off_o);
+        p.whole = plan.whole;
+        if (!plan.whole) {
+            uint8_t* ws = static_cast<uint8_t*>(workspace);
+            p.part_seg = reinterpret_cast<int4*>(ws);
+            p.part_ml = reinterpret_cast<float2*>(ws + plan.off_ml);
+            p.part_o = reinterpret_cast<float4*>(ws + plan.off_o);
+        }
         if ((st = encode_q_map(&p.tm_q, pr, p.rows.box_toks)) || (st = encode_pool_map(&p.tm_k, pr, pr.k, pr.k_st)) ||
             (st = encode_pool_map(&p.tm_v, pr, pr.v, pr.v_st)))
             return st;

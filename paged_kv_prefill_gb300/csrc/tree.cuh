@@ -60,6 +60,7 @@ struct TreeParams {  // 128-byte aligned through its CUtensorMap members
     TreeRows rows;
     int B, T, H, Hkv, D, page_size, max_pages, num_pages, max_q_len, max_kv_len, mask_words, window;
     int grid;              // CTAs of the attention kernel
+    int whole;             // no unit is cut (part_* are null)
     float scale_log2;      // bmm1_scale * log2(e)
     float bmm2;
     unsigned long long wait_limit_ns;
@@ -129,10 +130,15 @@ __device__ __forceinline__ TreeCut tree_cut(long long total, int grid)
 // one of them; but not a third of them to a run.  (8 nodes x 4 heads, 8 kv
 // heads, cut and whole: 8 requests of 512 keys 16.5 and 14.8 us, 24 of 768 28.2 and
 // 26.3, 40 of 512 31.7 and 28.7; but 40 of 768 39.3 and 41.8, one of 512 12.8 and 13.8.)
-__device__ __forceinline__ long long tree_snap(long long x, long long base, const TreeReq& r, const TreeCut& cut)
+// Where no unit can have more than kTreeWholeTiles, none is cut, and there is
+// nothing to merge.
+constexpr int kTreeWholeTiles = 4;
+
+__device__ __forceinline__ long long tree_snap(long long x, long long base, const TreeReq& r, const TreeCut& cut, bool whole)
 {
     const long long all = (long long)r.unit * cut.g;  // (a run: cut.total / cut.g)
-    if (r.tiles > 8 || all > 3 * cut.total || (r.tiles > 4 && 4 * all < 3 * cut.total) || r.unit <= 0)
+    const bool small = r.tiles <= 8 && all <= 3 * cut.total && (r.tiles <= kTreeWholeTiles || 4 * all >= 3 * cut.total);
+    if ((!small && !whole) || r.unit <= 0)
         return x;
     const long long u0 = base + (x - base) / r.unit * r.unit;
     return 2 * (x - u0) < r.unit ? u0 : u0 + r.unit;
