@@ -272,7 +272,13 @@ int plan_tree(const Problem& pr, int max_q_len, int max_kv_len, int window, cons
         const long long all = ((long long)max_kv_len + kKvTile - 1) / kKvTile;
         const long long seen = ((long long)window + max_q_len + kKvTile - 2) / kKvTile + 1;
         const long long kv_tiles = window >= 0 ? std::min(all, seen) : all;
-        t.whole = kv_tiles <= kTreeWholeTiles;
+        // Units stay whole, and nothing is merged, where they are small, or about as
+        // many as SMs: 8 nodes x 4 heads, 8 kv heads, cut and whole, 8 requests of 768
+        // keys 16.9 and 14.7 us, 24 of 1024 30.8 and 28.4; but 40 of 768 39.0 and 39.7, one of
+        // 1024 13.3 and 15.7.
+        const int item = t.tiles * tree_rows(G, t.stacked).tile_toks;
+        const long long units = (long long)pr.B * pr.Hkv * ((max_q_len + item - 1) / item);
+        t.whole = kv_tiles <= kTreeWholeTiles || (kv_tiles <= 8 && 3 * units >= di.sms && 2 * units <= 3 * di.sms);
         const size_t rows = (size_t)di.sms * 2 * t.tiles * kQRows;  // two segments of every CTA
         t.off_ml = ((size_t)di.sms * 2 * 2 * sizeof(int4) + 255) / 256 * 256;
         t.off_o = t.off_ml + rows * sizeof(float2);

@@ -130,8 +130,7 @@ __device__ __forceinline__ TreeCut tree_cut(long long total, int grid)
 // one of them; but not a third of them to a run.  (8 nodes x 4 heads, 8 kv
 // heads, cut and whole: 8 requests of 512 keys 16.5 and 14.8 us, 24 of 768 28.2 and
 // 26.3, 40 of 512 31.7 and 28.7; but 40 of 768 39.3 and 41.8, one of 512 12.8 and 13.8.)
-// Where no unit can have more than kTreeWholeTiles, none is cut, and there is
-// nothing to merge.
+// `whole`: the host knows that all are small (ops.cu); then there is nothing to merge.
 constexpr int kTreeWholeTiles = 4;
 
 __device__ __forceinline__ long long tree_snap(long long x, long long base, const TreeReq& r, const TreeCut& cut, bool whole)
