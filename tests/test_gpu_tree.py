@@ -417,6 +417,38 @@ def test_strides(cuda_lib):
     assert torch.equal(cuda_lib.tree_attention(**{**d, "kv_cache": perm, "kv_layout": "HND"}), out)
 
 
+def test_workspace_of_the_c_call(cuda_lib):
+    """Too little workspace: nothing runs.  Where every tree sees few keys none is needed."""
+    import ctypes
+
+    lib = cuda_lib.load()
+    for kv, window, small in ((300, -1, True), (512, -1, True), (513, -1, False), (4000, 100, True), (4000, 800, False)):
+        t = Batch([5], [kv], 4, 2, 128, 32, window=window)
+        d = t.dev()
+        out = torch.full_like(d["query"], 3.0)
+        need = ctypes.c_uint64(7)
+
+        def call(ws, n):
+            return lib.b2pa_tree_attention(
+                *(None if x is None else ctypes.byref(cuda_lib.desc(x)) for x in (
+                    d["query"], *d["kv_cache"], d["block_tables"], d["seq_lens"], d["cum_seq_lens_q"], d["tree_mask"],
+                    d["positions"])),
+                5, kv, t.bmm1, t.bmm2, window, None, 0, ctypes.byref(cuda_lib.desc(out)), ws, n, ctypes.byref(need),
+                torch.cuda.current_stream().cuda_stream)
+
+        if small:
+            assert call(None, 0) == 0 and need.value == 0
+        else:
+            assert call(None, 0) == -5 and need.value > 0
+            ws = torch.empty(need.value, dtype=torch.uint8, device=DEV)
+            assert call(ws.data_ptr(), need.value - 1) == -5
+            torch.cuda.synchronize()
+            assert (out == 3).all()
+            assert call(ws.data_ptr(), need.value) == 0
+        torch.cuda.synchronize()
+        t.check(out)
+
+
 def test_no_rows(cuda_lib):
     t = Batch([0, 0], [5, 9], 4, 2, 128, 16)
     assert cuda_lib.tree_attention(**t.dev()).shape == (0, 4, 128)
