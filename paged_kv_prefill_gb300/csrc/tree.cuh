@@ -101,10 +101,11 @@ __device__ __forceinline__ TreeReq tree_request(const TreeParams& p, int b, int 
     return r;
 }
 
-// First context key that a node at position pos sees.
+// First context key that a node at position pos sees (ctx: none; the window
+// does not say which nodes it sees).
 __device__ __forceinline__ int tree_row_lo(int pos, int ctx, int kv_len, int window)
 {
-    return window < 0 ? 0 : max(0, min(max(pos, ctx), kv_len - 1) - window);
+    return window < 0 ? 0 : min(ctx, max(0, min(max(pos, ctx), kv_len - 1) - window));
 }
 
 // The CTAs cut all requests' units, laid end to end, into equal runs: CTA i of

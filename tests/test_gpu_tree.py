@@ -191,6 +191,8 @@ CASES = {
     # CUDA cores
     "generic_d16": dict(ns=[5, 0, 40], kvs=[9, 4, 300], H=4, Hkv=2, D=16, P=4, sinks=True),
     "generic_d80_p3": dict(ns=[5, 7], kvs=[90, 7], H=6, Hkv=2, D=80, P=3, layout="NHD", window=20),
+    "generic_window_below_depth": dict(ns=[40, 7], kvs=[90, 30], H=4, Hkv=2, D=48, P=8, window=2, deep=True),
+    "window_below_depth": dict(ns=[40, 7], kvs=[290, 30], H=4, Hkv=2, D=128, P=8, window=2, deep=True),
     "generic_d256": dict(ns=[33], kvs=[200], H=2, Hkv=1, D=256, P=16),
     "generic_e4m3_d64": dict(ns=[9, 2], kvs=[200, 77], H=4, Hkv=1, D=64, P=16, cache="e4m3"),
 }
@@ -299,9 +301,11 @@ def test_rows_that_see_nothing(cuda_lib, cfg, sinks):
                                  dict(H=8, Hkv=2, D=128, P=16, cache="e4m3"), dict(H=16, Hkv=1, D=128, P=128),
                                  dict(H=4, Hkv=2, D=48, P=8, window=40), dict(H=4, Hkv=2, D=128, P=16, cache="e4m3"),
                                  dict(H=4, Hkv=2, D=128, P=16, cache="e4m3", window=40),
-                                 dict(H=16, Hkv=1, D=128, P=128, cache="e4m3")],
+                                 dict(H=16, Hkv=1, D=128, P=128, cache="e4m3"), dict(H=8, Hkv=2, D=64, P=16, window=2, deep=True),
+                                 dict(H=4, Hkv=2, D=48, P=8, window=2, deep=True)],
                          ids=["bf16", "d64_window", "e4m3", "two_tiles", "generic", "e4m3_rows_twice",
-                              "e4m3_rows_twice_window", "e4m3_two_tiles"])
+                              "e4m3_rows_twice_window", "e4m3_two_tiles", "d64_window_below_depth",
+                              "generic_window_below_depth"])
 @pytest.mark.parametrize("kv", [40, 260])
 def test_what_unseen_keys_hold_does_not_matter(cuda_lib, cfg, kv):
     """NaN and infinities in V (and NaN in K) of sibling nodes, of page tails, of pages nobody uses and before a window."""
