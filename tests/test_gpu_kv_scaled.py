@@ -208,3 +208,14 @@ def test_no_tokens_streams_and_graphs(cuda_lib):
     torch.cuda.synchronize()
     codes, unit = definition(y)
     assert same(k.cpu(), codes * unit[..., None]) and torch.equal(k, v)
+
+
+def test_outputs_larger_than_the_memory(cuda_lib):
+    """torch's own error for it, and the next call is fine."""
+    pool = torch.zeros((1, 64, 1, 256), dtype=torch.uint8, device=DEV).view(torch.float8_e4m3fn)
+    scale = torch.ones((1, 64, 1), device=DEV)
+    many = torch.zeros(8_000_000, dtype=torch.int32, device=DEV)  # 32 KiB of K and of V each
+    with pytest.raises(torch.cuda.OutOfMemoryError):
+        cuda_lib.read_kv_scaled((pool, pool), (scale, scale), many)
+    k, v = cuda_lib.read_kv_scaled((pool, pool), (scale, scale), many[:3])
+    assert (k == 0).all() and (v == 0).all() and cuda_lib.device_status() == 0
