@@ -202,7 +202,10 @@ class _On:
         if dev < 0:
             raise ValueError(f"tensors on {first.device}: CUDA tensors are needed")
         if stream is not None and not isinstance(stream, torch.cuda.Stream):
-            stream = torch.cuda.ExternalStream(int(stream), device=first.device)
+            # (0 is the default stream's handle; ExternalStream(0) is a new stream)
+            handle = int(stream)
+            stream = (torch.cuda.ExternalStream(handle, device=first.device) if handle != 0
+                      else torch.cuda.default_stream(first.device))
         if stream is not None and stream.device != first.device:
             raise ValueError(f"a stream of {stream.device} for tensors on {first.device}")
         # (torch.cuda.stream makes its stream's device current)
