@@ -492,8 +492,12 @@ B2PA_API int b2pa_read_kv_scaled(const b2pa_tensor* k_pool, const b2pa_tensor* v
  * sets B2PA_DEV_BAD_PAGE and its keys read as 0.  Page ids of keys that no row
  * sees (before every window, past the end) are not used.
  *
- * e4m3 pools take their scales in bmm1_scale and bmm2_scale.  Shapes that the
- * tensor-core path does not take (b2pa_query_path) run on CUDA cores.
+ * e4m3 pools take their scales in bmm1_scale and bmm2_scale.  On the tensor
+ * cores the probabilities are rounded to bf16 before they weigh V, over e4m3 pools
+ * to f16 (by half a step, 2^-11 of themselves, down to 2^-21 of their row's largest,
+ * and by 2^-32 of the largest below); scores over e4m3 pools take each q element to
+ * within 2^-17 of its row's largest.  Sums are fp32.  Shapes that the tensor-core
+ * path does not take (b2pa_query_path) run on CUDA cores, in fp32.
  * Asynchronous on `stream`, capturable after one call on the device; allocates
  * nothing of its own after that.
  */

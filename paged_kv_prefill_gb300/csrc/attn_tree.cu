@@ -10,7 +10,7 @@
 // kv head the time is that of the K/V stream from HBM, beyond that of the
 // tensor cores and the exponentials.  Measured: 32 requests of 512 to 8192 keys,
 // 9 to 16 nodes x 4 heads, D = 128: 104 us, 5.6 TB/s (0.83 of the copy rate);
-// the same with e4m3, up to 16384 keys and 8 nodes: 145 us, 4.5 TB/s (0.66);
+// the same with e4m3, up to 16384 keys and 8 nodes: 160 us, 4.1 TB/s (0.60);
 // 8 requests of up to 16384 keys, 64 nodes x 8 heads: 112 us, 940 TFLOP/s (0.49 of
 // the bf16 rate); one request, 8 nodes, 2048 keys: 14.4 us, latency.
 //
@@ -33,9 +33,8 @@
 //            kTiles 2: a query tile each, in turns.
 //   warp 3   loads Q (a TMA box per softmax warp's tokens and column block), and
 //            makes V safe where rows see different keys (see below).
-//   warps 4-7, 8-11   softmax A and B: one thread per MMA row.  e4m3 caches:
-//            they split the next segment's Q into two e4m3 terms while a segment's
-//            last P V runs (e4m3 batch: 146 us, 164 with warp 3 doing it).
+//   warps 4-7, 8-11   softmax A and B: one thread per MMA row.
+//   warps 12-15   (e4m3 caches only) split Q into two e4m3 terms and convert V to f16.
 //
 // kTiles 2 (more than one tile of rows in some request): A and B each have
 // their own query tile, and K/V are read once for both.  kTiles 1: there is
@@ -45,21 +44,24 @@
 // known, so that tensor core, both groups and loads overlap although there is
 // a single tile of rows; at the end each group writes half of the columns.
 //
-// e4m3 caches.  K and V go to the tensor core as they are (kind::f8f6f4), so
-// that no thread touches them; what is 16 or 32 bits wide is split instead.
-// A Q row is scaled by a power of two and split into two e4m3 terms whose sum
-// is exact for every element within 2^-9 of the row's largest, and off by at
-// most 2^-17 of the largest below; S = Qh K^T + Ql K^T.  A probability, kept in
-// (0, 2^8] with its row's largest at 2^4 or more, is split into its leading
-// four bits and the rest rounded to four: off by at most half a step of bf16
-// (2^-8), down to 2^-14 of the row's largest.  (The other four powers of two
-// let a row's maximum grow by that much before O has to be rescaled.)
-// With two MMAs for every one of a 16-bit cache, and 128 cycles for each P V
-// MMA of 32 keys, where one of 16 keys takes 80, these would be bound by the
-// tensor core.  So a tile of at most 64 rows is stacked: its rows are in it
-// twice, one copy's P holding the leading terms and the other's the rest, and
-// one set of P V MMAs does both; the copies' O are added at the end, through
-// shared memory (e4m3 batch of 8 nodes x 4 heads: 173 us, stacked 165).
+// e4m3 caches.  K goes to the tensor core as it is (kind::f8f6f4), and Q is split
+// instead: a Q row is scaled by a power of two and split into two e4m3 terms
+// whose sum is exact for every element within 2^-9 of the row's largest, and off
+// by at most 2^-17 of the largest below; S = Qh K^T + Ql K^T.  P V is done in f16
+// (kind::f16), V being converted to f16, exactly, on its way from the ring.  A
+// long tail of small probabilities is together as heavy as the row's largest, so
+// that P needs its relative precision over a wide range: kept in (0, 2^15] with
+// its row's largest at 2^7 or more, it is off by at most half a step of f16
+// (2^-11 of itself) down to 2^-21 of the row's largest, and by 2^-32 of the largest
+// below.  (P in two e4m3 terms with V as it is took 145 us for that batch, not 160,
+// but its steps end at 2^-14 of the row's largest: of a tail of 16384 keys behind a
+// lead of 11 nats 0.84 was lost.)  What bounds this: the ring.  V in f16, two tiles
+// of it, leaves room for 128 KB of K and V on their way (96 KB with two query tiles).
+// So one Q buffer does, and the converting warps free a V entry as soon as they
+// have its rows in registers (161 us; 164 once they are converted).
+//
+// bf16 caches.  P is bf16 (off by half a step, 2^-8 of itself, over all of fp32's
+// range), since both operands of an MMA have one type and V's range needs bf16.
 //
 // V and keys that some rows of a tile do not see: their P is 0, but 0 times
 // an infinity or NaN is NaN.  Keys before the item's first and past the last
@@ -81,38 +83,40 @@ namespace b2pa {
 
 namespace {
 
-constexpr int kTreeThreads = 384;
 constexpr int kTreeSlots = 4;     // posted segments in flight
-constexpr int kTreeConsumers = 12;  // reads of a posted segment: warps 1 and 2, twice by warp 3, the softmax warps
 constexpr int kBadSlots = 16;     // segments whose V was found not to be finite: a bit each
 
-template <int D, bool FP8, int kTiles, bool kStack>
+template <int D, bool FP8, int kTiles>
 struct TreeCfg {
     static constexpr int kBlockBytes = kQRows * 128;        // 128 rows of one 128-byte column block
     static constexpr int kHalves = FP8 ? 1 : D / 64;        // column blocks of a K/V row
     static constexpr int kQHalves = D / 64;                 // column blocks of a Q row (bf16; e4m3: its two terms)
     static constexpr int kKvBytes = kHalves * kBlockBytes;
     static constexpr int kQBytes = kQHalves * kBlockBytes;
-    static constexpr int kQBufs = D == 128 && !FP8 ? 1 : 2;
-    static constexpr int kAddBytes = kStack ? 2 * 64 * 128 : 0;  // per group: 64 rows x 32 columns of O's second copy
-    static constexpr int kRing = 224 * 1024 - kQBufs * kTiles * kQBytes - kAddBytes;
-    static constexpr int kEntries = kRing / kKvBytes;       // K and V tiles, alternating
+    static constexpr int kQBufs = D == 128 ? 1 : 2;
+    static constexpr int kVBufs = FP8 ? 2 : 0;              // V tiles converted to f16
+    static constexpr int kVBytes = 2 * kBlockBytes;
+    static constexpr int kRing = 224 * 1024 - kQBufs * kTiles * kQBytes - kVBufs * kVBytes;
+    // K and V tiles, alternating (e4m3: K in the even entries and V in the odd ones, which have other readers)
+    static constexpr int kEntries = FP8 ? kRing / kKvBytes / 2 * 2 : kRing / kKvBytes;
     static constexpr int kOffRing = kQBufs * kTiles * kQBytes;
-    static constexpr int kOffAdd = kOffRing + kEntries * kKvBytes;
-    static constexpr int kOffBar = kOffAdd + kAddBytes;
+    static constexpr int kOffV = kOffRing + kEntries * kKvBytes;
+    static constexpr int kOffBar = kOffV + kVBufs * kVBytes;
     static constexpr int kSBufs = kTiles == 1 ? 3 : 2;
-    static constexpr int kNumBars = 3 * kEntries + 3 * kQBufs + 3 * kSBufs + 2 + 8 + 2 + 2 + 2 * kTreeSlots + 1 + (kStack ? 4 : 0);
+    static constexpr int kNumBars = 3 * kEntries + 3 * kQBufs + 3 * kSBufs + 2 + 8 + 2 + 2 + 2 * kTreeSlots + 1 + 2 * kVBufs;
     static constexpr int kOffMisc = kOffBar + kNumBars * 8;  // tmem address, abort flag
     static constexpr int kOffItems = kOffMisc + 16;
     static constexpr int kOffBad = kOffItems + kTreeSlots * 12 * 4;
     static constexpr int kOffExp = kOffBad + 4;  // e4m3: exponent of each Q row (int8)
     static constexpr int kOffMl = (kOffExp + (FP8 ? kQBufs * kTiles * kQRows : 0) + 15) / 16 * 16;
     static constexpr int kSmemBytes = kOffMl + (kTiles == 1 ? 2 * kQRows * 8 : 0);  // ml; its first half: the running maxima
+    static constexpr int kThreads = FP8 ? 512 : 384;
+    // reads of a posted segment: warps 1 and 2, twice by warp 3, the softmax and the converting warps
+    static constexpr int kConsumers = FP8 ? 16 : 12;
     static constexpr int kTmemCols = 512;
     static constexpr int kOCol = kSBufs * kKvTile;
     static_assert(D == 64 || D == 128, "head_dim");
     static_assert(!FP8 || D == 128, "e4m3 caches: D = 128");
-    static_assert(!kStack || (FP8 && kTiles == 1), "stacked tiles: e4m3 caches");
     static_assert(kEntries >= 5 && kEntries <= 32, "ring");
     static_assert(kSmemBytes <= 232448, "shared memory");
 };
@@ -126,7 +130,7 @@ struct TreeCtx : Ctx {
     // both groups posted (m, l); both have read O
     uint64_t *m_ready, *met, *left;
     uint64_t* turn;                          // kTiles 2, [2]: this tile's MMAs next (m_ready's place)
-    uint64_t *add_full, *add_free;           // kStack, [2]: 32 columns of O's second copy posted, added
+    uint64_t *v_full, *v_empty;              // [kVBufs]: V in f16 there, its P V done
     uint64_t *drain /* [2] */, *it_full, *it_empty, *never;
 };
 
@@ -195,10 +199,10 @@ __device__ __forceinline__ int tile_tokens(const TreeRows& r, const Seg& s, int 
 // ---------------------------------------------------------------------------
 // warp 0
 // ---------------------------------------------------------------------------
-template <int D, bool FP8, int kTiles, bool kStack>
+template <int D, bool FP8, int kTiles>
 __device__ void tree_producer(const TreeParams& p, const TreeCtx& c, long long pos, long long end, int b, long long base)
 {
-    using C = TreeCfg<D, FP8, kTiles, kStack>;
+    using C = TreeCfg<D, FP8, kTiles>;
     const int lane = threadIdx.x & 31;
     const uint32_t ring = smem_u32(c.base + C::kOffRing);
     const int P = p.page_size, log2_p = 31 - __clz(P);  // the tensor-core path takes powers of two only
@@ -289,8 +293,8 @@ __device__ void tree_producer(const TreeParams& p, const TreeCtx& c, long long p
 // warps 1 and 2.  The whole warp waits and runs the issue code; MMAs and
 // commits are predicated on lane 0.
 // ---------------------------------------------------------------------------
-// f32 accumulators; bf16 operands (format 1 of kind::f16) or e4m3 (format 0 of
-// kind::f8f6f4); b_mn: B is MN-major (V).
+// f32 accumulators; bf16 operands (format 1 of kind::f16), or those of an e4m3 cache: e4m3 for
+// S (format 0 of kind::f8f6f4) and f16 for O (format 0 of kind::f16); b_mn: B is MN-major (V).
 __device__ __forceinline__ constexpr uint32_t tree_idesc(bool fp8, int n, bool b_mn)
 {
     const uint32_t fmt = fp8 ? 0u : 1u;
@@ -344,22 +348,21 @@ struct RingPos {
 };
 
 // The MMAs of one query tile and kv tile.
-template <int D, bool FP8, int kTiles, bool kStack>
+template <int D, bool FP8, int kTiles>
 struct TreeMma {
-    using C = TreeCfg<D, FP8, kTiles, kStack>;
+    using C = TreeCfg<D, FP8, kTiles>;
     static constexpr uint32_t kIdescS = tree_idesc(FP8, kKvTile, false), kIdescO = tree_idesc(FP8, D, true);
     static constexpr uint32_t kEntryW = C::kKvBytes >> 4, kQTileW = C::kQBytes >> 4, kBlockW = C::kBlockBytes >> 4;
-    // A step of P V is 8 columns of P: 16 keys (16 rows of V), or 32 of one e4m3
-    // term (both, stacked); kSteps of them are a tile.  Of a request's last tile
-    // the steps behind the last key are left out.
-    static constexpr int kStepsAtKeys = FP8 && !kStack ? 2 : 1, kKeys = FP8 ? 32 : 16;
-    static constexpr int kSteps = kKvTile / kKeys * kStepsAtKeys;
+    // A step of P V is 8 columns of P, 16 keys (16 rows of V).  Of a request's last
+    // tile the steps behind the last key are left out.
+    static constexpr int kKeys = 16, kSteps = kKvTile / kKeys;
+    static constexpr uint32_t kVEntryW = (FP8 ? C::kVBytes : C::kKvBytes) >> 4;
     uint32_t tmem, q_lo, k_lo, v_lo, issue;
     __device__ __forceinline__ explicit TreeMma(const TreeCtx& c)
         : tmem(c.tmem),
           q_lo(sdesc_lo(smem_u32(c.base), 16)),                           // K-major: LBO unused
           k_lo(sdesc_lo(smem_u32(c.base + C::kOffRing), 16)),
-          v_lo(sdesc_lo(smem_u32(c.base + C::kOffRing), C::kBlockBytes)),  // MN-major: LBO = next column block
+          v_lo(sdesc_lo(smem_u32(c.base + (FP8 ? C::kOffV : C::kOffRing)), C::kBlockBytes)),  // MN-major: LBO = next column block
           issue((threadIdx.x & 31) == 0 ? 1u : 0u)
     {
     }
@@ -378,16 +381,12 @@ struct TreeMma {
                 mma_ss_wp(d, a0 + block + step, b0 + block + step, kTreeDescHi, kIdescS, k > 0 ? 1u : 0u, issue);
         }
     }
-    // O (tile t) += P (buffer s) times V (ring entry e), of which `keys` are the request's
+    // O (tile t) += P (buffer s) times V (ring entry e, or e4m3: buffer e), of which `keys` are the request's
     __device__ __forceinline__ void values(uint32_t t, uint32_t s, uint32_t e, int keys, bool first) const
     {
-        const uint32_t b0 = v_lo + e * kEntryW, a = tmem + s * kKvTile, d = tmem + (uint32_t)C::kOCol + t * D;
+        const uint32_t b0 = v_lo + e * kVEntryW, a = tmem + s * kKvTile, d = tmem + (uint32_t)C::kOCol + t * D;
         auto step = [&](int k, uint32_t acc) {
-            const uint32_t ak = a + (uint32_t)(k * 8), bk = b0 + (uint32_t)(k / kStepsAtKeys * kKeys * 8);
-            if constexpr (FP8)
-                mma8_ts_wp(d, ak, bk, kTreeDescHi, kIdescO, acc, issue);
-            else
-                mma_ts_wp(d, ak, bk, kTreeDescHi, kIdescO, acc, issue);
+            mma_ts_wp(d, a + (uint32_t)(k * 8), b0 + (uint32_t)(k * kKeys * 8), kTreeDescHi, kIdescO, acc, issue);
         };
         step(0, first ? 0u : 1u);
         if (keys >= kKvTile) {
@@ -395,7 +394,7 @@ struct TreeMma {
             for (int k = 1; k < kSteps; ++k)
                 step(k, 1u);
         } else {
-            const int steps = (keys + kKeys - 1) / kKeys * kStepsAtKeys;
+            const int steps = (keys + kKeys - 1) / kKeys;
 #pragma unroll 1
             for (int k = 1; k < steps; ++k)
                 step(k, 1u);
@@ -415,12 +414,39 @@ __device__ __forceinline__ bool wait_v(const TreeCtx& c, const Ring& at, bool mi
     return ok;
 }
 
+// Where P V finds V: a ring entry, or, e4m3, one of two buffers in f16.
+template <int kEntries, bool FP8>
+struct VPos {
+    RingPos<kEntries> ring{1};
+    uint32_t buf = 0, phase = 0;
+    uint32_t ready_bits = 0;  // parity of each entry's next v_ready phase
+    __device__ __forceinline__ uint32_t at() const { return FP8 ? buf : ring.e; }
+    __device__ __forceinline__ bool wait(const TreeCtx& c, bool mixed)
+    {
+        return FP8 ? wait_at(smem_u32(c.v_full) + buf * 8, phase, c) : wait_v(c, ring, mixed, ready_bits);
+    }
+    // what to arrive on when its MMAs are done
+    __device__ __forceinline__ uint32_t done(const TreeCtx& c) const
+    {
+        return FP8 ? smem_u32(c.v_empty) + buf * 8 : smem_u32(c.kv_empty) + ring.e * 8;
+    }
+    __device__ __forceinline__ void next()
+    {
+        if (FP8) {
+            phase ^= buf;
+            buf ^= 1;
+        } else {
+            ring.next();
+        }
+    }
+};
+
 // kTiles 1, warp 1: S of every kv tile, three buffers in turn.
-template <int D, bool FP8, bool kStack>
+template <int D, bool FP8>
 __device__ void tree_s(const TreeParams& p, const TreeCtx& c)
 {
-    using C = TreeCfg<D, FP8, 1, kStack>;
-    const TreeMma<D, FP8, 1, kStack> mma(c);
+    using C = TreeCfg<D, FP8, 1>;
+    const TreeMma<D, FP8, 1> mma(c);
     const uint32_t kv_full = smem_u32(c.kv_full), s_full = smem_u32(c.s_full), s_free = smem_u32(c.s_free);
     RingPos<C::kEntries> at(0);
     uint32_t buf = 0, turn = 0;
@@ -457,15 +483,14 @@ __device__ void tree_s(const TreeParams& p, const TreeCtx& c)
 }
 
 // kTiles 1, warp 2: O += P V.
-template <int D, bool FP8, bool kStack>
+template <int D, bool FP8>
 __device__ void tree_pv(const TreeParams& p, const TreeCtx& c)
 {
-    using C = TreeCfg<D, FP8, 1, kStack>;
-    const TreeMma<D, FP8, 1, kStack> mma(c);
-    const uint32_t kv_empty = smem_u32(c.kv_empty), p_full = smem_u32(c.p_full), s_free = smem_u32(c.s_free);
-    RingPos<C::kEntries> at(1);
+    using C = TreeCfg<D, FP8, 1>;
+    const TreeMma<D, FP8, 1> mma(c);
+    const uint32_t p_full = smem_u32(c.p_full), s_free = smem_u32(c.s_free);
+    VPos<C::kEntries, FP8> at;
     uint32_t buf = 0, turn = 0;
-    uint32_t ready_bits = 0;  // parity of each entry's next v_ready phase
     bool ok = true;
     for (uint32_t n = 0; ok; ++n) {
         Seg s;
@@ -473,13 +498,13 @@ __device__ void tree_pv(const TreeParams& p, const TreeCtx& c)
             break;
         const int mixed0 = s.mixed0(p.window), mixed1 = s.mixed1();
         for (int i = 0; i < s.tiles; ++i) {
-            ok = wait_v(c, at, i < mixed0 || i >= mixed1, ready_bits) && wait_at(p_full + buf * 8, turn, c);
+            ok = at.wait(c, i < mixed0 || i >= mixed1) && wait_at(p_full + buf * 8, turn, c);
             if (!ok)
                 break;
             tc_fence_after();
-            mma.values(0, buf, at.e, s.kv_len - (s.j0 + i) * kKvTile, i == 0);
+            mma.values(0, buf, at.at(), s.kv_len - (s.j0 + i) * kKvTile, i == 0);
             mma_commit_at(s_free + buf * 8, mma.issue);
-            mma_commit_at(kv_empty + at.e * 8, mma.issue);
+            mma_commit_at(at.done(c), mma.issue);
             at.next();
             if (++buf == 3) {
                 buf = 0;
@@ -505,14 +530,14 @@ __device__ void tree_pv(const TreeParams& p, const TreeCtx& c)
 template <int D, bool FP8>
 __device__ void tree_tile(const TreeParams& p, const TreeCtx& c, int t)
 {
-    using C = TreeCfg<D, FP8, 2, false>;
-    const TreeMma<D, FP8, 2, false> mma(c);
+    using C = TreeCfg<D, FP8, 2>;
+    const TreeMma<D, FP8, 2> mma(c);
     const uint32_t kv_full = smem_u32(c.kv_full), kv_empty = smem_u32(c.kv_empty);
     const uint32_t p_full = smem_u32(c.p_full) + t * 8, s_full = smem_u32(c.s_full) + t * 8;
     const uint32_t my_turn = smem_u32(c.turn) + t * 8, your_turn = smem_u32(c.turn) + (t ^ 1) * 8;
-    RingPos<C::kEntries> at_k(0), at_v(1);
+    RingPos<C::kEntries> at_k(0);
+    VPos<C::kEntries, FP8> at_v;
     uint32_t p_phase = 0, turn_phase = t ^ 1;  // (tile 0 goes first)
-    uint32_t ready_bits = 0;  // parity of each entry's next v_ready phase
     bool ok = t != 0 || !p.inject_stall || wait_bar(c.never, 0, c);  // failure-detection tests
     for (uint32_t n = 0; ok; ++n) {
         Seg s;
@@ -526,7 +551,7 @@ __device__ void tree_tile(const TreeParams& p, const TreeCtx& c, int t)
         for (int i = -1; i < s.tiles; ++i) {  // P V of tile i, S of tile i + 1
             const bool pv = i >= 0, sc = i + 1 < s.tiles;
             if (pv) {
-                ok = ok && wait_v(c, at_v, i < mixed0 || i >= mixed1, ready_bits);
+                ok = ok && at_v.wait(c, i < mixed0 || i >= mixed1);
                 if (mine) {
                     ok = ok && wait_at(p_full, p_phase, c);
                     p_phase ^= 1;
@@ -542,7 +567,7 @@ __device__ void tree_tile(const TreeParams& p, const TreeCtx& c, int t)
                 break;
             tc_fence_after();
             if (mine && pv)
-                mma.values(t, t, at_v.e, s.kv_len - (s.j0 + i) * kKvTile, i == 0);
+                mma.values(t, t, at_v.at(), s.kv_len - (s.j0 + i) * kKvTile, i == 0);
             if (mine && sc)
                 mma.scores(t, qb * 2 + t, at_k.e);
             // before the commit, which waits for room among the MMAs
@@ -551,7 +576,7 @@ __device__ void tree_tile(const TreeParams& p, const TreeCtx& c, int t)
                 mma_commit_at(s_full, mma.issue);
             // K and V are released by the softmax group, which hears of it all the same
             if (pv) {
-                mbar_arrive_at(kv_empty + at_v.e * 8, mine ? 0u : mma.issue);
+                mbar_arrive_at(at_v.done(c), mine ? 0u : mma.issue);
                 at_v.next();
             }
             if (sc) {
@@ -590,29 +615,15 @@ __device__ __forceinline__ float2 from_e4m3x2(uint32_t two)
 // are the high bytes of the halves of `hi` and `lo`.  In f16, v 2^-8 has e4m3's
 // exponent field, subnormals included (2^-14 against 2^-6), so that a code is
 // the top of the f16 bits: the leading term by cutting, its remainder (exact in
-// f16) by rounding half up.  (The conversion instruction from f32 to e4m3 runs
-// at half the rate of an exponential on the same unit: with two of them per
-// pair of probabilities they were the bound.)
-template <bool kSigned>
+// f16) by rounding half up.
 __device__ __forceinline__ void split_e4m3(float2 v, uint32_t& hi, uint32_t& lo)
 {
     uint32_t f, r;
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(f) : "f"(v.y), "f"(v.x));
-    const uint32_t sign = kSigned ? f & 0x80008000u : 0u;
-    const uint32_t mag = kSigned ? f & 0x7FFF7FFFu : f;
+    const uint32_t sign = f & 0x80008000u, mag = f & 0x7FFF7FFFu;
     asm("sub.f16x2 %0, %1, %2;" : "=r"(r) : "r"(mag), "r"(mag & 0x7F807F80u));
     hi = mag << 1 | sign;
     lo = r * 2u + 0x00800080u | sign;
-}
-
-// One of those terms of two values: the leading one with cut = half = 0, the
-// other with split_e4m3's masks.
-__device__ __forceinline__ uint32_t term_e4m3(float2 v, uint32_t cut, uint32_t half)
-{
-    uint32_t f, r;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(f) : "f"(v.y), "f"(v.x));
-    asm("sub.f16x2 %0, %1, %2;" : "=r"(r) : "r"(f), "r"(f & cut));
-    return r * 2u + half;
 }
 
 // `count` Q rows of 128 bf16 values from row0 (a multiple of 16; at most 16) in
@@ -621,7 +632,7 @@ __device__ __forceinline__ uint32_t term_e4m3(float2 v, uint32_t cut, uint32_t h
 // the low one in the second.  exps[row] is the power of two a row was scaled
 // by, which brings its largest value to [2^7, 2^8).  A row that is not finite
 // becomes NaN, which is what every score of it makes of the softmax.
-__device__ __noinline__ void split_q_rows(uint8_t* tile, int block_bytes, int row0, int count, int8_t* exps)
+__device__ __forceinline__ void split_q_rows(uint8_t* tile, int block_bytes, int row0, int count, int8_t* exps)
 {
     const int lane = threadIdx.x & 31;
     // a row's maximum by two lanes, a block each
@@ -656,7 +667,7 @@ __device__ __noinline__ void split_q_rows(uint8_t* tile, int block_bytes, int ro
         uint32_t hi[4], lo[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            split_e4m3<true>(make_float2(__uint_as_float(u[i] << 16) * sc, __uint_as_float(u[i] & 0xFFFF0000u) * sc), hi[i], lo[i]);
+            split_e4m3(make_float2(__uint_as_float(u[i] << 16) * sc, __uint_as_float(u[i] & 0xFFFF0000u) * sc), hi[i], lo[i]);
         __syncwarp();  // the whole row is read
         if (on) {
             uint8_t* to = row + (((c >> 1) ^ sw) << 4) + (c & 1) * 8;
@@ -685,17 +696,17 @@ __device__ __forceinline__ bool not_finite(uint4 v)
 }
 
 // The Q tiles of a segment, into buffer qb.
-template <int D, bool FP8, int kTiles, bool kStack>
+template <int D, bool FP8, int kTiles>
 __device__ __forceinline__ void load_q(const TreeParams& p, const TreeCtx& c, const Seg& s, uint32_t qb)
 {
-    using C = TreeCfg<D, FP8, kTiles, kStack>;
+    using C = TreeCfg<D, FP8, kTiles>;
     const int lane = threadIdx.x & 31;
     const TreeRows& r = p.rows;
     // lane = (tile, warp's tokens, column block): one box each
     const int t = lane / (4 * C::kQHalves), w = lane / C::kQHalves % 4, h = lane % C::kQHalves;
     const int toks = t < kTiles ? tile_tokens(r, s, t) : 0;
-    const int per = r.by_warp ? (toks + r.warps - 1) / r.warps : r.tile_toks;
-    const int first = w % r.warps * per;  // this warp's first token
+    const int per = r.by_warp ? (toks + 3) / 4 : r.tile_toks;
+    const int first = w * per;  // this warp's first token
     const bool box = toks > 0 && first < toks && (r.by_warp || w == 0);
     const uint32_t boxes = __popc(__ballot_sync(0xffffffffu, box));
     mbar_arrive_expect_tx_p(&c.q_full[qb], boxes * (uint32_t)(r.G * r.box_toks * 128), lane == 0 ? 1u : 0u);
@@ -708,10 +719,10 @@ __device__ __forceinline__ void load_q(const TreeParams& p, const TreeCtx& c, co
 
 // V entry e, kv tile j of segment s (its n-th): keys that no row sees become
 // 0, and so do keys that some rows may not see and that are not finite.
-template <int D, bool FP8, int kTiles, bool kStack>
+template <int D, bool FP8, int kTiles>
 __device__ __forceinline__ void safe_v(const TreeParams& p, const TreeCtx& c, const Seg& s, uint32_t n, int j, uint32_t e)
 {
-    using C = TreeCfg<D, FP8, kTiles, kStack>;
+    using C = TreeCfg<D, FP8, kTiles>;
     constexpr int kChunks = 8 * C::kHalves;  // 16-byte pieces of a V row
     constexpr int kRowsAtOnce = 32 / kChunks;
     const int lane = threadIdx.x & 31;
@@ -723,7 +734,7 @@ __device__ __forceinline__ void safe_v(const TreeParams& p, const TreeCtx& c, co
     auto at = [&](int row) { return reinterpret_cast<uint4*>(v + row * 128); };
     const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
     // rows that no row of Q sees (they may never have been loaded)
-    constexpr int kStep = FP8 ? 32 : 16;  // keys of an MMA: the steps after the last key are not issued
+    constexpr int kStep = 16;  // keys of an MMA: the steps after the last key are not issued
     const int seen0 = min(max(lo - k0, 0), kKvTile), seen1 = min(s.kv_len - k0, kKvTile);
     for (int row = sub; row < seen0; row += kRowsAtOnce)
         *at(row) = zero;
@@ -759,10 +770,10 @@ __device__ __forceinline__ void safe_v(const TreeParams& p, const TreeCtx& c, co
 
 // Q runs up to a segment (and a buffer) ahead of V; what is possible next is
 // done, and this warp waits for neither while the other could go.
-template <int D, bool FP8, int kTiles, bool kStack>
+template <int D, bool FP8, int kTiles>
 __device__ void tree_feed(const TreeParams& p, const TreeCtx& c)
 {
-    using C = TreeCfg<D, FP8, kTiles, kStack>;
+    using C = TreeCfg<D, FP8, kTiles>;
     const int lane = threadIdx.x & 31;
     volatile int* bad = reinterpret_cast<volatile int*>(c.base + C::kOffBad);
     // (decided for the whole warp, which stays converged)
@@ -783,7 +794,7 @@ __device__ void tree_feed(const TreeParams& p, const TreeCtx& c)
         }
         const uint32_t qb = (qn - 1) % C::kQBufs, ph = ((qn - 1) / C::kQBufs) & 1;
         if (q_at == kEmpty && here(&c.q_empty[qb], ph ^ 1)) {
-            load_q<D, FP8, kTiles, kStack>(p, c, qs, qb);
+            load_q<D, FP8, kTiles>(p, c, qs, qb);
             loads = qn;
             q_at = kNext;
             did = true;
@@ -812,7 +823,7 @@ __device__ void tree_feed(const TreeParams& p, const TreeCtx& c)
                 const int j = vs.j0 + vs.tiles - (int)((q_end - q + 1) >> 1);
                 const bool mixed = (q & 1) && vs.mixed(j, p.window);
                 if (mixed)
-                    safe_v<D, FP8, kTiles, kStack>(p, c, vs, vn - 1, j, e);
+                    safe_v<D, FP8, kTiles>(p, c, vs, vn - 1, j, e);
                 if (lane == 0) {
                     if (mixed)
                         mbar_arrive(&c.v_ready[e]);
@@ -923,7 +934,7 @@ __device__ __forceinline__ float kv_elem(const void* base, long long at)
     return __uint_as_float((uint32_t) static_cast<const uint16_t*>(base)[at] << 16);
 }
 
-// Slow path: column d of the V rows that tree_v zeroed because they are not
+// Slow path: column d of the V rows that safe_v zeroed because they are not
 // finite, weighted for this row, with the stabiliser m of its exponentials.
 template <bool FP8>
 __device__ __noinline__ float tree_bad_column(const TreeParams& p, const int* row_pages, const RowView view, int lo_all,
@@ -956,50 +967,104 @@ __device__ __noinline__ float tree_bad_column(const TreeParams& p, const int* ro
     return sum;
 }
 
-// e4m3: this warp's share of the n-th segment's Q becomes e4m3 terms (each group
-// its own tile, or half of the one tile's rows), if there is such a segment.
-template <typename C, int kTiles>
-__device__ __forceinline__ bool split_q(const TreeParams& p, const TreeCtx& c, uint32_t n, int t)
+// ---------------------------------------------------------------------------
+// warps 12-15 (e4m3 caches): a segment's Q into its two e4m3 terms, then its V,
+// tile by tile, into f16; one thread per row of V
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ uint32_t f16x2_of_e4m3x2(uint32_t two)
 {
-    const int wq = (threadIdx.x >> 5) & 3;
-    const uint32_t slot = n % kTreeSlots, qb = n % C::kQBufs;
-    if (!wait_bar(&c.it_full[slot], (n / kTreeSlots) & 1, c))
-        return false;
-    const volatile int* rec = c.item_slot + slot * 12;  // (taken, and released, later)
-    if (rec[0] == 0)
-        return true;
-    const int qt = kTiles == 1 ? 0 : t;
-    const int toks = min(p.rows.tile_toks, rec[6] - qt * p.rows.tile_toks);
-    if (!wait_bar(&c.q_full[qb], (n / C::kQBufs) & 1, c))
-        return false;
-    const int per = (toks + p.rows.warps - 1) / p.rows.warps;  // tokens of a quadrant
-    const int count = !p.rows.by_warp                      ? min(32, p.rows.G * toks - wq * 32)
-                      : wq % p.rows.warps * per < toks ? p.rows.G * per
-                                                           : 0;
-    uint8_t* tile = c.base + (qb * kTiles + qt) * C::kQBytes;
-    int8_t* exps = reinterpret_cast<int8_t*>(c.base + C::kOffExp) + (qb * kTiles + qt) * kQRows;
-#pragma unroll 1
-    for (int h = kTiles == 1 ? t : 0; h < (kTiles == 1 ? t + 1 : 2); ++h)
-        if (count > h * 16)
-            split_q_rows(tile, C::kBlockBytes, wq * 32 + h * 16, min(16, count - h * 16), exps);
-    fence_proxy_async_smem();
-    __syncwarp();
-    mbar_arrive_p(&c.q_conv[qb], (threadIdx.x & 31) == 0 ? 1u : 0u);
-    return true;
+    uint32_t h;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)two));
+    return h;
 }
 
-template <int D, bool FP8, int kTiles, bool kStack>
+template <int kTiles>
+__device__ void tree_convert(const TreeParams& p, const TreeCtx& c)
+{
+    using C = TreeCfg<128, true, kTiles>;
+    const int wq = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31, row = wq * 32 + lane, sw = row & 7;
+    const uint32_t lane0 = lane == 0 ? 1u : 0u;
+    RingPos<C::kEntries> at(1);
+    uint32_t buf = 0, phase = 1;
+    uint32_t ready_bits = 0;  // parity of each entry's next v_ready phase
+    bool ok = true;
+    for (uint32_t n = 0; ok; ++n) {
+        Seg s;
+        if (!take_seg(c, n, &s) || !s.on)
+            break;
+        const uint32_t qb = n % C::kQBufs;
+        if (!wait_bar(&c.q_full[qb], (n / C::kQBufs) & 1, c))
+            break;
+        // this warp's quadrant of the tiles, 16 rows at a time
+#pragma unroll 1
+        for (int k = 0; k < 2 * kTiles; ++k) {
+            const int t = k >> 1, r0 = (k & 1) * 16, toks = tile_tokens(p.rows, s, t);
+            const int per = (toks + 3) / 4;  // tokens of a quadrant
+            const int count = toks <= 0             ? 0
+                              : !p.rows.by_warp     ? min(32, p.rows.G * toks - wq * 32)
+                              : wq * per < toks ? p.rows.G * per
+                                                    : 0;
+            if (count > r0)
+                split_q_rows(c.base + (qb * kTiles + t) * C::kQBytes, C::kBlockBytes, wq * 32 + r0, min(16, count - r0),
+                             reinterpret_cast<int8_t*>(c.base + C::kOffExp) + (qb * kTiles + t) * kQRows);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        mbar_arrive_p(&c.q_conv[qb], lane0);
+        const int mixed0 = s.mixed0(p.window), mixed1 = s.mixed1();
+        for (int i = 0; i < s.tiles; ++i) {
+            ok = wait_bar(&c.kv_full[at.e], at.phase, c);
+            if (ok && (i < mixed0 || i >= mixed1)) {
+                ok = wait_bar(&c.v_ready[at.e], ready_bits >> at.e & 1u, c);
+                ready_bits ^= 1u << at.e;
+            }
+            if (!ok)
+                break;
+            const uint8_t* from = c.base + C::kOffRing + at.e * C::kKvBytes + row * 128;
+            uint8_t* to = c.base + C::kOffV + buf * C::kVBytes + row * 128;
+            uint4 x[8];  // the row, so that its ring entry is free before there is room for it in f16
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                x[k] = ld_shared_v4(smem_u32(from) + ((k ^ sw) << 4));
+            fence_proxy_async_smem();  // the loads are done before the entry's next copy
+            __syncwarp();
+            mbar_arrive_p(&c.kv_empty[at.e], lane0);
+            if (!(ok = wait_bar(&c.v_empty[buf], phase, c)))
+                break;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                uint8_t* block = to + (k >> 2) * C::kBlockBytes;
+                const int ch = 2 * k & 7;
+                *reinterpret_cast<uint4*>(block + ((ch ^ sw) << 4)) =
+                    make_uint4(f16x2_of_e4m3x2(x[k].x), f16x2_of_e4m3x2(x[k].x >> 16), f16x2_of_e4m3x2(x[k].y),
+                               f16x2_of_e4m3x2(x[k].y >> 16));
+                *reinterpret_cast<uint4*>(block + (((ch + 1) ^ sw) << 4)) =
+                    make_uint4(f16x2_of_e4m3x2(x[k].z), f16x2_of_e4m3x2(x[k].z >> 16), f16x2_of_e4m3x2(x[k].w),
+                               f16x2_of_e4m3x2(x[k].w >> 16));
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            mbar_arrive_p(&c.v_full[buf], lane0);
+            at.next();
+            phase ^= buf;
+            buf ^= 1;
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// softmax A (t = 0) and B (t = 1)
+// ---------------------------------------------------------------------------
+template <int D, bool FP8, int kTiles>
 __device__ void tree_softmax(const TreeParams& p, const TreeCtx& c, int t)
 {
-    using C = TreeCfg<D, FP8, kTiles, kStack>;
+    using C = TreeCfg<D, FP8, kTiles>;
     constexpr float kLog2e = 1.4426950408889634f;
-    // P = 2^(x - m + kBias): e4m3 terms use their range from 2^kBias down.  The
-    // stabiliser is renewed once the row's maximum has grown by kSlack.  The
-    // exponentials that are summed are P 2^-kScale (see split_e4m3).
-    constexpr float kBias = FP8 ? 4.f : 0.f, kSlack = FP8 ? 4.f : 8.f;
-    constexpr float kScale = FP8 ? 8.f : 0.f;
+    // P = 2^(x - m + kBias), in f16 over an e4m3 cache: the bias uses its range (see
+    // the top).  The stabiliser is renewed once the row's maximum has grown by kSlack.
+    constexpr float kBias = FP8 ? 7.f : 0.f, kSlack = 8.f;
     // 32-key steps of the exponentials that are unrolled (see below)
-    constexpr int kUnroll = kTiles == 2 && !FP8 ? 4 : 2;
+    constexpr int kUnroll = (kTiles == 2 ? 4 : 2) / (FP8 ? 2 : 1);
     const int wq = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31, row = wq * 32 + lane;
     const uint32_t lane_off = (uint32_t)(wq * 32) << 16;
     const uint32_t s0_tmem = c.tmem + lane_off;  // + buffer * kKvTile
@@ -1010,13 +1075,11 @@ __device__ void tree_softmax(const TreeParams& p, const TreeCtx& c, int t)
     float2* ml = reinterpret_cast<float2*>(c.base + C::kOffMl);
     const volatile int* bad = reinterpret_cast<const volatile int*>(c.base + C::kOffBad);
 
-    // kStack: the term of P that this warp's copy of the rows holds
-    const bool second = kStack && wq >= 2;
-    const uint32_t term_cut = second ? 0x7F807F80u : 0u, term_half = second ? 0x00800080u : 0u;
-    uint32_t adds = 0;  // kStack: column groups that the copies have added
+    // kTiles 2: what tells that the P V of tile g is done
+    auto v_done = [&](uint32_t g) { return FP8 ? &c.v_empty[g & 1] : &c.kv_empty[(2 * g + 1) % C::kEntries]; };
     uint32_t g0 = 0;   // kv tiles before this segment
     uint32_t s_cnt = 0, o_cnt = 0;  // kTiles 2: S and O of this group awaited so far
-    bool ok = !FP8 || split_q<C, kTiles>(p, c, 0, t);
+    bool ok = true;
     for (uint32_t n = 0; ok; ++n) {
         Seg s;
         if (!take_seg(c, n, &s) || !s.on)
@@ -1043,7 +1106,6 @@ __device__ void tree_softmax(const TreeParams& p, const TreeCtx& c, int t)
         }
         if (kTiles == 2 && qt * rows.tile_toks >= s.toks) {
             g0 += (uint32_t)s.tiles;
-            ok = !FP8 || split_q<C, kTiles>(p, c, n + 1, t);
             continue;
         }
         const int toks = tile_tokens(rows, s, qt);
@@ -1081,7 +1143,7 @@ __device__ void tree_softmax(const TreeParams& p, const TreeCtx& c, int t)
                 const uint32_t lane0 = lane == 0 ? 1u : 0u;
                 mbar_arrive_p(&c.kv_empty[2 * g % C::kEntries], lane0);
                 if (kTiles == 2 && i > 0)
-                    mbar_arrive_p(&c.kv_empty[(2 * g - 1) % C::kEntries], lane0);
+                    mbar_arrive_p(v_done(g - 1), lane0);
             }
             if (!warp_on) {  // no row of this warp is anyone's
                 if (kTiles == 1)
@@ -1131,7 +1193,7 @@ __device__ void tree_softmax(const TreeParams& p, const TreeCtx& c, int t)
                 l *= ex2_approx(m_used - m_new);
             const float alpha = need ? ex2_approx(m_old - m_new) : 1.f;
             m_used = m_new;
-            const float neg = m_used == -INFINITY ? 0.f : kBias - kScale - m_used;
+            const float neg = m_used == -INFINITY ? 0.f : kBias - m_used;
             const float2 sc = make_float2(sl2, sl2), ng = make_float2(neg, neg);
             float2 acc[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
                              make_float2(0.f, 0.f)};
@@ -1144,54 +1206,18 @@ __device__ void tree_softmax(const TreeParams& p, const TreeCtx& c, int t)
                 if (q < 3)
                     tmem_ld32(s_tmem + (uint32_t)(q * 32 + 32), rb);
                 uint32_t pk[16];
-                if constexpr (kStack) {  // eight columns of this copy's term
 #pragma unroll
-                    for (int w = 0; w < 8; ++w) {
-                        uint32_t a[2];
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            const int k = w * 4 + h * 2;
-                            const float2 y =
-                                __ffma2_rn(make_float2(__uint_as_float(ra[k]), __uint_as_float(ra[k + 1])), sc, ng);
-                            const float2 e = make_float2(ex2_approx(y.x), ex2_approx(y.y));
-                            acc[w & 3] = __fadd2_rn(acc[w & 3], e);
-                            a[h] = term_e4m3(e, term_cut, term_half);
-                        }
-                        pk[w] = __byte_perm(a[0], a[1], 0x7531);
-                    }
-                    uint32_t p8[8];
-#pragma unroll
-                    for (int w = 0; w < 8; ++w)
-                        p8[w] = pk[w];
-                    tmem_st8(s_tmem + (uint32_t)(q * 8), p8);
-                } else if constexpr (FP8) {  // eight columns of the leading terms, eight of the others
-#pragma unroll
-                    for (int w = 0; w < 8; ++w) {
-                        uint32_t a[2], b[2];
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            const int k = w * 4 + h * 2;
-                            const float2 y =
-                                __ffma2_rn(make_float2(__uint_as_float(ra[k]), __uint_as_float(ra[k + 1])), sc, ng);
-                            const float2 e = make_float2(ex2_approx(y.x), ex2_approx(y.y));
-                            acc[w & 3] = __fadd2_rn(acc[w & 3], e);
-                            split_e4m3<false>(e, a[h], b[h]);
-                        }
-                        pk[w] = __byte_perm(a[0], a[1], 0x7531);
-                        pk[8 + w] = __byte_perm(b[0], b[1], 0x7531);
-                    }
-                } else {
-#pragma unroll
-                    for (int w = 0; w < 16; ++w) {
-                        const float2 y = __ffma2_rn(
-                            make_float2(__uint_as_float(ra[2 * w]), __uint_as_float(ra[2 * w + 1])), sc, ng);
-                        const float2 e = make_float2(ex2_approx(y.x), ex2_approx(y.y));
-                        acc[w & 3] = __fadd2_rn(acc[w & 3], e);
+                for (int w = 0; w < 16; ++w) {
+                    const float2 y =
+                        __ffma2_rn(make_float2(__uint_as_float(ra[2 * w]), __uint_as_float(ra[2 * w + 1])), sc, ng);
+                    const float2 e = make_float2(ex2_approx(y.x), ex2_approx(y.y));
+                    acc[w & 3] = __fadd2_rn(acc[w & 3], e);
+                    if constexpr (FP8)
+                        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(pk[w]) : "f"(e.y), "f"(e.x));
+                    else
                         pk[w] = pack_bf16x2(e.x, e.y);
-                    }
                 }
-                if constexpr (!kStack)
-                    tmem_st16(s_tmem + (uint32_t)(q * 16), pk);
+                tmem_st16(s_tmem + (uint32_t)(q * 16), pk);
                 tmem_wait_ld();
 #pragma unroll
                 for (int k = 0; k < 32; ++k)
@@ -1228,12 +1254,7 @@ __device__ void tree_softmax(const TreeParams& p, const TreeCtx& c, int t)
             const float2 a = __fadd2_rn(a01, a23);
             l += a.x + a.y;
         }
-        if (FP8)
-            l *= 256.f;  // 2^kScale
         g0 += (uint32_t)s.tiles;
-        // the next segment's Q, while the last P V runs
-        if (FP8)
-            ok = ok && split_q<C, kTiles>(p, c, n + 1, t);
         if (!ok)
             break;
         // the last P V of the segment (kTiles 1: one O, one wait per segment)
@@ -1243,7 +1264,7 @@ __device__ void tree_softmax(const TreeParams& p, const TreeCtx& c, int t)
         }
         ++o_cnt;
         if (kTiles == 2 && wq == 0)
-            mbar_arrive_p(&c.kv_empty[(2 * g0 - 1) % C::kEntries], lane == 0 ? 1u : 0u);  // (g0: the next segment's)
+            mbar_arrive_p(v_done(g0 - 1), lane == 0 ? 1u : 0u);  // (g0: the next segment's)
         if constexpr (kTiles == 1) {
             // both groups' sums, relative to the last tile's maximum (the larger one)
             ml[t * kQRows + row] = make_float2(m_used, l);
@@ -1283,7 +1304,7 @@ __device__ void tree_softmax(const TreeParams& p, const TreeCtx& c, int t)
             for (int d = d0; d < d1; ++d) {
                 float o = __uint_as_float(tmem_ld1(o_tmem + (uint32_t)d));
                 tmem_wait_ld();
-                if (valid && !second)
+                if (valid)
                     o += tree_bad_column<FP8>(p, p.block_tables + (long long)b * p.bt_stride, view, s.lo_all(p.window),
                                               s.j0 * kKvTile, (s.j0 + s.tiles) * kKvTile, tok, h, s.kvh, p.scale_log2, m, d);
                 __syncwarp();
@@ -1291,39 +1312,12 @@ __device__ void tree_softmax(const TreeParams& p, const TreeCtx& c, int t)
             }
             tmem_wait_st();
         }
-        if (warp_on || kStack) {
+        if (warp_on) {
 #pragma unroll 1
             for (int d = d0; d < d1; d += 32) {
                 uint32_t o[32];
                 tmem_ld32(o_tmem + (uint32_t)d, o);
                 tmem_wait_ld();
-                if constexpr (kStack) {
-                    // the second copy's columns by way of shared memory: four columns of all rows together
-                    float4* add = reinterpret_cast<float4*>(c.base + C::kOffAdd) + t * (64 * 8) + (row & 63);
-                    uint64_t* bar = second ? &c.add_free[t] : &c.add_full[t];
-                    if (!(second && adds == 0) && !wait_bar(bar, (second ? adds - 1 : adds) & 1, c)) {
-                        ok = false;
-                        break;
-                    }
-                    ++adds;
-#pragma unroll
-                    for (int v = 0; v < 8; ++v) {
-                        if (second) {
-                            add[v * 64] = make_float4(__uint_as_float(o[4 * v]), __uint_as_float(o[4 * v + 1]),
-                                                      __uint_as_float(o[4 * v + 2]), __uint_as_float(o[4 * v + 3]));
-                        } else {
-                            const float4 y = add[v * 64];
-                            o[4 * v] = __float_as_uint(__uint_as_float(o[4 * v]) + y.x);
-                            o[4 * v + 1] = __float_as_uint(__uint_as_float(o[4 * v + 1]) + y.y);
-                            o[4 * v + 2] = __float_as_uint(__uint_as_float(o[4 * v + 2]) + y.z);
-                            o[4 * v + 3] = __float_as_uint(__uint_as_float(o[4 * v + 3]) + y.w);
-                        }
-                    }
-                    __syncwarp();
-                    mbar_arrive_p(second ? &c.add_full[t] : &c.add_free[t], lane == 0 ? 1u : 0u);
-                    if (second)
-                        continue;
-                }
                 if (valid && s.whole) {
                     const float2 f = make_float2(out_scale, out_scale);
 #pragma unroll
@@ -1346,11 +1340,9 @@ __device__ void tree_softmax(const TreeParams& p, const TreeCtx& c, int t)
                                                      __uint_as_float(o[4 * v + 2]), __uint_as_float(o[4 * v + 3]));
                 }
             }
-            if (valid && !second && !s.whole && (kTiles == 2 || t == 0))
+            if (valid && !s.whole && (kTiles == 2 || t == 0))
                 p.part_ml[part * kQRows + row] = make_float2(m, l);
         }
-        if (!ok)
-            break;
         tc_fence_before();
         if constexpr (kTiles == 1) {
             __syncwarp();
@@ -1362,10 +1354,10 @@ __device__ void tree_softmax(const TreeParams& p, const TreeCtx& c, int t)
 
 // ---------------------------------------------------------------------------
 
-template <int D, bool FP8, int kTiles, bool kStack>
-__global__ void __launch_bounds__(kTreeThreads, 1) attention_tree_kernel(const __grid_constant__ TreeParams p)
+template <int D, bool FP8, int kTiles>
+__global__ void __launch_bounds__(TreeCfg<D, FP8, kTiles>::kThreads, 1) attention_tree_kernel(const __grid_constant__ TreeParams p)
 {
-    using C = TreeCfg<D, FP8, kTiles, kStack>;
+    using C = TreeCfg<D, FP8, kTiles>;
     extern __shared__ __align__(1024) uint8_t smem[];
     TreeCtx c;
     c.base = smem;
@@ -1388,8 +1380,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1) attention_tree_kernel(const _
     c.it_full = c.drain + 2;
     c.it_empty = c.it_full + kTreeSlots;
     c.never = c.it_empty + kTreeSlots;
-    c.add_full = c.never + 1;  // (kStack)
-    c.add_free = c.add_full + 2;
+    c.v_full = c.never + 1;
+    c.v_empty = c.v_full + C::kVBufs;
     uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
     c.abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 4);
     c.err = p.err;
@@ -1399,13 +1391,14 @@ __global__ void __launch_bounds__(kTreeThreads, 1) attention_tree_kernel(const _
     if (tid == 0) {
         for (int e = 0; e < C::kEntries; ++e) {
             mbar_init(&c.kv_full[e], 1);
-            mbar_init(&c.kv_empty[e], 1 + kTiles);  // its MMAs (kTiles 2: two tiles'), and warp 3
+            // its MMAs (kTiles 2: two tiles'; V of an e4m3 cache: the converting warps), and warp 3
+            mbar_init(&c.kv_empty[e], 1 + (FP8 && (e & 1) ? 4 : kTiles));
             mbar_init(&c.v_ready[e], 1);
         }
         for (int b = 0; b < C::kQBufs; ++b) {
             mbar_init(&c.q_full[b], 1);
             mbar_init(&c.q_empty[b], (FP8 ? 8 : 0) + kTiles);  // the MMAs that read it; e4m3: and the softmax warps
-            mbar_init(&c.q_conv[b], 8);
+            mbar_init(&c.q_conv[b], 4);
         }
         for (int k = 0; k < C::kSBufs; ++k) {
             mbar_init(&c.s_full[k], 1);
@@ -1415,9 +1408,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1) attention_tree_kernel(const _
         for (int k = 0; k < 2; ++k) {
             mbar_init(&c.o_full[k], 1);
             mbar_init(&c.drain[k], 1);
-            if (kStack) {
-                mbar_init(&c.add_full[k], 2);
-                mbar_init(&c.add_free[k], 2);
+            if (FP8) {
+                mbar_init(&c.v_full[k], 4);
+                mbar_init(&c.v_empty[k], kTiles);
             }
         }
         for (int k = 0; k < 8; ++k)
@@ -1426,7 +1419,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) attention_tree_kernel(const _
         mbar_init(c.left, 8);
         for (int s = 0; s < kTreeSlots; ++s) {
             mbar_init(&c.it_full[s], 1);
-            mbar_init(&c.it_empty[s], kTreeConsumers);
+            mbar_init(&c.it_empty[s], C::kConsumers);
         }
         mbar_init(c.never, 1);
         *c.abort_flag = 0;
@@ -1457,8 +1450,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1) attention_tree_kernel(const _
     long long start = 0, end = 0, base = 0;
     int first_b = 0;
     if (by_all || warp == 0) {
-        long long* scan = reinterpret_cast<long long*>(smem + C::kOffRing);  // (empty yet) 12 warp sums; [16 ..] the run
-        const int threads = by_all ? kTreeThreads : 32, share = (p.B + threads - 1) / threads;
+        long long* scan = reinterpret_cast<long long*>(smem + C::kOffRing);  // (empty yet) a sum per warp; [16 ..] the run
+        const int threads = by_all ? C::kThreads : 32, share = (p.B + threads - 1) / threads;
         const int b0 = min(p.B, tid * share), b1 = min(p.B, b0 + share);
         long long mine = 0;
         for (int b = b0; b < b1; ++b) {
@@ -1480,7 +1473,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) attention_tree_kernel(const _
                 scan[warp] = before;
             __syncthreads();
 #pragma unroll
-            for (int w = 0; w < kTreeThreads / 32; ++w) {
+            for (int w = 0; w < C::kThreads / 32; ++w) {
                 warps_before += w < warp ? scan[w] : 0;
                 total += scan[w];
             }
@@ -1532,22 +1525,26 @@ __global__ void __launch_bounds__(kTreeThreads, 1) attention_tree_kernel(const _
         }
     }
 
-    // 384 threads launch with 168 registers each (104 + 200 + 200 = 504 = 3 x 168)
+    // 384 threads launch with 168 registers each (104 + 200 + 200 = 504 = 3 x 168), 512 with 128 (96 + 160 +
+    // 160 + 96 = 512 = 4 x 128)
     if (warp < 4) {
-        regs_dec<104>();
+        regs_dec<FP8 ? 96 : 104>();
         if (warp == 0)
-            tree_producer<D, FP8, kTiles, kStack>(p, c, start, end, first_b, base);
+            tree_producer<D, FP8, kTiles>(p, c, start, end, first_b, base);
         else if (warp == 3)
-            tree_feed<D, FP8, kTiles, kStack>(p, c);
+            tree_feed<D, FP8, kTiles>(p, c);
         else if constexpr (kTiles == 2)
             tree_tile<D, FP8>(p, c, warp - 1);
         else if (warp == 1)
-            tree_s<D, FP8, kStack>(p, c);
+            tree_s<D, FP8>(p, c);
         else
-            tree_pv<D, FP8, kStack>(p, c);
-    } else {
-        regs_inc<200>();
-        tree_softmax<D, FP8, kTiles, kStack>(p, c, (warp - 4) >> 2);
+            tree_pv<D, FP8>(p, c);
+    } else if (!FP8 || warp < 12) {
+        regs_inc<FP8 ? 160 : 200>();
+        tree_softmax<D, FP8, kTiles>(p, c, (warp - 4) >> 2);
+    } else if constexpr (FP8) {
+        regs_dec<96>();
+        tree_convert<kTiles>(p, c);
     }
     tc_fence_before();
     __syncthreads();
@@ -1563,7 +1560,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) attention_tree_kernel(const _
 //   out = bmm2 * sum_c w_c O_c / (sum_c w_c l_c + [sinks] 2^(sink log2 e - m)),
 // in the order of the keys.  Block (i, y) takes the unit whose first segment is
 // CTA i's, if there is one that goes on in the next CTA, and of its query tile
-// y / 4 the 32 MMA rows of quadrant y % 4 (2 for stacked tiles): a lane per row, so that the partial
+// y / 4 the 32 MMA rows of quadrant y % 4: a lane per row, so that the partial
 // rows, four columns of all 128 rows together, are read and were written in
 // whole lines.  Each warp takes kCols4 groups of four columns.  Latency alone:
 // loads that do not depend on each other are issued together.
@@ -1575,7 +1572,7 @@ __global__ void __launch_bounds__(D * 2) tree_merge_kernel(const __grid_constant
     constexpr int kCols4 = 4;  // D / 16 warps
     pdl_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int first = blockIdx.x, qt = (int)blockIdx.y / p.rows.warps, row = (int)blockIdx.y % p.rows.warps * 32 + lane;
+    const int first = blockIdx.x, qt = (int)blockIdx.y / 4, row = (int)blockIdx.y % 4 * 32 + lane;
     // the segment that opens a unit is the CTA's last; the ones after it are
     // the first of the CTAs that follow, up to the one that reaches the end
     const int4* notes = p.part_seg;
@@ -1684,11 +1681,11 @@ cudaError_t launch_pdl(Kern kern, dim3 grid, unsigned threads, size_t smem, cuda
     return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
-template <int D, bool FP8, int kTiles, bool kStack>
+template <int D, bool FP8, int kTiles>
 cudaError_t launch_tree(const TreeParams& p, cudaStream_t stream)
 {
-    using C = TreeCfg<D, FP8, kTiles, kStack>;
-    auto kern = attention_tree_kernel<D, FP8, kTiles, kStack>;
+    using C = TreeCfg<D, FP8, kTiles>;
+    auto kern = attention_tree_kernel<D, FP8, kTiles>;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess)
@@ -1703,26 +1700,24 @@ cudaError_t launch_tree(const TreeParams& p, cudaStream_t stream)
     });
     if (err[dev] != cudaSuccess)
         return err[dev];
-    if ((e = launch_pdl(kern, dim3(p.grid), kTreeThreads, C::kSmemBytes, stream, p)) != cudaSuccess)
+    if ((e = launch_pdl(kern, dim3(p.grid), C::kThreads, C::kSmemBytes, stream, p)) != cudaSuccess)
         return e;
     if (p.whole)
         return cudaSuccess;
-    return launch_pdl(tree_merge_kernel<D>, dim3(p.grid, p.rows.warps * kTiles), D * 2, 0, stream, p, kTiles);
+    return launch_pdl(tree_merge_kernel<D>, dim3(p.grid, 4 * kTiles), D * 2, 0, stream, p, kTiles);
 }
 
 }  // namespace
 
-cudaError_t launch_attention_tree(const TreeParams& p, bool fp8, int tiles, bool stacked, cudaStream_t stream)
+cudaError_t launch_attention_tree(const TreeParams& p, bool fp8, int tiles, cudaStream_t stream)
 {
-    if (fp8)
-        return p.D != 128  ? cudaErrorInvalidValue
-               : stacked   ? launch_tree<128, true, 1, true>(p, stream)
-               : tiles == 1 ? launch_tree<128, true, 1, false>(p, stream)
-                            : launch_tree<128, true, 2, false>(p, stream);
-    if (p.D == 128)
-        return tiles == 1 ? launch_tree<128, false, 1, false>(p, stream) : launch_tree<128, false, 2, false>(p, stream);
-    if (p.D == 64)
-        return tiles == 1 ? launch_tree<64, false, 1, false>(p, stream) : launch_tree<64, false, 2, false>(p, stream);
+    if (p.D == 128) {
+        if (fp8)
+            return tiles == 1 ? launch_tree<128, true, 1>(p, stream) : launch_tree<128, true, 2>(p, stream);
+        return tiles == 1 ? launch_tree<128, false, 1>(p, stream) : launch_tree<128, false, 2>(p, stream);
+    }
+    if (p.D == 64 && !fp8)
+        return tiles == 1 ? launch_tree<64, false, 1>(p, stream) : launch_tree<64, false, 2>(p, stream);
     return cudaErrorInvalidValue;
 }
 

@@ -248,7 +248,6 @@ struct TreePlan {
     bool tc;
     int tiles;     // query tiles per item
     bool whole;    // no unit is cut
-    bool stacked;  // e4m3 rows twice in one tile
     size_t off_ml, off_o, bytes;
 };
 
@@ -265,9 +264,7 @@ int plan_tree(const Problem& pr, int max_q_len, int max_kv_len, int window, cons
         // one query tile where one is enough: both softmax groups work on it (8 nodes x
         // 4 heads over 2048 keys 15.1 us, 16.1 with the second group idle; 32 requests
         // of up to 16 nodes 104 and 109)
-        t.tiles = max_q_len <= tree_rows(G, false).tile_toks ? 1 : 2;
-        // e4m3 rows twice where they fit (146 us; once 161)
-        t.stacked = pr.fp8 && G <= 32 && max_q_len <= tree_rows(G, true).tile_toks;
+        t.tiles = max_q_len <= tree_rows(G).tile_toks ? 1 : 2;
         // kv tiles of a unit at most: its keys start at 0, or anywhere with a window
         const long long all = ((long long)max_kv_len + kKvTile - 1) / kKvTile;
         const long long seen = ((long long)window + max_q_len + kKvTile - 2) / kKvTile + 1;
@@ -276,7 +273,7 @@ int plan_tree(const Problem& pr, int max_q_len, int max_kv_len, int window, cons
         // many as SMs: 8 nodes x 4 heads, 8 kv heads, cut and whole, 8 requests of 768
         // keys 16.9 and 14.7 us, 24 of 1024 30.8 and 28.4; but 40 of 768 39.0 and 39.7, one of
         // 1024 13.3 and 15.7.
-        const int item = t.tiles * tree_rows(G, t.stacked).tile_toks;
+        const int item = t.tiles * tree_rows(G).tile_toks;
         const long long units = (long long)pr.B * pr.Hkv * ((max_q_len + item - 1) / item);
         t.whole = kv_tiles <= kTreeWholeTiles || (kv_tiles <= 8 && 3 * units >= di.sms && 2 * units <= 3 * di.sms);
         const size_t rows = (size_t)di.sms * 2 * t.tiles * kQRows;  // two segments of every CTA
@@ -345,7 +342,7 @@ int tree_impl(const b2pa_tensor* q, const b2pa_tensor* k_pool, const b2pa_tensor
     std::memset(&p, 0, sizeof p);
     if ((st = status_word(dev, stream, &p.err)))
         return st;
-    p.rows = tree_rows(pr.H / pr.Hkv, plan.stacked);
+    p.rows = tree_rows(pr.H / pr.Hkv);
     p.q = static_cast<const uint16_t*>(pr.q);
     p.k = pr.k;
     p.v = pr.v;
@@ -395,7 +392,7 @@ int tree_impl(const b2pa_tensor* q, const b2pa_tensor* k_pool, const b2pa_tensor
         if ((st = encode_q_map(&p.tm_q, pr, p.rows.box_toks)) || (st = encode_pool_map(&p.tm_k, pr, pr.k, pr.k_st)) ||
             (st = encode_pool_map(&p.tm_v, pr, pr.v, pr.v_st)))
             return st;
-        e = launch_attention_tree(p, pr.fp8, plan.tiles, plan.stacked, stream);
+        e = launch_attention_tree(p, pr.fp8, plan.tiles, stream);
     } else {
         e = launch_tree_generic(p, pr.fp8, stream);
     }

@@ -15,21 +15,18 @@ namespace b2pa {
 // per kv head, each of the four softmax warps gets whole tokens (box_toks at
 // most, in its first box_toks * G lanes), a tile's tokens being split evenly
 // over the warps so that a small tree still uses all four.  With more heads
-// row = token * G + head.  Stacked tiles (attn_tree.cu) hold their tokens in two
-// warps, and the same rows again in the other two.
+// row = token * G + head.
 struct TreeRows {
     int G, box_toks, tile_toks, by_warp;
-    int warps;  // warps that the tokens are split over (by_warp)
 };
 
-__host__ __device__ inline TreeRows tree_rows(int G, bool stacked)
+__host__ __device__ inline TreeRows tree_rows(int G)
 {
     TreeRows r;
     r.G = G;
     r.by_warp = G <= 32;
-    r.warps = stacked ? 2 : 4;
     r.box_toks = r.by_warp ? 32 / G : kQRows / G;
-    r.tile_toks = r.by_warp ? r.warps * r.box_toks : r.box_toks;
+    r.tile_toks = r.by_warp ? 4 * r.box_toks : r.box_toks;
     return r;
 }
 
@@ -69,7 +66,7 @@ struct TreeParams {  // 128-byte aligned through its CUtensorMap members
 
 // What a unit costs beyond its kv tiles, in kv tiles: its Q, the first scores,
 // the tree's own tile and the rows' way out.  (bf16 batch 114 us with 0, 105
-// with 2, 104.5 with 4, 105 with 6; e4m3 batch 154, 149, 146 and 147; 512 rows per
+// with 2, 104.5 with 4, 105 with 6; e4m3 batch 193, 162, 160 and 160; 512 rows per
 // kv head 125, 118, 114.6 and 116.)
 constexpr int kTreeUnitCost = 4;
 
@@ -120,7 +117,7 @@ struct TreeCut {
 __device__ __forceinline__ TreeCut tree_cut(long long total, int grid)
 {
     // two steps per CTA at least: fewer partial rows to merge where there is little
-    // work (8 nodes, 2048 keys: 16.6 us with one, 15.1 with two or three)
+    // work (8 nodes, 2048 keys, before the merge grew shorter: 16.6 us with one, 15.1 with two or three)
     return TreeCut{total, (int)min((long long)grid, (total + 1) / 2)};
 }
 
@@ -172,8 +169,8 @@ __device__ __forceinline__ TreeToken tree_token(const TreeRows& r, int row, int 
 {
     TreeToken t;
     if (r.by_warp) {
-        const int per = (toks + r.warps - 1) / r.warps, lane = row & 31, in = lane / r.G;
-        t.tok = (row >> 5) % r.warps * per + in;
+        const int per = (toks + 3) / 4, lane = row & 31, in = lane / r.G;
+        t.tok = (row >> 5) * per + in;
         t.head = lane - in * r.G;
         t.valid = in < per && t.tok < toks;
     } else {
@@ -184,8 +181,8 @@ __device__ __forceinline__ TreeToken tree_token(const TreeRows& r, int row, int 
     return t;
 }
 
-// tiles: query tiles per item (1 or 2); stacked: see tree_rows
-cudaError_t launch_attention_tree(const TreeParams& p, bool fp8, int tiles, bool stacked, cudaStream_t stream);
+// tiles: query tiles per item (1 or 2)
+cudaError_t launch_attention_tree(const TreeParams& p, bool fp8, int tiles, cudaStream_t stream);
 cudaError_t launch_tree_generic(const TreeParams& p, bool fp8, cudaStream_t stream);
 
 }  // namespace b2pa
