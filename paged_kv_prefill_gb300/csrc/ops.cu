@@ -321,8 +321,8 @@ int tree_impl(const b2pa_tensor* q, const b2pa_tensor* k_pool, const b2pa_tensor
     const int window = window_left < 0 ? -1 : window_left;
     if (window >= 0 && pr.T > 0 && !is_vec(positions, B2PA_INT32, pr.T))
         return fail(B2PA_ERR_INVALID_ARG, "a window needs positions, contiguous int32 [T]");
-    if (pr.T > 0 && ((pr.T > 1 && pr.out_st_tok < pr.D) || (pr.H > 1 && pr.out_st_head < pr.D)))
-        return fail(B2PA_ERR_INVALID_ARG, "out: its rows overlap");
+    if (pr.T > 0 && (st = check_rows_apart(out, "out")))
+        return st;
     if (pr.T > 0 && pr.out == pr.q)
         return fail(B2PA_ERR_INVALID_ARG, "out must not be q: rows are read by several blocks");
     *bytes_needed = 0;

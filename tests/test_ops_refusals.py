@@ -211,6 +211,12 @@ def test_tree_in_place_and_too_long(lib):
     assert b"max_kv_len" in lib.b2pa_last_error_message()
 
 
+@pytest.mark.parametrize("stride", [[128, 128, 1], [128, 1024, 1], [512, 64, 1], [256, 128, 1], [64, 1152, 1], [-512, 128, 1]])
+def test_tree_rows_of_the_output_apart(lib, stride):
+    assert tree(lib, out=fake([9, 4, 128], BF, stride, base=2 << 20)) == INVALID
+    assert b"its rows overlap" in lib.b2pa_last_error_message()
+
+
 def test_tree_of_nothing(lib):
     none = dict(q=fake([0, 4, 128], BF, base=0), out=fake([0, 4, 128], BF, base=0), mask=fake([0, 2], I32, base=0))
     assert tree(lib, **none) == OK
