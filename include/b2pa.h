@@ -393,8 +393,8 @@ B2PA_API int b2pa_append_kv(const b2pa_tensor* k_new, const b2pa_tensor* v_new, 
  *                D is a multiple of 8, at most 256; stride[2] == 1, the other
  *                strides multiples of 8, 16-byte aligned.  q_out may be q itself
  *                and k_out k itself (same pointer and strides); otherwise outputs
- *                must not overlap any input, and the rows of an output never
- *                overlap.
+ *                must not overlap any input, nor each other, and the rows of an
+ *                output never overlap.
  *  cos_sin       [max_position, R] fp32, stride[1] == 1, R even, 2 <= R <= D: row
  *                p holds the R / 2 cosines of position p, then its R / 2 sines
  *                (with any scaling of frequencies or amplitudes folded in).
@@ -448,7 +448,7 @@ B2PA_API int b2pa_append_kv_scaled(const b2pa_tensor* k_new, const b2pa_tensor* 
  * needs 16-bit K and V of a cached prefix: k_out and v_out may be views of bf16
  * pools that the attention reads.
  * A slot outside the pool reads as zeros and sets B2PA_DEV_BAD_SLOT.  The
- * outputs' rows must not overlap.  Otherwise as b2pa_append_kv_scaled.
+ * outputs and their rows must not overlap.  Otherwise as b2pa_append_kv_scaled.
  */
 B2PA_API int b2pa_read_kv_scaled(const b2pa_tensor* k_pool, const b2pa_tensor* v_pool, const b2pa_tensor* k_scales,
                                  const b2pa_tensor* v_scales, const b2pa_tensor* cache_loc, int32_t layout,

@@ -59,6 +59,25 @@ int check_rows_apart(const b2pa_tensor* t, const char* what)
     return B2PA_OK;
 }
 
+// Outputs of [T, heads, D] rows must be two, and one at an input's address that
+// input itself (rows are read ahead of others' writes).
+int check_places(const b2pa_tensor* const out[2], const char* const names[2], const b2pa_tensor* const in[2])
+{
+    if (out[0]->data == out[1]->data)
+        return fail(B2PA_ERR_INVALID_ARG, "%s in the place of %s", names[1], names[0]);
+    for (int i = 0; in && i < 2; ++i)
+        for (int j = 0; j < 2; ++j) {
+            if (out[i]->data != in[j]->data)
+                continue;
+            bool same = i == j;
+            for (int d = 0; d < 2; ++d)
+                same = same && (out[i]->shape[d] <= 1 || out[i]->stride[d] == in[j]->stride[d]);
+            if (!same)
+                return fail(B2PA_ERR_INVALID_ARG, "%s in the place of other rows of an input", names[i]);
+        }
+    return B2PA_OK;
+}
+
 int check_weight(const b2pa_tensor* w, const char* what, int64_t D)
 {
     if (!w)
@@ -116,6 +135,10 @@ int rope_impl(const b2pa_tensor* q, const b2pa_tensor* k, const b2pa_tensor* cos
     }
     if (T == 0)
         return B2PA_OK;
+    const b2pa_tensor *in[2] = {q, k}, *out[2] = {q_out, k_out}, *w[2] = {q_weight, k_weight};
+    const char* const names[2] = {"q_out", "k_out"};
+    if ((st = check_places(out, names, in)))
+        return st;
     for (int g = 0; g < (half + 3) / 4; ++g) {
         p.axis_of4[g] = 4 * g + 4 <= half ? p.axis_of[4 * g] : 255;
         for (int i = 4 * g; i < 4 * g + 4 && i < half; ++i)
@@ -126,7 +149,6 @@ int rope_impl(const b2pa_tensor* q, const b2pa_tensor* k, const b2pa_tensor* cos
     DevInfo di;
     if ((st = device_info(&dev, &di)) || (st = status_word(dev, stream, &p.err)))
         return st;
-    const b2pa_tensor *in[2] = {q, k}, *out[2] = {q_out, k_out}, *w[2] = {q_weight, k_weight};
     for (int i = 0; i < 2; ++i) {
         RopeTensor& x = p.x[i];
         x.in = static_cast<const uint16_t*>(in[i]->data);
@@ -210,6 +232,8 @@ int scaled_kv_impl(bool write, const b2pa_tensor* const rows[2], const char* con
         return B2PA_OK;
     if (!is_vec(cache_loc, B2PA_INT32, T))
         return fail(B2PA_ERR_INVALID_ARG, "cache_loc must be contiguous int32 [T]");
+    if (!write && (st = check_places(rows, names, nullptr)))
+        return st;
     int dev;
     DevInfo di;
     ScaledKvParams p;

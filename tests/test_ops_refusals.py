@@ -82,6 +82,20 @@ def test_rope(lib, change, status):
     assert lib.b2pa_last_error_message()
 
 
+def test_rope_outputs_in_place_of_other_rows(lib):
+    """An output at an input's address is that input, by the same strides; two outputs are two."""
+    M = 1 << 20
+    x = dict(q=fake([9, 4, 64], BF, base=M), k=fake([9, 2, 64], BF, base=2 * M))
+    q_out, k_out = fake([9, 4, 64], BF, base=3 * M), fake([9, 2, 64], BF, base=4 * M)
+    for change in (dict(q_out=q_out, k_out=fake([9, 2, 64], BF, base=3 * M)),
+                   dict(q_out=fake([9, 4, 64], BF, [64, 9 * 64, 1], base=M), k_out=k_out),
+                   dict(q_out=q_out, k_out=fake([9, 2, 64], BF, [256, 64, 1], base=2 * M)),
+                   dict(q_out=fake([9, 4, 64], BF, base=2 * M), k_out=k_out),
+                   dict(q_out=q_out, k_out=fake([9, 2, 64], BF, base=M))):
+        assert rope(lib, **x, **change) == INVALID
+        assert b"in the place of" in lib.b2pa_last_error_message()
+
+
 def test_rope_head_dims(lib):
     for D in (60, 264):
         x = dict(q=fake([9, 4, D], BF), k=fake([9, 2, D], BF), q_out=fake([9, 4, D], BF), k_out=fake([9, 2, D], BF))
@@ -143,6 +157,11 @@ def test_scaled_writes_need_places_apart(lib):
     assert scaled(lib, True, scales=[fake([5, 2, 16], F32, [32, 16, 0])] * 2) == INVALID
     assert scaled(lib, True, pools=[fake([5, 2, 16, 64], F8, [0, 1024, 64, 1])] * 2) == INVALID
     assert scaled(lib, False, rows=[fake([9, 2, 64], BF, [0, 64, 1])] * 2) == INVALID
+
+
+def test_scaled_read_into_one_buffer(lib):
+    assert scaled(lib, False) == INVALID
+    assert b"in the place of" in lib.b2pa_last_error_message()
 
 
 def test_scaled_of_no_tokens(lib):
