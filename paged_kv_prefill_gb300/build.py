@@ -63,9 +63,33 @@ def _native_commands(tmp: str) -> list:
     ]
 
 
+def _native_key() -> str:
+    """What _native.so is compiled against: it reaches into torch's C++ objects."""
+    import torch
+
+    return f"{sys.version}\n{torch.__version__}\n{torch._C._GLIBCXX_USE_CXX11_ABI}\n"
+
+
+def _native_is_current(key_file: str) -> bool:
+    try:
+        with open(key_file) as f:
+            return f.read() == _native_key()
+    except OSError:
+        return False
+
+
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
-    """Compile and link libb2pa.so if any source is newer; return its path."""
-    if not force and all(os.path.exists(f) and os.path.getmtime(f) >= _deps_mtime() for f in (LIB, NATIVE)):
+    """Compile and link what is older than its sources; return libb2pa.so's path.
+
+    _native.so is made anew for another Python or torch too.  Where it cannot be made, the
+    library is there all the same, and this raises."""
+    newest, key_file = _deps_mtime(), os.path.join(BUILD, "native.key")
+
+    def fresh(path: str) -> bool:
+        return not force and os.path.exists(path) and os.path.getmtime(path) >= newest
+
+    sources = [] if fresh(LIB) else SOURCES
+    if not sources and fresh(NATIVE) and _native_is_current(key_file):
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     nvcc = _nvcc()
@@ -86,17 +110,24 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
             raise RuntimeError(f"{what} failed:\n{r.stdout}\n{r.stderr}")
 
     native_tmp = NATIVE + f".tmp{os.getpid()}"
-    compile_native, link_native = _native_commands(native_tmp)
+
+    def compile_native() -> list:
+        compile_, link = _native_commands(native_tmp)
+        run(compile_, "compiling native.cpp")
+        return link
+
     with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
-        native = ex.submit(run, compile_native, "compiling native.cpp")
-        objs = list(ex.map(one, SOURCES))
-        native.result()
-    tmp = LIB + f".tmp{os.getpid()}"
-    run([nvcc] + ARCH + ["-shared", "-o", tmp] + objs + ["-cudart", "static", "-Xcompiler", "-fPIC",
-                                                        "-Xlinker", "-soname=libb2pa.so"], "link")
-    os.replace(tmp, LIB)
-    run(link_native, "linking native.o")
+        native = ex.submit(compile_native)
+        objs = list(ex.map(one, sources))
+    if objs:
+        tmp = LIB + f".tmp{os.getpid()}"
+        run([nvcc] + ARCH + ["-shared", "-o", tmp] + objs + ["-cudart", "static", "-Xcompiler", "-fPIC",
+                                                            "-Xlinker", "-soname=libb2pa.so"], "link")
+        os.replace(tmp, LIB)
+    run(native.result(), "linking native.o")
     os.replace(native_tmp, NATIVE)
+    with open(key_file, "w") as f:
+        f.write(_native_key())
     return LIB
 
 
