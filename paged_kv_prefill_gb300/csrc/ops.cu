@@ -286,8 +286,8 @@ int plan_tree(const Problem& pr, int max_q_len, int max_kv_len, int window, cons
     if (t.tc) {
         const int G = pr.H / pr.Hkv;
         // one query tile where one is enough: both softmax groups work on it (8 nodes x
-        // 4 heads over 2048 keys 15.1 us, 16.1 with the second group idle; 32 requests
-        // of up to 16 nodes 104 and 109)
+        // 4 heads over 2048 keys 14.3 us, 15.1 with the second group idle; 32 requests
+        // of up to 16 nodes 104 and 109, of up to 8 over an e4m3 cache 161 and 244)
         t.tiles = max_q_len <= tree_rows(G).tile_toks ? 1 : 2;
         // kv tiles of a unit at most: its keys start at 0, or anywhere with a window
         const long long all = ((long long)max_kv_len + kKvTile - 1) / kKvTile;
