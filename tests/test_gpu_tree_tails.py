@@ -161,3 +161,32 @@ def test_the_same_bits_every_time(cuda_lib, shape):
         outs = [cuda_lib.tree_attention(**case[0]) for _ in range(40)]
         assert all(torch.equal(x, first) for x in outs)
     assert cuda_lib.device_status() == 0
+
+
+def test_two_streams_and_two_graphs_at_once(cuda_lib):
+    """Calls over one e4m3 cache each, at the same time on two streams, then replayed from two graphs with other queries."""
+    cases = [make([8, 3, 0, 6], [9000, 700, 40, 2000 + i], 4, 9.0, 0.5, "mean", seed=i) for i in range(2)]
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        got = [cuda_lib.tree_attention(**c[0], stream=s) for c, s in zip(cases, streams)]
+    torch.cuda.synchronize()
+    for c, x in zip(cases, got):
+        check(c, x)
+    graphs, outs = [], []
+    for c in cases:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(cuda_lib.tree_attention(**c[0]))
+        graphs.append(g)
+    for c in cases:
+        c[0]["query"].copy_(c[0]["query"].flip(0))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    for c, x in zip(cases, outs):
+        check(c, x)
+    assert cuda_lib.device_status() == 0
