@@ -1063,7 +1063,8 @@ __device__ void tree_softmax(const TreeParams& p, const TreeCtx& c, int t)
     // P = 2^(x - m + kBias), in f16 over an e4m3 cache: the bias uses its range (see
     // the top).  The stabiliser is renewed once the row's maximum has grown by kSlack.
     constexpr float kBias = FP8 ? 7.f : 0.f, kSlack = 8.f;
-    // 32-key steps of the exponentials that are unrolled (see below)
+    // 32-key steps of the exponentials that are unrolled (see below; an e4m3 cache's kernel has one role
+    // more: its batch 161 us with one step, 172 with two, 512 rows per kv head 143 and 139)
     constexpr int kUnroll = (kTiles == 2 ? 4 : 2) / (FP8 ? 2 : 1);
     const int wq = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31, row = wq * 32 + lane;
     const uint32_t lane_off = (uint32_t)(wq * 32) << 16;
