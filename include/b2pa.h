@@ -26,7 +26,10 @@
  * the heads' norms and rotary rotation (b2pa_qk_norm_rope), writing the new
  * tokens' K and V into the pools (b2pa_append_kv, quantising to e4m3 for an FP8
  * cache; b2pa_append_kv_scaled with a scale per row, b2pa_read_kv_scaled back),
- * and the attention that verifies trees of drafted tokens (b2pa_tree_attention).
+ * and the attention that verifies trees of drafted tokens (b2pa_tree_attention);
+ * and it keeps a page ledger on the device (b2pa_fork_pages, b2pa_grow_pages,
+ * b2pa_free_pages), copies pages (b2pa_copy_pages) and moves the accepted nodes
+ * of a tree to their places (b2pa_compact_kv).
  *
  * Conventions for every entry point:
  *  - All tensors are described by b2pa_tensor: a pointer, a dtype, a rank,
@@ -99,8 +102,10 @@ enum b2pa_device_error {
                                    b2pa_read_kv_scaled: it reads as zeros */
     B2PA_DEV_BAD_SCALE = 64,    /* b2pa_context_attention_tensor_scales: the device bmm1_scale is not
                                    finite and > 0, or bmm2_scale is not finite; nothing is written */
-    B2PA_DEV_BAD_POSITION = 128 /* b2pa_qk_norm_rope: a position outside the table; that token's rows are
+    B2PA_DEV_BAD_POSITION = 128,/* b2pa_qk_norm_rope: a position outside the table; that token's rows are
                                    not written */
+    B2PA_DEV_NO_PAGES = 256     /* b2pa_fork_pages, b2pa_grow_pages: not enough free pages for a request, which
+                                   stays as it was */
 };
 
 /* Kernel paths (b2pa_set_kernel_path). */
@@ -508,6 +513,103 @@ B2PA_API int b2pa_tree_attention(const b2pa_tensor* q, const b2pa_tensor* k_pool
                                  int32_t window_left, const b2pa_tensor* sinks, int32_t layout, b2pa_tensor* out,
                                  void* workspace, uint64_t workspace_bytes, uint64_t* bytes_needed,
                                  b2pa_stream_t stream);
+
+/*
+ * b2pa_copy_pages -- page src[i] of the pools to page dst[i], all heads and
+ * slots, bit for bit: what b2pa_fork_pages cannot share, or pages that move.  No
+ * counterpart on the pages.
+ *
+ *  k_pool, v_pool      pools and layout as for b2pa_context_attention, bf16 or
+ *                      e4m3, any head_dim, positive strides, no rows that overlap.
+ *  k_scales, v_scales  both NULL, or the scales of b2pa_append_kv_scaled's cache (of
+ *                      either pool type): they are copied along.
+ *  src, dst            contiguous int32 [n].  A pair of -1 and -1 is passed over; a page
+ *                      id outside the pool otherwise sets B2PA_DEV_BAD_PAGE and its
+ *                      pair is passed over.  The pages in dst must be distinct and
+ *                      none of them in src: else which content lands is unspecified.
+ * Asynchronous on `stream`; one kernel.  n = 0 is a no-op.
+ */
+B2PA_API int b2pa_copy_pages(const b2pa_tensor* k_pool, const b2pa_tensor* v_pool, const b2pa_tensor* k_scales,
+                             const b2pa_tensor* v_scales, const b2pa_tensor* src, const b2pa_tensor* dst,
+                             int32_t layout, b2pa_stream_t stream);
+
+/*
+ * b2pa_compact_kv -- the keys and values of a tree's accepted nodes to the first
+ * places behind the context, where the next step finds them: the step after
+ * b2pa_tree_attention and the verification of its tokens.  No counterpart on
+ * the pages.
+ *
+ * Request b has n = cum_q[b+1] - cum_q[b] nodes, whose keys are the last n of its
+ * seq_lens[b]; with c = seq_lens[b] - n and its count k = counts[b],
+ *     key c + i  <-  key c + accepted[b][i]      (0 <= i < k, all read first)
+ *     new_lens[b] = c + k
+ * accepted[b][0 .. k-1] are nodes, 0 <= a < n, rising strictly (a path's nodes do:
+ * a parent comes before its children).  Keys from c + k on keep what they held, or
+ * what lay there.
+ *
+ *  k_pool, v_pool, k_scales, v_scales, layout   as for b2pa_copy_pages.
+ *  block_tables  [B, max_pages] int32, stride[1] == 1; a request's pages must be its
+ *                own where its nodes lie.
+ *  seq_lens, counts, new_lens  contiguous int32 [B]; new_lens none of the inputs.
+ *  cum_q         contiguous int32 [B + 1].
+ *  accepted      [B, width] int32, stride[1] == 1; columns from counts[b] on are not read.
+ * A malformed request (n < 0 or > seq_lens[b], more pages than max_pages, a count
+ * outside [0, min(n, width)], nodes that do not rise) sets B2PA_DEV_BAD_REQUEST:
+ * nothing of it moves and new_lens[b] = seq_lens[b].  A page id outside the pool
+ * sets B2PA_DEV_BAD_PAGE and rows from or to it stay.
+ * Asynchronous on `stream`; one kernel.  B = 0 is a no-op.
+ */
+B2PA_API int b2pa_compact_kv(const b2pa_tensor* k_pool, const b2pa_tensor* v_pool, const b2pa_tensor* k_scales,
+                             const b2pa_tensor* v_scales, const b2pa_tensor* block_tables, const b2pa_tensor* seq_lens,
+                             const b2pa_tensor* cum_q, const b2pa_tensor* accepted, const b2pa_tensor* counts,
+                             b2pa_tensor* new_lens, int32_t layout, b2pa_stream_t stream);
+
+/*
+ * The page ledger -- which request holds which pages, on the device.  No
+ * counterpart on the pages.  The caller owns it:
+ *
+ *  block_tables  [R, max_pages] int32, stride[1] == 1, max_pages < 2^30: row r holds the
+ *                pages of request r, ceil(seq_lens[r] / page_size) of them.
+ *  seq_lens      contiguous int32 [R]; 0: an empty row.
+ *  page_refs     contiguous int32 [num_pages], fewer than 2^30: how many rows hold the
+ *                page.  A page with 0 is free.
+ *  rows, ...     contiguous int32 [n], at most 4096 per call: the rows a call works on.
+ * Pages are given lowest number first, requests served in the order of the call.
+ * Results do not depend on timing.  All three are asynchronous on `stream`, one
+ * kernel, and no-ops for n = 0; the ledger's tensors are written in place and must
+ * not overlap one another or the other arguments.  A malformed request (a row outside
+ * [0, R), a length below 0 or of more than max_pages pages) sets B2PA_DEV_BAD_REQUEST
+ * and changes nothing; one for which there are not enough free pages (those that
+ * the requests before it want are counted, whether they got them or not) sets
+ * B2PA_DEV_NO_PAGES and changes nothing.  Page ids outside [0, num_pages) in a table
+ * set B2PA_DEV_BAD_PAGE and are not counted.
+ *
+ * b2pa_free_pages: the rows' pages lose a holder each, and the rows are empty.  A
+ * row named twice is freed once.  A page whose count is 0 already keeps it and sets
+ * B2PA_DEV_BAD_PAGE.
+ *
+ * b2pa_fork_pages: row children[i], which must be empty, becomes a copy of row
+ * parents[i] with the same length.  Whole pages are shared (their counts rise); a
+ * last page that is not full is replaced by a free one, count 1, and src[i] and
+ * dst[i] (contiguous int32 [n]) say which page to copy to which (b2pa_copy_pages,
+ * for each layer's pools); else both are -1.  Columns behind the copied ones stay.
+ * A parent may have many children.  A child that is named twice (the later ones),
+ * or that is a parent in the same call, is malformed; a request that fails leaves
+ * its child empty and -1 in src and dst.
+ *
+ * b2pa_grow_pages: row rows[i] gets free pages, count 1, behind those that it has,
+ * until they hold new_lens[i] >= seq_lens[rows[i]] tokens, and that length.  Of a
+ * row named twice the later ones are malformed.
+ */
+B2PA_API int b2pa_free_pages(const b2pa_tensor* block_tables, const b2pa_tensor* seq_lens,
+                             const b2pa_tensor* page_refs, const b2pa_tensor* rows, int32_t page_size,
+                             b2pa_stream_t stream);
+B2PA_API int b2pa_fork_pages(const b2pa_tensor* block_tables, const b2pa_tensor* seq_lens,
+                             const b2pa_tensor* page_refs, const b2pa_tensor* parents, const b2pa_tensor* children,
+                             int32_t page_size, b2pa_tensor* src, b2pa_tensor* dst, b2pa_stream_t stream);
+B2PA_API int b2pa_grow_pages(const b2pa_tensor* block_tables, const b2pa_tensor* seq_lens,
+                             const b2pa_tensor* page_refs, const b2pa_tensor* rows, const b2pa_tensor* new_lens,
+                             int32_t page_size, b2pa_stream_t stream);
 
 /*
  * b2pa_get_device_status -- synchronise `stream`, read and clear the device

@@ -33,7 +33,7 @@ PATH_AUTO, PATH_TCGEN05, PATH_GENERIC = 0, 1, 2
 STATUS = {0: "B2PA_OK", -1: "B2PA_ERR_INVALID_ARG", -2: "B2PA_ERR_UNSUPPORTED", -3: "B2PA_ERR_CUDA",
           -4: "B2PA_ERR_DEVICE", -5: "B2PA_ERR_WORKSPACE"}
 DEV_BAD_REQUEST, DEV_BAD_PAGE, DEV_TIMEOUT, DEV_BAD_CUM_KV, DEV_OVERFLOW = 1, 2, 4, 8, 16
-DEV_BAD_SLOT, DEV_BAD_SCALE, DEV_BAD_POSITION = 32, 64, 128
+DEV_BAD_SLOT, DEV_BAD_SCALE, DEV_BAD_POSITION, DEV_NO_PAGES = 32, 64, 128, 256
 
 _DTYPES = {
     torch.bfloat16: B2PA_BF16,
@@ -56,6 +56,11 @@ EXPORTED = [
     "b2pa_read_kv_scaled",
     "b2pa_qk_norm_rope",
     "b2pa_tree_attention",
+    "b2pa_copy_pages",
+    "b2pa_compact_kv",
+    "b2pa_free_pages",
+    "b2pa_fork_pages",
+    "b2pa_grow_pages",
     "b2pa_get_device_status",
     "b2pa_set_kernel_path",
     "b2pa_query_path",
@@ -134,6 +139,16 @@ def load(path: str = LIB_PATH):
     lib.b2pa_tree_attention.argtypes = [P] * 8 + [I, I, F, F, I, P, I, P, V, ctypes.c_uint64,
                                                   ctypes.POINTER(ctypes.c_uint64), V]
     lib.b2pa_tree_attention.restype = ctypes.c_int
+    lib.b2pa_copy_pages.argtypes = [P] * 6 + [I, V]
+    lib.b2pa_copy_pages.restype = ctypes.c_int
+    lib.b2pa_compact_kv.argtypes = [P] * 10 + [I, V]
+    lib.b2pa_compact_kv.restype = ctypes.c_int
+    lib.b2pa_free_pages.argtypes = [P] * 4 + [I, V]
+    lib.b2pa_free_pages.restype = ctypes.c_int
+    lib.b2pa_fork_pages.argtypes = [P] * 5 + [I, P, P, V]
+    lib.b2pa_fork_pages.restype = ctypes.c_int
+    lib.b2pa_grow_pages.argtypes = [P] * 5 + [I, V]
+    lib.b2pa_grow_pages.restype = ctypes.c_int
     lib.b2pa_get_device_status.argtypes = [ctypes.c_void_p, ctypes.c_void_p]
     lib.b2pa_get_device_status.restype = ctypes.c_int
     lib.b2pa_set_kernel_path.argtypes = [ctypes.c_int32]
@@ -622,6 +637,85 @@ def tree_attention(
         return _done(call(handle, *args), "b2pa_tree_attention")
     with _On(query, stream) as handle:
         return _done(call(handle, *args), "b2pa_tree_attention")
+
+
+def copy_pages(kv_cache, src: torch.Tensor, dst: torch.Tensor, kv_scales=None, kv_layout: str = "HND", stream=None):
+    """Copy pages src[i] (int32) of the pools to pages dst[i], in place; pairs of -1 are passed over.
+
+    kv_scales is (k_scales, v_scales) of a cache with a scale per row, copied along (see include/b2pa.h)."""
+    call = (_calls or native()).copy_pages
+    k, v = split_kv_cache(kv_cache, kv_layout)
+    ks, vs = (None, None) if kv_scales is None else _two(kv_scales, "kv_scales")
+    args = (k, v, ks, vs, src, dst, LAYOUTS[kv_layout])
+    handle = _here(k, stream)
+    if handle >= 0:
+        st = call(handle, *args)
+    else:
+        with _On(k, stream) as handle:
+            st = call(handle, *args)
+    if st != 0:
+        _check(st, "b2pa_copy_pages")
+
+
+def compact_kv(kv_cache, block_tables: torch.Tensor, seq_lens: torch.Tensor, cum_seq_lens_q: torch.Tensor,
+               accepted: torch.Tensor, num_accepted: torch.Tensor, kv_scales=None,
+               new_lens: Optional[torch.Tensor] = None, kv_layout: str = "HND", stream=None) -> torch.Tensor:
+    """Move the keys and values of the accepted nodes of each request's tree (accepted [B, width] int32,
+    of which num_accepted count) to the first places behind its context, in place; returns the
+    requests' new lengths, int32 [B] (see include/b2pa.h)."""
+    call = (_calls or native()).compact_kv
+    k, v = split_kv_cache(kv_cache, kv_layout)
+    ks, vs = (None, None) if kv_scales is None else _two(kv_scales, "kv_scales")
+    args = (k, v, ks, vs, block_tables, seq_lens, cum_seq_lens_q, accepted, num_accepted, new_lens, LAYOUTS[kv_layout])
+    handle = _here(k, stream)
+    if handle >= 0:
+        return _done(call(handle, *args), "b2pa_compact_kv")
+    with _On(k, stream) as handle:
+        return _done(call(handle, *args), "b2pa_compact_kv")
+
+
+def free_pages(block_tables: torch.Tensor, seq_lens: torch.Tensor, page_refs: torch.Tensor, rows: torch.Tensor,
+               page_size: int, stream=None):
+    """Empty rows (int32) of a page ledger, in place: their pages lose a holder each (see include/b2pa.h)."""
+    call = (_calls or native()).free_pages
+    handle = _here(page_refs, stream)
+    if handle >= 0:
+        st = call(handle, block_tables, seq_lens, page_refs, rows, page_size)
+    else:
+        with _On(page_refs, stream) as handle:
+            st = call(handle, block_tables, seq_lens, page_refs, rows, page_size)
+    if st != 0:
+        _check(st, "b2pa_free_pages")
+
+
+def fork_pages(block_tables: torch.Tensor, seq_lens: torch.Tensor, page_refs: torch.Tensor, parents: torch.Tensor,
+               children: torch.Tensor, page_size: int, src: Optional[torch.Tensor] = None,
+               dst: Optional[torch.Tensor] = None, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Make the empty rows children (int32) of a page ledger copies of the rows parents, in place:
+    whole pages are shared, and the last one, if it is not full, is to be copied; returns (src, dst),
+    the pages for copy_pages, -1 where there is nothing to copy (see include/b2pa.h)."""
+    call = (_calls or native()).fork_pages
+    args = (block_tables, seq_lens, page_refs, parents, children, page_size, src, dst)
+    handle = _here(page_refs, stream)
+    if handle >= 0:
+        return _done(call(handle, *args), "b2pa_fork_pages")
+    with _On(page_refs, stream) as handle:
+        return _done(call(handle, *args), "b2pa_fork_pages")
+
+
+def grow_pages(block_tables: torch.Tensor, seq_lens: torch.Tensor, page_refs: torch.Tensor, rows: torch.Tensor,
+               new_lens: torch.Tensor, page_size: int, stream=None):
+    """Give rows (int32) of a page ledger free pages for new_lens (int32) tokens, and those lengths, in
+    place (see include/b2pa.h)."""
+    call = (_calls or native()).grow_pages
+    handle = _here(page_refs, stream)
+    if handle >= 0:
+        st = call(handle, block_tables, seq_lens, page_refs, rows, new_lens, page_size)
+    else:
+        with _On(page_refs, stream) as handle:
+            st = call(handle, block_tables, seq_lens, page_refs, rows, new_lens, page_size)
+    if st != 0:
+        _check(st, "b2pa_grow_pages")
 
 
 def device_status(stream=None) -> int:

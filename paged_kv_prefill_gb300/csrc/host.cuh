@@ -1,6 +1,6 @@
 // host.cuh -- host-side helpers that the entry points of b2pa.cu and ops.cu
 // share: errors, device properties, status words, argument checks and tensor
-// maps.  Defined in b2pa.cu.
+// maps.  Defined in b2pa.cu where nothing else is said.
 #pragma once
 
 #include <cstddef>
@@ -16,6 +16,18 @@ namespace b2pa {
 int fail(int status, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
 int cuda_fail(cudaError_t e, const char* what);
 void clear_error();
+
+// No C++ exception (an allocation that failed) may leave a C entry point.
+template <typename F>
+int guarded(F&& f)
+{
+    try {
+        clear_error();
+        return f();
+    } catch (...) {
+        return B2PA_ERR_CUDA;
+    }
+}
 
 // the process-wide options
 int kernel_path();
@@ -67,5 +79,8 @@ const char* tc_reject(const Problem& pr, const DevInfo& di);
 // box: (64 columns, one kv head's query heads, rows_per_tile tokens)
 int encode_q_map(CUtensorMap* m, const Problem& pr, int rows_per_tile);
 int encode_pool_map(CUtensorMap* m, const Problem& pr, const void* base, const long long st[3]);
+
+// (ops.cu) a scale tensor: the pool's shape without head_dim, fp32
+int check_scales(const b2pa_tensor* s, const char* what, const b2pa_tensor* pool);
 
 }  // namespace b2pa

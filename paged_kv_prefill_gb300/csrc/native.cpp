@@ -111,39 +111,43 @@ public:
             throw Refused{};
         return reinterpret_cast<b2pa_stream_t>(v);
     }
-    // the tensor given, or a new contiguous bf16 one
+    // the tensor given, or a new contiguous one
+    template <typename T = at::BFloat16>
     at::Tensor output(int i, at::IntArrayRef shape)
     {
         if (!none(i))
             return tensor(i);
-        return part(memory(c10::multiply_integers(shape)), 0, shape);
+        return part<T>(memory<T>(c10::multiply_integers(shape)), 0, shape);
     }
     // Two of them.  New ones share one allocation, the second behind the first
-    // (16-byte aligned: its rows are multiples of 8 elements): an allocation and
+    // (bf16: 16-byte aligned, its rows are multiples of 8 elements): an allocation and
     // its release cost about as much as the launch of a small kernel.
+    template <typename T = at::BFloat16>
     std::pair<at::Tensor, at::Tensor> outputs(int i, at::IntArrayRef a, int j, at::IntArrayRef b)
     {
         if (!none(i) || !none(j))
-            return {output(i, a), output(j, b)};
+            return {output<T>(i, a), output<T>(j, b)};
         const int64_t n = c10::multiply_integers(a);
-        const c10::Storage both = memory(n + c10::multiply_integers(b));
-        return {part(both, 0, a), part(both, n, b)};
+        const c10::Storage both = memory<T>(n + c10::multiply_integers(b));
+        return {part<T>(both, 0, a), part<T>(both, n, b)};
     }
 
 private:
     // What at::empty takes too, from the same allocator, without its dispatch and
     // device guard (the device is current).
+    template <typename T>
     static c10::Storage memory(int64_t elements)
     {
         c10::Allocator* const from = c10::cuda::CUDACachingAllocator::get();
-        const size_t bytes = (size_t)elements * sizeof(at::BFloat16);
+        const size_t bytes = (size_t)elements * sizeof(T);
         return c10::Storage(c10::Storage::use_byte_size_t(), bytes, from->allocate(bytes), from, true);
     }
-    // a contiguous bf16 tensor over memory from element `at` on
+    // a contiguous tensor over memory from element `at` on
+    template <typename T>
     static at::Tensor part(c10::Storage all, int64_t at, at::IntArrayRef shape)
     {
         at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(
-            std::move(all), c10::DispatchKeySet(c10::DispatchKey::CUDA), caffe2::TypeMeta::Make<at::BFloat16>());
+            std::move(all), c10::DispatchKeySet(c10::DispatchKey::CUDA), caffe2::TypeMeta::Make<T>());
         t.unsafeGetTensorImpl()->set_sizes_contiguous(shape);
         t.unsafeGetTensorImpl()->set_storage_offset(at);
         return t;
@@ -269,6 +273,64 @@ PyObject* tree_attention(PyObject*, PyObject* const* args, Py_ssize_t n)
     });
 }
 
+// stream, k_pool, v_pool, k_scales, v_scales, src, dst, layout
+PyObject* copy_pages(PyObject*, PyObject* const* args, Py_ssize_t n)
+{
+    return guarded([&]() -> PyObject* {
+        Args a(args, n, 8);
+        const b2pa_tensor *k = a.desc(1), *v = a.desc(2), *ks = a.desc(3, true), *vs = a.desc(4, true);
+        const b2pa_tensor *src = a.desc(5), *dst = a.desc(6);
+        return PyLong_FromLong(b2pa_copy_pages(k, v, ks, vs, src, dst, a.int32(7), a.stream()));
+    });
+}
+
+// stream, k_pool, v_pool, k_scales, v_scales, block_tables, seq_lens, cum_q, accepted, counts, new_lens, layout
+PyObject* compact_kv(PyObject*, PyObject* const* args, Py_ssize_t n)
+{
+    return guarded([&]() -> PyObject* {
+        Args a(args, n, 12);
+        const b2pa_tensor *k = a.desc(1), *v = a.desc(2), *ks = a.desc(3, true), *vs = a.desc(4, true);
+        const b2pa_tensor *bt = a.desc(5), *seq = a.desc(6), *cum = a.desc(7), *acc = a.desc(8), *cnt = a.desc(9);
+        const at::Tensor lens = a.output<int32_t>(10, a.tensor(6).sizes());
+        const int st = b2pa_compact_kv(k, v, ks, vs, bt, seq, cum, acc, cnt, const_cast<b2pa_tensor*>(a.describe(lens)),
+                                       a.int32(11), a.stream());
+        return st == B2PA_OK ? THPVariable_Wrap(lens) : PyLong_FromLong(st);
+    });
+}
+
+// stream, block_tables, seq_lens, page_refs, rows, page_size
+PyObject* free_pages(PyObject*, PyObject* const* args, Py_ssize_t n)
+{
+    return guarded([&]() -> PyObject* {
+        Args a(args, n, 6);
+        const b2pa_tensor *bt = a.desc(1), *seq = a.desc(2), *refs = a.desc(3), *rows = a.desc(4);
+        return PyLong_FromLong(b2pa_free_pages(bt, seq, refs, rows, a.int32(5), a.stream()));
+    });
+}
+
+// stream, block_tables, seq_lens, page_refs, parents, children, page_size, src, dst
+PyObject* fork_pages(PyObject*, PyObject* const* args, Py_ssize_t n)
+{
+    return guarded([&]() -> PyObject* {
+        Args a(args, n, 9);
+        const b2pa_tensor *bt = a.desc(1), *seq = a.desc(2), *refs = a.desc(3), *from = a.desc(4), *to = a.desc(5);
+        const auto [src, dst] = a.outputs<int32_t>(7, a.tensor(5).sizes(), 8, a.tensor(5).sizes());
+        return two(b2pa_fork_pages(bt, seq, refs, from, to, a.int32(6), const_cast<b2pa_tensor*>(a.describe(src)),
+                                   const_cast<b2pa_tensor*>(a.describe(dst)), a.stream()),
+                   src, dst);
+    });
+}
+
+// stream, block_tables, seq_lens, page_refs, rows, new_lens, page_size
+PyObject* grow_pages(PyObject*, PyObject* const* args, Py_ssize_t n)
+{
+    return guarded([&]() -> PyObject* {
+        Args a(args, n, 7);
+        const b2pa_tensor *bt = a.desc(1), *seq = a.desc(2), *refs = a.desc(3), *rows = a.desc(4), *to = a.desc(5);
+        return PyLong_FromLong(b2pa_grow_pages(bt, seq, refs, rows, to, a.int32(6), a.stream()));
+    });
+}
+
 PyMethodDef methods[] = {
     {"qk_norm_rope", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(qk_norm_rope)), METH_FASTCALL, nullptr},
     {"append_kv_scaled", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(append_kv_scaled)), METH_FASTCALL,
@@ -277,6 +339,11 @@ PyMethodDef methods[] = {
      nullptr},
     {"tree_attention", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(tree_attention)), METH_FASTCALL,
      nullptr},
+    {"copy_pages", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(copy_pages)), METH_FASTCALL, nullptr},
+    {"compact_kv", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(compact_kv)), METH_FASTCALL, nullptr},
+    {"free_pages", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(free_pages)), METH_FASTCALL, nullptr},
+    {"fork_pages", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(fork_pages)), METH_FASTCALL, nullptr},
+    {"grow_pages", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(grow_pages)), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_native", "Direct bindings of a few calls of libb2pa.so.", -1, methods,

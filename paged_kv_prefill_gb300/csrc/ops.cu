@@ -13,19 +13,19 @@
 
 using namespace b2pa;
 
-namespace {
-
-// No C++ exception (an allocation that failed) may leave a C entry point.
-template <typename F>
-int guarded(F&& f)
+int b2pa::check_scales(const b2pa_tensor* s, const char* what, const b2pa_tensor* pool)
 {
-    try {
-        clear_error();
-        return f();
-    } catch (...) {
-        return B2PA_ERR_CUDA;
-    }
+    if (!s || !s->data || s->dtype != B2PA_FP32 || s->ndim != 3)
+        return fail(B2PA_ERR_INVALID_ARG, "%s must be fp32 with the pool's shape without head_dim", what);
+    for (int i = 0; i < 3; ++i)
+        if (s->shape[i] != pool->shape[i])
+            return fail(B2PA_ERR_INVALID_ARG, "%s must be fp32 with the pool's shape without head_dim", what);
+    if (reinterpret_cast<uintptr_t>(s->data) & 3u)
+        return fail(B2PA_ERR_INVALID_ARG, "%s must be 4-byte aligned", what);
+    return B2PA_OK;
 }
+
+namespace {
 
 // t is [T, heads, D] bf16, contiguous in head_dim, in 16-byte steps.
 int check_rows(const b2pa_tensor* t, const char* what, int64_t T, int64_t heads, int64_t D)
@@ -175,19 +175,6 @@ int rope_impl(const b2pa_tensor* q, const b2pa_tensor* k, const b2pa_tensor* cos
     p.inv_d = 1.f / (float)D;
     const cudaError_t e = launch_qk_norm_rope(p, interleaved != 0, di.sms, stream);
     return e == cudaSuccess ? B2PA_OK : cuda_fail(e, "norm and rotation launch");
-}
-
-// A scale tensor: the pool's shape without head_dim, fp32.
-int check_scales(const b2pa_tensor* s, const char* what, const b2pa_tensor* pool)
-{
-    if (!s || !s->data || s->dtype != B2PA_FP32 || s->ndim != 3)
-        return fail(B2PA_ERR_INVALID_ARG, "%s must be fp32 with the pool's shape without head_dim", what);
-    for (int i = 0; i < 3; ++i)
-        if (s->shape[i] != pool->shape[i])
-            return fail(B2PA_ERR_INVALID_ARG, "%s must be fp32 with the pool's shape without head_dim", what);
-    if (reinterpret_cast<uintptr_t>(s->data) & 3u)
-        return fail(B2PA_ERR_INVALID_ARG, "%s must be 4-byte aligned", what);
-    return B2PA_OK;
 }
 
 // What the write and the read share; rows: k_new/v_new or k_out/v_out.
