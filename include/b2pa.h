@@ -26,7 +26,8 @@
  * the heads' norms and rotary rotation (b2pa_qk_norm_rope), writing the new
  * tokens' K and V into the pools (b2pa_append_kv, quantising to e4m3 for an FP8
  * cache; b2pa_append_kv_scaled with a scale per row, b2pa_read_kv_scaled back),
- * and the attention that verifies trees of drafted tokens (b2pa_tree_attention);
+ * and the attention that verifies trees of drafted tokens (b2pa_tree_attention),
+ * with the verification itself (b2pa_verify_trees);
  * and it keeps a page ledger on the device (b2pa_fork_pages, b2pa_grow_pages,
  * b2pa_free_pages), copies pages (b2pa_copy_pages) and moves the accepted nodes
  * of a tree to their places (b2pa_compact_kv).
@@ -104,8 +105,9 @@ enum b2pa_device_error {
                                    finite and > 0, or bmm2_scale is not finite; nothing is written */
     B2PA_DEV_BAD_POSITION = 128,/* b2pa_qk_norm_rope: a position outside the table; that token's rows are
                                    not written */
-    B2PA_DEV_NO_PAGES = 256     /* b2pa_fork_pages, b2pa_grow_pages: not enough free pages for a request, which
+    B2PA_DEV_NO_PAGES = 256,    /* b2pa_fork_pages, b2pa_grow_pages: not enough free pages for a request, which
                                    stays as it was */
+    B2PA_DEV_BAD_PROBS = 512    /* b2pa_verify_trees: a target row without a positive finite value; no next token */
 };
 
 /* Kernel paths (b2pa_set_kernel_path). */
@@ -513,6 +515,54 @@ B2PA_API int b2pa_tree_attention(const b2pa_tensor* q, const b2pa_tensor* k_pool
                                  int32_t window_left, const b2pa_tensor* sinks, int32_t layout, b2pa_tensor* out,
                                  void* workspace, uint64_t workspace_bytes, uint64_t* bytes_needed,
                                  b2pa_stream_t stream);
+
+/*
+ * b2pa_verify_trees -- which drafted nodes the target accepts, and the token that
+ * follows them, from given random numbers: the step after the target model has
+ * scored the trees that b2pa_tree_attention attended.  The tokens that come out are
+ * distributed as the target's own.  No counterpart on the pages.
+ *
+ * Request b owns rows cum_q[b] .. cum_q[b+1] - 1, the nodes of its tree.  Node 0 is
+ * its root, the last token that is certain, and always accepted; every other
+ * node hangs on parents[row] (a node number below its own).  Row i of target_probs
+ * (and draft_probs) is the distribution of what follows node i.  From the last
+ * accepted node on, with p and q its rows, its children x_1, x_2, .. in the order of
+ * their numbers are tried:
+ *   with draft_probs (children drawn from q, independently):
+ *     R = p, M = 1; child r is accepted if R(x_r) > 0 and u_r q(x_r) M < R(x_r), u_r its
+ *     row of uniforms; else a += M (0 before), R = max(p - a q, 0), M = sum R;
+ *   without (children that the draft chose, as its likeliest tokens):
+ *     accepted if R(x_r) > 0 and u_r M < R(x_r); else M -= R(x_r), R(x_r) = 0.
+ * Where no child is accepted the path ends, and the next token is the first i with
+ * R(0) + .. + R(i) > last_uniforms[b] * sum R (R = p where sum R is 0).  All of it as in
+ * 64 bits: values R to 2^-46 of p, sums and comparisons in binary64.
+ *
+ *  target_probs  [T, V] fp32, stride[1] == 1, 1 <= V < 2^30, rows that sum to 1 (the
+ *                first child of a node is tried with M = 1, whatever the sum).
+ *                Values below 0, infinities and NaN count as 0.
+ *  draft_probs   NULL, or the same.
+ *  tokens        contiguous int32 [T]: each node's token (the root's is not read).  One
+ *                outside [0, V) is not accepted.
+ *  parents       contiguous int32 [T] (the root's is not read).
+ *  uniforms      contiguous fp32 [T], in [0, 1) (the root's is not read; NaN: refused).
+ *  last_uniforms contiguous fp32 [B], in [0, 1).
+ *  cum_q         contiguous int32 [B + 1].
+ *  max_q_len     upper bound on every tree's nodes; at most 4096.
+ *  accepted      out: [B, width] int32, stride[1] == 1, width >= max_q_len: the path's
+ *                nodes, 0 first, then -1 (what b2pa_compact_kv takes).
+ *  counts        out: contiguous int32 [B], the nodes on the path.
+ *  next_tokens   out: contiguous int32 [B].
+ * A tree of no nodes has count 0 and next token -1; so has a malformed request (a
+ * parent that does not come before its child, more than max_q_len nodes, rows
+ * outside [0, T)), which sets B2PA_DEV_BAD_REQUEST.  A last row without a positive
+ * finite value has next token -1 and sets B2PA_DEV_BAD_PROBS.
+ * Outputs must not overlap inputs.  Asynchronous on `stream`; one kernel.
+ */
+B2PA_API int b2pa_verify_trees(const b2pa_tensor* target_probs, const b2pa_tensor* draft_probs,
+                               const b2pa_tensor* tokens, const b2pa_tensor* parents, const b2pa_tensor* uniforms,
+                               const b2pa_tensor* last_uniforms, const b2pa_tensor* cum_q, int32_t max_q_len,
+                               b2pa_tensor* accepted, b2pa_tensor* counts, b2pa_tensor* next_tokens,
+                               b2pa_stream_t stream);
 
 /*
  * b2pa_copy_pages -- page src[i] of the pools to page dst[i], all heads and

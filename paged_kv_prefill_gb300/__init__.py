@@ -33,7 +33,7 @@ PATH_AUTO, PATH_TCGEN05, PATH_GENERIC = 0, 1, 2
 STATUS = {0: "B2PA_OK", -1: "B2PA_ERR_INVALID_ARG", -2: "B2PA_ERR_UNSUPPORTED", -3: "B2PA_ERR_CUDA",
           -4: "B2PA_ERR_DEVICE", -5: "B2PA_ERR_WORKSPACE"}
 DEV_BAD_REQUEST, DEV_BAD_PAGE, DEV_TIMEOUT, DEV_BAD_CUM_KV, DEV_OVERFLOW = 1, 2, 4, 8, 16
-DEV_BAD_SLOT, DEV_BAD_SCALE, DEV_BAD_POSITION, DEV_NO_PAGES = 32, 64, 128, 256
+DEV_BAD_SLOT, DEV_BAD_SCALE, DEV_BAD_POSITION, DEV_NO_PAGES, DEV_BAD_PROBS = 32, 64, 128, 256, 512
 
 _DTYPES = {
     torch.bfloat16: B2PA_BF16,
@@ -56,6 +56,7 @@ EXPORTED = [
     "b2pa_read_kv_scaled",
     "b2pa_qk_norm_rope",
     "b2pa_tree_attention",
+    "b2pa_verify_trees",
     "b2pa_copy_pages",
     "b2pa_compact_kv",
     "b2pa_free_pages",
@@ -139,6 +140,8 @@ def load(path: str = LIB_PATH):
     lib.b2pa_tree_attention.argtypes = [P] * 8 + [I, I, F, F, I, P, I, P, V, ctypes.c_uint64,
                                                   ctypes.POINTER(ctypes.c_uint64), V]
     lib.b2pa_tree_attention.restype = ctypes.c_int
+    lib.b2pa_verify_trees.argtypes = [P] * 7 + [I, P, P, P, V]
+    lib.b2pa_verify_trees.restype = ctypes.c_int
     lib.b2pa_copy_pages.argtypes = [P] * 6 + [I, V]
     lib.b2pa_copy_pages.restype = ctypes.c_int
     lib.b2pa_compact_kv.argtypes = [P] * 10 + [I, V]
@@ -637,6 +640,36 @@ def tree_attention(
         return _done(call(handle, *args), "b2pa_tree_attention")
     with _On(query, stream) as handle:
         return _done(call(handle, *args), "b2pa_tree_attention")
+
+
+def verify_trees(
+    target_probs: torch.Tensor,
+    tokens: torch.Tensor,
+    parents: torch.Tensor,
+    uniforms: torch.Tensor,
+    last_uniforms: torch.Tensor,
+    max_q_len: int,
+    cum_seq_lens_q: torch.Tensor,
+    draft_probs: Optional[torch.Tensor] = None,
+    accepted: Optional[torch.Tensor] = None,
+    num_accepted: Optional[torch.Tensor] = None,
+    next_tokens: Optional[torch.Tensor] = None,
+    stream=None,
+) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    """Which nodes of drafted trees the target accepts, from given random numbers; returns (accepted
+    [B, max_q_len], num_accepted [B], next_tokens [B]), int32 (see include/b2pa.h).
+
+    target_probs [T, V] fp32 holds, for each node, the target's probabilities of what follows it;
+    draft_probs the draft's, where the nodes' tokens were drawn from them, None where the draft chose
+    them.  parents int32 [T] names each node's parent within its request, whose node 0 is the root."""
+    call = (_calls or native()).verify_trees
+    args = (target_probs, draft_probs, tokens, parents, uniforms, last_uniforms, cum_seq_lens_q, max_q_len, accepted,
+            num_accepted, next_tokens)
+    handle = _here(target_probs, stream)
+    if handle >= 0:
+        return _done(call(handle, *args), "b2pa_verify_trees")
+    with _On(target_probs, stream) as handle:
+        return _done(call(handle, *args), "b2pa_verify_trees")
 
 
 def copy_pages(kv_cache, src: torch.Tensor, dst: torch.Tensor, kv_scales=None, kv_layout: str = "HND", stream=None):

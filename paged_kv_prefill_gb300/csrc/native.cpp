@@ -273,6 +273,32 @@ PyObject* tree_attention(PyObject*, PyObject* const* args, Py_ssize_t n)
     });
 }
 
+// stream, target_probs, draft_probs, tokens, parents, uniforms, last_uniforms, cum_q, max_q_len, accepted, counts,
+// next_tokens
+PyObject* verify_trees(PyObject*, PyObject* const* args, Py_ssize_t n)
+{
+    return guarded([&]() -> PyObject* {
+        Args a(args, n, 12);
+        const b2pa_tensor *p = a.desc(1), *q = a.desc(2, true), *tok = a.desc(3), *par = a.desc(4), *u = a.desc(5);
+        const b2pa_tensor *last = a.desc(6), *cum = a.desc(7);
+        const int32_t width = a.int32(8);
+        // (shapes that cannot be are refused by the call)
+        const int64_t B = last->ndim == 1 ? last->shape[0] : 0;
+        const at::Tensor acc = a.output<int32_t>(9, {B, width > 0 ? width : 0});
+        const auto [cnt, next] = a.outputs<int32_t>(10, {B}, 11, {B});
+        const int st = b2pa_verify_trees(p, q, tok, par, u, last, cum, width, const_cast<b2pa_tensor*>(a.describe(acc)),
+                                         const_cast<b2pa_tensor*>(a.describe(cnt)),
+                                         const_cast<b2pa_tensor*>(a.describe(next)), a.stream());
+        if (st != B2PA_OK)
+            return PyLong_FromLong(st);
+        PyObject* o[3] = {THPVariable_Wrap(acc), THPVariable_Wrap(cnt), THPVariable_Wrap(next)};
+        PyObject* t = o[0] && o[1] && o[2] ? PyTuple_Pack(3, o[0], o[1], o[2]) : nullptr;
+        for (PyObject* x : o)
+            Py_XDECREF(x);
+        return t;
+    });
+}
+
 // stream, k_pool, v_pool, k_scales, v_scales, src, dst, layout
 PyObject* copy_pages(PyObject*, PyObject* const* args, Py_ssize_t n)
 {
@@ -339,6 +365,7 @@ PyMethodDef methods[] = {
      nullptr},
     {"tree_attention", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(tree_attention)), METH_FASTCALL,
      nullptr},
+    {"verify_trees", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(verify_trees)), METH_FASTCALL, nullptr},
     {"copy_pages", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(copy_pages)), METH_FASTCALL, nullptr},
     {"compact_kv", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(compact_kv)), METH_FASTCALL, nullptr},
     {"free_pages", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(free_pages)), METH_FASTCALL, nullptr},

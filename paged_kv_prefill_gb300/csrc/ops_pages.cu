@@ -1,6 +1,6 @@
-// ops_pages.cu -- host side of the page ledger, of copying pages and of
-// moving the accepted nodes' rows.  Argument checks and launches; nothing
-// here synchronises.
+// ops_pages.cu -- host side of the page ledger, of copying pages, of the
+// verification of drafted trees and of moving the accepted nodes' rows.
+// Argument checks and launches; nothing here synchronises.
 #include <algorithm>
 #include <cstring>
 #include <utility>
@@ -8,6 +8,7 @@
 #include "../../include/b2pa.h"
 #include "host.cuh"
 #include "pages.cuh"
+#include "verify.cuh"
 
 using namespace b2pa;
 
@@ -183,6 +184,89 @@ int compact_impl(const b2pa_tensor* k_pool, const b2pa_tensor* v_pool, const b2p
     return e == cudaSuccess ? B2PA_OK : cuda_fail(e, "compaction launch");
 }
 
+// fp32 rows [T, V], contiguous in V
+int check_probs(const b2pa_tensor* t, const char* what, int64_t T, int64_t V)
+{
+    if (!t || t->ndim != 2 || t->dtype != B2PA_FP32 || t->shape[0] != T || t->shape[1] != V ||
+        (V > 1 && t->stride[1] != 1) || (T > 1 && t->stride[0] < 0) || (T > 0 && !t->data))
+        return fail(B2PA_ERR_INVALID_ARG, "%s must be fp32 [%lld, %lld], contiguous in its rows", what, (long long)T,
+                    (long long)V);
+    if (T > 0 && (reinterpret_cast<uintptr_t>(t->data) & 3u))
+        return fail(B2PA_ERR_INVALID_ARG, "%s must be 4-byte aligned", what);
+    return B2PA_OK;
+}
+
+int verify_impl(const b2pa_tensor* target, const b2pa_tensor* draft, const b2pa_tensor* tokens,
+                const b2pa_tensor* parents, const b2pa_tensor* uniforms, const b2pa_tensor* last,
+                const b2pa_tensor* cum_q, int32_t max_q_len, b2pa_tensor* accepted, b2pa_tensor* counts,
+                b2pa_tensor* next, cudaStream_t stream)
+{
+    if (!target || target->ndim != 2 || target->shape[0] < 0 || target->shape[0] > 0x7FFFFFFF || target->shape[1] < 1 ||
+        target->shape[1] >= 1 << 30)
+        return fail(B2PA_ERR_INVALID_ARG, "target_probs must be fp32 [T, V], 1 <= V < 2^30");
+    const int64_t T = target->shape[0], V = target->shape[1];
+    int st;
+    if ((st = check_probs(target, "target_probs", T, V)) || (draft && (st = check_probs(draft, "draft_probs", T, V))) ||
+        (st = check_ints(tokens, "tokens", T)) || (st = check_ints(parents, "parents", T)))
+        return st;
+    if (!uniforms || uniforms->dtype != B2PA_FP32 || uniforms->ndim != 1 || uniforms->shape[0] != T ||
+        (T > 0 && !is_vec(uniforms, B2PA_FP32, T)))
+        return fail(B2PA_ERR_INVALID_ARG, "uniforms must be contiguous fp32 [T]");
+    if (!counts || counts->ndim != 1 || counts->shape[0] < 0 || counts->shape[0] > 0x7FFFFFF)
+        return fail(B2PA_ERR_INVALID_ARG, "counts must be contiguous int32 [B]");
+    const int64_t B = counts->shape[0];
+    if ((st = check_ints(counts, "counts", B)) || (st = check_ints(next, "next_tokens", B)) ||
+        (st = check_ints(cum_q, "cum_q", B + 1)))
+        return st;
+    if (!last || last->dtype != B2PA_FP32 || last->ndim != 1 || last->shape[0] != B || (B > 0 && !is_vec(last, B2PA_FP32, B)))
+        return fail(B2PA_ERR_INVALID_ARG, "last_uniforms must be contiguous fp32 [B]");
+    if (max_q_len < 0)
+        return fail(B2PA_ERR_INVALID_ARG, "max_q_len must be >= 0");
+    if (max_q_len > kVerifyMaxNodes)
+        return fail(B2PA_ERR_UNSUPPORTED, "max_q_len must be at most %d", kVerifyMaxNodes);
+    if (!accepted || accepted->ndim != 2 || accepted->dtype != B2PA_INT32 || accepted->shape[0] != B ||
+        accepted->shape[1] < max_q_len || accepted->shape[1] > 0x7FFFFFFF ||
+        (accepted->shape[1] > 1 && accepted->stride[1] != 1) || (B > 1 && accepted->stride[0] < accepted->shape[1]) ||
+        (B > 0 && accepted->shape[1] > 0 && !accepted->data))
+        return fail(B2PA_ERR_INVALID_ARG,
+                    "accepted must be int32 [B, width] with unit column stride, its rows apart and width >= max_q_len");
+    if (B == 0)
+        return B2PA_OK;
+    if (counts->data == next->data || accepted->data == counts->data || accepted->data == next->data)
+        return fail(B2PA_ERR_INVALID_ARG, "accepted, counts and next_tokens must be three tensors");
+    int dev;
+    DevInfo di;
+    VerifyParams p;
+    std::memset(&p, 0, sizeof p);
+    if ((st = device_info(&dev, &di)) || (st = status_word(dev, stream, &p.err)))
+        return st;
+    p.target = static_cast<const float*>(target->data);
+    p.target_st = target->stride[0];
+    bool aligned = aligned16(p.target) && (T <= 1 || p.target_st % 4 == 0);
+    if (draft) {
+        p.draft = static_cast<const float*>(draft->data);
+        p.draft_st = draft->stride[0];
+        aligned = aligned && aligned16(p.draft) && (T <= 1 || p.draft_st % 4 == 0);
+    }
+    p.aligned = aligned;
+    p.tokens = ints(tokens);
+    p.parents = ints(parents);
+    p.uniforms = static_cast<const float*>(uniforms->data);
+    p.last = static_cast<const float*>(last->data);
+    p.cum_q = ints(cum_q);
+    p.accepted = ints(accepted);
+    p.acc_st = accepted->stride[0];
+    p.counts = ints(counts);
+    p.next = ints(next);
+    p.B = (int)B;
+    p.T = (int)T;
+    p.V = (int)V;
+    p.max_q = max_q_len;
+    p.width = (int)accepted->shape[1];
+    const cudaError_t e = launch_verify(p, di.sms, stream);
+    return e == cudaSuccess ? B2PA_OK : cuda_fail(e, "verification launch");
+}
+
 // What the ledger's calls share; `rows` are [n].
 int parse_ledger(const b2pa_tensor* block_tables, const b2pa_tensor* seq_lens, const b2pa_tensor* page_refs,
                  const b2pa_tensor* rows, const char* what, int32_t page_size, LedgerParams* p)
@@ -258,6 +342,17 @@ int b2pa_compact_kv(const b2pa_tensor* k_pool, const b2pa_tensor* v_pool, const 
     return guarded([&] {
         return compact_impl(k_pool, v_pool, k_scales, v_scales, block_tables, seq_lens, cum_q, accepted, counts,
                             new_lens, layout, reinterpret_cast<cudaStream_t>(stream));
+    });
+}
+
+int b2pa_verify_trees(const b2pa_tensor* target_probs, const b2pa_tensor* draft_probs, const b2pa_tensor* tokens,
+                      const b2pa_tensor* parents, const b2pa_tensor* uniforms, const b2pa_tensor* last_uniforms,
+                      const b2pa_tensor* cum_q, int32_t max_q_len, b2pa_tensor* accepted, b2pa_tensor* counts,
+                      b2pa_tensor* next_tokens, b2pa_stream_t stream)
+{
+    return guarded([&] {
+        return verify_impl(target_probs, draft_probs, tokens, parents, uniforms, last_uniforms, cum_q, max_q_len,
+                           accepted, counts, next_tokens, reinterpret_cast<cudaStream_t>(stream));
     });
 }
 
