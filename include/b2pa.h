@@ -27,7 +27,8 @@
  * tokens' K and V into the pools (b2pa_append_kv, quantising to e4m3 for an FP8
  * cache; b2pa_append_kv_scaled with a scale per row, b2pa_read_kv_scaled back),
  * and the attention that verifies trees of drafted tokens (b2pa_tree_attention),
- * with the verification itself (b2pa_verify_trees);
+ * with the verification itself (b2pa_verify_trees), and the attention of requests
+ * that share a cached prefix (b2pa_prefix_attention);
  * and it keeps a page ledger on the device (b2pa_fork_pages, b2pa_grow_pages,
  * b2pa_free_pages), copies pages (b2pa_copy_pages) and moves the accepted nodes
  * of a tree to their places (b2pa_compact_kv).
@@ -86,7 +87,8 @@ enum b2pa_status {
     B2PA_ERR_UNSUPPORTED = -2, /* valid but not implemented (e.g. a forced kernel path that cannot run the shape) */
     B2PA_ERR_CUDA = -3,        /* a CUDA runtime/driver call failed; see b2pa_last_error_message */
     B2PA_ERR_DEVICE = -4,      /* b2pa_get_device_status: the device error word was non-zero */
-    B2PA_ERR_WORKSPACE = -5    /* b2pa_tree_attention: workspace_bytes is less than *bytes_needed; nothing ran */
+    B2PA_ERR_WORKSPACE = -5    /* b2pa_tree_attention, b2pa_prefix_attention: workspace_bytes is less than
+                                  *bytes_needed; nothing ran */
 };
 
 /* Bits of the device error word (b2pa_get_device_status). */
@@ -515,6 +517,51 @@ B2PA_API int b2pa_tree_attention(const b2pa_tensor* q, const b2pa_tensor* k_pool
                                  int32_t window_left, const b2pa_tensor* sinks, int32_t layout, b2pa_tensor* out,
                                  void* workspace, uint64_t workspace_bytes, uint64_t* bytes_needed,
                                  b2pa_stream_t stream);
+
+/*
+ * b2pa_prefix_attention -- attention of requests in groups that share a cached
+ * prefix (one prompt sampled several times, a common system prompt, questions
+ * about one document): the prefix's keys and values are read once for a group.  No
+ * counterpart on the pages.
+ *
+ * Requests cum_groups[g] .. cum_groups[g+1] - 1 are group g and share the first
+ * prefix_lens[g] keys, on the pages of prefix_tables[g].  Behind them request b has
+ * seq_lens[b] keys of its own, on the pages of block_tables[b]; its n = cum_q[b+1] -
+ * cum_q[b] query rows are the tokens of the last n of these.  Row i sees the whole
+ * prefix and the request's own keys 0 .. seq_lens[b] - n + i.  With s_j = bmm1_scale
+ * <q, K_j> over all those keys and m their largest:
+ *   out = bmm2_scale * sum_j e^{s_j - m} V_j / (sum_j e^{s_j - m} + [sinks] e^{sinks[h] - m})
+ * A request before cum_groups[0] or from cum_groups[groups] on has no prefix; an
+ * empty group, and a prefix of length 0, are allowed.  Positions play no part: the
+ * keys are cached with theirs.
+ *
+ * q, pools, block_tables, seq_lens, cum_q, scales, sinks, layout and out as for
+ * b2pa_context_attention (out must not overlap any input, nor its rows one
+ * another), and:
+ *  prefix_tables  [groups, columns] int32, stride[1] == 1.
+ *  prefix_lens    contiguous int32 [groups].
+ *  cum_groups     contiguous int32 [groups + 1], not falling, within 0 .. B.
+ *  max_q_len      upper bound on every n.
+ *  max_group_q_len  a group's tokens at most, or any larger number (it is taken as T at
+ *                 most): sizes the query tiles; results are right for any value.
+ *  max_prefix_len, max_kv_len   upper bounds on prefix_lens and seq_lens; at most 2^31 - 257.
+ *  workspace, bytes_needed   as for b2pa_tree_attention.
+ * A malformed request (as for b2pa_context_attention) or group (a prefix longer than
+ * max_prefix_len or its table, cum_groups that falls or leaves 0 .. B) sets
+ * B2PA_DEV_BAD_REQUEST, and its rows are not written; which groups hold which
+ * requests is unspecified where cum_groups falls.  A page id outside the pool sets
+ * B2PA_DEV_BAD_PAGE and its keys read as 0.
+ *
+ * Precision, paths, capture and allocation are those of b2pa_tree_attention.
+ */
+B2PA_API int b2pa_prefix_attention(const b2pa_tensor* q, const b2pa_tensor* k_pool, const b2pa_tensor* v_pool,
+                                   const b2pa_tensor* prefix_tables, const b2pa_tensor* prefix_lens,
+                                   const b2pa_tensor* cum_groups, const b2pa_tensor* block_tables,
+                                   const b2pa_tensor* seq_lens, const b2pa_tensor* cum_q, int32_t max_q_len,
+                                   int32_t max_group_q_len, int32_t max_prefix_len, int32_t max_kv_len,
+                                   float bmm1_scale, float bmm2_scale, const b2pa_tensor* sinks, int32_t layout,
+                                   b2pa_tensor* out, void* workspace, uint64_t workspace_bytes,
+                                   uint64_t* bytes_needed, b2pa_stream_t stream);
 
 /*
  * b2pa_verify_trees -- which drafted nodes the target accepts, and the token that

@@ -56,6 +56,7 @@ EXPORTED = [
     "b2pa_read_kv_scaled",
     "b2pa_qk_norm_rope",
     "b2pa_tree_attention",
+    "b2pa_prefix_attention",
     "b2pa_verify_trees",
     "b2pa_copy_pages",
     "b2pa_compact_kv",
@@ -140,6 +141,9 @@ def load(path: str = LIB_PATH):
     lib.b2pa_tree_attention.argtypes = [P] * 8 + [I, I, F, F, I, P, I, P, V, ctypes.c_uint64,
                                                   ctypes.POINTER(ctypes.c_uint64), V]
     lib.b2pa_tree_attention.restype = ctypes.c_int
+    lib.b2pa_prefix_attention.argtypes = [P] * 9 + [I, I, I, I, F, F, P, I, P, V, ctypes.c_uint64,
+                                                    ctypes.POINTER(ctypes.c_uint64), V]
+    lib.b2pa_prefix_attention.restype = ctypes.c_int
     lib.b2pa_verify_trees.argtypes = [P] * 7 + [I, P, P, P, V]
     lib.b2pa_verify_trees.restype = ctypes.c_int
     lib.b2pa_copy_pages.argtypes = [P] * 6 + [I, V]
@@ -640,6 +644,49 @@ def tree_attention(
         return _done(call(handle, *args), "b2pa_tree_attention")
     with _On(query, stream) as handle:
         return _done(call(handle, *args), "b2pa_tree_attention")
+
+
+def prefix_attention(
+    query: torch.Tensor,
+    kv_cache: Union[torch.Tensor, Sequence[torch.Tensor]],
+    prefix_tables: torch.Tensor,
+    prefix_lens: torch.Tensor,
+    cum_groups: torch.Tensor,
+    block_tables: torch.Tensor,
+    seq_lens: torch.Tensor,
+    max_q_len: int,
+    max_prefix_len: int,
+    max_kv_len: int,
+    bmm1_scale: float,
+    bmm2_scale: float,
+    cum_seq_lens_q: torch.Tensor,
+    max_group_q_len: Optional[int] = None,
+    out: Optional[torch.Tensor] = None,
+    kv_layout: str = "HND",
+    sinks: Optional[torch.Tensor] = None,
+    stream=None,
+) -> torch.Tensor:
+    """Attention of requests in groups that share a cached prefix (see include/b2pa.h).
+
+    Requests cum_groups[g] .. cum_groups[g + 1] - 1 share the prefix_lens[g] keys on the pages of
+    prefix_tables[g]; behind them each has seq_lens[b] keys of its own on those of block_tables[b],
+    whose last ones are its query rows'.  max_group_q_len, the most tokens that a group has, sizes the
+    query tiles (None: all tokens may be one group's).  The call's workspace comes from torch's
+    allocator."""
+    call = (_calls or native()).prefix_attention
+    k, v = split_kv_cache(kv_cache, kv_layout)
+    if isinstance(sinks, (list, tuple)):
+        if len(sinks) != 1:
+            raise ValueError("sinks: one fp32 [num_heads] tensor")
+        sinks = sinks[0]
+    args = (query, k, v, prefix_tables, prefix_lens, cum_groups, block_tables, seq_lens, cum_seq_lens_q, max_q_len,
+            0x7FFFFFFF if max_group_q_len is None else max_group_q_len, max_prefix_len, max_kv_len, bmm1_scale,
+            bmm2_scale, sinks, LAYOUTS[kv_layout], out)
+    handle = _here(query, stream)
+    if handle >= 0:
+        return _done(call(handle, *args), "b2pa_prefix_attention")
+    with _On(query, stream) as handle:
+        return _done(call(handle, *args), "b2pa_prefix_attention")
 
 
 def verify_trees(

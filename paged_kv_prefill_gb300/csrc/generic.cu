@@ -292,6 +292,133 @@ __global__ void __launch_bounds__(kGenericWarps * 32) tree_generic_kernel(const 
     }
 }
 
+// The same for requests that share prefixes (prefix_request): the prefix's keys,
+// then the request's own up to the row's.
+template <bool FP8>
+__global__ void __launch_bounds__(kGenericWarps * 32) prefix_generic_kernel(const __grid_constant__ TreeParams p)
+{
+    extern __shared__ float qs_all[];
+    constexpr float kLog2e = 1.4426950408889634f;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, groups = p.prefix.groups;
+    float* qs = qs_all + warp * p.D;
+    if (blockIdx.x == 0)
+        for (int v = threadIdx.x; v < groups + p.B; v += blockDim.x)
+            if (!prefix_request(p, v, 1).ok)
+                atomicOr(p.err, (unsigned)B2PA_DEV_BAD_REQUEST);
+    const long long rowid = (long long)blockIdx.x * kGenericWarps + warp;
+    if (rowid >= (long long)p.T * p.H)
+        return;
+    const int tok = (int)(rowid / p.H), h = (int)(rowid % p.H), hk = h / p.rows.G;
+    int lo_b = 0, hi_b = p.B - 1;  // the last request that starts at or before tok
+    while (lo_b < hi_b) {
+        const int mid = (lo_b + hi_b + 1) >> 1;
+        if (p.cum_q[mid] <= tok)
+            lo_b = mid;
+        else
+            hi_b = mid - 1;
+    }
+    const TreeReq own = prefix_request(p, groups + lo_b, 1);
+    if (!own.ok || tok < own.q0 || tok >= own.q0 + own.n)
+        return;  // a rejected request, or a token no request owns
+    const int g = prefix_group(p, lo_b);
+    int keys[2] = {0, own.kv_len - own.n + tok - own.q0 + 1};  // seen of the prefix, and of its own
+    if (g >= 0) {
+        const TreeReq r = prefix_request(p, g, 1);
+        if (!r.ok)
+            return;
+        keys[0] = r.kv_len;
+    }
+    const uint16_t* qrow = p.q + (long long)tok * p.q_st_tok + (long long)h * p.q_st_head;
+    for (int d = lane; d < p.D; d += 32)
+        qs[d] = __uint_as_float(static_cast<uint32_t>(qrow[d]) << 16);
+    __syncwarp();
+
+    constexpr int kPer = kGenericMaxD / 32;
+    float o[kPer];
+#pragma unroll
+    for (int k = 0; k < kPer; ++k)
+        o[k] = 0.f;
+    float m = -INFINITY, l = 0.f;
+    for (int part = 0; part < 2; ++part) {
+        const int* pages = prefix_pages(p, part == 0 ? max(g, 0) : groups + lo_b);
+        for (int base = 0; base < keys[part]; base += 32) {
+            const int key = base + lane;
+            const bool vis = key < keys[part];
+            long long v_off = -1;
+            float s = -INFINITY;
+            if (vis) {
+                const int page = pages[key / p.page_size], slot = key % p.page_size;
+                if (page >= 0 && page < p.num_pages) {
+                    const long long k_off =
+                        (long long)page * p.k_st[0] + (long long)hk * p.k_st[1] + (long long)slot * p.k_st[2];
+                    v_off = (long long)page * p.v_st[0] + (long long)hk * p.v_st[1] + (long long)slot * p.v_st[2];
+                    float dot = 0.f;
+                    for (int d = 0; d < p.D; ++d)
+                        dot = fmaf(qs[d], load_elem<FP8>(p.k, k_off + d), dot);
+                    s = dot * p.scale_log2;
+                } else {
+                    atomicOr(p.err, (unsigned)B2PA_DEV_BAD_PAGE);
+                    s = 0.f;  // K = V = 0
+                }
+            }
+            float cm = s;
+#pragma unroll
+            for (int w = 16; w > 0; w >>= 1)
+                cm = fmaxf(cm, __shfl_xor_sync(0xffffffffu, cm, w));
+            const float m_new = fmaxf(m, cm);
+            const float ref = m_new == -INFINITY ? 0.f : m_new;
+            const float alpha = m == -INFINITY ? 0.f : exp2f(m - ref);
+            const float pj = vis ? exp2f(s - ref) : 0.f;
+            float ps = pj;
+#pragma unroll
+            for (int w = 16; w > 0; w >>= 1)
+                ps += __shfl_xor_sync(0xffffffffu, ps, w);
+            l = (m == -INFINITY && l == 0.f ? 0.f : l * alpha) + ps;
+#pragma unroll
+            for (int k = 0; k < kPer; ++k)
+                o[k] *= alpha;
+            for (int kk = 0; kk < 32; ++kk) {
+                const float pk = __shfl_sync(0xffffffffu, pj, kk);
+                const long long vo = __shfl_sync(0xffffffffu, v_off, kk);
+                if (vo < 0)
+                    continue;  // not seen, or V = 0
+#pragma unroll
+                for (int k = 0; k < kPer; ++k) {
+                    const int d = lane + 32 * k;
+                    if (d < p.D)
+                        o[k] = fmaf(pk, load_elem<FP8>(p.v, vo + d), o[k]);
+                }
+            }
+            m = m_new;
+        }
+    }
+    float total = l;
+    if (p.sinks != nullptr && m != -INFINITY)
+        total += exp2f(fmaf(p.sinks[h], kLog2e, -m));
+    const float inv = total == 0.f ? 0.f : p.bmm2 / total;
+    uint16_t* orow = p.out + (long long)tok * p.out_st_tok + (long long)h * p.out_st_head;
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+        const int d = lane + 32 * k;
+        if (d < p.D)
+            orow[d] = to_bf16(o[k] * inv);
+    }
+}
+
+cudaError_t launch_prefix_generic(const TreeParams& p, bool fp8, cudaStream_t stream)
+{
+    const long long rows = (long long)p.T * p.H;
+    const long long blocks = (rows + kGenericWarps - 1) / kGenericWarps;
+    if (blocks > 0x7FFFFFFFLL)
+        return cudaErrorInvalidValue;
+    const size_t smem = sizeof(float) * kGenericWarps * p.D;
+    if (fp8)
+        prefix_generic_kernel<true><<<(unsigned)blocks, kGenericWarps * 32, smem, stream>>>(p);
+    else
+        prefix_generic_kernel<false><<<(unsigned)blocks, kGenericWarps * 32, smem, stream>>>(p);
+    return cudaGetLastError();
+}
+
 cudaError_t launch_tree_generic(const TreeParams& p, bool fp8, cudaStream_t stream)
 {
     const long long rows = (long long)p.T * p.H;

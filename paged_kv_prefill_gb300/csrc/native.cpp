@@ -247,6 +247,19 @@ PyObject* read_kv_scaled(PyObject*, PyObject* const* args, Py_ssize_t n)
     });
 }
 
+// A call that says how much workspace it needs.  That comes from torch's allocator
+// for this call, so that every captured graph keeps its own.
+template <typename F>
+int with_workspace(F&& call)
+{
+    uint64_t need = 0;
+    const int st = call(nullptr, 0, &need);
+    if (st != B2PA_ERR_WORKSPACE)
+        return st;
+    const c10::DataPtr workspace = c10::cuda::CUDACachingAllocator::get()->allocate(need);
+    return call(workspace.get(), need, &need);
+}
+
 // stream, q, k_pool, v_pool, block_tables, seq_lens, cum_q, tree_mask, positions, max_q_len, max_kv_len, bmm1_scale,
 // bmm2_scale, window_left, sinks, layout, out
 PyObject* tree_attention(PyObject*, PyObject* const* args, Py_ssize_t n)
@@ -257,18 +270,30 @@ PyObject* tree_attention(PyObject*, PyObject* const* args, Py_ssize_t n)
         const b2pa_tensor *cum = a.desc(6), *mask = a.desc(7), *pos = a.desc(8, true), *sinks = a.desc(14, true);
         const at::Tensor out = a.output(16, a.tensor(1).sizes());
         b2pa_tensor* o = const_cast<b2pa_tensor*>(a.describe(out));
-        uint64_t need = 0;
-        auto call = [&](void* workspace, uint64_t bytes) {
+        const int st = with_workspace([&](void* workspace, uint64_t bytes, uint64_t* need) {
             return b2pa_tree_attention(q, k, v, bt, seq, cum, mask, pos, a.int32(9), a.int32(10), a.number(11),
-                                       a.number(12), a.int32(13), sinks, a.int32(15), o, workspace, bytes, &need,
+                                       a.number(12), a.int32(13), sinks, a.int32(15), o, workspace, bytes, need,
                                        a.stream());
-        };
-        int st = call(nullptr, 0);
-        if (st == B2PA_ERR_WORKSPACE) {
-            // from torch's allocator for this call, so that every captured graph keeps its own
-            const c10::DataPtr workspace = c10::cuda::CUDACachingAllocator::get()->allocate(need);
-            st = call(workspace.get(), need);
-        }
+        });
+        return st == B2PA_OK ? THPVariable_Wrap(out) : PyLong_FromLong(st);
+    });
+}
+
+// stream, q, k_pool, v_pool, prefix_tables, prefix_lens, cum_groups, block_tables, seq_lens, cum_q, max_q_len,
+// max_group_q_len, max_prefix_len, max_kv_len, bmm1_scale, bmm2_scale, sinks, layout, out
+PyObject* prefix_attention(PyObject*, PyObject* const* args, Py_ssize_t n)
+{
+    return guarded([&]() -> PyObject* {
+        Args a(args, n, 19);
+        const b2pa_tensor *q = a.desc(1), *k = a.desc(2), *v = a.desc(3), *pt = a.desc(4), *pl = a.desc(5);
+        const b2pa_tensor *cg = a.desc(6), *bt = a.desc(7), *seq = a.desc(8), *cum = a.desc(9), *sinks = a.desc(16, true);
+        const at::Tensor out = a.output(18, a.tensor(1).sizes());
+        b2pa_tensor* o = const_cast<b2pa_tensor*>(a.describe(out));
+        const int st = with_workspace([&](void* workspace, uint64_t bytes, uint64_t* need) {
+            return b2pa_prefix_attention(q, k, v, pt, pl, cg, bt, seq, cum, a.int32(10), a.int32(11), a.int32(12),
+                                         a.int32(13), a.number(14), a.number(15), sinks, a.int32(17), o, workspace,
+                                         bytes, need, a.stream());
+        });
         return st == B2PA_OK ? THPVariable_Wrap(out) : PyLong_FromLong(st);
     });
 }
@@ -364,6 +389,8 @@ PyMethodDef methods[] = {
     {"read_kv_scaled", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(read_kv_scaled)), METH_FASTCALL,
      nullptr},
     {"tree_attention", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(tree_attention)), METH_FASTCALL,
+     nullptr},
+    {"prefix_attention", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(prefix_attention)), METH_FASTCALL,
      nullptr},
     {"verify_trees", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(verify_trees)), METH_FASTCALL, nullptr},
     {"copy_pages", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(copy_pages)), METH_FASTCALL, nullptr},

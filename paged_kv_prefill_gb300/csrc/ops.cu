@@ -1,6 +1,7 @@
 // ops.cu -- host side of the entry points around the attention call: the
 // query/key norm with the rotation, the write and read of a cache with one
-// scale per row, and the attention of token trees.  Argument checks and launches; nothing here synchronises.
+// scale per row, and the attention of token trees and of requests that share
+// prefixes.  Argument checks and launches; nothing here synchronises.
 #include <algorithm>
 #include <cmath>
 #include <cstring>
@@ -296,6 +297,61 @@ int plan_tree(const Problem& pr, int max_q_len, int max_kv_len, int window, cons
     return B2PA_OK;
 }
 
+// What the calls of a few rows per request hand to their kernels alike.
+int fill_tree(const Problem& pr, int max_q_len, int max_kv_len, float bmm1_scale, float bmm2_scale, const DevInfo& di,
+              int dev, cudaStream_t stream, TreeParams* out)
+{
+    TreeParams& p = *out;
+    std::memset(&p, 0, sizeof p);
+    if (const int st = status_word(dev, stream, &p.err))
+        return st;
+    p.rows = tree_rows(pr.H / pr.Hkv);
+    p.q = static_cast<const uint16_t*>(pr.q);
+    p.k = pr.k;
+    p.v = pr.v;
+    p.out = static_cast<uint16_t*>(pr.out);
+    p.q_st_tok = pr.q_st_tok;
+    p.q_st_head = pr.q_st_head;
+    p.out_st_tok = pr.out_st_tok;
+    p.out_st_head = pr.out_st_head;
+    for (int i = 0; i < 3; ++i) {
+        p.k_st[i] = pr.k_st[i];
+        p.v_st[i] = pr.v_st[i];
+    }
+    p.cum_q = pr.cum_q;
+    p.seq_lens = pr.seq;
+    p.block_tables = pr.bt;
+    p.bt_stride = pr.bt_stride;
+    p.sinks = pr.sinks;
+    p.B = pr.B;
+    p.T = pr.T;
+    p.H = pr.H;
+    p.Hkv = pr.Hkv;
+    p.D = pr.D;
+    p.page_size = pr.P;
+    p.max_pages = pr.max_pages;
+    p.num_pages = pr.N;
+    p.max_q_len = max_q_len;
+    p.max_kv_len = max_kv_len;
+    p.window = -1;
+    p.grid = di.sms;
+    p.scale_log2 = (float)((double)bmm1_scale * 1.4426950408889634);
+    p.bmm2 = bmm2_scale;
+    p.wait_limit_ns = wait_limit_ns();
+    p.inject_stall = inject_stall();
+    return B2PA_OK;
+}
+
+// The tensor maps of the tensor-core path.
+int encode_tree_maps(const Problem& pr, TreeParams* p)
+{
+    int st;
+    if ((st = encode_q_map(&p->tm_q, pr, p->rows.box_toks)) || (st = encode_pool_map(&p->tm_k, pr, pr.k, pr.k_st)) ||
+        (st = encode_pool_map(&p->tm_v, pr, pr.v, pr.v_st)))
+        return st;
+    return B2PA_OK;
+}
+
 int tree_impl(const b2pa_tensor* q, const b2pa_tensor* k_pool, const b2pa_tensor* v_pool,
               const b2pa_tensor* block_tables, const b2pa_tensor* seq_lens, const b2pa_tensor* cum_q,
               const b2pa_tensor* tree_mask, const b2pa_tensor* positions, int32_t max_q_len, int32_t max_kv_len,
@@ -350,47 +406,13 @@ int tree_impl(const b2pa_tensor* q, const b2pa_tensor* k_pool, const b2pa_tensor
     if (plan.bytes && (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u)))
         return fail(B2PA_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
     TreeParams p;
-    std::memset(&p, 0, sizeof p);
-    if ((st = status_word(dev, stream, &p.err)))
+    if ((st = fill_tree(pr, max_q_len, max_kv_len, bmm1_scale, bmm2_scale, di, dev, stream, &p)))
         return st;
-    p.rows = tree_rows(pr.H / pr.Hkv);
-    p.q = static_cast<const uint16_t*>(pr.q);
-    p.k = pr.k;
-    p.v = pr.v;
-    p.out = static_cast<uint16_t*>(pr.out);
-    p.q_st_tok = pr.q_st_tok;
-    p.q_st_head = pr.q_st_head;
-    p.out_st_tok = pr.out_st_tok;
-    p.out_st_head = pr.out_st_head;
-    for (int i = 0; i < 3; ++i) {
-        p.k_st[i] = pr.k_st[i];
-        p.v_st[i] = pr.v_st[i];
-    }
-    p.cum_q = pr.cum_q;
-    p.seq_lens = pr.seq;
-    p.block_tables = pr.bt;
-    p.bt_stride = pr.bt_stride;
     p.mask = static_cast<const unsigned*>(tree_mask->data);
     p.mask_stride = tree_mask->stride[0];
     p.mask_words = (int)tree_mask->shape[1];
     p.positions = window >= 0 ? static_cast<const int*>(positions->data) : nullptr;
-    p.sinks = pr.sinks;
-    p.B = pr.B;
-    p.T = pr.T;
-    p.H = pr.H;
-    p.Hkv = pr.Hkv;
-    p.D = pr.D;
-    p.page_size = pr.P;
-    p.max_pages = pr.max_pages;
-    p.num_pages = pr.N;
-    p.max_q_len = max_q_len;
-    p.max_kv_len = max_kv_len;
     p.window = window;
-    p.grid = di.sms;
-    p.scale_log2 = (float)((double)bmm1_scale * 1.4426950408889634);
-    p.bmm2 = bmm2_scale;
-    p.wait_limit_ns = wait_limit_ns();
-    p.inject_stall = inject_stall();
     cudaError_t e;
     if (plan.tc) {
         p.whole = plan.whole;
@@ -400,14 +422,137 @@ int tree_impl(const b2pa_tensor* q, const b2pa_tensor* k_pool, const b2pa_tensor
             p.part_ml = reinterpret_cast<float2*>(ws + plan.off_ml);
             p.part_o = reinterpret_cast<float4*>(ws + plan.off_o);
         }
-        if ((st = encode_q_map(&p.tm_q, pr, p.rows.box_toks)) || (st = encode_pool_map(&p.tm_k, pr, pr.k, pr.k_st)) ||
-            (st = encode_pool_map(&p.tm_v, pr, pr.v, pr.v_st)))
+        if ((st = encode_tree_maps(pr, &p)))
             return st;
         e = launch_attention_tree(p, pr.fp8, plan.tiles, stream);
     } else {
         e = launch_tree_generic(p, pr.fp8, stream);
     }
     return e == cudaSuccess ? B2PA_OK : cuda_fail(e, "tree attention launch");
+}
+
+// Scratch of a prefix attention call on the tensor cores.
+struct PrefixPlan {
+    bool tc;
+    int tiles;  // query tiles per item
+    size_t off_o[2], off_rec[2], off_cut_o, off_cut_rec, off_ends, bytes;
+};
+
+int plan_prefix(const Problem& pr, int max_q_len, int max_group_q_len, const DevInfo& di, PrefixPlan* out)
+{
+    const char* why = tc_reject(pr, di);
+    const int path = kernel_path();
+    if (path == B2PA_PATH_TCGEN05 && why)
+        return fail(B2PA_ERR_UNSUPPORTED, "tensor-core path: %s", why);
+    PrefixPlan t{};
+    t.tc = path != B2PA_PATH_GENERIC && !why;
+    if (t.tc) {
+        t.tiles = std::max(max_q_len, max_group_q_len) <= tree_rows(pr.H / pr.Hkv).tile_toks ? 1 : 2;
+        size_t at = 0;
+        auto take = [&](size_t bytes) {
+            const size_t here = at;
+            at += (bytes + 255) / 256 * 256;
+            return here;
+        };
+        const size_t rows = (size_t)pr.T * pr.H, cut = (size_t)di.sms * t.tiles * kQRows;
+        for (int i = 0; i < 2; ++i) {
+            t.off_o[i] = take(rows * pr.D * sizeof(float));
+            t.off_rec[i] = take(rows * sizeof(float4));
+        }
+        t.off_cut_o = take(cut * pr.D * sizeof(float));
+        t.off_cut_rec = take(cut * sizeof(float4));
+        t.off_ends = take((size_t)di.sms * sizeof(int));
+        t.bytes = at;
+    }
+    *out = t;
+    return B2PA_OK;
+}
+
+int prefix_impl(const b2pa_tensor* q, const b2pa_tensor* k_pool, const b2pa_tensor* v_pool,
+                const b2pa_tensor* prefix_tables, const b2pa_tensor* prefix_lens, const b2pa_tensor* cum_groups,
+                const b2pa_tensor* block_tables, const b2pa_tensor* seq_lens, const b2pa_tensor* cum_q,
+                int32_t max_q_len, int32_t max_group_q_len, int32_t max_prefix_len, int32_t max_kv_len,
+                float bmm1_scale, float bmm2_scale, const b2pa_tensor* sinks, int32_t layout, b2pa_tensor* out,
+                void* workspace, uint64_t workspace_bytes, uint64_t* bytes_needed, cudaStream_t stream)
+{
+    if (!bytes_needed)
+        return fail(B2PA_ERR_INVALID_ARG, "bytes_needed: null");
+    // empty tensors may carry null data pointers
+    b2pa_tensor no_q, no_out;
+    if (q && out && k_pool && q->ndim == 3 && q->shape[0] == 0) {
+        no_q = *q;
+        no_out = *out;
+        no_q.data = no_out.data = k_pool->data;
+        q = &no_q;
+        out = &no_out;
+    }
+    Problem pr;
+    int st = parse_problem(q, k_pool, v_pool, block_tables, seq_lens, cum_q, nullptr, sinks, layout, out, &pr);
+    if (st)
+        return st;
+    if (max_q_len < 0 || max_group_q_len < 0 || max_prefix_len < 0 || max_kv_len < 0)
+        return fail(B2PA_ERR_INVALID_ARG, "max_q_len / max_group_q_len / max_prefix_len / max_kv_len must be >= 0");
+    if (max_kv_len > 0x7FFFFFFF - 2 * kKvTile || max_prefix_len > 0x7FFFFFFF - 2 * kKvTile)
+        return fail(B2PA_ERR_UNSUPPORTED, "max_prefix_len and max_kv_len must be at most 2^31 - 257");
+    if (!std::isfinite(bmm1_scale) || !(bmm1_scale > 0.f) || !std::isfinite(bmm2_scale))
+        return fail(B2PA_ERR_INVALID_ARG, "bmm1_scale must be finite and > 0, bmm2_scale finite");
+    if (!prefix_lens || prefix_lens->ndim != 1 || prefix_lens->shape[0] < 0 || prefix_lens->shape[0] > 0x7FFFFFF ||
+        (prefix_lens->shape[0] > 0 && !is_vec(prefix_lens, B2PA_INT32, prefix_lens->shape[0])))
+        return fail(B2PA_ERR_INVALID_ARG, "prefix_lens must be contiguous int32 [groups]");
+    const int64_t groups = prefix_lens->shape[0];
+    if (!is_vec(cum_groups, B2PA_INT32, groups + 1))
+        return fail(B2PA_ERR_INVALID_ARG, "cum_groups must be contiguous int32 [groups + 1]");
+    if (!prefix_tables || prefix_tables->ndim != 2 || prefix_tables->dtype != B2PA_INT32 ||
+        prefix_tables->shape[0] != groups || prefix_tables->shape[1] < 0 || prefix_tables->shape[1] > 0x7FFFFFFF ||
+        (prefix_tables->shape[1] > 1 && prefix_tables->stride[1] != 1) ||
+        (groups > 0 && prefix_tables->shape[1] > 0 && !prefix_tables->data))
+        return fail(B2PA_ERR_INVALID_ARG, "prefix_tables must be int32 [groups, max_pages] with unit column stride");
+    if (pr.T > 0 && (st = check_rows_apart(out, "out")))
+        return st;
+    if (pr.T > 0 && pr.out == pr.q)
+        return fail(B2PA_ERR_INVALID_ARG, "out must not be q: rows are read by several blocks");
+    *bytes_needed = 0;
+    if (pr.B == 0 || pr.T == 0)
+        return B2PA_OK;
+    int dev;
+    DevInfo di;
+    PrefixPlan plan;
+    if ((st = device_info(&dev, &di)) ||
+        (st = plan_prefix(pr, max_q_len, std::min(max_group_q_len, pr.T), di, &plan)))
+        return st;
+    *bytes_needed = plan.bytes;
+    if (workspace_bytes < plan.bytes)
+        return fail(B2PA_ERR_WORKSPACE, "workspace: %llu bytes are needed", (unsigned long long)plan.bytes);
+    if (plan.bytes && (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u)))
+        return fail(B2PA_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
+    TreeParams p;
+    if ((st = fill_tree(pr, max_q_len, max_kv_len, bmm1_scale, bmm2_scale, di, dev, stream, &p)))
+        return st;
+    PrefixParams& x = p.prefix;
+    x.tables = static_cast<const int*>(prefix_tables->data);
+    x.stride = prefix_tables->stride[0];
+    x.lens = static_cast<const int*>(prefix_lens->data);
+    x.cum_groups = static_cast<const int*>(cum_groups->data);
+    x.groups = (int)groups;
+    x.max_pages = (int)prefix_tables->shape[1];
+    x.max_len = max_prefix_len;
+    cudaError_t e;
+    if (plan.tc) {
+        uint8_t* ws = static_cast<uint8_t*>(workspace);
+        for (int i = 0; i < 2; ++i) {
+            x.part_o[i] = reinterpret_cast<float4*>(ws + plan.off_o[i]);
+            x.part_rec[i] = reinterpret_cast<float4*>(ws + plan.off_rec[i]);
+        }
+        x.cut_o = reinterpret_cast<float4*>(ws + plan.off_cut_o);
+        x.cut_rec = reinterpret_cast<float4*>(ws + plan.off_cut_rec);
+        x.cut_ends = reinterpret_cast<int*>(ws + plan.off_ends);
+        if ((st = encode_tree_maps(pr, &p)))
+            return st;
+        e = launch_attention_prefix(p, pr.fp8, plan.tiles, stream);
+    } else {
+        e = launch_prefix_generic(p, pr.fp8, stream);
+    }
+    return e == cudaSuccess ? B2PA_OK : cuda_fail(e, "prefix attention launch");
 }
 
 }  // namespace
@@ -462,6 +607,21 @@ int b2pa_tree_attention(const b2pa_tensor* q, const b2pa_tensor* k_pool, const b
         return tree_impl(q, k_pool, v_pool, block_tables, seq_lens, cum_q, tree_mask, positions, max_q_len, max_kv_len,
                          bmm1_scale, bmm2_scale, window_left, sinks, layout, out, workspace, workspace_bytes,
                          bytes_needed, reinterpret_cast<cudaStream_t>(stream));
+    });
+}
+
+int b2pa_prefix_attention(const b2pa_tensor* q, const b2pa_tensor* k_pool, const b2pa_tensor* v_pool,
+                          const b2pa_tensor* prefix_tables, const b2pa_tensor* prefix_lens,
+                          const b2pa_tensor* cum_groups, const b2pa_tensor* block_tables, const b2pa_tensor* seq_lens,
+                          const b2pa_tensor* cum_q, int32_t max_q_len, int32_t max_group_q_len, int32_t max_prefix_len,
+                          int32_t max_kv_len, float bmm1_scale, float bmm2_scale, const b2pa_tensor* sinks,
+                          int32_t layout, b2pa_tensor* out, void* workspace, uint64_t workspace_bytes,
+                          uint64_t* bytes_needed, b2pa_stream_t stream)
+{
+    return guarded([&] {
+        return prefix_impl(q, k_pool, v_pool, prefix_tables, prefix_lens, cum_groups, block_tables, seq_lens, cum_q,
+                           max_q_len, max_group_q_len, max_prefix_len, max_kv_len, bmm1_scale, bmm2_scale, sinks, layout,
+                           out, workspace, workspace_bytes, bytes_needed, reinterpret_cast<cudaStream_t>(stream));
     });
 }
 

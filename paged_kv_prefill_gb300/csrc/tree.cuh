@@ -1,5 +1,7 @@
-// tree.cuh -- parameters and geometry of the tree attention kernels
-// (attn_tree.cu, and tree_generic_kernel in generic.cu), filled in ops.cu.
+// tree.cuh -- parameters and geometry of the kernels for a few rows per request
+// (attn_tree.cuh, and tree_generic_kernel and prefix_generic_kernel in
+// generic.cu), filled in ops.cu: attention of drafted token trees, and of
+// requests that share a prefix (kPrefix; see prefix_request).
 //
 // Request b brings n = cum_q[b+1] - cum_q[b] drafted nodes, whose own keys are
 // the last n of its kv_len keys; c = kv_len - n keys before them are context.
@@ -29,6 +31,26 @@ __host__ __device__ inline TreeRows tree_rows(int G)
     r.tile_toks = r.by_warp ? 4 * r.box_toks : r.box_toks;
     return r;
 }
+
+// What the attention of requests with shared prefixes has besides: requests
+// cum_groups[g] .. cum_groups[g + 1] - 1 share the prefix of row g of `tables`.
+// Rows leave unnormalised, with their maximum and sum: part_*[kPrefixShared] and
+// [kPrefixOwn] hold, for each (kv head, token, head of it), the segment that
+// begins with the first key of the prefix, and of the request's own keys;
+// cut_* what each CTA's first segment continues.
+enum { kPrefixShared = 0, kPrefixOwn = 1, kPrefixCut = 2 };
+struct PrefixParams {
+    const int* tables;
+    long long stride;
+    const int* lens;
+    const int* cum_groups;
+    int groups, max_pages, max_len;
+    float4* part_o[2];    // [Hkv * T * G] rows, those of a tile together, four columns of all of them at a time
+    float4* part_rec[2];  // [Hkv * T * G] PrefixRow
+    float4* cut_o;        // [grid * tiles][128 rows], the same
+    float4* cut_rec;      // [grid * tiles][128]
+    int* cut_ends;        // [grid]: whether the unit ends there
+};
 
 struct TreeParams {  // 128-byte aligned through its CUtensorMap members
     CUtensorMap tm_q;  // 3-D: (D, H, T), box (64, G, box_toks)
@@ -62,6 +84,7 @@ struct TreeParams {  // 128-byte aligned through its CUtensorMap members
     float bmm2;
     unsigned long long wait_limit_ns;
     int inject_stall;
+    PrefixParams prefix;
 };
 
 // What a unit costs beyond its kv tiles, in kv tiles: its Q, the first scores,
@@ -97,6 +120,91 @@ __device__ __forceinline__ TreeReq tree_request(const TreeParams& p, int b, int 
     r.unit = r.tiles + kTreeUnitCost;
     return r;
 }
+
+// The same of requests that share prefixes.  They are attended as groups + B of
+// them: group g's rows, all of its requests' tokens, over the keys of its prefix
+// (all context); and each request's rows over its own keys, the last n of which
+// are its tokens' (token i sees those up to its own; a single token sees all, so
+// that they are all context).
+__device__ __forceinline__ TreeReq prefix_request(const TreeParams& p, int v, int item_toks)
+{
+    const PrefixParams& x = p.prefix;
+    TreeReq r;
+    if (v < x.groups) {
+        const int r0 = x.cum_groups[v], r1 = x.cum_groups[v + 1];
+        r.kv_len = x.lens[v];
+        r.ok = r0 >= 0 && r0 <= r1 && r1 <= p.B && r.kv_len >= 0 && r.kv_len <= x.max_len &&
+               ((long long)r.kv_len + p.page_size - 1) / p.page_size <= x.max_pages;
+        r.q0 = r.ok ? p.cum_q[r0] : 0;
+        r.n = r.ok ? p.cum_q[r1] - r.q0 : 0;
+        r.ok = r.ok && r.n >= 0 && r.q0 >= 0 && r.q0 <= p.T - r.n;
+        r.ctx = r.kv_len;
+    } else {
+        const RequestView w = load_request(QStarts{p.cum_q, 0}, p.seq_lens, v - x.groups, p.max_q_len, p.max_kv_len,
+                                           p.page_size, p.max_pages, p.T);
+        r.q0 = w.q_start;
+        r.n = w.q_len;
+        r.kv_len = w.kv_len;
+        r.ok = w.ok;
+        r.ctx = w.kv_len - (w.q_len > 1 ? w.q_len : 0);
+    }
+    r.lo = r.n_lo = 0;
+    const bool any = r.ok && r.n > 0 && r.kv_len > 0;
+    r.items = any ? (r.n + item_toks - 1) / item_toks : 0;
+    r.tiles = any ? (r.kv_len - 1) / kKvTile + 1 : 0;
+    r.unit = r.tiles + kTreeUnitCost;
+    return r;
+}
+
+__device__ __forceinline__ const int* prefix_pages(const TreeParams& p, int v)
+{
+    return v < p.prefix.groups ? p.prefix.tables + (long long)v * p.prefix.stride
+                               : p.block_tables + (long long)(v - p.prefix.groups) * p.bt_stride;
+}
+
+template <bool kPrefix>
+__device__ __forceinline__ TreeReq request_of(const TreeParams& p, int v, int item_toks)
+{
+    return kPrefix ? prefix_request(p, v, item_toks) : tree_request(p, v, item_toks);
+}
+template <bool kPrefix>
+__device__ __forceinline__ int requests_of(const TreeParams& p)
+{
+    return kPrefix ? p.prefix.groups + p.B : p.B;
+}
+
+// The group of request b, by a whole warp; -1: none.  (cum_groups rise; of empty
+// groups that start there, the last starts the one that holds b.)
+__device__ __forceinline__ int prefix_group(const TreeParams& p, int b)
+{
+    const int lane = threadIdx.x & 31;
+    int upto = 0;
+    for (int i = 0; i <= p.prefix.groups; i += 32) {
+        const bool in = i + lane <= p.prefix.groups && p.prefix.cum_groups[i + lane] <= b;
+        upto += __popc(__ballot_sync(0xffffffffu, in));
+    }
+    return upto > p.prefix.groups ? -1 : upto - 1;
+}
+
+// A partial row: its maximum (log2 units) and sum; the CTA whose successors
+// have the rest of its keys (-1: there is none); how many rows its tile has,
+// which of them it is, and which query tile of its CTA that is.
+struct PrefixRow {
+    float m, l;
+    int cta, tile_rows, tile_row, qt;
+    __device__ __forceinline__ float4 pack() const
+    {
+        return make_float4(m, l, __int_as_float(cta), __int_as_float(tile_rows | tile_row << 8 | qt << 16));
+    }
+    // Row `at` of its plane.  (After a wait that gave up, rows were not written:
+    // whatever they hold stays within the workspace.)
+    static __device__ __forceinline__ PrefixRow unpack(float4 x, long long at, int tiles)
+    {
+        const int w = __float_as_int(x.w), rows = min(w & 255, kQRows);
+        return PrefixRow{x.x, x.y, __float_as_int(x.z), rows, (int)min((long long)min(w >> 8 & 255, kQRows - 1), at),
+                         w >> 16 & (tiles - 1)};
+    }
+};
 
 // First context key that a node at position pos sees (ctx: none; the window
 // does not say which nodes it sees).
@@ -183,6 +291,8 @@ __device__ __forceinline__ TreeToken tree_token(const TreeRows& r, int row, int 
 
 // tiles: query tiles per item (1 or 2)
 cudaError_t launch_attention_tree(const TreeParams& p, bool fp8, int tiles, cudaStream_t stream);
+cudaError_t launch_attention_prefix(const TreeParams& p, bool fp8, int tiles, cudaStream_t stream);
+cudaError_t launch_prefix_generic(const TreeParams& p, bool fp8, cudaStream_t stream);
 cudaError_t launch_tree_generic(const TreeParams& p, bool fp8, cudaStream_t stream);
 
 }  // namespace b2pa
