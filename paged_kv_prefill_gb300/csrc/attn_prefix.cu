@@ -12,6 +12,11 @@
 // HBM.  All units' kv tiles, laid end to end, are cut into equal runs, one per
 // CTA.  Every row has two parts at least, so that all rows leave unnormalised
 // and a second kernel merges them.
+//
+// Where a group has more rows than a query tile, prefixes want two tiles that share
+// K and V, and the requests' own keys one, on which both softmax groups work: then
+// some CTAs run the one kind of kernel and the others the other
+// (prefix_split_kernel).
 #include <algorithm>
 
 #include "attn_tree.cuh"
@@ -20,12 +25,38 @@ namespace b2pa {
 
 namespace {
 
+template <int D, bool FP8>
+struct SplitCfg {
+    using Two = TreeCfg<D, FP8, 2>;
+    using One = TreeCfg<D, FP8, 1>;
+    static constexpr int kThreads = Two::kThreads;
+    static constexpr int kSmemBytes = Two::kSmemBytes > One::kSmemBytes ? Two::kSmemBytes : One::kSmemBytes;
+    static_assert(One::kThreads == kThreads, "the same roles");
+};
+
+template <int D, bool FP8>
+__global__ void __launch_bounds__(SplitCfg<D, FP8>::kThreads, 1) prefix_split_kernel(const __grid_constant__ TreeParams p)
+{
+    extern __shared__ __align__(1024) uint8_t smem[];
+    pdl_wait();
+    const TreeRun run = tree_run<SplitCfg<D, FP8>::kThreads, FP8, true, true>(p, 2 * p.rows.tile_toks, p.rows.tile_toks,
+                                                                        reinterpret_cast<long long*>(smem));
+    TreeCtx c;
+    if (run.own) {
+        tree_setup<D, FP8, 1>(p, smem, c);
+        tree_roles<D, FP8, 1, true>(p, c, run);
+    } else {
+        tree_setup<D, FP8, 2>(p, smem, c);
+        tree_roles<D, FP8, 2, true>(p, c, run);
+    }
+}
+
 // Block (x, b): 32 of request b's rows (kv head, token, head of it), a lane each;
 // each warp takes four groups of four columns.  Parts are added in the order of
 // the keys.  Latency alone: loads that do not depend on one another are issued
 // together.
 template <int D>
-__global__ void __launch_bounds__(D * 2) prefix_merge_kernel(const __grid_constant__ TreeParams p, int tiles)
+__global__ void __launch_bounds__(D * 2) prefix_merge_kernel(const __grid_constant__ TreeParams p)
 {
     constexpr float kLog2e = 1.4426950408889634f;
     constexpr int kCols4 = 4;  // D / 16 warps
@@ -80,7 +111,7 @@ __global__ void __launch_bounds__(D * 2) prefix_merge_kernel(const __grid_consta
     for (int i = 0; i < 2; ++i) {
         x[i] = PrefixRow{-INFINITY, 0.f, -1, 0, 0, 0};
         if (valid && (i == kPrefixOwn || shared))
-            x[i] = PrefixRow::unpack(p.prefix.part_rec[i][at], at, tiles);
+            x[i] = PrefixRow::unpack(p.prefix.part_rec[i][at], at);
     }
 #pragma unroll
     for (int i = 0; i < 2; ++i)
@@ -91,7 +122,7 @@ __global__ void __launch_bounds__(D * 2) prefix_merge_kernel(const __grid_consta
         if (valid && (i == kPrefixOwn || shared))
             merge(x[i].m, x[i].l, v[i]);
         for (int c = x[i].cta; c >= 0 && c + 1 < p.grid;) {  // (a lane's own)
-            const long long rows0 = (long long)(++c * tiles + x[i].qt) * kQRows;
+            const long long rows0 = (long long)(++c * 2 + x[i].qt) * kQRows;
             const float4 y = p.prefix.cut_rec[rows0 + x[i].tile_row];
             const int ends = p.prefix.cut_ends[c];
             float4 z[kCols4];
@@ -117,13 +148,16 @@ __global__ void __launch_bounds__(D * 2) prefix_merge_kernel(const __grid_consta
 template <int D, bool FP8, int kTiles>
 cudaError_t launch_prefix(const TreeParams& p, cudaStream_t stream)
 {
-    const cudaError_t e = launch_tree_kernel<D, FP8, kTiles, true>(p, stream);
+    using C = SplitCfg<D, FP8>;
+    const cudaError_t e = kTiles == 2 && p.max_q_len <= p.rows.tile_toks
+                              ? launch_per_sm<prefix_split_kernel<D, FP8>>(p, C::kThreads, C::kSmemBytes, stream)
+                              : launch_tree_kernel<D, FP8, kTiles, true>(p, stream);
     if (e != cudaSuccess)
         return e;
     const long long rows = (long long)std::min(p.max_q_len, p.T) * p.H;
     if (rows == 0)
         return e;  // (no request may have a token)
-    return launch_pdl(prefix_merge_kernel<D>, dim3((unsigned)((rows + 31) / 32), p.B), D * 2, 0, stream, p, kTiles);
+    return launch_pdl(prefix_merge_kernel<D>, dim3((unsigned)((rows + 31) / 32), p.B), D * 2, 0, stream, p);
 }
 
 }  // namespace

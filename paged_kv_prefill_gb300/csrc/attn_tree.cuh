@@ -946,14 +946,14 @@ __device__ __forceinline__ float kv_elem(const void* base, long long at)
 // finite, weighted for this row, with the stabiliser m of its exponentials.
 template <bool FP8>
 __device__ __noinline__ float tree_bad_column(const TreeParams& p, const int* row_pages, const RowView view, int lo_all,
-                                              int ctx, int key0, int key1, int tok, int head, int kvh, float sl2, float m, int d)
+                                              int key0, int key1, int tok, int head, int kvh, float sl2, float m, int d)
 {
     float sum = 0.f;
     const uint16_t* q = p.q + (long long)tok * p.q_st_tok + (long long)head * p.q_st_head;
     const int last = view.ctx + view.n;
     for (int key = max(key0, view.lo); key < min(key1, last); ++key) {
-        if (key >= lo_all && key < ctx)
-            key = ctx;  // these were not looked at
+        if (key >= lo_all && key < view.ctx)
+            key = view.ctx;  // these were not looked at
         if (key >= min(key1, last))
             break;
         if (!(view.sees(key) & 1u))
@@ -986,8 +986,9 @@ __device__ __forceinline__ uint32_t f16x2_of_e4m3x2(uint32_t two)
     return h;
 }
 
+// (not inlined: the e4m3 batch 157 us, 163 with its code among the other roles')
 template <int kTiles>
-__device__ void tree_convert(const TreeParams& p, const TreeCtx& c)
+__device__ __noinline__ void tree_convert(const TreeParams& p, const TreeCtx& c)
 {
     using C = TreeCfg<128, true, kTiles>;
     const int wq = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31, row = wq * 32 + lane, sw = row & 7;
@@ -1313,7 +1314,7 @@ __device__ void tree_softmax(const TreeParams& p, const TreeCtx& c, int t)
         const int tile_rows = toks * G, tile_row = mine.tok * G + head;
         float4* prow = nullptr;
         if constexpr (kPrefix) {
-            const long long rows0 = s.slot == kPrefixCut ? (long long)(blockIdx.x * kTiles + qt) * kQRows
+            const long long rows0 = s.slot == kPrefixCut ? (long long)(blockIdx.x * 2 + qt) * kQRows
                                                          : ((long long)s.kvh * p.T + tok) * G + head - tile_row;
             prow = (s.slot == kPrefixCut ? p.prefix.cut_o : p.prefix.part_o[s.slot]) + rows0 * (D / 4) + tile_row;
             if (valid && (kTiles == 2 || t == 0)) {
@@ -1331,8 +1332,10 @@ __device__ void tree_softmax(const TreeParams& p, const TreeCtx& c, int t)
                 float o = __uint_as_float(tmem_ld1(o_tmem + (uint32_t)d));
                 tmem_wait_ld();
                 if (valid)
-                    o += tree_bad_column<FP8>(p, p.block_tables + (long long)b * p.bt_stride, view, s.lo_all(p.window),
-                                              s.ctx(), s.j0 * kKvTile, (s.j0 + s.tiles) * kKvTile, tok, h, s.kvh, p.scale_log2, m, d);
+                    o += tree_bad_column<FP8>(p, p.block_tables + (long long)b * p.bt_stride, view,
+                                              kPrefix ? 0x7FFFFFFF : s.lo_all(p.window),
+                                              kPrefix ? max(s.ctx(), s.j0 * kKvTile) : s.j0 * kKvTile,
+                                              (s.j0 + s.tiles) * kKvTile, tok, h, s.kvh, p.scale_log2, m, d);
                 __syncwarp();
                 tmem_st1(o_tmem + (uint32_t)d, __float_as_uint(o));
             }
@@ -1386,12 +1389,10 @@ __device__ void tree_softmax(const TreeParams& p, const TreeCtx& c, int t)
 
 // ---------------------------------------------------------------------------
 
-template <int D, bool FP8, int kTiles, bool kPrefix>
-__global__ void __launch_bounds__(TreeCfg<D, FP8, kTiles>::kThreads, 1) attention_tree_kernel(const __grid_constant__ TreeParams p)
+template <int D, bool FP8, int kTiles>
+__device__ __forceinline__ void tree_setup(const TreeParams& p, uint8_t* smem, TreeCtx& c)
 {
     using C = TreeCfg<D, FP8, kTiles>;
-    extern __shared__ __align__(1024) uint8_t smem[];
-    TreeCtx c;
     c.base = smem;
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
     c.kv_full = bars;
@@ -1471,27 +1472,51 @@ __global__ void __launch_bounds__(TreeCfg<D, FP8, kTiles>::kThreads, 1) attentio
     __syncthreads();
     tc_fence_after();
     c.tmem = *tmem_holder;
+}
 
-    pdl_wait();  // inputs may come from the kernel this launch follows
+// Where a CTA's run starts and ends, and the request (the sum of work before it)
+// in which it starts.
+struct TreeRun {
+    long long start, end, base;
+    int first_b;
+    bool own;  // kSplit: of the requests' own keys
+};
 
+// A step of a prefix, whose two query tiles share its keys, takes longer than one of
+// a request's own keys with their single tile.  (64 requests behind 16384 keys: 102 us with
+// 0.75, 71.5 with 1.5, 61.4 with 2, 62.1 with 3; 8 e4m3 groups 134 with 1.5, 153 with 1.9.)
+template <bool FP8>
+constexpr float kPrefixStep = FP8 ? 1.5f : 2.2f;
+
+// kSplit (kPrefix only): prefixes' units for the first CTAs, with item_toks tokens to
+// an item, the requests' own, with own_toks, for the others.  Else one run through
+// all.  `scan`: room for 36 sums in shared memory that nothing else uses yet.
+template <int kThreads, bool FP8, bool kPrefix, bool kSplit>
+__device__ __forceinline__ TreeRun tree_run(const TreeParams& p, int item_toks, int own_toks, long long* scan)
+{
     // Where this CTA's run starts: the first request whose work, with that of the
     // requests before it, passes the run's start.  warp 0 alone needs to know; for
     // more than a request per lane all threads add up.
-    const int item_toks = kTiles * p.rows.tile_toks;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int n_req = requests_of<kPrefix>(p);
-    const bool by_all = n_req > 32;  // (of the whole grid)
-    long long start = 0, end = 0, base = 0;
-    int first_b = 0;
+    const bool by_all = kSplit || n_req > 32;  // (of the whole grid)
+    auto request = [&](int b) {
+        return request_of<kPrefix>(p, b, kSplit && b >= p.prefix.groups ? own_toks : item_toks);
+    };
+    TreeRun run{};
+    long long &start = run.start, &end = run.end, &base = run.base;
+    int& first_b = run.first_b;
     if (by_all || warp == 0) {
-        long long* scan = reinterpret_cast<long long*>(smem + C::kOffRing);  // (empty yet) a sum per warp; [16 ..] the run
-        const int threads = by_all ? C::kThreads : 32, share = (n_req + threads - 1) / threads;
+        const int threads = by_all ? kThreads : 32, share = (n_req + threads - 1) / threads;
         const int b0 = min(n_req, tid * share), b1 = min(n_req, b0 + share);
-        long long mine = 0;
+        long long mine = 0, shared = 0;  // (of prefixes)
         for (int b = b0; b < b1; ++b) {
-            const TreeReq r = request_of<kPrefix>(p, b, item_toks);
+            const TreeReq r = request(b);
             if (!r.ok && blockIdx.x == 0)
                 atomicOr(p.err, (unsigned)B2PA_DEV_BAD_REQUEST);
             mine += r.work(p.Hkv);
+            if (kSplit && b < p.prefix.groups)
+                shared += r.work(p.Hkv);
         }
         long long before = mine;
 #pragma unroll
@@ -1506,7 +1531,7 @@ __global__ void __launch_bounds__(TreeCfg<D, FP8, kTiles>::kThreads, 1) attentio
                 scan[warp] = before;
             __syncthreads();
 #pragma unroll
-            for (int w = 0; w < C::kThreads / 32; ++w) {
+            for (int w = 0; w < kThreads / 32; ++w) {
                 warps_before += w < warp ? scan[w] : 0;
                 total += scan[w];
             }
@@ -1514,15 +1539,37 @@ __global__ void __launch_bounds__(TreeCfg<D, FP8, kTiles>::kThreads, 1) attentio
             total = __shfl_sync(0xffffffffu, before, 31);
         }
         before += warps_before - mine;
-        const TreeCut cut = tree_cut(total, gridDim.x);
-        const bool works = (int)blockIdx.x < cut.g;
-        start = works ? cut.start(blockIdx.x) : 0;
-        end = works ? cut.start(blockIdx.x + 1) : 0;
+        TreeCut cut = tree_cut(total, gridDim.x);
+        int cta = blockIdx.x;
+        long long from0 = 0;
+        if constexpr (kSplit) {
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1)
+                shared += __shfl_xor_sync(0xffffffffu, shared, o);
+            if (lane == 0)
+                scan[20 + warp] = shared;
+            __syncthreads();
+            shared = 0;
+#pragma unroll
+            for (int w = 0; w < kThreads / 32; ++w)
+                shared += scan[20 + w];
+            // CTAs by the time that the work takes, at least one each
+            const int grid = gridDim.x;
+            const float a = kPrefixStep<FP8> * (float)shared, b = (float)(total - shared);
+            int g = shared == 0 ? 0 : total == shared ? grid : min(grid - 1, max(1, __float2int_rn((float)grid * (a / (a + b)))));
+            run.own = cta >= g;
+            cut = run.own ? tree_cut(total - shared, grid - g) : tree_cut(shared, g);
+            from0 = run.own ? shared : 0;
+            cta -= run.own ? g : 0;
+        }
+        const bool works = cta < cut.g;
+        start = works ? from0 + cut.start(cta) : 0;
+        end = works ? from0 + cut.start(cta + 1) : 0;
         // the run's ends, moved off units that are not cut, by the threads whose
         // requests they are in
         const bool has_start = start >= before && start < before + mine, has_end = end >= before && end < before + mine;
         if (!by_all) {  // a request per lane
-            const TreeReq r = request_of<kPrefix>(p, min(b0, n_req - 1), item_toks);
+            const TreeReq r = request(min(b0, n_req - 1));
             const long long s0 = has_start ? tree_snap(start, before, r, cut, p.whole) : 0, e0 = has_end ? tree_snap(end, before, r, cut, p.whole) : 0;
             const unsigned ws = __ballot_sync(0xffffffffu, has_start), we = __ballot_sync(0xffffffffu, has_end);
             first_b = ws != 0 ? __ffs(ws) - 1 : 0;
@@ -1537,8 +1584,8 @@ __global__ void __launch_bounds__(TreeCfg<D, FP8, kTiles>::kThreads, 1) attentio
                 const long long x = k ? end : start;
                 long long from = before;
                 int b = b0;
-                TreeReq r = request_of<kPrefix>(p, b, item_toks);
-                for (; b + 1 < b1 && x >= from + r.work(p.Hkv); r = request_of<kPrefix>(p, ++b, item_toks))
+                TreeReq r = request(b);
+                for (; b + 1 < b1 && x >= from + r.work(p.Hkv); r = request(++b))
                     from += r.work(p.Hkv);
                 scan[16 + k] = tree_snap(x, from, r, cut, p.whole);
                 if (k == 0) {
@@ -1557,13 +1604,20 @@ __global__ void __launch_bounds__(TreeCfg<D, FP8, kTiles>::kThreads, 1) attentio
             __syncthreads();
         }
     }
+    return run;
+}
 
+template <int D, bool FP8, int kTiles, bool kPrefix>
+__device__ __forceinline__ void tree_roles(const TreeParams& p, const TreeCtx& c, const TreeRun& run)
+{
+    using C = TreeCfg<D, FP8, kTiles>;
+    const int warp = threadIdx.x >> 5;
     // 384 threads launch with 168 registers each (104 + 200 + 200 = 504 = 3 x 168), 512 with 128 (96 + 160 +
     // 160 + 96 = 512 = 4 x 128)
     if (warp < 4) {
         regs_dec<FP8 ? 96 : 104>();
         if (warp == 0)
-            tree_producer<D, FP8, kTiles, kPrefix>(p, c, start, end, first_b, base);
+            tree_producer<D, FP8, kTiles, kPrefix>(p, c, run.start, run.end, run.first_b, run.base);
         else if (warp == 3)
             tree_feed<D, FP8, kTiles>(p, c);
         else if constexpr (kTiles == 2)
@@ -1587,6 +1641,20 @@ __global__ void __launch_bounds__(TreeCfg<D, FP8, kTiles>::kThreads, 1) attentio
     }
 }
 
+template <int D, bool FP8, int kTiles, bool kPrefix>
+__global__ void __launch_bounds__(TreeCfg<D, FP8, kTiles>::kThreads, 1) attention_tree_kernel(const __grid_constant__ TreeParams p)
+{
+    using C = TreeCfg<D, FP8, kTiles>;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    TreeCtx c;
+    tree_setup<D, FP8, kTiles>(p, smem, c);
+    pdl_wait();  // inputs may come from the kernel this launch follows
+    // (the ring is empty yet)
+    const TreeRun run = tree_run<C::kThreads, FP8, kPrefix, false>(p, kTiles * p.rows.tile_toks, 0,
+                                                              reinterpret_cast<long long*>(smem + C::kOffRing));
+    tree_roles<D, FP8, kTiles, kPrefix>(p, c, run);
+}
+
 template <typename Kern, typename... Args>
 cudaError_t launch_pdl(Kern kern, dim3 grid, unsigned threads, size_t smem, cudaStream_t stream, const Args&... args)
 {
@@ -1603,26 +1671,30 @@ cudaError_t launch_pdl(Kern kern, dim3 grid, unsigned threads, size_t smem, cuda
     return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
-template <int D, bool FP8, int kTiles, bool kPrefix>
-cudaError_t launch_tree_kernel(const TreeParams& p, cudaStream_t stream)
+// Launch a kernel of one CTA per SM; once per device and instantiation it is
+// allowed its shared memory (any host thread).
+template <auto kern>
+cudaError_t launch_per_sm(const TreeParams& p, int threads, int smem, cudaStream_t stream)
 {
-    using C = TreeCfg<D, FP8, kTiles>;
-    auto kern = attention_tree_kernel<D, FP8, kTiles, kPrefix>;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess)
         return e;
     if (dev < 0 || dev >= 64)
         return cudaErrorInvalidDevice;
-    // the shared-memory opt-in, once per device and instantiation (any host thread)
     static std::once_flag once[64];
     static cudaError_t err[64];
-    std::call_once(once[dev], [&] {
-        err[dev] = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
-    });
+    std::call_once(once[dev], [&] { err[dev] = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem); });
     if (err[dev] != cudaSuccess)
         return err[dev];
-    return launch_pdl(kern, dim3(p.grid), C::kThreads, C::kSmemBytes, stream, p);
+    return launch_pdl(kern, dim3(p.grid), threads, smem, stream, p);
+}
+
+template <int D, bool FP8, int kTiles, bool kPrefix>
+cudaError_t launch_tree_kernel(const TreeParams& p, cudaStream_t stream)
+{
+    using C = TreeCfg<D, FP8, kTiles>;
+    return launch_per_sm<attention_tree_kernel<D, FP8, kTiles, kPrefix>>(p, C::kThreads, C::kSmemBytes, stream);
 }
 
 }  // namespace

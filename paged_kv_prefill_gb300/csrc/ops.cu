@@ -454,7 +454,7 @@ int plan_prefix(const Problem& pr, int max_q_len, int max_group_q_len, const Dev
             at += (bytes + 255) / 256 * 256;
             return here;
         };
-        const size_t rows = (size_t)pr.T * pr.H, cut = (size_t)di.sms * t.tiles * kQRows;
+        const size_t rows = (size_t)pr.T * pr.H, cut = (size_t)di.sms * 2 * kQRows;
         for (int i = 0; i < 2; ++i) {
             t.off_o[i] = take(rows * pr.D * sizeof(float));
             t.off_rec[i] = take(rows * sizeof(float4));

@@ -47,8 +47,8 @@ struct PrefixParams {
     int groups, max_pages, max_len;
     float4* part_o[2];    // [Hkv * T * G] rows, those of a tile together, four columns of all of them at a time
     float4* part_rec[2];  // [Hkv * T * G] PrefixRow
-    float4* cut_o;        // [grid * tiles][128 rows], the same
-    float4* cut_rec;      // [grid * tiles][128]
+    float4* cut_o;        // [grid * 2][128 rows], the same
+    float4* cut_rec;      // [grid * 2][128]
     int* cut_ends;        // [grid]: whether the unit ends there
 };
 
@@ -198,11 +198,11 @@ struct PrefixRow {
     }
     // Row `at` of its plane.  (After a wait that gave up, rows were not written:
     // whatever they hold stays within the workspace.)
-    static __device__ __forceinline__ PrefixRow unpack(float4 x, long long at, int tiles)
+    static __device__ __forceinline__ PrefixRow unpack(float4 x, long long at)
     {
         const int w = __float_as_int(x.w), rows = min(w & 255, kQRows);
         return PrefixRow{x.x, x.y, __float_as_int(x.z), rows, (int)min((long long)min(w >> 8 & 255, kQRows - 1), at),
-                         w >> 16 & (tiles - 1)};
+                         w >> 16 & 1};
     }
 };
 
