@@ -581,8 +581,8 @@ B2PA_API int b2pa_prefix_attention(const b2pa_tensor* q, const b2pa_tensor* k_po
  *   without (children that the draft chose, as its likeliest tokens):
  *     accepted if R(x_r) > 0 and u_r M < R(x_r); else M -= R(x_r), R(x_r) = 0.
  * Where no child is accepted the path ends, and the next token is the first i with
- * R(0) + .. + R(i) > last_uniforms[b] * sum R (R = p where sum R is 0).  All of it as in
- * 64 bits: values R to 2^-46 of p, sums and comparisons in binary64.
+ * R(0) + .. + R(i) > last_uniforms[b] * sum R (R = p where sum R is 0).  Values R are
+ * computed to about 2^-46 of p, sums and products to 2^-46 of themselves.
  *
  *  target_probs  [T, V] fp32, stride[1] == 1, 1 <= V < 2^30, rows that sum to 1 (the
  *                first child of a node is tried with M = 1, whatever the sum).

@@ -1486,7 +1486,7 @@ struct TreeRun {
 // a request's own keys with their single tile.  (64 requests behind 16384 keys: 102 us with
 // 0.75, 71.5 with 1.5, 61.4 with 2, 62.1 with 3; 8 e4m3 groups 134 with 1.5, 153 with 1.9.)
 template <bool FP8>
-constexpr float kPrefixStep = FP8 ? 1.5f : 2.2f;
+constexpr float kPrefixStep = FP8 ? 1.5f : 2.f;
 
 // kSplit (kPrefix only): prefixes' units for the first CTAs, with item_toks tokens to
 // an item, the requests' own, with own_toks, for the others.  Else one run through
