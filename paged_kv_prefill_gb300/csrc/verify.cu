@@ -223,6 +223,8 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const __grid_constant_
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, b = (int)(blockIdx.x / (unsigned)ctas);
     int *par = nodes, *tok = par + p.max_q, *out = tok + p.max_q;
     float *u = reinterpret_cast<float*>(out + p.max_q), *pt = u + p.max_q, *qt = pt + p.max_q;
+    if (ctas > 1)
+        cluster.barrier_arrive();  // (awaited before CTAs write one another's shared memory: all have to be there)
     pdl_wait();
     const int q0 = p.cum_q[b], n = p.cum_q[b + 1] - q0;
     bool bad = n < 0 || n > p.max_q || q0 < 0 || q0 > p.T - n;
@@ -242,6 +244,8 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const __grid_constant_
             qt[i] = in && p.draft != nullptr ? sane(p.draft[(long long)(q0 + up) * p.draft_st + t]) : 0.f;
         }
     bad = __syncthreads_or(bad);  // (and acc is filled)
+    if (ctas > 1)
+        cluster.barrier_wait();
     if (bad || n == 0) {
         if (tid == 0 && rank == 0) {
             p.counts[b] = 0;
