@@ -22,7 +22,8 @@ LIB = os.path.join(HERE, "libb2pa.so")
 NATIVE = os.path.join(HERE, "_native.so")
 SOURCES = ["b2pa.cu", "attn_tc.cu", "attn_win.cu", "sched_gather.cu", "generic.cu", "append.cu", "decode.cu",
            "ops.cu", "rope.cu", "kv_scaled.cu", "attn_tree.cu", "ops_pages.cu", "pages.cu",
-           "verify.cu", "attn_prefix.cu"]
+           "verify.cu", "attn_prefix.cu",
+           "attn_split.cu", "attn_split64.cu", "attn_split8.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
                 "--expt-relaxed-constexpr", "-I", os.path.join(os.path.dirname(HERE), "include")]

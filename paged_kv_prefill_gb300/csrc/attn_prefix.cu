@@ -13,50 +13,22 @@
 // CTA.  Every row has two parts at least, so that all rows leave unnormalised
 // and a second kernel merges them.
 //
-// Where a group has more rows than a query tile, prefixes want two tiles that share
-// K and V, and the requests' own keys one, on which both softmax groups work: then
-// some CTAs run the one kind of kernel and the others the other
-// (prefix_split_kernel).
+// Where that is another kind of work, prefixes and the requests' own keys have CTAs
+// of their own (attn_split.cuh).
 #include <algorithm>
 
-#include "attn_tree.cuh"
+#include "attn_split.cuh"
 
 namespace b2pa {
 
 namespace {
-
-template <int D, bool FP8>
-struct SplitCfg {
-    using Two = TreeCfg<D, FP8, 2>;
-    using One = TreeCfg<D, FP8, 1>;
-    static constexpr int kThreads = Two::kThreads;
-    static constexpr int kSmemBytes = Two::kSmemBytes > One::kSmemBytes ? Two::kSmemBytes : One::kSmemBytes;
-    static_assert(One::kThreads == kThreads, "the same roles");
-};
-
-template <int D, bool FP8>
-__global__ void __launch_bounds__(SplitCfg<D, FP8>::kThreads, 1) prefix_split_kernel(const __grid_constant__ TreeParams p)
-{
-    extern __shared__ __align__(1024) uint8_t smem[];
-    pdl_wait();
-    const TreeRun run = tree_run<SplitCfg<D, FP8>::kThreads, FP8, true, true>(p, 2 * p.rows.tile_toks, p.rows.tile_toks,
-                                                                        reinterpret_cast<long long*>(smem));
-    TreeCtx c;
-    if (run.own) {
-        tree_setup<D, FP8, 1>(p, smem, c);
-        tree_roles<D, FP8, 1, true>(p, c, run);
-    } else {
-        tree_setup<D, FP8, 2>(p, smem, c);
-        tree_roles<D, FP8, 2, true>(p, c, run);
-    }
-}
 
 // Block (x, b): 32 of request b's rows (kv head, token, head of it), a lane each;
 // each warp takes four groups of four columns.  Parts are added in the order of
 // the keys.  Latency alone: loads that do not depend on one another are issued
 // together.
 template <int D>
-__global__ void __launch_bounds__(D * 2) prefix_merge_kernel(const __grid_constant__ TreeParams p)
+__global__ void __launch_bounds__(D * 2, 2) prefix_merge_kernel(const __grid_constant__ TreeParams p)
 {
     constexpr float kLog2e = 1.4426950408889634f;
     constexpr int kCols4 = 4;  // D / 16 warps
@@ -69,6 +41,16 @@ __global__ void __launch_bounds__(D * 2) prefix_merge_kernel(const __grid_consta
     const int row = blockIdx.x * 32 + lane, all = own.n * p.H;
     if (blockIdx.x * 32 >= all)
         return;
+    const bool valid = row < all;
+    const int per = own.n * G, kvh = valid ? row / per : 0, in = valid ? row - kvh * per : 0;
+    const int tok = own.q0 + in / G, h = kvh * G + in % G;
+    const long long at = ((long long)kvh * p.T + own.q0) * G + in;
+    // (both records, although there may be no prefix: that is known an access later)
+    PrefixRow x[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+        x[i] = PrefixRow::unpack(p.prefix.part_rec[i][at], at);
+    const float sink = p.sinks != nullptr ? p.sinks[h] * kLog2e : -INFINITY;
     bool shared = false;
     if (g >= 0) {
         const TreeReq r = prefix_request(p, g, 1);
@@ -76,11 +58,6 @@ __global__ void __launch_bounds__(D * 2) prefix_merge_kernel(const __grid_consta
             return;
         shared = r.kv_len > 0;
     }
-    const bool valid = row < all;
-    const int per = own.n * G, kvh = valid ? row / per : 0, in = valid ? row - kvh * per : 0;
-    const int tok = own.q0 + in / G, h = kvh * G + in % G;
-    const long long at = ((long long)kvh * p.T + own.q0) * G + in;
-    const float sink = p.sinks != nullptr ? p.sinks[h] * kLog2e : -INFINITY;
     float m = -INFINITY, den = 0.f;
     float4 a[kCols4];
 #pragma unroll
@@ -105,31 +82,43 @@ __global__ void __launch_bounds__(D * 2) prefix_merge_kernel(const __grid_consta
                                fmaf(a[k].w, old, w * y.w));
         }
     };
-    PrefixRow x[2];
     float4 v[2][kCols4];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        x[i] = PrefixRow{-INFINITY, 0.f, -1, 0, 0, 0};
-        if (valid && (i == kPrefixOwn || shared))
-            x[i] = PrefixRow::unpack(p.prefix.part_rec[i][at], at);
-    }
 #pragma unroll
     for (int i = 0; i < 2; ++i)
         if (valid && (i == kPrefixOwn || shared))
             load(p.prefix.part_o[i], at - x[i].tile_row, x[i], v[i]);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-        if (valid && (i == kPrefixOwn || shared))
-            merge(x[i].m, x[i].l, v[i]);
-        for (int c = x[i].cta; c >= 0 && c + 1 < p.grid;) {  // (a lane's own)
-            const long long rows0 = (long long)(++c * 2 + x[i].qt) * kQRows;
-            const float4 y = p.prefix.cut_rec[rows0 + x[i].tile_row];
-            const int ends = p.prefix.cut_ends[c];
-            float4 z[kCols4];
-            load(p.prefix.cut_o, rows0, x[i], z);
-            merge(y.x, y.y, z);
-            if (ends)
-                break;
+        if (!valid || !(i == kPrefixOwn || shared))
+            continue;
+        // the rest of the unit: parts of the CTAs behind, looked at kBatch together
+        constexpr int kBatch = 2;
+        bool more = x[i].cta >= 0 && x[i].cta < p.grid;
+        for (int c0 = x[i].cta + 1, first = 1; first || more; c0 += kBatch, first = 0) {
+            float2 ml[kBatch];
+            float4 z[kBatch][kCols4];
+            bool ends[kBatch];
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) {
+                const int c = c0 + k;
+                ends[k] = true;
+                ml[k] = make_float2(-INFINITY, 0.f);
+                if (more && c < p.grid) {
+                    const long long rows0 = (long long)(c * 2 + x[i].qt) * kQRows;
+                    const float4 y = p.prefix.cut_rec[rows0 + x[i].tile_row];
+                    ml[k] = make_float2(y.x, y.y);
+                    ends[k] = p.prefix.cut_ends[c] != 0;
+                    load(p.prefix.cut_o, rows0, x[i], z[k]);
+                }
+            }
+            if (first)
+                merge(x[i].m, x[i].l, v[i]);
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k)
+                if (more) {
+                    merge(ml[k].x, ml[k].y, z[k]);
+                    more = !ends[k];
+                }
         }
     }
     if (!valid)
@@ -145,13 +134,19 @@ __global__ void __launch_bounds__(D * 2) prefix_merge_kernel(const __grid_consta
                        pack_bf16x2(a[k + 1].x * f, a[k + 1].y * f), pack_bf16x2(a[k + 1].z * f, a[k + 1].w * f));
 }
 
-template <int D, bool FP8, int kTiles>
-cudaError_t launch_prefix(const TreeParams& p, cudaStream_t stream)
+template <int D, bool FP8>
+cudaError_t launch_prefix(TreeParams& p, int tiles, bool few, cudaStream_t stream)
 {
-    using C = SplitCfg<D, FP8>;
-    const cudaError_t e = kTiles == 2 && p.max_q_len <= p.rows.tile_toks
-                              ? launch_per_sm<prefix_split_kernel<D, FP8>>(p, C::kThreads, C::kSmemBytes, stream)
-                              : launch_tree_kernel<D, FP8, kTiles, true>(p, stream);
+    const int G = p.rows.G;
+    p.prefix.own_cost = kTreeUnitCost;
+    cudaError_t e;
+    if (few && p.prefix.split)
+        e = tiles == 1 ? G <= 8 ? launch_split<D, FP8, 1, 1>(p, stream) : launch_split<D, FP8, 1, 2>(p, stream)
+                       : G <= 8 ? launch_split<D, FP8, 2, 1>(p, stream) : launch_split<D, FP8, 2, 2>(p, stream);
+    else if (tiles == 2 && p.max_q_len <= p.rows.tile_toks && p.prefix.split)
+        e = launch_split<D, FP8, 2, 0>(p, stream);
+    else
+        e = tiles == 1 ? launch_tree_kernel<D, FP8, 1, true>(p, stream) : launch_tree_kernel<D, FP8, 2, true>(p, stream);
     if (e != cudaSuccess)
         return e;
     const long long rows = (long long)std::min(p.max_q_len, p.T) * p.H;
@@ -162,15 +157,13 @@ cudaError_t launch_prefix(const TreeParams& p, cudaStream_t stream)
 
 }  // namespace
 
-cudaError_t launch_attention_prefix(const TreeParams& p, bool fp8, int tiles, cudaStream_t stream)
+cudaError_t launch_attention_prefix(const TreeParams& q, bool fp8, int tiles, bool few, cudaStream_t stream)
 {
-    if (p.D == 128) {
-        if (fp8)
-            return tiles == 1 ? launch_prefix<128, true, 1>(p, stream) : launch_prefix<128, true, 2>(p, stream);
-        return tiles == 1 ? launch_prefix<128, false, 1>(p, stream) : launch_prefix<128, false, 2>(p, stream);
-    }
+    TreeParams p = q;
+    if (p.D == 128)
+        return fp8 ? launch_prefix<128, true>(p, tiles, few, stream) : launch_prefix<128, false>(p, tiles, few, stream);
     if (p.D == 64 && !fp8)
-        return tiles == 1 ? launch_prefix<64, false, 1>(p, stream) : launch_prefix<64, false, 2>(p, stream);
+        return launch_prefix<64, false>(p, tiles, few, stream);
     return cudaErrorInvalidValue;
 }
 

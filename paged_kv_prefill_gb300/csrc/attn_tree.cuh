@@ -202,10 +202,9 @@ __device__ __forceinline__ int tile_tokens(const TreeRows& r, const Seg& s, int 
 // ---------------------------------------------------------------------------
 // warp 0
 // ---------------------------------------------------------------------------
-template <int D, bool FP8, int kTiles, bool kPrefix>
+template <typename C, int kTiles, bool kPrefix>
 __device__ void tree_producer(const TreeParams& p, const TreeCtx& c, long long pos, long long end, int b, long long base)
 {
-    using C = TreeCfg<D, FP8, kTiles>;
     const int lane = threadIdx.x & 31;
     const uint32_t ring = smem_u32(c.base + C::kOffRing);
     const int P = p.page_size, log2_p = 31 - __clz(P);  // the tensor-core path takes powers of two only
@@ -230,8 +229,9 @@ __device__ void tree_producer(const TreeParams& p, const TreeCtx& c, long long p
             }
             const long long unit = (pos - base) / r.unit;
             const long long u0 = base + unit * r.unit;
-            const int off = max(0, (int)(pos - u0) - kTreeUnitCost);
-            const int to = max(0, (int)min((long long)r.unit, end - u0) - kTreeUnitCost);
+            const int cost = kPrefix ? r.unit - r.tiles : kTreeUnitCost;
+            const int off = max(0, (int)(pos - u0) - cost);
+            const int to = max(0, (int)min((long long)r.unit, end - u0) - cost);
             pos = min(end, u0 + r.unit);
             if (to <= off)
                 continue;  // none of its tiles
@@ -1479,44 +1479,32 @@ __device__ __forceinline__ void tree_setup(const TreeParams& p, uint8_t* smem, T
 struct TreeRun {
     long long start, end, base;
     int first_b;
-    bool own;  // kSplit: of the requests' own keys
 };
 
-// A step of a prefix, whose two query tiles share its keys, takes longer than one of
-// a request's own keys with their single tile.  (64 requests behind 16384 keys: 102 us with
-// 0.75, 71.5 with 1.5, 61.4 with 2, 62.1 with 3; 8 e4m3 groups 134 with 1.5, 153 with 1.9.)
-template <bool FP8>
-constexpr float kPrefixStep = FP8 ? 1.5f : 2.f;
-
-// kSplit (kPrefix only): prefixes' units for the first CTAs, with item_toks tokens to
-// an item, the requests' own, with own_toks, for the others.  Else one run through
-// all.  `scan`: room for 36 sums in shared memory that nothing else uses yet.
-template <int kThreads, bool FP8, bool kPrefix, bool kSplit>
-__device__ __forceinline__ TreeRun tree_run(const TreeParams& p, int item_toks, int own_toks, long long* scan)
+// One run through all requests.  `scan`: room for 20 sums in shared memory that
+// nothing else uses yet.
+template <int kThreads, bool kPrefix>
+__device__ __forceinline__ TreeRun tree_run(const TreeParams& p, int item_toks, long long* scan)
 {
     // Where this CTA's run starts: the first request whose work, with that of the
     // requests before it, passes the run's start.  warp 0 alone needs to know; for
     // more than a request per lane all threads add up.
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int n_req = requests_of<kPrefix>(p);
-    const bool by_all = kSplit || n_req > 32;  // (of the whole grid)
-    auto request = [&](int b) {
-        return request_of<kPrefix>(p, b, kSplit && b >= p.prefix.groups ? own_toks : item_toks);
-    };
+    const bool by_all = n_req > 32;  // (of the whole grid)
+    auto request = [&](int b) { return request_of<kPrefix>(p, b, item_toks); };
     TreeRun run{};
     long long &start = run.start, &end = run.end, &base = run.base;
     int& first_b = run.first_b;
     if (by_all || warp == 0) {
         const int threads = by_all ? kThreads : 32, share = (n_req + threads - 1) / threads;
         const int b0 = min(n_req, tid * share), b1 = min(n_req, b0 + share);
-        long long mine = 0, shared = 0;  // (of prefixes)
+        long long mine = 0;
         for (int b = b0; b < b1; ++b) {
             const TreeReq r = request(b);
             if (!r.ok && blockIdx.x == 0)
                 atomicOr(p.err, (unsigned)B2PA_DEV_BAD_REQUEST);
             mine += r.work(p.Hkv);
-            if (kSplit && b < p.prefix.groups)
-                shared += r.work(p.Hkv);
         }
         long long before = mine;
 #pragma unroll
@@ -1539,32 +1527,10 @@ __device__ __forceinline__ TreeRun tree_run(const TreeParams& p, int item_toks, 
             total = __shfl_sync(0xffffffffu, before, 31);
         }
         before += warps_before - mine;
-        TreeCut cut = tree_cut(total, gridDim.x);
-        int cta = blockIdx.x;
-        long long from0 = 0;
-        if constexpr (kSplit) {
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1)
-                shared += __shfl_xor_sync(0xffffffffu, shared, o);
-            if (lane == 0)
-                scan[20 + warp] = shared;
-            __syncthreads();
-            shared = 0;
-#pragma unroll
-            for (int w = 0; w < kThreads / 32; ++w)
-                shared += scan[20 + w];
-            // CTAs by the time that the work takes, at least one each
-            const int grid = gridDim.x;
-            const float a = kPrefixStep<FP8> * (float)shared, b = (float)(total - shared);
-            int g = shared == 0 ? 0 : total == shared ? grid : min(grid - 1, max(1, __float2int_rn((float)grid * (a / (a + b)))));
-            run.own = cta >= g;
-            cut = run.own ? tree_cut(total - shared, grid - g) : tree_cut(shared, g);
-            from0 = run.own ? shared : 0;
-            cta -= run.own ? g : 0;
-        }
-        const bool works = cta < cut.g;
-        start = works ? from0 + cut.start(cta) : 0;
-        end = works ? from0 + cut.start(cta + 1) : 0;
+        const TreeCut cut = tree_cut(total, gridDim.x);
+        const bool works = (int)blockIdx.x < cut.g;
+        start = works ? cut.start(blockIdx.x) : 0;
+        end = works ? cut.start(blockIdx.x + 1) : 0;
         // the run's ends, moved off units that are not cut, by the threads whose
         // requests they are in
         const bool has_start = start >= before && start < before + mine, has_end = end >= before && end < before + mine;
@@ -1617,7 +1583,7 @@ __device__ __forceinline__ void tree_roles(const TreeParams& p, const TreeCtx& c
     if (warp < 4) {
         regs_dec<FP8 ? 96 : 104>();
         if (warp == 0)
-            tree_producer<D, FP8, kTiles, kPrefix>(p, c, run.start, run.end, run.first_b, run.base);
+            tree_producer<C, kTiles, kPrefix>(p, c, run.start, run.end, run.first_b, run.base);
         else if (warp == 3)
             tree_feed<D, FP8, kTiles>(p, c);
         else if constexpr (kTiles == 2)
@@ -1650,8 +1616,8 @@ __global__ void __launch_bounds__(TreeCfg<D, FP8, kTiles>::kThreads, 1) attentio
     tree_setup<D, FP8, kTiles>(p, smem, c);
     pdl_wait();  // inputs may come from the kernel this launch follows
     // (the ring is empty yet)
-    const TreeRun run = tree_run<C::kThreads, FP8, kPrefix, false>(p, kTiles * p.rows.tile_toks, 0,
-                                                              reinterpret_cast<long long*>(smem + C::kOffRing));
+    const TreeRun run = tree_run<C::kThreads, kPrefix>(p, kTiles * p.rows.tile_toks,
+                                                       reinterpret_cast<long long*>(smem + C::kOffRing));
     tree_roles<D, FP8, kTiles, kPrefix>(p, c, run);
 }
 

@@ -434,7 +434,8 @@ int tree_impl(const b2pa_tensor* q, const b2pa_tensor* k_pool, const b2pa_tensor
 // Scratch of a prefix attention call on the tensor cores.
 struct PrefixPlan {
     bool tc;
-    int tiles;  // query tiles per item
+    int tiles;  // query tiles per item of a prefix
+    bool few;   // the requests' own keys as single tokens with few heads
     size_t off_o[2], off_rec[2], off_cut_o, off_cut_rec, off_ends, bytes;
 };
 
@@ -447,6 +448,7 @@ int plan_prefix(const Problem& pr, int max_q_len, int max_group_q_len, const Dev
     PrefixPlan t{};
     t.tc = path != B2PA_PATH_GENERIC && !why;
     if (t.tc) {
+        t.few = max_q_len <= 1 && pr.H / pr.Hkv <= 16;
         t.tiles = std::max(max_q_len, max_group_q_len) <= tree_rows(pr.H / pr.Hkv).tile_toks ? 1 : 2;
         size_t at = 0;
         auto take = [&](size_t bytes) {
@@ -536,6 +538,10 @@ int prefix_impl(const b2pa_tensor* q, const b2pa_tensor* k_pool, const b2pa_tens
     x.groups = (int)groups;
     x.max_pages = (int)prefix_tables->shape[1];
     x.max_len = max_prefix_len;
+    // (steps of a unit, units of a kv head: both at most)
+    const long long steps = std::max(max_prefix_len, max_kv_len) / kKvTile + 1 + kTreeUnitCost;
+    const long long units = 2LL * (pr.T / p.rows.tile_toks + 1) + groups + pr.B;
+    x.split = (double)steps * (double)units * (double)pr.Hkv < 2e9;
     cudaError_t e;
     if (plan.tc) {
         uint8_t* ws = static_cast<uint8_t*>(workspace);
@@ -548,7 +554,7 @@ int prefix_impl(const b2pa_tensor* q, const b2pa_tensor* k_pool, const b2pa_tens
         x.cut_ends = reinterpret_cast<int*>(ws + plan.off_ends);
         if ((st = encode_tree_maps(pr, &p)))
             return st;
-        e = launch_attention_prefix(p, pr.fp8, plan.tiles, stream);
+        e = launch_attention_prefix(p, pr.fp8, plan.tiles, plan.few, stream);
     } else {
         e = launch_prefix_generic(p, pr.fp8, stream);
     }

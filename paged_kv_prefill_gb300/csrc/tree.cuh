@@ -50,6 +50,12 @@ struct PrefixParams {
     float4* cut_o;        // [grid * 2][128 rows], the same
     float4* cut_rec;      // [grid * 2][128]
     int* cut_ends;        // [grid]: whether the unit ends there
+    // where prefixes and own keys have CTAs of their own: what a step (a kv tile, or
+    // one of those that a unit costs beyond them) of a prefix takes against one of a
+    // request's own; and how many of the latter a unit costs
+    float step;
+    int own_cost;
+    bool split;           // all units' steps fit 31 bits
 };
 
 struct TreeParams {  // 128-byte aligned through its CUtensorMap members
@@ -87,7 +93,7 @@ struct TreeParams {  // 128-byte aligned through its CUtensorMap members
     PrefixParams prefix;
 };
 
-// What a unit costs beyond its kv tiles, in kv tiles: its Q, the first scores,
+// What a unit of the tree attention's kernel costs beyond its kv tiles, in kv tiles: its Q, the first scores,
 // the tree's own tile and the rows' way out.  (bf16 batch 114 us with 0, 105
 // with 2, 104.5 with 4, 105 with 6; e4m3 batch 193, 162, 160 and 160; 512 rows per
 // kv head 125, 118, 114.6 and 116.)
@@ -152,7 +158,7 @@ __device__ __forceinline__ TreeReq prefix_request(const TreeParams& p, int v, in
     const bool any = r.ok && r.n > 0 && r.kv_len > 0;
     r.items = any ? (r.n + item_toks - 1) / item_toks : 0;
     r.tiles = any ? (r.kv_len - 1) / kKvTile + 1 : 0;
-    r.unit = r.tiles + kTreeUnitCost;
+    r.unit = r.tiles + (v < x.groups ? kTreeUnitCost : x.own_cost);
     return r;
 }
 
@@ -239,13 +245,14 @@ __device__ __forceinline__ TreeCut tree_cut(long long total, int grid)
 // `whole`: the host knows that all are small (ops.cu); then there is nothing to merge.
 constexpr int kTreeWholeTiles = 4;
 
-__device__ __forceinline__ long long tree_snap(long long x, long long base, const TreeReq& r, const TreeCut& cut, bool whole)
+template <typename Int>  // a 32-bit one where the caller's numbers fit it
+__device__ __forceinline__ Int tree_snap(Int x, Int base, const TreeReq& r, const TreeCut& cut, bool whole)
 {
     const long long all = (long long)r.unit * cut.g;  // (a run: cut.total / cut.g)
     const bool small = r.tiles <= 8 && all <= 3 * cut.total && (r.tiles <= kTreeWholeTiles || 4 * all >= 3 * cut.total);
     if ((!small && !whole) || r.unit <= 0)
         return x;
-    const long long u0 = base + (x - base) / r.unit * r.unit;
+    const Int u0 = base + (x - base) / r.unit * r.unit;
     return 2 * (x - u0) < r.unit ? u0 : u0 + r.unit;
 }
 
@@ -291,7 +298,9 @@ __device__ __forceinline__ TreeToken tree_token(const TreeRows& r, int row, int 
 
 // tiles: query tiles per item (1 or 2)
 cudaError_t launch_attention_tree(const TreeParams& p, bool fp8, int tiles, cudaStream_t stream);
-cudaError_t launch_attention_prefix(const TreeParams& p, bool fp8, int tiles, cudaStream_t stream);
+// tiles: query tiles per item of a prefix; few: the requests' own keys with
+// attn_few.cuh
+cudaError_t launch_attention_prefix(const TreeParams& p, bool fp8, int tiles, bool few, cudaStream_t stream);
 cudaError_t launch_prefix_generic(const TreeParams& p, bool fp8, cudaStream_t stream);
 cudaError_t launch_tree_generic(const TreeParams& p, bool fp8, cudaStream_t stream);
 
