@@ -695,8 +695,11 @@ B2PA_API int b2pa_compact_kv(const b2pa_tensor* k_pool, const b2pa_tensor* v_poo
  * its child empty and -1 in src and dst.
  *
  * b2pa_grow_pages: row rows[i] gets free pages, count 1, behind those that it has,
- * until they hold new_lens[i] >= seq_lens[rows[i]] tokens, and that length.  Of a
- * row named twice the later ones are malformed.
+ * until they hold new_lens[i] tokens, and that length.  A row that becomes shorter
+ * (the tokens of a tree that were not accepted) gives back the pages behind: they
+ * lose a holder, and are free from the next call on.  Of a row named twice the later
+ * ones are malformed.  (A page that is not full must have one holder before tokens
+ * are written to it; b2pa_fork_pages sees to that.)
  */
 B2PA_API int b2pa_free_pages(const b2pa_tensor* block_tables, const b2pa_tensor* seq_lens,
                              const b2pa_tensor* page_refs, const b2pa_tensor* rows, int32_t page_size,

@@ -786,7 +786,7 @@ def fork_pages(block_tables: torch.Tensor, seq_lens: torch.Tensor, page_refs: to
 def grow_pages(block_tables: torch.Tensor, seq_lens: torch.Tensor, page_refs: torch.Tensor, rows: torch.Tensor,
                new_lens: torch.Tensor, page_size: int, stream=None):
     """Give rows (int32) of a page ledger free pages for new_lens (int32) tokens, and those lengths, in
-    place (see include/b2pa.h)."""
+    place; a row that becomes shorter gives pages back (see include/b2pa.h)."""
     call = (_calls or native()).grow_pages
     handle = _here(page_refs, stream)
     if handle >= 0:

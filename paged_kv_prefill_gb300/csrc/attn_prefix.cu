@@ -23,51 +23,54 @@ namespace b2pa {
 
 namespace {
 
-// Block (x, b): 32 of request b's rows (kv head, token, head of it), a lane each;
-// each warp takes four groups of four columns.  Parts are added in the order of
-// the keys.  Latency alone: loads that do not depend on one another are issued
-// together.
+// Block (x, b, z): 32 of request b's rows (kv head, token, head of it), a lane each, and
+// kMergeWarps * kMergeCols4 * 4 columns from z times that on.  Parts are added in the
+// order of the keys.  Latency alone, about four accesses that depend on one another:
+// lengths, the row's records, its parts; so nothing waits to know whether it is
+// needed (what was not written is read within the workspace and left out), a unit's
+// further parts are loaded kBatch together, and a row's columns are spread over
+// several SMs (a block of all of them had 1200 instructions for each of 16 warps).
+constexpr int kMergeCols4 = 4, kMergeWarps = 2;
+
 template <int D>
-__global__ void __launch_bounds__(D * 2, 2) prefix_merge_kernel(const __grid_constant__ TreeParams p)
+__global__ void __launch_bounds__(32 * kMergeWarps) prefix_merge_kernel(const __grid_constant__ TreeParams p)
 {
     constexpr float kLog2e = 1.4426950408889634f;
-    constexpr int kCols4 = 4;  // D / 16 warps
+    constexpr int kBatch = 4, kCols4 = kMergeCols4;
     pdl_wait();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, b = blockIdx.y, G = p.rows.G;
+    const int lane = threadIdx.x & 31, warp = blockIdx.z * kMergeWarps + (threadIdx.x >> 5), b = blockIdx.y, G = p.rows.G;
     const TreeReq own = prefix_request(p, p.prefix.groups + b, 1);
     const int g = prefix_group(p, b);
-    if (!own.ok)
+    const int all = own.n * p.H;
+    if (!own.ok || blockIdx.x * 32 >= all)
         return;
-    const int row = blockIdx.x * 32 + lane, all = own.n * p.H;
-    if (blockIdx.x * 32 >= all)
-        return;
-    const bool valid = row < all;
-    const int per = own.n * G, kvh = valid ? row / per : 0, in = valid ? row - kvh * per : 0;
+    const int row = min((int)blockIdx.x * 32 + lane, all - 1);  // (the last row several times)
+    const int per = own.n * G, kvh = row / per, in = row - kvh * per;
     const int tok = own.q0 + in / G, h = kvh * G + in % G;
     const long long at = ((long long)kvh * p.T + own.q0) * G + in;
-    // (both records, although there may be no prefix: that is known an access later)
     PrefixRow x[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-        x[i] = PrefixRow::unpack(p.prefix.part_rec[i][at], at);
-    const float sink = p.sinks != nullptr ? p.sinks[h] * kLog2e : -INFINITY;
-    bool shared = false;
-    if (g >= 0) {
-        const TreeReq r = prefix_request(p, g, 1);
-        if (!r.ok)
-            return;
-        shared = r.kv_len > 0;
-    }
-    float m = -INFINITY, den = 0.f;
-    float4 a[kCols4];
-#pragma unroll
-    for (int k = 0; k < kCols4; ++k)
-        a[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+    float4 v[2][kCols4];
     auto load = [&](const float4* o, long long rows0, const PrefixRow& x, float4 v[kCols4]) {
 #pragma unroll
         for (int k = 0; k < kCols4; ++k)
             v[k] = o[rows0 * (D / 4) + (long long)(warp * kCols4 + k) * x.tile_rows + x.tile_row];
     };
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+        x[i] = PrefixRow::unpack(p.prefix.part_rec[i][at], at);
+    const float sink = p.sinks != nullptr ? p.sinks[h] * kLog2e : -INFINITY;
+    const TreeReq group = prefix_request(p, max(g, 0), 1);  // (of no group: not used)
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+        load(p.prefix.part_o[i], at - x[i].tile_row, x[i], v[i]);
+    if (g >= 0 && !group.ok)
+        return;
+    const bool shared = g >= 0 && group.kv_len > 0;
+    float m = -INFINITY, den = 0.f;
+    float4 a[kCols4];
+#pragma unroll
+    for (int k = 0; k < kCols4; ++k)
+        a[k] = make_float4(0.f, 0.f, 0.f, 0.f);
     auto merge = [&](float x_m, float x_l, const float4 v[kCols4]) {
         const float top = fmaxf(m, x_m);
         const float old = m == top ? 1.f : ex2_approx(m - top);
@@ -82,46 +85,35 @@ __global__ void __launch_bounds__(D * 2, 2) prefix_merge_kernel(const __grid_con
                                fmaf(a[k].w, old, w * y.w));
         }
     };
-    float4 v[2][kCols4];
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-        if (valid && (i == kPrefixOwn || shared))
-            load(p.prefix.part_o[i], at - x[i].tile_row, x[i], v[i]);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-        if (!valid || !(i == kPrefixOwn || shared))
+        if (i == kPrefixShared && !shared)
             continue;
-        // the rest of the unit: parts of the CTAs behind, looked at kBatch together
-        constexpr int kBatch = 2;
+        merge(x[i].m, x[i].l, v[i]);
+        // the rest of the unit: parts of the CTAs behind
         bool more = x[i].cta >= 0 && x[i].cta < p.grid;
-        for (int c0 = x[i].cta + 1, first = 1; first || more; c0 += kBatch, first = 0) {
+        for (int c0 = x[i].cta + 1; __any_sync(0xffffffffu, more); c0 += kBatch) {
             float2 ml[kBatch];
             float4 z[kBatch][kCols4];
-            bool ends[kBatch];
+            unsigned ends = 0;
 #pragma unroll
             for (int k = 0; k < kBatch; ++k) {
-                const int c = c0 + k;
-                ends[k] = true;
-                ml[k] = make_float2(-INFINITY, 0.f);
-                if (more && c < p.grid) {
-                    const long long rows0 = (long long)(c * 2 + x[i].qt) * kQRows;
-                    const float4 y = p.prefix.cut_rec[rows0 + x[i].tile_row];
-                    ml[k] = make_float2(y.x, y.y);
-                    ends[k] = p.prefix.cut_ends[c] != 0;
-                    load(p.prefix.cut_o, rows0, x[i], z[k]);
-                }
+                const int c = more ? min(c0 + k, p.grid - 1) : 0;
+                const long long rows0 = (long long)(c * 2 + x[i].qt) * kQRows;
+                const float4 y = p.prefix.cut_rec[rows0 + x[i].tile_row];
+                ml[k] = make_float2(y.x, y.y);
+                ends |= (unsigned)(p.prefix.cut_ends[c] != 0 || c0 + k >= p.grid - 1) << k;
+                load(p.prefix.cut_o, rows0, x[i], z[k]);
             }
-            if (first)
-                merge(x[i].m, x[i].l, v[i]);
 #pragma unroll
             for (int k = 0; k < kBatch; ++k)
                 if (more) {
                     merge(ml[k].x, ml[k].y, z[k]);
-                    more = !ends[k];
+                    more = !(ends >> k & 1u);
                 }
         }
     }
-    if (!valid)
+    if ((int)blockIdx.x * 32 + lane >= all)
         return;
     if (m != -INFINITY)
         den += ex2_approx(sink - m);
@@ -152,7 +144,8 @@ cudaError_t launch_prefix(TreeParams& p, int tiles, bool few, cudaStream_t strea
     const long long rows = (long long)std::min(p.max_q_len, p.T) * p.H;
     if (rows == 0)
         return e;  // (no request may have a token)
-    return launch_pdl(prefix_merge_kernel<D>, dim3((unsigned)((rows + 31) / 32), p.B), D * 2, 0, stream, p);
+    const dim3 grid((unsigned)((rows + 31) / 32), p.B, D / (4 * kMergeCols4 * kMergeWarps));
+    return launch_pdl(prefix_merge_kernel<D>, grid, 32 * kMergeWarps, 0, stream, p);
 }
 
 }  // namespace

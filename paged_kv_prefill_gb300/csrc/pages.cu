@@ -170,10 +170,21 @@ __global__ void __launch_bounds__(kCompactThreads) compact_kernel(const __grid_c
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ int pages_of(int tokens, int page_size) { return (int)(((long long)tokens + page_size - 1) / page_size); }
 
+// A page loses a holder.  (Only such calls may be under way for the page, and a count
+// that would fall below 0 is put back, so that their order does not show.)
+__device__ __forceinline__ void give_back(const LedgerParams& p, int page)
+{
+    if (page < 0 || page >= p.N) {
+        atomicOr(p.err, (unsigned)B2PA_DEV_BAD_PAGE);
+    } else if (atomicSub(p.refs + page, 1) <= 0) {
+        atomicAdd(p.refs + page, 1);
+        atomicOr(p.err, (unsigned)B2PA_DEV_BAD_PAGE);
+    }
+}
+
 constexpr int kFreeThreads = 128;
 
-// A block per row.  (Counts only fall here, and a count that would fall below 0
-// is put back, so that the order of the blocks does not show.)
+// A block per row.
 __global__ void __launch_bounds__(kFreeThreads) free_pages_kernel(const __grid_constant__ LedgerParams p)
 {
     __shared__ int held;
@@ -195,12 +206,7 @@ __global__ void __launch_bounds__(kFreeThreads) free_pages_kernel(const __grid_c
     __syncthreads();
     for (int c = tid; c < held; c += kFreeThreads) {
         page = c == tid ? page : row[c];
-        if (page < 0 || page >= p.N) {
-            atomicOr(p.err, (unsigned)B2PA_DEV_BAD_PAGE);
-        } else if (atomicSub(p.refs + page, 1) <= 0) {
-            atomicAdd(p.refs + page, 1);
-            atomicOr(p.err, (unsigned)B2PA_DEV_BAD_PAGE);
-        }
+        give_back(p, page);
     }
 }
 
@@ -208,7 +214,8 @@ __global__ void __launch_bounds__(kFreeThreads) free_pages_kernel(const __grid_c
 // in the order of the requests.  One cluster: what the requests want, summed up (by
 // every CTA); the free pages counted, each CTA those of its part of the pool; then
 // whoever finds the k-th free page looks up whose it is.  A request of which some
-// page would be missing gets none.  Bound by latency: about ten dependent accesses to
+// page would be missing gets none; pages that rows give back are free from the next
+// call on.  Bound by latency: about ten dependent accesses to
 // memory and shared memory.  16 samples each of 16 prompts, free, fork, grow and copy:
 // 27.3 us (of which the copy takes 9) with eight CTAs, 45.9 with one, 30.8 with four; a thread
 // that looks up all of its 16 free pages one after the other: 42.
@@ -319,9 +326,9 @@ __global__ void __launch_bounds__(kTakeThreads) take_pages_kernel(const __grid_c
                 }
             } else {
                 const int to = p.to[i];
-                if (have >= 0 && to >= have && pages_of(to, p.page_size) <= p.max_pages) {
+                if (have >= 0 && to >= 0 && pages_of(max(have, to), p.page_size) <= p.max_pages) {
                     col = pages_of(have, p.page_size);
-                    want = pages_of(to, p.page_size) - col;
+                    want = max(pages_of(to, p.page_size) - col, 0);
                 }
             }
         }
@@ -451,8 +458,13 @@ __global__ void __launch_bounds__(kTakeThreads) take_pages_kernel(const __grid_c
                         atomicAdd(p.refs + page[k], 1);
                 }
             }
-        } else if (!bad && !none && lane == 0) {
-            p.seq[rows[i]] = p.to[i];
+        } else if (!bad && !none) {
+            const int r = rows[i], to = p.to[i];
+            if (lane == 0)
+                p.seq[r] = to;
+            // pages that a shorter row gives back
+            for (int c = pages_of(to, p.page_size) + lane; c < base[i] >> 1; c += 32)
+                give_back(p, p.tables[(long long)r * p.stride + c]);
         }
     }
 }

@@ -97,14 +97,14 @@ class Ledger:
         return src, dst, bad
 
     def grow(self, rows, to):
-        bad, ok, seen = 0, [], set()
+        bad, ok, seen, back = 0, [], set(), []
         for r, t in zip(rows, to):
-            good = 0 <= r < self.R and r not in seen and t >= self.seq[r] and self.pages(t) <= self.width
+            good = 0 <= r < self.R and r not in seen and t >= 0 and self.pages(t) <= self.width
             if 0 <= r < self.R:
                 seen.add(r)
             ok.append(good)
             bad |= 0 if good else BAD_REQUEST
-        wants = [self.pages(t) - self.pages(self.seq[r]) if g else 0 for g, r, t in zip(ok, rows, to)]
+        wants = [max(self.pages(t) - self.pages(self.seq[r]), 0) if g else 0 for g, r, t in zip(ok, rows, to)]
         for g, r, t, w, got in zip(ok, rows, to, wants, self.take(wants)):
             if not g:
                 continue
@@ -115,7 +115,10 @@ class Ledger:
             for i in range(w):
                 self.table[r][first + i] = got[i]
                 self.refs[got[i]] = 1
+            back += self.table[r][self.pages(t) : first]
             self.seq[r] = t
+        for pg in back:  # free from the next call on
+            self.refs[pg] -= 1
         return bad
 
 
@@ -153,7 +156,8 @@ def test_ledger_of_random_steps(cuda_lib, P, seed):
         what = r.choice(["grow", "fork", "free", "grow"])
         if what == "grow":
             rows = r.sample(range(led.R), r.randint(1, 12))
-            run_grow(cuda_lib, led, rows, [min(33 * P, led.seq[i] + r.choice([0, 1, P, r.randint(0, 9 * P)])) for i in rows])
+            run_grow(cuda_lib, led, rows, [max(0, min(33 * P, led.seq[i] + r.choice([0, 1, P, -1, r.randint(-9 * P, 9 * P)])))
+                                           for i in rows])
         elif what == "fork" and full and empty:
             kids = r.sample(empty, r.randint(1, len(empty)))
             run_fork(cuda_lib, led, [r.choice(full) for _ in kids], kids)
@@ -208,7 +212,7 @@ def test_requests_that_are_malformed(cuda_lib):
     led.dev()
     # rows outside the table, a child twice, one that is a parent, one that is not empty
     run_fork(cuda_lib, led, [0, -1, 12, 0, 1, 4, 0, 2], [4, 5, 6, 4, 12, 7, 3, 8])
-    run_grow(cuda_lib, led, [0, 0, 1, 2, -3, 9], [25, 40, 29, 65, 5, 64])
+    run_grow(cuda_lib, led, [0, 0, 1, 2, -3, 9, 3], [25, 40, 29, 65, 5, 64, -1])
 
 
 def test_pages_run_out(cuda_lib):
@@ -231,6 +235,18 @@ def test_more_pages_wanted_than_an_int_counts(cuda_lib):
     cuda_lib.grow_pages(table, seq, refs, ints([3, 0, 1, 2, 4]), ints([1, most, most, most, 1]), 1)
     assert seq.tolist() == [0, 0, 0, 1, 0] and refs.tolist() == [1, 1, 0, 1] and table[3, :2].tolist() == [1, -1]
     assert cuda_lib.device_status() == NO_PAGES
+
+
+def test_rows_that_become_shorter(cuda_lib):
+    """Pages behind the new length go back, those that others hold stay theirs, and nobody gets them in the same call."""
+    led = Ledger(8, 12, 4, 9, 4)
+    led.fill(0, 33)
+    led.dev()
+    run_grow(cuda_lib, led, [0, 1, 2], [5, 12, 1])   # 3 free pages: the first two thirds of what is asked for
+    run_grow(cuda_lib, led, [2, 1, 0], [4, 36, 0])
+    run_fork(cuda_lib, led, [1], [3])
+    run_grow(cuda_lib, led, [1, 3], [1, 40])
+    run_grow(cuda_lib, led, [3], [0])
 
 
 def test_free_twice(cuda_lib):
