@@ -660,9 +660,11 @@ __device__ __forceinline__ void split_q_rows(uint8_t* tile, int block_bytes, int
     if (lane < count)
         exps[row0 + lane] = (int8_t)mine;
     __syncwarp();
-    // two rows at a time, eight elements per lane
+    // two rows at a time, eight elements per lane (not unrolled, nor the two halves of a
+    // row of V below: the roles' code competes for the instruction caches; the e4m3 batch
+    // 146 us, 158 with both unrolled)
     const int c = lane & 15;
-#pragma unroll 2
+#pragma unroll 1
     for (int k = 0; k < count; k += 2) {
         const int r = k + (lane >> 4), sw = r & 7;
         const bool on = r < count;
@@ -728,7 +730,7 @@ __device__ __forceinline__ void load_q(const TreeParams& p, const TreeCtx& c, co
 // V entry e, kv tile j of segment s (its n-th): keys that no row sees become
 // 0, and so do keys that some rows may not see and that are not finite.
 template <int D, bool FP8, int kTiles>
-__device__ __forceinline__ void safe_v(const TreeParams& p, const TreeCtx& c, const Seg& s, uint32_t n, int j, uint32_t e)
+__device__ __noinline__ void safe_v(const TreeParams& p, const TreeCtx& c, const Seg& s, uint32_t n, int j, uint32_t e)
 {
     using C = TreeCfg<D, FP8, kTiles>;
     constexpr int kChunks = 8 * C::kHalves;  // 16-byte pieces of a V row
@@ -750,7 +752,7 @@ __device__ __forceinline__ void safe_v(const TreeParams& p, const TreeCtx& c, co
         *at(row) = zero;
     // rows that some may not see: before the last window's edge, and the nodes
     auto look = [&](int r0, int r1) {
-        constexpr int kBatch = 8;  // loads in flight
+        constexpr int kBatch = 4;  // loads in flight
         for (int r = r0; r < r1; r += kBatch * kRowsAtOnce) {
             uint32_t hit = 0;
 #pragma unroll
@@ -986,9 +988,8 @@ __device__ __forceinline__ uint32_t f16x2_of_e4m3x2(uint32_t two)
     return h;
 }
 
-// (not inlined: the e4m3 batch 157 us, 163 with its code among the other roles')
 template <int kTiles>
-__device__ __noinline__ void tree_convert(const TreeParams& p, const TreeCtx& c)
+__device__ void tree_convert(const TreeParams& p, const TreeCtx& c)
 {
     using C = TreeCfg<128, true, kTiles>;
     const int wq = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31, row = wq * 32 + lane, sw = row & 7;
@@ -1031,25 +1032,30 @@ __device__ __noinline__ void tree_convert(const TreeParams& p, const TreeCtx& c)
                 break;
             const uint8_t* from = c.base + C::kOffRing + at.e * C::kKvBytes + row * 128;
             uint8_t* to = c.base + C::kOffV + buf * C::kVBytes + row * 128;
-            uint4 x[8];  // the row, so that its ring entry is free before there is room for it in f16
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-                x[k] = ld_shared_v4(smem_u32(from) + ((k ^ sw) << 4));
-            fence_proxy_async_smem();  // the loads are done before the entry's next copy
-            __syncwarp();
-            mbar_arrive_p(&c.kv_empty[at.e], lane0);
             if (!(ok = wait_bar(&c.v_empty[buf], phase, c)))
                 break;
+#pragma unroll 1
+            for (int h = 0; h < 2; ++h) {
+                uint4 x[4];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                uint8_t* block = to + (k >> 2) * C::kBlockBytes;
-                const int ch = 2 * k & 7;
-                *reinterpret_cast<uint4*>(block + ((ch ^ sw) << 4)) =
-                    make_uint4(f16x2_of_e4m3x2(x[k].x), f16x2_of_e4m3x2(x[k].x >> 16), f16x2_of_e4m3x2(x[k].y),
-                               f16x2_of_e4m3x2(x[k].y >> 16));
-                *reinterpret_cast<uint4*>(block + (((ch + 1) ^ sw) << 4)) =
-                    make_uint4(f16x2_of_e4m3x2(x[k].z), f16x2_of_e4m3x2(x[k].z >> 16), f16x2_of_e4m3x2(x[k].w),
-                               f16x2_of_e4m3x2(x[k].w >> 16));
+                for (int k = 0; k < 4; ++k)
+                    x[k] = ld_shared_v4(smem_u32(from) + (((4 * h + k) ^ sw) << 4));
+                if (h == 1) {
+                    fence_proxy_async_smem();  // the loads are done before the entry's next copy
+                    __syncwarp();
+                    mbar_arrive_p(&c.kv_empty[at.e], lane0);
+                }
+                uint8_t* block = to + h * C::kBlockBytes;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int ch = 2 * k;
+                    *reinterpret_cast<uint4*>(block + ((ch ^ sw) << 4)) =
+                        make_uint4(f16x2_of_e4m3x2(x[k].x), f16x2_of_e4m3x2(x[k].x >> 16), f16x2_of_e4m3x2(x[k].y),
+                                   f16x2_of_e4m3x2(x[k].y >> 16));
+                    *reinterpret_cast<uint4*>(block + (((ch + 1) ^ sw) << 4)) =
+                        make_uint4(f16x2_of_e4m3x2(x[k].z), f16x2_of_e4m3x2(x[k].z >> 16), f16x2_of_e4m3x2(x[k].w),
+                                   f16x2_of_e4m3x2(x[k].w >> 16));
+                }
             }
             fence_proxy_async_smem();
             __syncwarp();
@@ -1073,8 +1079,8 @@ __device__ void tree_softmax(const TreeParams& p, const TreeCtx& c, int t)
     // the top).  The stabiliser is renewed once the row's maximum has grown by kSlack.
     constexpr float kBias = FP8 ? 7.f : 0.f, kSlack = 8.f;
     // 32-key steps of the exponentials that are unrolled (see below; an e4m3 cache's kernel has one role
-    // more: its batch 161 us with one step, 172 with two, 512 rows per kv head 143 and 139)
-    constexpr int kUnroll = (kTiles == 2 ? 4 : 2) / (FP8 ? 2 : 1);
+    // more: its batch 157 us with one step, 183 with two; 512 rows per kv head 136 with two, 131 with four)
+    constexpr int kUnroll = kTiles == 2 ? 4 : FP8 ? 1 : 2;
     const int wq = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31, row = wq * 32 + lane;
     const uint32_t lane_off = (uint32_t)(wq * 32) << 16;
     const uint32_t s0_tmem = c.tmem + lane_off;  // + buffer * kKvTile
