@@ -672,8 +672,9 @@ B2PA_API int b2pa_compact_kv(const b2pa_tensor* k_pool, const b2pa_tensor* v_poo
  *                page.  A page with 0 is free.
  *  rows, ...     contiguous int32 [n], at most 4096 per call: the rows a call works on.
  * Pages are given lowest number first, requests served in the order of the call.
- * Results do not depend on timing.  All three are asynchronous on `stream`, one
- * kernel, and no-ops for n = 0; the ledger's tensors are written in place and must
+ * Results do not depend on timing, as long as calls on one ledger are ordered (by
+ * one stream, or events).  All three are asynchronous on `stream`, one kernel, and
+ * no-ops for n = 0; the ledger's tensors are written in place and must
  * not overlap one another or the other arguments.  A malformed request (a row outside
  * [0, R), a length below 0 or of more than max_pages pages) sets B2PA_DEV_BAD_REQUEST
  * and changes nothing; one for which there are not enough free pages (those that

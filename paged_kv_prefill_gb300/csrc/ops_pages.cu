@@ -153,7 +153,7 @@ int compact_impl(const b2pa_tensor* k_pool, const b2pa_tensor* v_pool, const b2p
         return fail(B2PA_ERR_INVALID_ARG, "accepted must be int32 [B, width] with unit column stride");
     if (B == 0)
         return B2PA_OK;
-    for (const b2pa_tensor* t : {seq_lens, counts, cum_q})
+    for (const b2pa_tensor* t : {seq_lens, counts, cum_q, accepted, block_tables})
         if (t->data == new_lens->data)
             return fail(B2PA_ERR_INVALID_ARG, "new_lens must not be an input: several blocks read those");
     long long pieces = 0;

@@ -162,6 +162,13 @@ CASES = {
     "heads_128": dict(reqs=[2, 3], prefix=[333, 200], ns=[1, 1, 2, 1, 1], kvs=[40] * 5, H=128, Hkv=1, D=128, P=32),
     "heads_1_d64": dict(reqs=[130, 7], prefix=[1333, 70], ns=[1] * 137, kvs=[1 + i % 9 for i in range(137)], H=4, Hkv=4,
                         D=64, P=8),
+    "heads_12": dict(reqs=[3, 14], prefix=[333, 555], ns=[1] * 17, kvs=[9 + 50 * i for i in range(17)], H=24, Hkv=2, D=128,
+                     P=32, sinks=True),
+    "heads_16_d64": dict(reqs=[30], prefix=[700], ns=[1] * 30, kvs=[1 + 31 * i for i in range(30)], H=16, Hkv=1, D=64, P=16),
+    "heads_9_e4m3": dict(reqs=[30, 2], prefix=[700, 3], ns=[1] * 32, kvs=[1 + 31 * i for i in range(32)], H=18, Hkv=2, D=128,
+                         P=64, layout="NHD", cache="e4m3"),
+    "heads_16_e4m3": dict(reqs=[5], prefix=[300], ns=[1] * 5, kvs=[1, 128, 129, 600, 5], H=16, Hkv=1, D=128, P=16,
+                          cache="e4m3", sinks=True),
     "page_256": dict(reqs=[3], prefix=[1000], ns=[1, 2, 1], kvs=[257, 12, 600], H=4, Hkv=1, D=128, P=256),
     "e4m3": dict(reqs=[6, 9], prefix=[700, 300], ns=[1] * 15, kvs=[1 + 40 * i for i in range(15)], H=32, Hkv=8, D=128,
                  P=32, cache="e4m3"),
@@ -223,6 +230,31 @@ def test_long_keys_cut_over_all_sms(cuda_lib, cache, prefix, own):
     t.check(out)
     for _ in range(3):
         assert torch.equal(out, cuda_lib.prefix_attention(**d))
+    assert cuda_lib.device_status() == 0
+
+
+@pytest.mark.parametrize("cfg", [dict(H=8, Hkv=2, D=128), dict(H=16, Hkv=1, D=128), dict(H=8, Hkv=1, D=64),
+                                 dict(H=16, Hkv=1, D=64), dict(H=8, Hkv=1, D=128, cache="e4m3"),
+                                 dict(H=15, Hkv=1, D=128, cache="e4m3")], ids=lambda c: "-".join(map(str, c.values())))
+@pytest.mark.parametrize("count", [3, 40])
+def test_single_tokens_with_long_keys_of_their_own(cuda_lib, cfg, count):
+    """Own keys in many parts, beside others of a single key; q 8 times as large in every other request."""
+    t = Batch([count], [130], [1] * count, [1 + 9000 * (i % 3 == 0) + 37 * i for i in range(count)], P=32, seed=count, **cfg)
+    t.q[::2] *= 8
+    d = t.dev()
+    out = cuda_lib.prefix_attention(**d)
+    t.check(out)
+    assert torch.equal(out, cuda_lib.prefix_attention(**d))
+    assert cuda_lib.device_status() == 0
+
+
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+@pytest.mark.parametrize("scale", [1e-30, 1e-6, 3e4])
+def test_queries_small_and_large(cuda_lib, cache, scale):
+    """Rows of queries over bf16's range: over e4m3 caches each is scaled to its own f16 range."""
+    t = Batch([6], [150], [1] * 6, [40, 1, 200, 7, 130, 64], 16, 2, 128, 16, cache=cache, seed=3)
+    t.q = (t.q.double() * scale * torch.tensor([1.0, 2.0 ** -20, 1.0, 2.0 ** -9, 1.0, 1.0])[:, None, None]).to(BF)
+    t.check(cuda_lib.prefix_attention(**t.dev()))
     assert cuda_lib.device_status() == 0
 
 
