@@ -10,10 +10,10 @@
 // context, so K and V are read once for all of them: up to about 280 rows per
 // kv head the time is that of the K/V stream from HBM, beyond that of the
 // tensor cores and the exponentials.  Measured: 32 requests of 512 to 8192 keys,
-// 9 to 16 nodes x 4 heads, D = 128: 104 us, 5.6 TB/s (0.83 of the copy rate);
-// the same with e4m3, up to 16384 keys and 8 nodes: 160 us, 4.1 TB/s (0.60);
-// 8 requests of up to 16384 keys, 64 nodes x 8 heads: 112 us, 940 TFLOP/s (0.49 of
-// the bf16 rate); one request, 8 nodes, 2048 keys: 14.4 us, latency.
+// 9 to 16 nodes x 4 heads, D = 128: 102 us, 5.7 TB/s (0.85 of the copy rate);
+// the same with e4m3, up to 16384 keys and 8 nodes: 145 us, 4.5 TB/s (0.67);
+// 8 requests of up to 16384 keys, 64 nodes x 8 heads: 105 us, 1000 TFLOP/s (0.51 of
+// the bf16 rate; at D = 64 76 us); one request, 8 nodes, 2048 keys: 13.9 us, latency.
 //
 // Work.  A unit is (request, kv head, up to kTiles query tiles of 128 rows);
 // all units' kv tiles of 128 keys, laid end to end, are cut into equal runs,
@@ -31,7 +31,7 @@
 //            MMA waits for takes a few hundred cycles to look at, and one warp
 //            that did all of it left the tensor core idle meanwhile (512 rows per
 //            kv head: 126 us with one).  kTiles 1: S = Q K^T and O += P V.
-//            kTiles 2: a query tile each, in turns.
+//            kTiles 2: a query tile each, in turns; at D = 64 (kPairs) all S and all P V.
 //   warp 3   loads Q (a TMA box per softmax warp's tokens and column block), and
 //            makes V safe where rows see different keys (see below).
 //   warps 4-7, 8-11   softmax A and B: one thread per MMA row.
@@ -54,12 +54,13 @@
 // that P needs its relative precision over a wide range: kept in (0, 2^15] with
 // its row's largest at 2^7 or more, it is off by at most half a step of f16
 // (2^-11 of itself) down to 2^-21 of the row's largest, and by 2^-32 of the largest
-// below.  (P in two e4m3 terms with V as it is took 145 us for that batch, not 160,
+// below.  (P in two e4m3 terms with V as it is took 145 us for that batch when this took 160,
 // but its steps end at 2^-14 of the row's largest: of a tail of 16384 keys behind a
 // lead of 11 nats 0.84 was lost.)  What bounds this: the ring.  V in f16, two tiles
 // of it, leaves room for 128 KB of K and V on their way (96 KB with two query tiles).
 // So one Q buffer does, and the converting warps free a V entry as soon as they
-// have its rows in registers (161 us; 164 once they are converted).
+// have its rows in registers (161 us; 164 once they are converted), and its roles'
+// code is kept short (146 us; 158 unrolled: the instruction caches).
 //
 // bf16 caches.  P is bf16 (off by half a step, 2^-8 of itself, over all of fp32's
 // range), since both operands of an MMA have one type and V's range needs bf16.
@@ -71,8 +72,8 @@
 // rows that see it in the epilogue, from global memory, in fp32.
 //
 // TMEM (512 columns).  kTiles 1: S [0,128) [128,256) [256,384), O [384,384+D).
-// kTiles 2: S [0,128) [128,256), O [256,256+D) [256+D,256+2D).  P overwrites the
-// first 64 columns of its S.
+// kTiles 2: S [0,128) [128,256), O [256,256+D) [256+D,256+2D); D = 64: three S, O at
+// 384.  P overwrites the first 64 columns of its S.
 //
 // Every wait is bounded, as in attn_tc.cu.
 #pragma once
@@ -105,7 +106,9 @@ struct TreeCfg {
     static constexpr int kOffRing = kQBufs * kTiles * kQBytes;
     static constexpr int kOffV = kOffRing + kEntries * kKvBytes;
     static constexpr int kOffBar = kOffV + kVBufs * kVBytes;
-    static constexpr int kSBufs = kTiles == 1 ? 3 : 2;
+    // two query tiles, and TMEM has room for a third S (see tree_s_pairs)
+    static constexpr bool kPairs = kTiles == 2 && D == 64;
+    static constexpr int kSBufs = kTiles == 1 || kPairs ? 3 : 2;
     static constexpr int kNumBars = 3 * kEntries + 3 * kQBufs + 3 * kSBufs + 2 + 8 + 2 + 2 + 2 * kTreeSlots + 1 + 2 * kVBufs;
     static constexpr int kOffMisc = kOffBar + kNumBars * 8;  // tmem address, abort flag
     static constexpr int kOffItems = kOffMisc + 16;
@@ -133,6 +136,7 @@ struct TreeCtx : Ctx {
     // both groups posted (m, l); both have read O
     uint64_t *m_ready, *met, *left;
     uint64_t* turn;                          // kTiles 2, [2]: this tile's MMAs next (m_ready's place)
+    uint64_t* s_pair;                        // kPairs, [2][3] (there too): query tile t's S, in turn
     uint64_t *v_full, *v_empty;              // [kVBufs]: V in f16 there, its P V done
     uint64_t *drain /* [2] */, *it_full, *it_empty, *never;
 };
@@ -602,6 +606,104 @@ __device__ void tree_tile(const TreeParams& p, const TreeCtx& c, int t)
         mma_commit(&c.drain[t]);
     __syncwarp();
     drain_wait(&c.drain[t], 0);
+}
+
+// kPairs (kTiles 2, D = 64), warp 1: S of every (kv tile, query tile), the query tiles in
+// turn, into three buffers in turn.  With one buffer more than query tiles a tile's next
+// S is computed while its P V waits for P, so that a softmax group finds it when it is
+// done with the last: the chain S - softmax - P V of a tile loses its first part.  512 rows
+// per kv head: 76 us, 89 with two buffers in turns as above; 512 rows behind one prefix
+// of 32768 keys 194 us, 222 with two.
+template <int D, bool FP8>
+__device__ void tree_s_pairs(const TreeParams& p, const TreeCtx& c)
+{
+    using C = TreeCfg<D, FP8, 2>;
+    const TreeMma<D, FP8, 2> mma(c);
+    const uint32_t kv_full = smem_u32(c.kv_full), kv_empty = smem_u32(c.kv_empty);
+    const uint32_t s_pair = smem_u32(c.s_pair), s_free = smem_u32(c.s_free);
+    RingPos<C::kEntries> at(0);
+    uint32_t buf = 0, turn = 0;
+    uint32_t at0 = s_pair, at1 = s_pair + 24;  // the query tiles' next barriers
+    bool ok = !p.inject_stall || wait_bar(c.never, 0, c);  // failure-detection tests
+    for (uint32_t n = 0; ok; ++n) {
+        Seg s;
+        if (!take_seg(c, n, &s) || !s.on)
+            break;
+        const uint32_t qb = n % C::kQBufs;
+        const int tiles = s.toks > p.rows.tile_toks ? 2 : 1;
+        if (!wait_bar(&c.q_full[qb], (n / C::kQBufs) & 1, c))
+            break;
+        for (int i = s.tiles; ok && i > 0; --i) {
+            ok = wait_at(kv_full + at.e * 8, at.phase, c);
+            for (int t = 0; ok && t < tiles; ++t) {
+                if (!(ok = wait_at(s_free + buf * 8, turn ^ 1, c)))  // the buffer's last P used
+                    break;
+                tc_fence_after();
+                mma.scores(buf, qb * 2 + t, at.e);
+                mma_commit_at(t == 0 ? at0 : at1, mma.issue);
+                if (t == 0)
+                    at0 = at0 == s_pair + 16 ? s_pair : at0 + 8;
+                else
+                    at1 = at1 == s_pair + 40 ? s_pair + 24 : at1 + 8;
+                if (++buf == 3) {
+                    buf = 0;
+                    turn ^= 1;
+                }
+            }
+            if (ok)
+                mma_commit_at(kv_empty + at.e * 8, mma.issue);
+            at.next();
+        }
+        if (ok)
+            mma_commit_p(&c.q_empty[qb], mma.issue);
+    }
+    // every MMA this thread issued has completed once the drain barrier flips
+    if (mma.issue)
+        mma_commit(&c.drain[0]);
+    __syncwarp();
+    drain_wait(&c.drain[0], 0);
+}
+
+// kPairs, warp 2: O += P V, in the same order.
+template <int D, bool FP8>
+__device__ void tree_pv_pairs(const TreeParams& p, const TreeCtx& c)
+{
+    using C = TreeCfg<D, FP8, 2>;
+    const TreeMma<D, FP8, 2> mma(c);
+    const uint32_t p_full = smem_u32(c.p_full), s_free = smem_u32(c.s_free);
+    VPos<C::kEntries, FP8> at;
+    uint32_t buf = 0, turn = 0;
+    bool ok = true;
+    for (uint32_t n = 0; ok; ++n) {
+        Seg s;
+        if (!take_seg(c, n, &s) || !s.on)
+            break;
+        const int tiles = s.toks > p.rows.tile_toks ? 2 : 1;
+        const int mixed0 = s.mixed0(p.window), mixed1 = s.mixed1();
+        for (int i = 0; ok && i < s.tiles; ++i) {
+            ok = at.wait(c, i < mixed0 || i >= mixed1);
+            for (int t = 0; ok && t < tiles; ++t) {
+                if (!(ok = wait_at(p_full + buf * 8, turn, c)))
+                    break;
+                tc_fence_after();
+                mma.values(t, buf, at.at(), s.kv_len - (s.j0 + i) * kKvTile, i == 0);
+                mma_commit_at(s_free + buf * 8, mma.issue);
+                if (++buf == 3) {
+                    buf = 0;
+                    turn ^= 1;
+                }
+            }
+            if (ok)
+                mma_commit_at(at.done(c), mma.issue);
+            at.next();
+        }
+        for (int t = 0; ok && t < tiles; ++t)
+            mma_commit_p(&c.o_full[t], mma.issue);
+    }
+    if (mma.issue)
+        mma_commit(&c.drain[1]);
+    __syncwarp();
+    drain_wait(&c.drain[1], 0);
 }
 
 // ---------------------------------------------------------------------------
@@ -1094,6 +1196,7 @@ __device__ void tree_softmax(const TreeParams& p, const TreeCtx& c, int t)
     // kTiles 2: what tells that the P V of tile g is done
     auto v_done = [&](uint32_t g) { return FP8 ? &c.v_empty[g & 1] : &c.kv_empty[(2 * g + 1) % C::kEntries]; };
     uint32_t g0 = 0;   // kv tiles before this segment
+    uint32_t pair0 = 0;  // kPairs: (kv tile, query tile) before this segment
     uint32_t s_cnt = 0, o_cnt = 0;  // kTiles 2: S and O of this group awaited so far
     bool ok = true;
     for (uint32_t n = 0; ok; ++n) {
@@ -1120,6 +1223,9 @@ __device__ void tree_softmax(const TreeParams& p, const TreeCtx& c, int t)
             ok = false;
             break;
         }
+        const bool two = kTiles == 2 && s.toks > rows.tile_toks;
+        const uint32_t pairs = pair0;
+        pair0 += (uint32_t)s.tiles * (two ? 2 : 1);
         if (kTiles == 2 && qt * rows.tile_toks >= s.toks) {
             g0 += (uint32_t)s.tiles;
             continue;
@@ -1147,7 +1253,9 @@ __device__ void tree_softmax(const TreeParams& p, const TreeCtx& c, int t)
         // kTiles 1: the tiles of this group's parity over all segments
         for (int i = kTiles == 1 ? (int)((t ^ g0) & 1) : 0; i < s.tiles; i += kTiles == 1 ? 2 : 1) {
             const uint32_t g = g0 + (uint32_t)i;
-            const int buf = kTiles == 1 ? (int)(g % 3) : t;
+            // kPairs: which S this is, and the one before of this query tile
+            const uint32_t pair = pairs + (two ? 2 * (uint32_t)i + (uint32_t)t : (uint32_t)i), last_pair = pair - (two ? 2 : 1);
+            const int buf = kTiles == 1 ? (int)(g % 3) : C::kPairs ? (int)(pair % 3) : t;
             const uint32_t s_tmem = s0_tmem + (uint32_t)(buf * kKvTile);
             const int k0 = (s.j0 + i) * kKvTile;
             // rows that are nobody's count as seeing everything; what they compute
@@ -1155,12 +1263,15 @@ __device__ void tree_softmax(const TreeParams& p, const TreeCtx& c, int t)
             const bool mixed = !__all_sync(0xffffffffu, !valid || (k0 >= view.lo && k0 + kKvTile <= view.ctx));
             if (!kPrefix && mixed)  // the mask row, while S is on its way
                 asm volatile("prefetch.global.L1 [%0];" ::"l"(view.mask + min(max(k0 - view.ctx, 0) >> 5, view.words - 1)));
-            if (!wait_bar(&c.s_full[buf], kTiles == 1 ? (g / 3) & 1 : s_cnt & 1, c)) {
+            // (kPairs: barriers of this group's own, for it does not follow the other's segments; three,
+            // for a segment of one query tile has all three buffers)
+            if (!wait_bar(C::kPairs ? &c.s_pair[t * 3 + s_cnt % 3] : &c.s_full[buf],
+                          kTiles == 1 ? (g / 3) & 1 : C::kPairs ? (s_cnt / 3) & 1 : s_cnt & 1, c)) {
                 ok = false;
                 break;
             }
             ++s_cnt;
-            if (wq == 0) {  // K has been read; kTiles 2: and V of the tile before
+            if (!C::kPairs && wq == 0) {  // K has been read; kTiles 2: and V of the tile before
                 const uint32_t lane0 = lane == 0 ? 1u : 0u;
                 mbar_arrive_p(&c.kv_empty[2 * g % C::kEntries], lane0);
                 if (kTiles == 2 && i > 0)
@@ -1251,6 +1362,10 @@ __device__ void tree_softmax(const TreeParams& p, const TreeCtx& c, int t)
                     ok = false;
                     break;
                 }
+                if (C::kPairs && !wait_bar(&c.s_free[last_pair % 3], (last_pair / 3) & 1, c)) {
+                    ok = false;
+                    break;
+                }
                 tc_fence_after();
                 const float2 ff = make_float2(alpha, alpha);
 #pragma unroll 1
@@ -1284,7 +1399,7 @@ __device__ void tree_softmax(const TreeParams& p, const TreeCtx& c, int t)
             break;
         }
         ++o_cnt;
-        if (kTiles == 2 && wq == 0)
+        if (kTiles == 2 && !C::kPairs && wq == 0)
             mbar_arrive_p(v_done(g0 - 1), lane == 0 ? 1u : 0u);  // (g0: the next segment's)
         if constexpr (kTiles == 1) {
             // both groups' sums, relative to the last tile's maximum (the larger one)
@@ -1412,7 +1527,7 @@ __device__ __forceinline__ void tree_setup(const TreeParams& p, uint8_t* smem, T
     c.s_free = c.p_full + C::kSBufs;
     c.o_full = c.s_free + C::kSBufs;
     c.m_ready = c.o_full + 2;
-    c.turn = c.m_ready;
+    c.turn = c.s_pair = c.m_ready;
     c.met = c.m_ready + 8;
     c.left = c.met + 1;
     c.drain = c.left + 1;
@@ -1431,12 +1546,12 @@ __device__ __forceinline__ void tree_setup(const TreeParams& p, uint8_t* smem, T
         for (int e = 0; e < C::kEntries; ++e) {
             mbar_init(&c.kv_full[e], 1);
             // its MMAs (kTiles 2: two tiles'; V of an e4m3 cache: the converting warps), and warp 3
-            mbar_init(&c.kv_empty[e], 1 + (FP8 && (e & 1) ? 4 : kTiles));
+            mbar_init(&c.kv_empty[e], 1 + (FP8 && (e & 1) ? 4 : C::kPairs ? 1 : kTiles));
             mbar_init(&c.v_ready[e], 1);
         }
         for (int b = 0; b < C::kQBufs; ++b) {
             mbar_init(&c.q_full[b], 1);
-            mbar_init(&c.q_empty[b], (FP8 ? 8 : 0) + kTiles);  // the MMAs that read it; e4m3: and the softmax warps
+            mbar_init(&c.q_empty[b], (FP8 ? 8 : 0) + (C::kPairs ? 1 : kTiles));  // the MMAs that read it; e4m3: and the softmax warps
             mbar_init(&c.q_conv[b], 4);
         }
         for (int k = 0; k < C::kSBufs; ++k) {
@@ -1592,6 +1707,8 @@ __device__ __forceinline__ void tree_roles(const TreeParams& p, const TreeCtx& c
             tree_producer<C, kTiles, kPrefix>(p, c, run.start, run.end, run.first_b, run.base);
         else if (warp == 3)
             tree_feed<D, FP8, kTiles>(p, c);
+        else if constexpr (C::kPairs)
+            warp == 1 ? tree_s_pairs<D, FP8>(p, c) : tree_pv_pairs<D, FP8>(p, c);
         else if constexpr (kTiles == 2)
             tree_tile<D, FP8>(p, c, warp - 1);
         else if (warp == 1)
