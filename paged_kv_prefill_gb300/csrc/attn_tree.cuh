@@ -611,9 +611,11 @@ __device__ void tree_tile(const TreeParams& p, const TreeCtx& c, int t)
 // kPairs (kTiles 2, D = 64), warp 1: S of every (kv tile, query tile), the query tiles in
 // turn, into three buffers in turn.  With one buffer more than query tiles a tile's next
 // S is computed while its P V waits for P, so that a softmax group finds it when it is
-// done with the last: the chain S - softmax - P V of a tile loses its first part.  512 rows
-// per kv head: 76 us, 89 with two buffers in turns as above; 512 rows behind one prefix
-// of 32768 keys 194 us, 222 with two.
+// done with the last: the chain S - softmax - P V of a tile loses its first part.  8 trees
+// of 64 nodes x 8 heads: 76 us, 89 with two buffers in turns as above; 16 questions of 16 to 64
+// tokens behind 32768 keys 194 us, 222 with two, 254 with a warp for each query tile here
+// too.  Now P V's issuer is the slowest: 8 MMAs are issued in 620 cycles of the 1150 that a
+// (kv tile, query tile) takes, and a softmax group, busy for 1250 of 2300, waits for S.
 template <int D, bool FP8>
 __device__ void tree_s_pairs(const TreeParams& p, const TreeCtx& c)
 {
@@ -1181,7 +1183,8 @@ __device__ void tree_softmax(const TreeParams& p, const TreeCtx& c, int t)
     // the top).  The stabiliser is renewed once the row's maximum has grown by kSlack.
     constexpr float kBias = FP8 ? 7.f : 0.f, kSlack = 8.f;
     // 32-key steps of the exponentials that are unrolled (see below; an e4m3 cache's kernel has one role
-    // more: its batch 157 us with one step, 183 with two; 512 rows per kv head 136 with two, 131 with four)
+    // more: its batch 157 us with one step, 183 with two, before the roles' code was shortened; 512 rows per kv
+    // head 136 with two, 131 with four)
     constexpr int kUnroll = kTiles == 2 ? 4 : FP8 ? 1 : 2;
     const int wq = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31, row = wq * 32 + lane;
     const uint32_t lane_off = (uint32_t)(wq * 32) << 16;

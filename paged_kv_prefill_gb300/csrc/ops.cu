@@ -448,7 +448,7 @@ int plan_prefix(const Problem& pr, int max_q_len, int max_group_q_len, const Dev
     PrefixPlan t{};
     t.tc = path != B2PA_PATH_GENERIC && !why;
     if (t.tc) {
-        t.few = max_q_len <= 1 && pr.H / pr.Hkv <= 16;
+        t.few = max_q_len <= 1 && pr.H / pr.Hkv <= 16;  // (two sets of eight rows; see launch_prefix)
         t.tiles = std::max(max_q_len, max_group_q_len) <= tree_rows(pr.H / pr.Hkv).tile_toks ? 1 : 2;
         size_t at = 0;
         auto take = [&](size_t bytes) {
