@@ -603,7 +603,8 @@ B2PA_API int b2pa_prefix_attention(const b2pa_tensor* q, const b2pa_tensor* k_po
  * parent that does not come before its child, more than max_q_len nodes, rows
  * outside [0, T)), which sets B2PA_DEV_BAD_REQUEST.  A last row without a positive
  * finite value has next token -1 and sets B2PA_DEV_BAD_PROBS.
- * Outputs must not overlap inputs.  Asynchronous on `stream`; one kernel.
+ * Outputs must not overlap inputs or one another (refused).  Asynchronous on `stream`;
+ * one kernel.
  */
 B2PA_API int b2pa_verify_trees(const b2pa_tensor* target_probs, const b2pa_tensor* draft_probs,
                                const b2pa_tensor* tokens, const b2pa_tensor* parents, const b2pa_tensor* uniforms,
@@ -647,7 +648,7 @@ B2PA_API int b2pa_copy_pages(const b2pa_tensor* k_pool, const b2pa_tensor* v_poo
  *  k_pool, v_pool, k_scales, v_scales, layout   as for b2pa_copy_pages.
  *  block_tables  [B, max_pages] int32, stride[1] == 1; a request's pages must be its
  *                own where its nodes lie.
- *  seq_lens, counts, new_lens  contiguous int32 [B]; new_lens none of the inputs.
+ *  seq_lens, counts, new_lens  contiguous int32 [B]; new_lens over none of the inputs.
  *  cum_q         contiguous int32 [B + 1].
  *  accepted      [B, width] int32, stride[1] == 1; columns from counts[b] on are not read.
  * A malformed request (n < 0 or > seq_lens[b], more pages than max_pages, a count

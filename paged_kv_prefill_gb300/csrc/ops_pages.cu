@@ -67,6 +67,24 @@ int check_ints(const b2pa_tensor* t, const char* what, int64_t n)
 
 int* ints(const b2pa_tensor* t) { return static_cast<int*>(t->data); }
 
+// Whether two tensors of 4-byte elements, strides >= 0, lie over one another (from the
+// first to the last element of each).
+bool meet(const b2pa_tensor* a, const b2pa_tensor* b)
+{
+    auto bytes = [](const b2pa_tensor* t) {
+        int64_t last = 0;
+        for (int k = 0; k < t->ndim; ++k) {
+            if (t->shape[k] == 0)
+                return (int64_t)0;
+            last += (t->shape[k] - 1) * t->stride[k];
+        }
+        return 4 * (last + 1);
+    };
+    const int64_t na = bytes(a), nb = bytes(b);
+    const uintptr_t pa = reinterpret_cast<uintptr_t>(a->data), pb = reinterpret_cast<uintptr_t>(b->data);
+    return na > 0 && nb > 0 && pa < pb + (uintptr_t)nb && pb < pa + (uintptr_t)na;
+}
+
 int copy_impl(const b2pa_tensor* k_pool, const b2pa_tensor* v_pool, const b2pa_tensor* k_scales,
               const b2pa_tensor* v_scales, const b2pa_tensor* src, const b2pa_tensor* dst, int32_t layout,
               cudaStream_t stream)
@@ -154,7 +172,7 @@ int compact_impl(const b2pa_tensor* k_pool, const b2pa_tensor* v_pool, const b2p
     if (B == 0)
         return B2PA_OK;
     for (const b2pa_tensor* t : {seq_lens, counts, cum_q, accepted, block_tables})
-        if (t->data == new_lens->data)
+        if (meet(t, new_lens))
             return fail(B2PA_ERR_INVALID_ARG, "new_lens must not be an input: several blocks read those");
     long long pieces = 0;
     for (int i = 0; i < p.planes; ++i)
@@ -232,8 +250,15 @@ int verify_impl(const b2pa_tensor* target, const b2pa_tensor* draft, const b2pa_
                     "accepted must be int32 [B, width] with unit column stride, its rows apart and width >= max_q_len");
     if (B == 0)
         return B2PA_OK;
-    if (counts->data == next->data || accepted->data == counts->data || accepted->data == next->data)
-        return fail(B2PA_ERR_INVALID_ARG, "accepted, counts and next_tokens must be three tensors");
+    // (a request's CTAs each read its nodes and have to find the same)
+    const b2pa_tensor* outs[3] = {accepted, counts, next};
+    for (int i = 0; i < 3; ++i) {
+        for (const b2pa_tensor* t : {target, draft, tokens, parents, uniforms, last, cum_q})
+            if (t && meet(t, outs[i]))
+                return fail(B2PA_ERR_INVALID_ARG, "outputs must not overlap inputs");
+        if (meet(outs[i], outs[(i + 1) % 3]))
+            return fail(B2PA_ERR_INVALID_ARG, "accepted, counts and next_tokens must be three tensors");
+    }
     int dev;
     DevInfo di;
     VerifyParams p;

@@ -389,7 +389,7 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const __grid_constant_
             const Pair own = sum_rest(w, out, here, c0, c1, 4, p.aligned), upto = before + own.scan();
             const unsigned over = __ballot_sync(0xffffffffu, own.positive() && want < upto);
             const unsigned some = __ballot_sync(0xffffffffu, own.positive());
-            const int lucky = over != 0 ? __ffs(over) - 1 : 31 - __clz(some);
+            const int lucky = over != 0 ? __ffs(over) - 1 : max(31 - __clz(some), 0);
             Pair run = lucky > 0 ? upto.shfl(max(lucky - 1, 0)) : before;
             const int f0 = i0 + lucky * chunk, f1 = min(i1, f0 + chunk);
             int token = -1;

@@ -71,6 +71,16 @@ def test_compact(lib, change):  # noqa: F811
     assert lib.b2pa_last_error_message()
 
 
+@pytest.mark.parametrize("change", [
+    dict(out=fake([3], I32, base=M + 4)),                   # in the tables, the lengths, the nodes
+    dict(counts=fake([3], I32, base=2 * M - 8)),            # the last one is new_lens[0]
+    dict(acc=fake([3, 7], I32, [32, 1], base=2 * M - 256)),
+])
+def test_compact_over_inputs(lib, change):  # noqa: F811
+    assert compact(lib, **change) == INVALID
+    assert lib.b2pa_last_error_message()
+
+
 def test_compact_of_no_requests(lib):  # noqa: F811
     none = fake([0], I32, base=0)
     assert compact(lib, table=fake([0, 4], I32, base=0), seq=none, cum=fake([1], I32), acc=fake([0, 7], I32, base=0),

@@ -61,6 +61,21 @@ def test_verify(lib, change, status):  # noqa: F811
     assert lib.b2pa_last_error_message()
 
 
+@pytest.mark.parametrize("change", [
+    dict(acc=fake([2, 7], I32)),                                           # begins where inputs do
+    dict(target=fake([9, 50], F32, base=3 * M - 1796)),                    # its last value is counts[0]
+    dict(draft=fake([9, 50], F32, [64, 1], base=4 * M - 400)),             # next_tokens in its first row
+    dict(parents=fake([9], I32, base=2 * M + 52)),                         # behind accepted's first row
+    dict(cum=fake([3], I32, base=3 * M + 4)),
+    dict(counts=fake([2], I32, base=2 * M + 32)),                          # in accepted's rows
+    dict(next=fake([2], I32, base=3 * M + 4)),
+])
+def test_outputs_over_tensors(lib, change):  # noqa: F811
+    """A request's thread blocks each read its nodes: what one writes must not be what another reads."""
+    assert verify(lib, **change) == INVALID
+    assert lib.b2pa_last_error_message()
+
+
 def test_no_requests(lib):  # noqa: F811
     z = dict(tokens=fake([0], I32, base=0), parents=fake([0], I32, base=0), uniforms=fake([0], F32, base=0))
     assert verify(lib, target=fake([0, 50], F32, base=0), last=fake([0], F32, base=0), cum=fake([1], I32),
