@@ -538,9 +538,9 @@ int prefix_impl(const b2pa_tensor* q, const b2pa_tensor* k_pool, const b2pa_tens
     x.groups = (int)groups;
     x.max_pages = (int)prefix_tables->shape[1];
     x.max_len = max_prefix_len;
-    // (steps of a unit, units of a kv head: both at most)
+    // (steps of a unit, units of a kv head: both at most, whatever cum_groups and cum_q hold)
     const long long steps = std::max(max_prefix_len, max_kv_len) / kKvTile + 1 + kTreeUnitCost;
-    const long long units = 2LL * (pr.T / p.rows.tile_toks + 1) + groups + pr.B;
+    const long long units = groups * (pr.T / p.rows.tile_toks + 1LL) + pr.B;
     x.split = (double)steps * (double)units * (double)pr.Hkv < 2e9;
     cudaError_t e;
     if (plan.tc) {

@@ -341,6 +341,20 @@ def test_malformed_requests_and_groups(cuda_lib, path):
         cuda_lib.set_kernel_path("auto")
 
 
+@pytest.mark.parametrize("heads", [(8, 2), (32, 1)], ids=["one-tile", "two-tiles"])
+def test_groups_over_one_another(cuda_lib, heads):
+    """cum_groups that fall: flagged, nothing but the groups' rows written, and the next call is right."""
+    t = Batch([3, 2, 2], [200, 140, 60], [1] * 7, [12, 30, 300, 9, 200, 5, 7], *heads, 128, 16, seed=3)
+    d = t.dev()
+    room = torch.full((9, heads[0], 128), 5.0, dtype=torch.bfloat16, device=DEV)
+    for groups in ([0, 7, 0, 7], [3, 3, 0, 7]):
+        change = dict(cum_groups=torch.tensor(groups, dtype=torch.int32, device=DEV))
+        cuda_lib.prefix_attention(**t.dev(**change), out=room[1:8])
+        assert cuda_lib.device_status() == BAD_REQUEST
+        assert (room[0] == 5).all() and (room[8] == 5).all()
+    t.check(cuda_lib.prefix_attention(**d))
+
+
 @pytest.mark.parametrize("path", ["auto", "generic"])
 def test_bad_pages_read_as_zero(cuda_lib, path):
     t = Batch([2, 1], [200, 40], [1, 1, 1], [40, 30, 20], 8, 2, 128, 16, seed=3)
