@@ -267,7 +267,9 @@ __device__ void few_merge(const TreeParams& p, const TreeCtx& c, int w)
     }
 }
 
-// The warps that compute (w = 0 .. 7).
+// The warps that compute (w = 0 .. 7).  (No calls here, wait_at's neither: with one in a role that
+// has taken registers over, setmaxnreg has no effect on the whole kernel, and roles of both
+// kinds of CTA lose values to local memory.)
 template <int D, bool FP8, int kSets>
 __device__ void few_rows(const TreeParams& p, const TreeCtx& c, int w)
 {
@@ -318,7 +320,7 @@ __device__ void few_rows(const TreeParams& p, const TreeCtx& c, int w)
         }
         for (int i = 0; i < s.tiles; ++i) {
             const int left = s.kv_len - (s.j0 + i) * kKvTile - 16 * w;  // keys from this warp's first on
-            if (!wait_at(smem_u32(c.kv_full) + at_k.e * 8, at_k.phase, c))
+            if (!wait_bar(&c.kv_full[at_k.e], at_k.phase, c))
                 return;
             float x[kSets][4];
 #pragma unroll
@@ -406,7 +408,7 @@ __device__ void few_rows(const TreeParams& p, const TreeCtx& c, int w)
                 pt[a][0] = transposed(lo);
                 pt[a][1] = transposed(hi);
             }
-            if (!wait_at(smem_u32(c.kv_full) + at_v.e * 8, at_v.phase, c))
+            if (!wait_bar(&c.kv_full[at_v.e], at_v.phase, c))
                 return;
             const uint32_t v0 = ring + at_v.e * C::kKvBytes + key_v * 128;
             // keys behind the last: whatever lies there becomes 0

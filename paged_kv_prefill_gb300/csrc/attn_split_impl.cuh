@@ -146,12 +146,13 @@ cudaError_t launch_split(const TreeParams& q, cudaStream_t stream)
     TreeParams p = q;
     // What steps take, found by timing.  Batch: 64 single tokens of 8 x 4 heads behind 16384
     // shared keys, bf16; groups: 100 of 8 x 8 heads in 8 groups, e4m3.
-    //   step, batch: 2 / 2.5 / 3: 57 / 54 / 56 us;  groups: 3 / 3.5 / 4 / 5: 91 / 90 / 87 / 101
+    //   step, batch: 2 / 2.5 / 3: 57 / 54 / 56 us;  groups: 3 / 3.75 / 4: 82.8 / 81.8 / 84.7, with 17
+    //   requests each at least 115 / 107 / 110, with 16 at most (one query tile) 1.25 / 1.75 / 2 / 3: 76 / 64 / 66 / 73
     //   own_cost 1 / 2 / 3: batch 56 / 52 / 53, groups 99 / 86 / 89
     //   step, own keys by query tiles, batch: 0.75 / 1.5 / 2 / 3: 102 / 72 / 61 / 62
     if (kSets > 0) {
         p.prefix.own_cost = 2;
-        p.prefix.step = FP8 ? 4.f : kTiles == 2 ? 2.5f : 1.5f;
+        p.prefix.step = kTiles == 2 ? (FP8 ? 3.75f : 2.5f) : FP8 ? 1.75f : 1.5f;
     } else {
         p.prefix.step = FP8 ? 1.5f : 2.f;
     }
