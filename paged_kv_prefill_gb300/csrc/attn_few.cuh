@@ -489,7 +489,7 @@ __device__ __forceinline__ void few_roles(const TreeParams& p, const TreeCtx& c,
     if (warp < 4) {
         regs_dec<FP8 ? 96 : 104>();
         if (warp == 0)
-            tree_producer<C, 1, true>(p, c, run.start, run.end, run.first_b, run.base);
+            tree_producer<C, 1, true, kAll>(p, c, run.start, run.end, run.first_b, run.base);
         else if (warp == 1)
             few_feed<D, FP8, kSets>(p, c);
         else

@@ -203,10 +203,13 @@ __device__ __forceinline__ int tile_tokens(const TreeRows& r, const Seg& s, int 
     return min(r.tile_toks, s.toks - t * r.tile_toks);
 }
 
+// Which prefixes a CTA works on: all, those of more tokens than a query tile has, the others.
+enum TreeOnly { kAll, kMore, kOneTileOnly };
+
 // ---------------------------------------------------------------------------
 // warp 0
 // ---------------------------------------------------------------------------
-template <typename C, int kTiles, bool kPrefix>
+template <typename C, int kTiles, bool kPrefix, TreeOnly kOnly>
 __device__ void tree_producer(const TreeParams& p, const TreeCtx& c, long long pos, long long end, int b, long long base)
 {
     const int lane = threadIdx.x & 31;
@@ -216,7 +219,13 @@ __device__ void tree_producer(const TreeParams& p, const TreeCtx& c, long long p
     const int item_toks = kTiles * p.rows.tile_toks;
     uint32_t q = 0;  // ring entries filled
     bool ok = true;
-    TreeReq r = pos < end ? request_of<kPrefix>(p, b, item_toks) : TreeReq{};
+    auto request = [&](int v) {
+        TreeReq r = request_of<kPrefix>(p, v, item_toks);
+        if (kOnly != kAll && v < p.prefix.groups && (r.n > p.rows.tile_toks) != (kOnly == kMore))
+            r.items = 0;
+        return r;
+    };
+    TreeReq r = pos < end ? request(b) : TreeReq{};
     int4* note = p.part_seg + (long long)blockIdx.x * 4;  // of slots 0 and 1
     if (!kPrefix && lane < 2 && !p.whole)
         TreePart{}.write(note + 2 * lane);
@@ -229,7 +238,7 @@ __device__ void tree_producer(const TreeParams& p, const TreeCtx& c, long long p
         while (pos < end && !s.on) {
             while (pos - base >= r.work(p.Hkv) && b + 1 < requests_of<kPrefix>(p)) {
                 base += r.work(p.Hkv);
-                r = request_of<kPrefix>(p, ++b, item_toks);
+                r = request(++b);
             }
             const long long unit = (pos - base) / r.unit;
             const long long u0 = base + unit * r.unit;
@@ -1697,7 +1706,7 @@ __device__ __forceinline__ TreeRun tree_run(const TreeParams& p, int item_toks, 
     return run;
 }
 
-template <int D, bool FP8, int kTiles, bool kPrefix>
+template <int D, bool FP8, int kTiles, bool kPrefix, TreeOnly kOnly = kAll>
 __device__ __forceinline__ void tree_roles(const TreeParams& p, const TreeCtx& c, const TreeRun& run)
 {
     using C = TreeCfg<D, FP8, kTiles>;
@@ -1707,7 +1716,7 @@ __device__ __forceinline__ void tree_roles(const TreeParams& p, const TreeCtx& c
     if (warp < 4) {
         regs_dec<FP8 ? 96 : 104>();
         if (warp == 0)
-            tree_producer<C, kTiles, kPrefix>(p, c, run.start, run.end, run.first_b, run.base);
+            tree_producer<C, kTiles, kPrefix, kOnly>(p, c, run.start, run.end, run.first_b, run.base);
         else if (warp == 3)
             tree_feed<D, FP8, kTiles>(p, c);
         else if constexpr (C::kPairs)

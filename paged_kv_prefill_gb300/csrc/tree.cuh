@@ -51,9 +51,9 @@ struct PrefixParams {
     float4* cut_rec;      // [grid * 2][128]
     int* cut_ends;        // [grid]: whether the unit ends there
     // where prefixes and own keys have CTAs of their own: what a step (a kv tile, or
-    // one of those that a unit costs beyond them) of a prefix takes against one of a
-    // request's own; and how many of the latter a unit costs
-    float step;
+    // one of those that a unit costs beyond them) of a prefix with two query tiles, and
+    // with one, takes against one of a request's own; and how many of the latter a unit costs
+    float step[2];
     int own_cost;
     bool split;           // all units' steps fit 31 bits
 };

@@ -341,6 +341,23 @@ def test_malformed_requests_and_groups(cuda_lib, path):
         cuda_lib.set_kernel_path("auto")
 
 
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+@pytest.mark.parametrize("heads", [(16, 2), (32, 2)], ids=["8-heads", "16-heads"])
+@pytest.mark.parametrize("n", [1, 3])
+@pytest.mark.parametrize("reqs", [[3, 40, 16, 17, 1, 0, 33, 8], [20, 18], [4, 5, 6], [1, 0, 0, 48]],
+                         ids=["mixed", "large", "small", "ends"])
+def test_groups_of_all_sizes(cuda_lib, cache, heads, n, reqs):
+    """Groups of one query tile, of two and of more in one call."""
+    g = torch.Generator().manual_seed(11)
+    prefix = [0 if x == 0 else int(torch.randint(1, 900, (1,), generator=g)) for x in reqs]
+    if len(reqs) > 2:
+        prefix[2] = 0
+    R = sum(reqs)
+    t = Batch(reqs, prefix, [n] * R, torch.randint(n, 300, (R,), generator=g).tolist(), *heads, 128, 32, cache=cache, seed=5)
+    t.check(cuda_lib.prefix_attention(**t.dev()))
+    assert cuda_lib.device_status() == 0
+
+
 @pytest.mark.parametrize("heads", [(8, 2), (32, 1)], ids=["one-tile", "two-tiles"])
 def test_groups_over_one_another(cuda_lib, heads):
     """cum_groups that fall: flagged, nothing but the groups' rows written, and the next call is right."""
