@@ -1,8 +1,9 @@
-// attn_split.cuh -- attention of requests that share prefixes with two kinds of CTAs:
-// some attend the prefixes, on the tensor cores, with one query tile or with two that
-// share K and V (attn_tree.cuh); the others each request's own keys, with one query
-// tile or, for single tokens with few heads, as attn_few.cuh does.  How many of each is
-// found by every CTA from the lengths, by what a step of either kind takes.
+// attn_split.cuh -- attention of requests that share prefixes with several kinds of
+// CTAs: some attend the prefixes, on the tensor cores, with one query tile or with two
+// that share K and V (attn_tree.cuh; over an e4m3 cache there can be both); others each
+// request's own keys, with one query tile or, for single tokens with few heads, as
+// attn_few.cuh does.  How many of each is found by every CTA from the lengths, by what a
+// step of its kind takes.
 #pragma once
 
 #include "attn_few.cuh"
