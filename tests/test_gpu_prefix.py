@@ -279,6 +279,26 @@ def test_many_requests_and_groups(cuda_lib):
     assert cuda_lib.device_status() == 0
 
 
+@pytest.mark.parametrize("cache,D", [("bf16", 128), ("e4m3", 128), ("bf16", 64)], ids=["bf16", "e4m3", "d64"])
+@pytest.mark.parametrize("sizes", [[0, 1, 2, 5, 20, 40], [0, 1, 2, 5, 16]], ids=["two-tiles", "one-tile"])
+@pytest.mark.parametrize("most", [1, 2])
+def test_several_requests_per_thread(cuda_lib, cache, D, sizes, most):
+    """More requests and groups than threads in a CTA, of a query tile (16 tokens) and of more, with tokens and without."""
+    r = random.Random(len(sizes) + most)
+    reqs = [r.choice(sizes) for _ in range(160)]
+    B = sum(reqs) + 4
+    ns = [r.choice([0, 1, 1, most]) for _ in range(B)]
+    kvs = [max(n, r.randint(1, 200)) for n in ns]
+    t = Batch(reqs, [r.randint(0, 300) for _ in reqs], ns, kvs, 8, 1, D, 32, cache=cache, seed=6, alone=2)
+    assert B + 160 > 512
+    d, at = t.dev(), [t.cum[b] for b in t.starts]
+    t.check(cuda_lib.prefix_attention(**d))
+    # told how many tokens a group has at most (one query tile then, where none has more), or fewer than it has
+    for count in (max(y - x for x, y in zip(at, at[1:])), 1):
+        t.check(cuda_lib.prefix_attention(**d, max_group_q_len=count))
+    assert cuda_lib.device_status() == 0
+
+
 def test_a_shared_prefix_is_the_decode_batch(cuda_lib):
     """The same batch with the prefix's pages in every request's table: both within the bounds of the formula."""
     B, P, pre = 7, 32, 320
