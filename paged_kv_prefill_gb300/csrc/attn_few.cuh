@@ -246,13 +246,11 @@ __device__ void few_merge(const TreeParams& p, const TreeCtx& c, int w)
                 float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
                 for (int k = 0; k < kFewWarps; ++k) {
-                    // (a sum that is no number keeps its weight, whatever its maximum)
-                    const float f = x[k].x == -INFINITY && x[k].y == 0.f ? 0.f : x[k].x == top ? 1.f : ex2_approx(x[k].x - top);
+                    // (as in prefix_merge_kernel: what is no number stays so whatever its weight)
+                    const float f = x[k].x == top ? 1.f : ex2_approx(x[k].x - top);
                     const float4 v = *reinterpret_cast<const float4*>(sum + (k * C::kRows + row) * C::kCols + few_place(row, 4 * d4));
-                    if (f != 0.f) {
-                        total = fmaf(f, x[k].y, total);
-                        y = make_float4(fmaf(f, v.x, y.x), fmaf(f, v.y, y.y), fmaf(f, v.z, y.z), fmaf(f, v.w, y.w));
-                    }
+                    total = fmaf(f, x[k].y, total);
+                    y = make_float4(fmaf(f, v.x, y.x), fmaf(f, v.y, y.y), fmaf(f, v.z, y.z), fmaf(f, v.w, y.w));
                 }
                 if (r0 + lane / kLanes < rows) {
                     to[(long long)(c0 / 4 + d4) * rows + row] = y;

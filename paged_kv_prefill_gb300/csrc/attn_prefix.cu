@@ -78,18 +78,16 @@ __global__ void __launch_bounds__(32 * kMergeWarps) prefix_merge_kernel(const __
     for (int k = 0; k < kCols4; ++k)
         a[k] = make_float4(0.f, 0.f, 0.f, 0.f);
     auto merge = [&](float x_m, float x_l, const float4 v[kCols4]) {
+        // (nothing is left out where a weight is 0: a part that is no number, of a maximum
+        // below all others' or of none, stays so)
         const float top = fmaxf(m, x_m);
-        const float old = m == top ? 1.f : ex2_approx(m - top);
-        // (a sum that is no number keeps its weight, whatever its maximum)
-        const float w = x_m == -INFINITY && x_l == 0.f ? 0.f : x_m == top ? 1.f : ex2_approx(x_m - top);
+        const float old = m == top ? 1.f : ex2_approx(m - top), w = x_m == top ? 1.f : ex2_approx(x_m - top);
         m = top;
-        den = fmaf(den, old, w != 0.f ? w * x_l : 0.f);
+        den = fmaf(den, old, w * x_l);
 #pragma unroll
-        for (int k = 0; k < kCols4; ++k) {
-            const float4 y = w != 0.f ? v[k] : make_float4(0.f, 0.f, 0.f, 0.f);
-            a[k] = make_float4(fmaf(a[k].x, old, w * y.x), fmaf(a[k].y, old, w * y.y), fmaf(a[k].z, old, w * y.z),
-                               fmaf(a[k].w, old, w * y.w));
-        }
+        for (int k = 0; k < kCols4; ++k)
+            a[k] = make_float4(fmaf(a[k].x, old, w * v[k].x), fmaf(a[k].y, old, w * v[k].y),
+                               fmaf(a[k].z, old, w * v[k].z), fmaf(a[k].w, old, w * v[k].w));
     };
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
