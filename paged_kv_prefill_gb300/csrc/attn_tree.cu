@@ -90,17 +90,18 @@ __global__ void __launch_bounds__(D * 2) tree_merge_kernel(const __grid_constant
             a[k] = make_float4(a[k].x * old, a[k].y * old, a[k].z * old, a[k].w * old);
 #pragma unroll
         for (int c = 0; c < kBatch; ++c) {
-            // (a sum that is no number keeps its weight, whatever its maximum)
-            const float w = ml[c].x == -INFINITY && ml[c].y == 0.f ? 0.f : top == -INFINITY ? 1.f : ex2_approx(ml[c].x - top);
-            if (w != 0.f) {
-                den = fmaf(w, ml[c].y, den);
+            if (c0 + c >= segs || !at.valid)
+                break;
+            // (nothing is left out where a weight is 0: a part that is no number, of a
+            // maximum below all others' or of none, stays so)
+            const float w = ml[c].x == top ? 1.f : ex2_approx(ml[c].x - top);
+            den = fmaf(w, ml[c].y, den);
 #pragma unroll
-                for (int k = 0; k < kCols4; ++k) {
-                    a[k].x = fmaf(w, v[c][k].x, a[k].x);
-                    a[k].y = fmaf(w, v[c][k].y, a[k].y);
-                    a[k].z = fmaf(w, v[c][k].z, a[k].z);
-                    a[k].w = fmaf(w, v[c][k].w, a[k].w);
-                }
+            for (int k = 0; k < kCols4; ++k) {
+                a[k].x = fmaf(w, v[c][k].x, a[k].x);
+                a[k].y = fmaf(w, v[c][k].y, a[k].y);
+                a[k].z = fmaf(w, v[c][k].z, a[k].z);
+                a[k].w = fmaf(w, v[c][k].w, a[k].w);
             }
         }
     }

@@ -6,6 +6,7 @@ import pytest
 import torch
 
 from test_gpu_prefix import F8, Batch
+from test_gpu_tree import Batch as Trees
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda:0"
@@ -119,4 +120,46 @@ def test_values_behind_weights_that_underflow(cuda_lib, path, cfg):
     put(t, t.v, t.table[0], 2, slice(9, 10))   # in another warp's keys than the large one
     out = cuda_lib.prefix_attention(**t.dev())
     assert torch.isnan(out[0, :, 9]).all() and torch.isfinite(out[1, :, 9]).all()
+    assert cuda_lib.device_status() == 0
+
+
+TREES = {"bf16": dict(H=8, Hkv=2, D=128), "d64": dict(H=8, Hkv=2, D=64), "e4m3": dict(H=8, Hkv=2, D=128, cache="e4m3")}
+
+
+@pytest.mark.parametrize("cfg", TREES)
+@pytest.mark.parametrize("n", [5, 40])
+@pytest.mark.parametrize("tiles", [16, 64])
+def test_trees_cut_over_ctas(cuda_lib, cfg, n, tiles):
+    """The same for the context of a drafted tree."""
+    t = Trees([n], [tiles * 128 + n], P=128, seed=4, **TREES[cfg])
+    d = t.dev()
+    pool = d["kv_cache"][0]
+    for count in (1, 2, 3):
+        for first in range(0, tiles - count + 1):
+            pages = [int(x) for x in t.table[0, first : first + count]]
+            for pg in pages:
+                nan(pool[pg])
+            out = cuda_lib.tree_attention(**d)
+            assert torch.isnan(out).all(), (count, first)
+            for pg in pages:
+                pool[pg].view(torch.uint8).copy_(t.k[pg].view(torch.uint8))
+    t.check(cuda_lib.tree_attention(**d))
+    assert cuda_lib.device_status() == 0
+
+
+@pytest.mark.parametrize("cfg", TREES)
+def test_tree_values_behind_weights_that_underflow(cuda_lib, cfg):
+    """Scores 0 in the context, 181 and more in the nodes' own keys; NaN among the context's values."""
+    n, tiles = 5, 32
+    t = Trees([n], [tiles * 128 + n], P=128, seed=4, **TREES[cfg])
+    t.q.fill_(4.0 * math.sqrt(128 / t.D))
+    t.k.copy_(torch.zeros(t.k.shape))
+    for key in range(tiles * 128, tiles * 128 + n):
+        t.k[int(t.table[0, key // 128]), :, key % 128] = torch.full(
+            (t.Hkv, t.D), 200.0 if t.cache == "e4m3" else 4.0).to(t.k.dtype)
+    for tile in (0, 9, 31):
+        put(t, t.v, t.table[0], tile * 128 + 3, slice(tile, tile + 1))
+    out = cuda_lib.tree_attention(**t.dev())
+    assert torch.isnan(out[..., [0, 9, 31]]).all()
+    assert torch.isfinite(out[..., 1:9]).all()
     assert cuda_lib.device_status() == 0
