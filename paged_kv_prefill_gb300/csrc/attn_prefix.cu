@@ -29,13 +29,15 @@ namespace b2pa {
 
 namespace {
 
-// Block (x, b, z): 32 of request b's rows (kv head, token, head of it), a lane each, and
-// kMergeWarps * kMergeCols4 * 4 columns from z times that on.  Parts are added in the
+// Block (x, y): 32 of all rows (kv head, token, head of it), a lane each, and
+// kMergeWarps * kMergeCols4 * 4 columns from y times that on: as many blocks as rows
+// take, whatever the bounds on the requests say.  Parts are added in the
 // order of the keys.  Latency alone, about four accesses that depend on one another:
-// lengths, the row's records, its parts; so nothing waits to know whether it is
-// needed (what was not written is read within the workspace and left out), a unit's
-// further parts are loaded kBatch together, and a row's columns are spread over
-// several SMs (a block of all of them had 1200 instructions for each of 16 warps).
+// the row's records and the search for its request, lengths, its parts; so nothing
+// waits to know whether it is needed (what was not written is read within the
+// workspace and left out), a unit's further parts are loaded kBatch together, and a row's
+// columns are spread over several SMs (a block of all of them had 1200
+// instructions for each of 16 warps).
 constexpr int kMergeCols4 = 4, kMergeWarps = 2;
 
 template <int D>
@@ -44,16 +46,11 @@ __global__ void __launch_bounds__(32 * kMergeWarps) prefix_merge_kernel(const __
     constexpr float kLog2e = 1.4426950408889634f;
     constexpr int kBatch = 4, kCols4 = kMergeCols4;
     pdl_wait();
-    const int lane = threadIdx.x & 31, warp = blockIdx.z * kMergeWarps + (threadIdx.x >> 5), b = blockIdx.y, G = p.rows.G;
-    const TreeReq own = prefix_request(p, p.prefix.groups + b, 1);
-    const int g = prefix_group(p, b);
-    const int all = own.n * p.H;
-    if (!own.ok || blockIdx.x * 32 >= all)
-        return;
-    const int row = min((int)blockIdx.x * 32 + lane, all - 1);  // (the last row several times)
-    const int per = own.n * G, kvh = row / per, in = row - kvh * per;
-    const int tok = own.q0 + in / G, h = kvh * G + in % G;
-    const long long at = ((long long)kvh * p.T + own.q0) * G + in;
+    const int lane = threadIdx.x & 31, warp = blockIdx.y * kMergeWarps + (threadIdx.x >> 5);
+    const unsigned G = p.rows.G, rows = (unsigned)p.T * (unsigned)p.H;
+    const unsigned at = min(blockIdx.x * 32 + lane, rows - 1);  // (the last row several times)
+    const unsigned kvh = at / (p.T * G), in = at - kvh * (p.T * G);
+    const int tok = (int)(in / G), h = (int)(kvh * G + in % G);
     PrefixRow x[2];
     float4 v[2][kCols4];
     auto load = [&](const float4* o, long long rows0, const PrefixRow& x, float4 v[kCols4]) {
@@ -65,12 +62,14 @@ __global__ void __launch_bounds__(32 * kMergeWarps) prefix_merge_kernel(const __
     for (int i = 0; i < 2; ++i)
         x[i] = PrefixRow::unpack(p.prefix.part_rec[i][at], at);
     const float sink = p.sinks != nullptr ? p.sinks[h] * kLog2e : -INFINITY;
-    const TreeReq group = prefix_request(p, max(g, 0), 1);  // (of no group: not used)
+    const Rising cum(p.cum_q, p.B), groups = prefix_groups(p);
 #pragma unroll
     for (int i = 0; i < 2; ++i)
-        load(p.prefix.part_o[i], at - x[i].tile_row, x[i], v[i]);
-    if (g >= 0 && !group.ok)
-        return;
+        load(p.prefix.part_o[i], (long long)at - x[i].tile_row, x[i], v[i]);
+    TreeReq own;
+    const int b = prefix_owner(p, cum, tok, &own), g = prefix_group(p, groups, b);
+    const TreeReq group = prefix_request(p, max(g, 0), 1);  // (of no group: not used)
+    const bool mine = blockIdx.x * 32 + lane < rows && b >= 0 && !(g >= 0 && !group.ok);
     const bool shared = g >= 0 && group.kv_len > 0;
     float m = -INFINITY, den = 0.f;
     float4 a[kCols4];
@@ -91,11 +90,11 @@ __global__ void __launch_bounds__(32 * kMergeWarps) prefix_merge_kernel(const __
     };
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-        if (i == kPrefixShared && !shared)
-            continue;
-        merge(x[i].m, x[i].l, v[i]);
+        const bool some = mine && (i == kPrefixOwn || shared);
+        if (some)
+            merge(x[i].m, x[i].l, v[i]);
         // the rest of the unit: parts of the CTAs behind
-        bool more = x[i].cta >= 0 && x[i].cta < p.grid;
+        bool more = some && x[i].cta >= 0 && x[i].cta < p.grid;
         for (int c0 = x[i].cta + 1; __any_sync(0xffffffffu, more); c0 += kBatch) {
             float2 ml[kBatch];
             float4 z[kBatch][kCols4];
@@ -117,7 +116,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) prefix_merge_kernel(const __
                 }
         }
     }
-    if ((int)blockIdx.x * 32 + lane >= all)
+    if (!mine)
         return;
     if (m != -INFINITY)
         den += ex2_approx(sink - m);
@@ -134,6 +133,9 @@ template <int D, bool FP8>
 cudaError_t launch_prefix(TreeParams& p, int tiles, bool few, cudaStream_t stream)
 {
     const int G = p.rows.G;
+    const long long rows = (long long)p.T * p.H;
+    if (rows > 0x7FFFFFFF)  // (more than 2^40 bytes of workspace)
+        return cudaErrorInvalidValue;
     p.prefix.own_cost = kTreeUnitCost;
     // The batch and the groups of attn_split_impl.cuh: 75 and 164 us with all work in one
     // kind of CTA, 61 and 135 with own keys by query tiles on CTAs of their own, 52 and 77 with
@@ -149,10 +151,7 @@ cudaError_t launch_prefix(TreeParams& p, int tiles, bool few, cudaStream_t strea
         e = tiles == 1 ? launch_tree_kernel<D, FP8, 1, true>(p, stream) : launch_tree_kernel<D, FP8, 2, true>(p, stream);
     if (e != cudaSuccess)
         return e;
-    const long long rows = (long long)std::min(p.max_q_len, p.T) * p.H;
-    if (rows == 0)
-        return e;  // (no request may have a token)
-    const dim3 grid((unsigned)((rows + 31) / 32), p.B, D / (4 * kMergeCols4 * kMergeWarps));
+    const dim3 grid((unsigned)((rows + 31) / 32), D / (4 * kMergeCols4 * kMergeWarps));
     return launch_pdl(prefix_merge_kernel<D>, grid, 32 * kMergeWarps, 0, stream, p);
 }
 

@@ -320,7 +320,7 @@ __global__ void __launch_bounds__(kGenericWarps * 32) prefix_generic_kernel(cons
     const TreeReq own = prefix_request(p, groups + lo_b, 1);
     if (!own.ok || tok < own.q0 || tok >= own.q0 + own.n)
         return;  // a rejected request, or a token no request owns
-    const int g = prefix_group(p, lo_b);
+    const int g = prefix_group(p, prefix_groups(p), lo_b);
     int keys[2] = {0, own.kv_len - own.n + tok - own.q0 + 1};  // seen of the prefix, and of its own
     if (g >= 0) {
         const TreeReq r = prefix_request(p, g, 1);

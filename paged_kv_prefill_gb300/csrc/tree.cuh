@@ -183,17 +183,75 @@ __device__ __forceinline__ int requests_of(const TreeParams& p)
     return kPrefix ? p.prefix.groups + p.B : p.B;
 }
 
-// The group of request b, by a whole warp; -1: none.  (cum_groups rise; of empty
-// groups that start there, the last starts the one that holds b.)
-__device__ __forceinline__ int prefix_group(const TreeParams& p, int b)
-{
-    const int lane = threadIdx.x & 31;
-    int upto = 0;
-    for (int i = 0; i <= p.prefix.groups; i += 32) {
-        const bool in = i + lane <= p.prefix.groups && p.prefix.cum_groups[i + lane] <= b;
-        upto += __popc(__ballot_sync(0xffffffffu, in));
+// Numbers that rise, to be looked through by a whole warp: each lane holds one of 32
+// of them, so that a search ends in registers or in the few between two of these.
+struct Rising {
+    const int* x;
+    int n, step, some;
+    __device__ __forceinline__ Rising(const int* x_, int n_) : x(x_), n(n_), step(n_ / 32 + 1)
+    {
+        const int lane = threadIdx.x & 31;
+        some = lane * step < n ? x[lane * step] : 0x7FFFFFFF;
     }
-    return upto > p.prefix.groups ? -1 : upto - 1;
+    // The last i with x[i] <= value, a lane's own; -1: none.
+    __device__ __forceinline__ int last_at_most(int value) const
+    {
+        int lo = 0;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+            lo += __shfl_sync(0xffffffffu, some, lo + o) <= value && (lo + o) * step < n ? o : 0;
+        if (__shfl_sync(0xffffffffu, some, lo) > value || lo * step >= n)
+            return -1;
+        int hi = min(lo * step + step, n) - 1;
+        lo *= step;
+        while (lo < hi) {
+            const int mid = lo + (hi - lo + 1) / 2;
+            if (x[mid] <= value)
+                lo = mid;
+            else
+                hi = mid - 1;
+        }
+        return lo;
+    }
+};
+
+// The group of request b, by a whole warp; -1: none.  (Of empty groups that start
+// there, the last starts the one that holds b.)
+__device__ __forceinline__ Rising prefix_groups(const TreeParams& p) { return Rising(p.prefix.cum_groups, p.prefix.groups + 1); }
+__device__ __forceinline__ int prefix_group(const TreeParams& p, const Rising& groups, int b)
+{
+    const int g = groups.last_at_most(b);
+    return g < p.prefix.groups ? g : -1;
+}
+
+// The request whose token tok is, by a whole warp; -1: it is nobody's, or a malformed
+// request's.  cum: cum_q's first B; *r: that request.
+__device__ __forceinline__ int prefix_owner(const TreeParams& p, const Rising& cum, int tok, TreeReq* r)
+{
+    auto owns = [&](int b) {
+        *r = prefix_request(p, p.prefix.groups + b, 1);
+        return r->ok && tok >= r->q0 && tok < r->q0 + r->n;
+    };
+    int b = max(cum.last_at_most(tok), 0);
+    bool found = owns(b);
+    if (!__all_sync(0xffffffffu, found)) {
+        // behind the last request or before the first; else something is malformed, cum_q
+        // may fall, and all requests are asked
+        const int lane = threadIdx.x & 31;
+        int least = 0x7FFFFFFF, most = -0x7FFFFFFF;
+        for (int i = lane; i <= p.B; i += 32) {
+            least = min(least, p.cum_q[i]);
+            most = max(most, p.cum_q[i]);
+        }
+        least = __reduce_min_sync(0xffffffffu, least);
+        most = __reduce_max_sync(0xffffffffu, most);
+        if (tok >= least && tok < most)
+            for (int i = 0; i < p.B && !found; ++i)
+                if (p.cum_q[i] <= tok && tok < p.cum_q[i + 1])
+                    found = owns(b = i);
+        __syncwarp();
+    }
+    return found ? b : -1;
 }
 
 // A partial row: its maximum (log2 units) and sum; the CTA whose successors
