@@ -692,6 +692,8 @@ B2PA_API int b2pa_compact_kv(const b2pa_tensor* k_pool, const b2pa_tensor* v_poo
  * last page that is not full is replaced by a free one, count 1, and src[i] and
  * dst[i] (contiguous int32 [n]) say which page to copy to which (b2pa_copy_pages,
  * for each layer's pools); else both are -1.  Columns behind the copied ones stay.
+ * (A last page whose id is outside the pool stands in src[i] as it is: the copy passes
+ * it over.)
  * A parent may have many children.  A child that is named twice (the later ones),
  * or that is a parent in the same call, is malformed; a request that fails leaves
  * its child empty and -1 in src and dst.

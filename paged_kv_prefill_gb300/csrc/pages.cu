@@ -452,9 +452,12 @@ __global__ void __launch_bounds__(kTakeThreads) take_pages_kernel(const __grid_c
             const int from = parents[i], r = rows[i], whole = base[i] >> 1;
             const int* in = p.tables + (long long)from * p.stride;
             if (lane == 0) {
-                p.src[i] = rest ? in[whole] : -1;
+                const int page = rest ? in[whole] : -1;
+                p.src[i] = page;
                 if (!rest)
                     p.dst[i] = -1;
+                else if (page < 0 || page >= p.N)
+                    atomicOr(p.err, (unsigned)B2PA_DEV_BAD_PAGE);
             }
             if (bad || none)
                 continue;

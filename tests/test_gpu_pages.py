@@ -204,6 +204,29 @@ def test_fork_of_parents_on_page_borders(cuda_lib):
     run_fork(cuda_lib, led, [0, 1, 2, 3, 4, 5, 2, 2, 5], [10, 11, 12, 13, 14, 15, 16, 17, 18])
 
 
+@pytest.mark.parametrize("bad", [-1, -3, 40, 2 ** 31 - 1])
+def test_fork_of_a_last_page_outside_the_pool(cuda_lib, bad):
+    """Flagged; the child has a page of its own there, and what there is to copy names the page as it stands, so that
+    the copy passes it over and flags it too.  Pages of parents that are whole are flagged as before."""
+    led = Ledger(5, 40, 16, 4)
+    led.fill(0, 50)
+    led.fill(1, 39)
+    led.table[0][3] = bad
+    led.dev()
+    src, dst = cuda_lib.fork_pages(led.t, led.s, led.c, ints([0, 1]), ints([2, 3]), 16)
+    assert cuda_lib.device_status() == BAD_PAGE
+    free = [i for i in range(40) if led.refs[i] == 0]
+    assert src.tolist() == [bad, led.table[1][2]] and dst.tolist() == free[:2]
+    assert led.s.tolist() == [50, 39, 50, 39, 0]
+    assert led.t[2].tolist() == led.table[0][:3] + [free[0]] and led.t[3, :3].tolist() == led.table[1][:2] + [free[1]]
+    pool = torch.randint(0, 100, (40, 2, 16, 16), device=DEV).to(torch.bfloat16)
+    k, v = pool.clone(), pool.clone()
+    cuda_lib.copy_pages((k, v), src, dst)
+    assert cuda_lib.device_status() == BAD_PAGE
+    pool[free[1]] = pool[led.table[1][2]]
+    assert torch.equal(k, pool) and torch.equal(v, pool)
+
+
 def test_requests_that_are_malformed(cuda_lib):
     """They change nothing, and those beside them are served."""
     led = Ledger(12, 60, 16, 4, 9)
