@@ -676,7 +676,8 @@ B2PA_API int b2pa_compact_kv(const b2pa_tensor* k_pool, const b2pa_tensor* v_poo
  * Results do not depend on timing, as long as calls on one ledger are ordered (by
  * one stream, or events).  All three are asynchronous on `stream`, one kernel, and
  * no-ops for n = 0; the ledger's tensors are written in place and must
- * not overlap one another or the other arguments.  A malformed request (a row outside
+ * not overlap one another or the other arguments, nor src dst (refused; what lies between
+ * the rows of block_tables is no part of it).  A malformed request (a row outside
  * [0, R), a length below 0 or of more than max_pages pages) sets B2PA_DEV_BAD_REQUEST
  * and changes nothing; one for which there are not enough free pages (those that
  * the requests before it want are counted, whether they got them or not) sets

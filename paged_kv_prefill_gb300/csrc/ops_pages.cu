@@ -3,6 +3,7 @@
 // Argument checks and launches; nothing here synchronises.
 #include <algorithm>
 #include <cstring>
+#include <initializer_list>
 #include <utility>
 
 #include "../../include/b2pa.h"
@@ -67,22 +68,55 @@ int check_ints(const b2pa_tensor* t, const char* what, int64_t n)
 
 int* ints(const b2pa_tensor* t) { return static_cast<int*>(t->data); }
 
-// Whether two tensors of 4-byte elements, strides >= 0, lie over one another (from the
-// first to the last element of each).
+// A tensor of 4-byte elements as rows of bytes.
+struct RowBytes {
+    long long at, bytes, step, n;
+    explicit RowBytes(const b2pa_tensor* t)
+        : at((long long)reinterpret_cast<uintptr_t>(t->data)),
+          bytes(4 * t->shape[t->ndim - 1]),
+          step(t->ndim == 2 ? 4 * t->stride[0] : 0),
+          n(t->ndim == 2 ? t->shape[0] : 1)
+    {
+        if (step < 0) {  // from the other end
+            at += (n - 1) * step;
+            step = -step;
+        }
+        if (step <= bytes && n > 1) {  // in one piece
+            bytes += (n - 1) * step;
+            n = 1;
+        }
+    }
+    // whether the bytes [from, from + count) reach into a row
+    bool reached(long long from, long long count) const
+    {
+        if (n <= 0 || bytes <= 0 || count <= 0 || from + count <= at)
+            return false;
+        const long long last = n > 1 ? std::min(n - 1, (from + count - 1 - at) / step) : 0;  // that starts before their end
+        return from < at + last * step + bytes;
+    }
+};
+
+// Whether two tensors of 4-byte elements, unit stride in their rows, share any.  (What
+// lies between the rows of one is no part of it.)
 bool meet(const b2pa_tensor* a, const b2pa_tensor* b)
 {
-    auto bytes = [](const b2pa_tensor* t) {
-        int64_t last = 0;
-        for (int k = 0; k < t->ndim; ++k) {
-            if (t->shape[k] == 0)
-                return (int64_t)0;
-            last += (t->shape[k] - 1) * t->stride[k];
-        }
-        return 4 * (last + 1);
-    };
-    const int64_t na = bytes(a), nb = bytes(b);
-    const uintptr_t pa = reinterpret_cast<uintptr_t>(a->data), pb = reinterpret_cast<uintptr_t>(b->data);
-    return na > 0 && nb > 0 && pa < pb + (uintptr_t)nb && pb < pa + (uintptr_t)na;
+    RowBytes x(a), y(b);
+    if (x.n > y.n)
+        std::swap(x, y);
+    // (of two with room between their rows, row by row of the one that has fewer)
+    for (long long i = 0; i < x.n; ++i)
+        if (y.reached(x.at + i * x.step, x.bytes))
+            return true;
+    return false;
+}
+
+// Whether `out` shares any element with one of the others (null: none).
+bool meets_any(const b2pa_tensor* out, std::initializer_list<const b2pa_tensor*> others)
+{
+    for (const b2pa_tensor* t : others)
+        if (t && meet(out, t))
+            return true;
+    return false;
 }
 
 int copy_impl(const b2pa_tensor* k_pool, const b2pa_tensor* v_pool, const b2pa_tensor* k_scales,
@@ -171,9 +205,8 @@ int compact_impl(const b2pa_tensor* k_pool, const b2pa_tensor* v_pool, const b2p
         return fail(B2PA_ERR_INVALID_ARG, "accepted must be int32 [B, width] with unit column stride");
     if (B == 0)
         return B2PA_OK;
-    for (const b2pa_tensor* t : {seq_lens, counts, cum_q, accepted, block_tables})
-        if (meet(t, new_lens))
-            return fail(B2PA_ERR_INVALID_ARG, "new_lens must not be an input: several blocks read those");
+    if (meets_any(new_lens, {seq_lens, counts, cum_q, accepted, block_tables}))
+        return fail(B2PA_ERR_INVALID_ARG, "new_lens must not be an input: several blocks read those");
     long long pieces = 0;
     for (int i = 0; i < p.planes; ++i)
         pieces += (long long)p.plane[i].row / p.plane[i].vec * pr.Hkv;
@@ -253,9 +286,8 @@ int verify_impl(const b2pa_tensor* target, const b2pa_tensor* draft, const b2pa_
     // (a request's CTAs each read its nodes and have to find the same)
     const b2pa_tensor* outs[3] = {accepted, counts, next};
     for (int i = 0; i < 3; ++i) {
-        for (const b2pa_tensor* t : {target, draft, tokens, parents, uniforms, last, cum_q})
-            if (t && meet(t, outs[i]))
-                return fail(B2PA_ERR_INVALID_ARG, "outputs must not overlap inputs");
+        if (meets_any(outs[i], {target, draft, tokens, parents, uniforms, last, cum_q}))
+            return fail(B2PA_ERR_INVALID_ARG, "outputs must not overlap inputs");
         if (meet(outs[i], outs[(i + 1) % 3]))
             return fail(B2PA_ERR_INVALID_ARG, "accepted, counts and next_tokens must be three tensors");
     }
@@ -332,10 +364,21 @@ int parse_ledger(const b2pa_tensor* block_tables, const b2pa_tensor* seq_lens, c
     return B2PA_OK;
 }
 
+// The ledger's three are written in place, and read and written by several CTAs:
+// nothing else of a call may lie over them.
+int check_apart(const b2pa_tensor* block_tables, const b2pa_tensor* seq_lens, const b2pa_tensor* page_refs,
+                std::initializer_list<const b2pa_tensor*> others)
+{
+    bool over = meets_any(block_tables, {seq_lens, page_refs}) || meet(seq_lens, page_refs);
+    for (const b2pa_tensor* t : others)
+        over = over || meets_any(t, {block_tables, seq_lens, page_refs});
+    return over ? fail(B2PA_ERR_INVALID_ARG,
+                       "block_tables, seq_lens and page_refs must not overlap one another or other arguments")
+                : B2PA_OK;
+}
+
 int run_ledger(LedgerParams& p, cudaStream_t stream, int which)
 {
-    if (p.n == 0)
-        return B2PA_OK;
     int dev, st;
     DevInfo di;
     if ((st = device_info(&dev, &di)) || (st = status_word(dev, stream, &p.err)))
@@ -386,8 +429,10 @@ int b2pa_free_pages(const b2pa_tensor* block_tables, const b2pa_tensor* seq_lens
 {
     return guarded([&] {
         LedgerParams p;
-        const int st = parse_ledger(block_tables, seq_lens, page_refs, rows, "rows", page_size, &p);
-        return st ? st : run_ledger(p, reinterpret_cast<cudaStream_t>(stream), 0);
+        int st = parse_ledger(block_tables, seq_lens, page_refs, rows, "rows", page_size, &p);
+        if (st || p.n == 0 || (st = check_apart(block_tables, seq_lens, page_refs, {rows})))
+            return st;
+        return run_ledger(p, reinterpret_cast<cudaStream_t>(stream), 0);
     });
 }
 
@@ -399,10 +444,11 @@ int b2pa_fork_pages(const b2pa_tensor* block_tables, const b2pa_tensor* seq_lens
         LedgerParams p;
         int st = parse_ledger(block_tables, seq_lens, page_refs, children, "children", page_size, &p);
         if (st || (st = check_ints(parents, "parents", p.n)) || (st = check_ints(src, "src", p.n)) ||
-            (st = check_ints(dst, "dst", p.n)))
+            (st = check_ints(dst, "dst", p.n)) || p.n == 0 ||
+            (st = check_apart(block_tables, seq_lens, page_refs, {children, parents, src, dst})))
             return st;
-        if (p.n > 0 && src->data == dst->data)
-            return fail(B2PA_ERR_INVALID_ARG, "dst in the place of src");
+        if (meet(src, dst))
+            return fail(B2PA_ERR_INVALID_ARG, "src and dst must not overlap");
         p.parents = ints(parents);
         p.src = ints(src);
         p.dst = ints(dst);
@@ -416,7 +462,8 @@ int b2pa_grow_pages(const b2pa_tensor* block_tables, const b2pa_tensor* seq_lens
     return guarded([&] {
         LedgerParams p;
         int st = parse_ledger(block_tables, seq_lens, page_refs, rows, "rows", page_size, &p);
-        if (st || (st = check_ints(new_lens, "new_lens", p.n)))
+        if (st || (st = check_ints(new_lens, "new_lens", p.n)) || p.n == 0 ||
+            (st = check_apart(block_tables, seq_lens, page_refs, {rows, new_lens})))
             return st;
         p.to = ints(new_lens);
         return run_ledger(p, reinterpret_cast<cudaStream_t>(stream), 2);

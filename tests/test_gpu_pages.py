@@ -260,6 +260,24 @@ def test_more_pages_wanted_than_an_int_counts(cuda_lib):
     assert cuda_lib.device_status() == NO_PAGES
 
 
+def test_arguments_between_the_rows_of_a_table(cuda_lib):
+    """The room behind a table's rows is no part of it: lengths and rows may lie there."""
+    led = Ledger(6, 40, 16, 4, 3, stride=12)
+    led.fill(0, 20)
+    led.dev()
+    room = led.t.as_strided((6, 12), (12, 1))
+    room[2, 4:7], room[3, 4:7] = ints([0, 1, 3]), ints([33, 16, 1])
+    bad = led.grow([0, 1, 3], [33, 16, 1])
+    cuda_lib.grow_pages(led.t, led.s, led.c, room[2, 4:7], room[3, 4:7], 16)
+    led.same()
+    assert cuda_lib.device_status() == bad == 0
+    src, dst, bad = led.fork([0, 1], [2, 4])
+    cuda_lib.fork_pages(led.t, led.s, led.c, ints([0, 1]), ints([2, 4]), 16, src=room[5, 5:7], dst=room[5, 7:9])
+    led.same()
+    assert room[5, 5:9].tolist() == src + dst and cuda_lib.device_status() == bad == 0
+    assert room[2, 4:7].tolist() == [0, 1, 3] and (room[0, 4:] == 0).all()
+
+
 def test_rows_that_become_shorter(cuda_lib):
     """Pages behind the new length go back, those that others hold stay theirs, and nobody gets them in the same call."""
     led = Ledger(8, 12, 4, 9, 4)

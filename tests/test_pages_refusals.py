@@ -140,6 +140,36 @@ def test_ledger_of_no_requests(lib, call):  # noqa: F811
     assert ledger(lib, call, rows=none, more=none, src=none, dst=none) == OK
 
 
+APART = dict(table=fake([6, 9], I32, [12, 1], base=5 * M), seq=fake([6], I32, base=6 * M), refs=fake([50], I32, base=7 * M),
+             rows=fake([3], I32, base=8 * M))
+AT = dict(table=5 * M, seq=6 * M, refs=7 * M, rows=8 * M, more=2 * M, src=3 * M, dst=4 * M)
+PAIRS = [("free", a, b) for a, b in (("table", "seq"), ("table", "refs"), ("table", "rows"), ("seq", "refs"), ("seq", "rows"),
+                                     ("refs", "rows"))]
+PAIRS += [(call, a, "more") for call in ("fork", "grow") for a in ("table", "seq", "refs")]
+PAIRS += [("fork", a, b) for b in ("src", "dst") for a in ("table", "seq", "refs")] + [("fork", "src", "dst")]
+
+
+def place(name, base):
+    return fake([6, 9], I32, [12, 1], base=base) if name == "table" else fake(
+        [dict(seq=6, refs=50).get(name, 3)], I32, base=base)
+
+
+@pytest.mark.parametrize("call,a,b", PAIRS)
+def test_ledger_over_itself_or_its_arguments(lib, call, a, b):  # noqa: F811
+    """A tensor that is written over any that is read or written: by its first and by its last element."""
+    last = {"table": 4 * (5 * 12 + 8), "seq": 4 * 5, "refs": 4 * 49}
+    for base in (AT[a], AT[a] + last.get(a, 8), AT[a] - last.get(b, 8)):
+        assert ledger(lib, call, **{**APART, b: place(b, base)}) == INVALID
+        assert b"overlap" in lib.b2pa_last_error_message()
+
+
+def test_ledger_arguments_that_reach_into_a_row(lib):  # noqa: F811
+    """(Between a table's rows there may be room, in which a tensor may lie whole.)"""
+    for at in (12 + 8, 12 + 10, 2 * 12 - 1, 5 * 12 + 8, -2):
+        assert ledger(lib, "grow", **{**APART, "more": fake([3], I32, base=5 * M + 4 * at)}) == INVALID
+        assert b"overlap" in lib.b2pa_last_error_message()
+
+
 def test_python_functions_want_cuda_tensors(lib):  # noqa: F811
     import paged_kv_prefill_gb300 as b2pa
 
