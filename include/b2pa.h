@@ -521,8 +521,8 @@ B2PA_API int b2pa_tree_attention(const b2pa_tensor* q, const b2pa_tensor* k_pool
 /*
  * b2pa_prefix_attention -- attention of requests in groups that share a cached
  * prefix (one prompt sampled several times, a common system prompt, questions
- * about one document): the prefix's keys and values are read once for a group.  No
- * counterpart on the pages.
+ * about one document): the prefix's keys and values are read once for a group (shapes
+ * that take the CUDA-core path: by every row).  No counterpart on the pages.
  *
  * Requests cum_groups[g] .. cum_groups[g+1] - 1 are group g and share the first
  * prefix_lens[g] keys, on the pages of prefix_tables[g].  Behind them request b has
@@ -541,7 +541,8 @@ B2PA_API int b2pa_tree_attention(const b2pa_tensor* q, const b2pa_tensor* k_pool
  *  prefix_tables  [groups, columns] int32, stride[1] == 1.
  *  prefix_lens    contiguous int32 [groups].
  *  cum_groups     contiguous int32 [groups + 1], not falling, within 0 .. B.
- *  max_q_len      upper bound on every n.
+ *  max_q_len      upper bound on every n.  (Results are right for any; 1, and at most a query tile's
+ *                 tokens, 128 / (H / Hkv), have kernels of their own for the requests' own keys.)
  *  max_group_q_len  a group's tokens at most, or any larger number (it is taken as T at
  *                 most): sizes the query tiles; results are right for any value.
  *  max_prefix_len, max_kv_len   upper bounds on prefix_lens and seq_lens; at most 2^31 - 257.
@@ -703,8 +704,10 @@ B2PA_API int b2pa_compact_kv(const b2pa_tensor* k_pool, const b2pa_tensor* v_poo
  * until they hold new_lens[i] tokens, and that length.  A row that becomes shorter
  * (the tokens of a tree that were not accepted) gives back the pages behind: they
  * lose a holder, and are free from the next call on.  Of a row named twice the later
- * ones are malformed.  (A page that is not full must have one holder before tokens
- * are written to it; b2pa_fork_pages sees to that.)
+ * ones are malformed.  A page that is not full must have one holder before tokens
+ * are written to it.  b2pa_fork_pages sees to that; a row that is made shorter than what
+ * it shares with others may end inside a page of theirs, and is for reading alone: to
+ * write there, fork it to an empty row, which gets its own copy of that page, and free it.
  */
 B2PA_API int b2pa_free_pages(const b2pa_tensor* block_tables, const b2pa_tensor* seq_lens,
                              const b2pa_tensor* page_refs, const b2pa_tensor* rows, int32_t page_size,

@@ -17,10 +17,10 @@
 // of their own (attn_split.cuh).
 //
 // Measured: 64 single tokens of 8 x 4 heads, D = 128, behind 16384 shared keys and 64 to
-// 1024 of their own: 52 us, 3.9 TB/s (0.58 of the copy rate); 100 tokens of 8 x 8 heads in 8
+// 1024 of their own: 51 us, 3.9 TB/s (0.59 of the copy rate); 100 tokens of 8 x 8 heads in 8
 // groups over an e4m3 cache: 77 us, 0.53; 16 questions of 16 to 64 tokens behind 32768 keys,
 // D = 64: 194 us, 914 TFLOP/s (0.47 of the bf16 rate); 8 samples of one prompt of 2048
-// keys: 15.7 us, latency.
+// keys: 15.2 us, latency.
 #include <algorithm>
 
 #include "attn_split.cuh"
@@ -137,8 +137,8 @@ cudaError_t launch_prefix(TreeParams& p, int tiles, bool few, cudaStream_t strea
     if (rows > 0x7FFFFFFF)  // (more than 2^40 bytes of workspace)
         return cudaErrorInvalidValue;
     p.prefix.own_cost = kTreeUnitCost;
-    // The batch and the groups of attn_split_impl.cuh: 75 and 164 us with all work in one
-    // kind of CTA, 61 and 135 with own keys by query tiles on CTAs of their own, 52 and 77 with
+    // The batch and the groups of attn_split_impl.cuh: 73 and 163 us with all work in one
+    // kind of CTA, 62 and 126 with own keys by query tiles on CTAs of their own, 51 and 77 with
     // single tokens' by warps.  A request of more than a query tile is the same work as a
     // prefix, and has nothing from the split.
     cudaError_t e;

@@ -186,11 +186,14 @@ cudaError_t launch_split(const TreeParams& q, cudaStream_t stream)
     TreeParams p = q;
     // What steps take, found by timing.  Batch: 64 single tokens of 8 x 4 heads behind 16384
     // shared keys, bf16; groups: 100 of 8 x 8 heads in 8 groups of 3 to 24, e4m3.
-    //   step[0], batch: 2 / 2.5 / 3: 57 / 54 / 56 us;  groups: 3 / 3.75 / 4: 83 / 82 / 85, with 17
-    //   requests each at least: 115 / 107 / 110
-    //   step[1], groups: 1.75 / 2.25 / 2.75: 84 / 77 / 81;  with at most 16 requests each, where
-    //   that is the only kind of prefix (kTiles 1): 1.25 / 1.75 / 2 / 3: 76 / 64 / 66 / 73
-    //   own_cost 1 / 2 / 3: batch 56 / 52 / 53, groups 99 / 86 / 89
+    //   step[0], batch: 2 / 2.5 / 3: 53 / 51 / 56 us;  groups: 3 / 3.75 / 4.25: 86 / 77 / 77, with 17
+    //   requests each at least: 115 / 107 / 111
+    //   step[1], groups: 1.75 / 2.25 / 2.75: 82 / 77 / 83;  with at most 16 requests each, where
+    //   that is the only kind of prefix (kTiles 1): 1.25 / 1.75 / 2.25: 76 / 66 / 65
+    //   own_cost 1 / 2 / 3: batch 53 / 51 / 53, groups 80 / 77 / 83
+    // Other shapes have the same numbers, which are not the best for all.  The batch at D = 64:
+    // 38 us, 40 with step[0] 2, 42 with 3.  With 16 heads per kv head (two sets of rows, whose own keys take
+    // longer): the batch 43, 38 with step[0] 2; the groups 78, 74 with step[0] 3, 73 with own_cost 3.
     //   own keys by query tiles, step[0], batch: 0.75 / 1.5 / 2 / 3: 102 / 72 / 61 / 62
     if (kSets > 0) {
         p.prefix.own_cost = 2;

@@ -58,9 +58,10 @@
 // but its steps end at 2^-14 of the row's largest: of a tail of 16384 keys behind a
 // lead of 11 nats 0.84 was lost.)  What bounds this: the ring.  V in f16, two tiles
 // of it, leaves room for 128 KB of K and V on their way (96 KB with two query tiles).
-// So one Q buffer does, and the converting warps free a V entry as soon as they
-// have its rows in registers (161 us; 164 once they are converted), and its roles'
-// code is kept short (146 us; 158 unrolled: the instruction caches).
+// So one Q buffer does.  The converting warps free a V entry when they have the second
+// half of its rows in registers, which no longer gains anything over freeing it once all is
+// converted (145 us; 143 then), and the roles' code is kept short (158 us unrolled: the
+// instruction caches).
 //
 // bf16 caches.  P is bf16 (off by half a step, 2^-8 of itself, over all of fp32's
 // range), since both operands of an MMA have one type and V's range needs bf16.
@@ -1553,7 +1554,7 @@ __device__ __forceinline__ void tree_setup(const TreeParams& p, uint8_t* smem, T
     c.err = p.err;
     c.wait_limit_ns = p.wait_limit_ns;
     c.item_slot = reinterpret_cast<volatile int*>(smem + C::kOffItems);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = tid >> 5;
     if (tid == 0) {
         for (int e = 0; e < C::kEntries; ++e) {
             mbar_init(&c.kv_full[e], 1);

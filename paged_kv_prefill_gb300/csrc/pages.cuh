@@ -43,7 +43,7 @@ struct CompactParams {
     int B;
 };
 
-// Requests of one fork or grow call: each keeps two words in shared memory.
+// Requests of one fork or grow call: each keeps four words in shared memory (grow: uses three).
 constexpr int kLedgerMax = 4096;
 
 struct LedgerParams {

@@ -128,7 +128,7 @@ __device__ __forceinline__ TreeReq tree_request(const TreeParams& p, int b, int 
 }
 
 // (of a shared prefix, whose units are cut between many CTAs, with a first segment
-// each: 8 samples 15.7 us with 2, 16.2 with 4; 8 e4m3 groups 93 with 2, 99 with 1)
+// each: 8 samples 15.1 us with 1, 15.2 with 2, 15.8 with 4; 8 e4m3 groups 83, 77 and 82)
 constexpr int kPrefixUnitCost = 2;
 
 // The same of requests that share prefixes.  They are attended as groups + B of

@@ -7,7 +7,7 @@
 
 namespace b2pa {
 
-// Nodes of a request at most: five words each in shared memory.
+// Nodes of a request at most: six words each in shared memory.
 constexpr int kVerifyMaxNodes = 4096;
 
 struct VerifyParams {

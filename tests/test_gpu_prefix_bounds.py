@@ -122,3 +122,32 @@ def test_requests_beside_offsets_that_fall(cuda_lib, cache, first):
     assert cuda_lib.device_status() == 1  # BAD_REQUEST
     assert (out[3] == 5).all() and (out[10:] == 5).all()
     t.check(out, [0, 1, 3, 4, 5, 6])
+
+
+@pytest.mark.parametrize("length", [96, 100, 127, 64])
+def test_rows_of_a_ledger(cuda_lib, length):
+    """A prompt forked to neighbouring rows, which grow: the prefix and the own keys are views of the ledger's rows."""
+    P, R, N, pre = 32, 6, 40, length // 32
+    g = torch.Generator(device=DEV).manual_seed(length)
+    pools = tuple(torch.randn((N, 2, P, 128), generator=g, device=DEV).to(BF) for _ in "kv")
+    i = lambda x: torch.tensor(x, dtype=torch.int32, device=DEV)  # noqa: E731
+    table, seq, refs = torch.zeros((R, 12), dtype=torch.int32, device=DEV), i([0] * R), i([0] * N)
+    cuda_lib.grow_pages(table, seq, refs, i([0]), i([length]), P)
+    src, dst = cuda_lib.fork_pages(table, seq, refs, i([0] * 4), i([1, 2, 3, 4]), P)
+    cuda_lib.copy_pages(pools, src, dst)
+    cuda_lib.grow_pages(table, seq, refs, i([1, 2, 3, 4]), seq[1:5] + i([1, 40, 33, 7]), P)
+    assert cuda_lib.device_status() == 0
+    q = torch.randn((4, 8, 128), generator=g, device=DEV).to(BF)
+    out = cuda_lib.prefix_attention(q, pools, table[:1, :pre], i([pre * P]), i([0, 4]), table[1:5, pre:],
+                                    seq[1:5] - pre * P, 1, pre * P, 4 * P, 128 ** -0.5, 1.0, i([0, 1, 2, 3, 4]))
+    assert cuda_lib.device_status() == 0
+    rows, lens = table.tolist(), seq.tolist()
+    for b in range(4):
+        k, v = (x[rows[1 + b][: -(-lens[1 + b] // P)]].transpose(0, 1).reshape(2, -1, 128)[:, : lens[1 + b]].double()
+                for x in pools)
+        x = q[b].double().view(2, 4, 128)
+        p = torch.softmax(x @ k.transpose(1, 2) * 128 ** -0.5, -1)
+        want, mean = (p @ v).view(8, 128), (p @ v.abs()).view(8, 128)
+        # bf16's half step of the result, of each probability, and what is in 32 bits (see test_gpu_prefix.py)
+        ds = 2.0 ** -24 * 136 * (x.abs() @ k.abs().transpose(1, 2)).amax() * 128 ** -0.5
+        assert ((out[b].double() - want).abs() <= 2.0 ** -8 * want.abs() + mean * (2.0 ** -8 + 2 * ds + 2.0 ** -15)).all()
